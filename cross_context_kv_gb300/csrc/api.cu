@@ -85,6 +85,64 @@ static bool overlaps_bytes(const void* a, size_t na, const void* b, size_t nb) {
     return a0 < b0 + nb && b0 < a0 + na;
 }
 
+// Checks a pool: format, shape, strides, pointers and their alignment.
+static kvfix_status check_pool(const kvfix_pool& p, const char* fn) {
+    if (p.format != KVFIX_POOL_BF16 && p.format != KVFIX_POOL_E4M3 && p.format != KVFIX_POOL_INT4)
+        return fail(KVFIX_EINVAL, "%s: unknown pool format %d", fn, p.format);
+    if (p.layers < 0 || p.slots < 0) return fail(KVFIX_EINVAL, "%s: negative pool layers/slots", fn);
+    if (p.kv_heads < 1 || (p.head_dim != 64 && p.head_dim != 128))
+        return fail(KVFIX_EINVAL, "%s: a pool needs kv_heads >= 1 and head_dim 64 or 128 (got %d heads x %d)", fn,
+                    p.kv_heads, p.head_dim);
+    const long long head = p.format == KVFIX_POOL_BF16 ? 2 * p.head_dim
+                           : p.format == KVFIX_POOL_E4M3 ? p.head_dim : p.head_dim / 2;
+    if (p.stride_layer < 0 || p.stride_slot < 0 || p.stride_layer % 16 || p.stride_slot % 16)
+        return fail(KVFIX_EINVAL, "%s: pool strides must be non-negative multiples of 16 bytes", fn);
+    if (p.slots > 1 && p.stride_slot < p.kv_heads * head)
+        return fail(KVFIX_EINVAL, "%s: pool stride_slot %lld is smaller than a slot's codes (%lld bytes)", fn,
+                    (long long)p.stride_slot, p.kv_heads * head);
+    if (!p.k || !p.v || !aligned16(p.k) || !aligned16(p.v))
+        return fail(KVFIX_EINVAL, "%s: pool planes must be 16-byte aligned device pointers", fn);
+    if (p.format != KVFIX_POOL_BF16 && (!p.k_scales || !p.v_scales))
+        return fail(KVFIX_EINVAL, "%s: a quantised pool needs k_scales and v_scales", fn);
+    if (p.format == KVFIX_POOL_INT4 && (((uintptr_t)p.k_scales | (uintptr_t)p.v_scales) & 3u))
+        return fail(KVFIX_EINVAL, "%s: int4 scales must be 4-byte aligned", fn);
+    return KVFIX_OK;
+}
+
+// Bytes a pool's code plane and its scales extend over.
+static size_t pool_code_bytes(const kvfix_pool& p) {
+    if (p.layers == 0 || p.slots == 0) return 0;
+    const size_t head = p.format == KVFIX_POOL_BF16 ? 2 * p.head_dim
+                        : p.format == KVFIX_POOL_E4M3 ? p.head_dim : p.head_dim / 2;
+    return (size_t)(p.layers - 1) * (size_t)p.stride_layer + (size_t)(p.slots - 1) * (size_t)p.stride_slot +
+           (size_t)p.kv_heads * head;
+}
+static size_t pool_scale_bytes(const kvfix_pool& p) {
+    const size_t rows = (size_t)p.layers * (size_t)p.kv_heads * (size_t)p.slots;
+    return p.format == KVFIX_POOL_BF16 ? 0 : p.format == KVFIX_POOL_E4M3 ? rows : rows * (size_t)(p.head_dim / 32) * 4;
+}
+
+// Whether [a, a + n) meets any of the pool's four buffers.
+static bool pool_meets(const kvfix_pool& p, const void* a, size_t n) {
+    const size_t c = pool_code_bytes(p), s = pool_scale_bytes(p);
+    return overlaps_bytes(p.k, c, a, n) || overlaps_bytes(p.v, c, a, n) || overlaps_bytes(p.k_scales, s, a, n) ||
+           overlaps_bytes(p.v_scales, s, a, n);
+}
+static bool pool_meets_plane(const kvfix_pool& p, const void* a, const kvfix_kv_desc& d) {
+    uintptr_t lo, hi;
+    extent(a, d, &lo, &hi);
+    return pool_meets(p, (const void*)lo, (size_t)(hi - lo));
+}
+// Whether two of the pool's own buffers meet (a pool that is written needs them apart).
+static bool pool_meets_itself(const kvfix_pool& p) {
+    const void* b[4] = {p.k, p.v, p.k_scales, p.v_scales};
+    const size_t n[4] = {pool_code_bytes(p), pool_code_bytes(p), pool_scale_bytes(p), pool_scale_bytes(p)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlaps_bytes(b[i], n[i], b[j], n[j])) return true;
+    return false;
+}
+
 static kvfix_status launched(cudaError_t e, const char* what) {
     if (e != cudaSuccess) return cuda_fail(e, what);
     return KVFIX_OK;
@@ -106,7 +164,7 @@ kvfix_status kvfix_check_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "kvfix_check_status: stream synchronize");
     unsigned bits = read_status_repair(s) | read_status_diff(s) | read_status_draft(s) | read_status_lowrank(s) |
                     read_status_anchor(s) | read_status_layout(s) | read_status_selftest(s) |
-                    read_status_lowrank_draft(s);
+                    read_status_lowrank_draft(s) | read_status_pool(s);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "kvfix_check_status: status read");
     if (bits & 8u) return fail(KVFIX_EDEVICE, "a kernel's shared-memory layout check failed; its work was skipped");
@@ -857,6 +915,52 @@ kvfix_status kvfix_diff_gather_split(const kvfix_bf16* master_k, const kvfix_bf1
                                        block_tokens, out_k, out_v, out, (cudaStream_t)stream, mask_v, offsets_v,
                                        payload_v, entries_v),
                     fn);
+}
+
+// The checks kvfix_pool_write and kvfix_pool_read share.
+static kvfix_status check_pool_rows(const char* fn, const kvfix_bf16* k, const kvfix_bf16* v, const kvfix_kv_desc& d,
+                                    const int32_t* delta, double rope_base, const int32_t* slot_mapping,
+                                    const kvfix_pool& pool) {
+    kvfix_status st;
+    char what[64];
+    snprintf(what, sizeof what, "%s: k", fn);
+    if ((st = check_plane(k, d, what)) != KVFIX_OK) return st;
+    snprintf(what, sizeof what, "%s: v", fn);
+    if ((st = check_plane(v, d, what)) != KVFIX_OK) return st;
+    if ((st = check_pool(pool, fn)) != KVFIX_OK) return st;
+    if (pool.layers != d.layers || pool.kv_heads != d.kv_heads || pool.head_dim != d.head_dim)
+        return fail(KVFIX_EINVAL, "%s: the pool must have the planes' layers, heads and head_dim", fn);
+    if ((long long)d.chunks * d.layers > 0x7fffffffll)
+        return fail(KVFIX_EINVAL, "%s: chunks * layers must be below 2^31", fn);
+    // a (token, head) of a run is counted in 32 bits
+    if ((long long)d.tokens * d.kv_heads > 0x7fff0000ll)
+        return fail(KVFIX_EINVAL, "%s: tokens * kv_heads must be at most 2^31 - 2^16", fn);
+    if (d.chunks > 0 && d.tokens > 0 && !slot_mapping) return fail(KVFIX_EINVAL, "%s: slot_mapping is null", fn);
+    if (delta && (!(rope_base > 1.0) || !isfinite(rope_base)))
+        return fail(KVFIX_EINVAL, "%s: rope_base must be finite and > 1", fn);
+    if (pool_meets_plane(pool, k, d) || pool_meets_plane(pool, v, d))
+        return fail(KVFIX_EINVAL, "%s: the pool overlaps the planes", fn);
+    return KVFIX_OK;
+}
+
+kvfix_status kvfix_pool_write(const kvfix_bf16* k, const kvfix_bf16* v, kvfix_kv_desc src, const int32_t* delta,
+                              double rope_base, const int32_t* slot_mapping, kvfix_pool pool, void* stream) {
+    const char* fn = "kvfix_pool_write";
+    kvfix_status st = check_pool_rows(fn, k, v, src, delta, rope_base, slot_mapping, pool);
+    if (st != KVFIX_OK) return st;
+    if (pool_meets_itself(pool)) return fail(KVFIX_EINVAL, "%s: the pool's buffers overlap each other", fn);
+    RopeTheta th = make_theta(delta ? rope_base : 2.0, src.head_dim);
+    return launched(launch_pool_write(k, v, src, delta, th, slot_mapping, pool, (cudaStream_t)stream), fn);
+}
+
+kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapping, const int32_t* delta, double rope_base,
+                             kvfix_bf16* k, kvfix_bf16* v, kvfix_kv_desc out, void* stream) {
+    const char* fn = "kvfix_pool_read";
+    kvfix_status st = check_pool_rows(fn, k, v, out, delta, rope_base, slot_mapping, pool);
+    if (st != KVFIX_OK) return st;
+    if (overlaps(k, out, v, out)) return fail(KVFIX_EINVAL, "%s: k and v overlap", fn);
+    RopeTheta th = make_theta(delta ? rope_base : 2.0, out.head_dim);
+    return launched(launch_pool_read(pool, slot_mapping, delta, th, k, v, out, (cudaStream_t)stream), fn);
 }
 
 kvfix_status kvfix_selftest_wait(int64_t limit_cycles, const int32_t* flag, void* stream) {

@@ -159,6 +159,13 @@ cudaError_t launch_anchor_correct(const AnchorPlanes& pl, const kvfix_kv_desc& d
                                   const int32_t* delta, const RopeTheta& th, const int32_t* accept,
                                   cudaStream_t s, const AnchorGateOut* gate = nullptr);
 
+// Paged pools: rows in (quantised) and out.
+unsigned read_status_pool(cudaStream_t stream);
+cudaError_t launch_pool_write(const uint16_t* k, const uint16_t* v, const kvfix_kv_desc& d, const int32_t* delta,
+                              const RopeTheta& th, const int32_t* slots, const kvfix_pool& pool, cudaStream_t s);
+cudaError_t launch_pool_read(const kvfix_pool& pool, const int32_t* slots, const int32_t* delta, const RopeTheta& th,
+                             uint16_t* k, uint16_t* v, const kvfix_kv_desc& d, cudaStream_t s);
+
 // Bounded-wait self test.
 unsigned read_status_selftest(cudaStream_t stream);
 cudaError_t launch_selftest_wait(long long limit_cycles, const int* flag, cudaStream_t s);

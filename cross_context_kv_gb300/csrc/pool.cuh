@@ -1,0 +1,125 @@
+// pool.cuh -- the stored forms of a paged pool's rows (kvfix_pool), shared by the kernels
+// that write, read and attend over a pool.
+//
+//   bf16  the values.
+//   e4m3  one byte per value and one byte b per (slot, head): value = e4m3(code) 2^(b-127).
+//         The scale is a power of two, so scaling a value to its code's range is exact, and
+//         every stored value is exactly a bf16 value (4 significant bits, an exponent within
+//         [-110-9, 119+8]): nothing is lost when rows are read back or become bf16
+//         tensor-core operands.
+//   int4  groups of 32 values share a scale and a zero, both bf16: value =
+//         bf16(scale code + zero), code in 0..15.  A 32-bit word holds 8 codes, value 2i in
+//         nibble i and value 2i+1 in nibble i+4, so that (word >> 4i) & 0x000f000f is the
+//         pair (2i, 2i+1) as two 16-bit lanes.
+#pragma once
+
+#include "common.cuh"
+
+namespace kvfix {
+
+constexpr int kQGroup = 32;         // values per int4 group
+constexpr int kE4m3MinExp = -110;   // smallest and largest power-of-two scale of a row
+constexpr int kE4m3MaxExp = 119;
+
+// One layer-major code plane and its scales.
+struct PoolPlane {
+    unsigned char* codes;
+    unsigned char* scales;  // e4m3: [layers][heads][slots] bytes; int4: [layers][heads][slots][dim/32] words
+};
+
+struct PoolView {
+    int format, layers, slots, heads, dim;
+    long long sl, ss;  // byte strides of layer and slot
+    PoolPlane plane[2];
+};
+
+inline PoolView view_of(const kvfix_pool& p) {
+    PoolView v;
+    v.format = p.format;
+    v.layers = p.layers;
+    v.slots = p.slots;
+    v.heads = p.kv_heads;
+    v.dim = p.head_dim;
+    v.sl = p.stride_layer;
+    v.ss = p.stride_slot;
+    v.plane[0] = {(unsigned char*)p.k, (unsigned char*)p.k_scales};
+    v.plane[1] = {(unsigned char*)p.v, (unsigned char*)p.v_scales};
+    return v;
+}
+
+// Code bytes of one (slot, head).
+__host__ __device__ constexpr int pool_head_bytes(int format, int dim) {
+    return format == KVFIX_POOL_BF16 ? 2 * dim : format == KVFIX_POOL_E4M3 ? dim : dim / 2;
+}
+
+// 2^k, k in [-126, 127].
+__device__ __forceinline__ float pow2f(int k) { return __uint_as_float((unsigned)(k + 127) << 23); }
+
+// ------------------------------------------------------------- e4m3 -> bf16, exactly
+// A code s eeee mmm moved to the bf16 fields s 0000eeee mmm0000 is the value times 2^-120
+// (subnormal codes included, as bf16 subnormals), so one or two exact multiplications by
+// powers of two give the stored value: mul holds (2^(120+min(k,7)), 2^max(k-7,0)) as pairs.
+struct E4m3Scale {
+    __nv_bfloat162 a, b;
+    bool two;
+};
+
+__device__ __forceinline__ E4m3Scale e4m3_scale(int k) {
+    E4m3Scale s;
+    const unsigned a = (unsigned)(min(k, 7) + 120 + 127) << 7, b = (unsigned)(max(k - 7, 0) + 127) << 7;
+    const unsigned aa = a | (a << 16), bb = b | (b << 16);
+    s.a = *reinterpret_cast<const __nv_bfloat162*>(&aa);
+    s.b = *reinterpret_cast<const __nv_bfloat162*>(&bb);
+    s.two = k > 7;
+    return s;
+}
+
+// Four codes (bytes in order) to two bf16 pairs.  The code 0x7f (NaN) would read as 480:
+// it is replaced by bf16 NaN.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(unsigned codes, const E4m3Scale& s) {
+    const unsigned y0 = __byte_perm(codes, 0u, 0x1404), y1 = __byte_perm(codes, 0u, 0x3424);
+    unsigned r0 = (y0 & 0x80008000u) | ((y0 >> 4) & 0x07f007f0u);
+    unsigned r1 = (y1 & 0x80008000u) | ((y1 >> 4) & 0x07f007f0u);
+    __nv_bfloat162 p0 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r0), s.a);
+    __nv_bfloat162 p1 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r1), s.a);
+    if (s.two) {
+        p0 = __hmul2(p0, s.b);
+        p1 = __hmul2(p1, s.b);
+    }
+    return make_uint2(*reinterpret_cast<unsigned*>(&p0), *reinterpret_cast<unsigned*>(&p1));
+}
+
+// Whether one of four codes is NaN (0x7f or 0xff).
+__device__ __forceinline__ bool e4m3x4_has_nan(unsigned codes) {
+    const unsigned m = (codes & 0x7f7f7f7fu) + 0x01010101u;  // a byte's top bit: its code is 0x7f
+    return (m & 0x80808080u) != 0u;
+}
+
+__device__ __forceinline__ uint2 e4m3x4_nan(unsigned codes, uint2 v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (((codes >> (8 * i)) & 0x7fu) == 0x7fu) {
+            unsigned& w = i < 2 ? v.x : v.y;
+            w = (i & 1) ? (w & 0xffffu) | 0x7fff0000u : (w & 0xffff0000u) | 0x7fffu;
+        }
+    return v;
+}
+
+// ------------------------------------------------------------- int4 -> bf16
+// Eight codes to four bf16 pairs: 128 + code is exact in bf16, so is the difference, and one
+// fused multiply-add rounds once.
+__device__ __forceinline__ uint4 int4x8_to_bf16(unsigned word, __nv_bfloat162 scale, __nv_bfloat162 zero) {
+    unsigned r[4];
+    const unsigned k128 = 0x43004300u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        unsigned c = ((word >> (4 * i)) & 0x000f000fu) | k128;
+        const __nv_bfloat162 n =
+            __hsub2(*reinterpret_cast<__nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&k128));
+        const __nv_bfloat162 v = __hfma2(n, scale, zero);
+        r[i] = *reinterpret_cast<const unsigned*>(&v);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+}  // namespace kvfix

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -34,9 +35,19 @@ class KvDesc(ctypes.Structure):
                 ("stride_token", ctypes.c_int64)]
 
 
+class PoolDesc(ctypes.Structure):
+    """kvfix_pool: strides in bytes."""
+    _fields_ = [("format", ctypes.c_int32), ("layers", ctypes.c_int32), ("slots", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("stride_layer", ctypes.c_int64), ("stride_slot", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
 # name -> (restype, argtypes); mirrors include/kvfix.h
 P, I32, I64, F64, SZ, D = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double,
                            ctypes.c_size_t, KvDesc)
+PD = PoolDesc
 SIGNATURES = {
     "kvfix_version": (ctypes.c_int, []),
     "kvfix_last_error": (ctypes.c_char_p, []),
@@ -62,6 +73,8 @@ SIGNATURES = {
     "kvfix_diff_gather_split": (ctypes.c_int, [P, P, D, P, P, P, P, P, P, I64, I64, I32, I32, P, P, D, P]),
     "kvfix_diff_restore_split": (ctypes.c_int, [P, P, D, P, P, P, P, P, P, I64, I64, I32, I32, P, F64, P, P, P, D,
                                                 P]),
+    "kvfix_pool_write": (ctypes.c_int, [P, P, D, P, F64, P, PD, P]),
+    "kvfix_pool_read": (ctypes.c_int, [PD, P, P, F64, P, P, D, P]),
     "kvfix_repair_rows": (ctypes.c_int, [P, P, D, P, P, D, P, I32, P, P]),
     "kvfix_anchor_gate_workspace_bytes": (SZ, [D, I32, I32]),
     "kvfix_anchor_gate": (ctypes.c_int, [P, D, P, P, I32, I32, I32, F64, F64, P, P, P, P, P, SZ, P]),
@@ -569,3 +582,116 @@ def anchor_gate_correct(k_src, v_src, factors: dict, prefix: int, delta, rope_ba
                                          _ptr(d), _ptr(g), _ptr(hbar), _ptr(acc), _ptr(w_k), _ptr(w_v), _ptr(out_k),
                                          _ptr(out_v), plane_desc(out_k), _ptr(ws), ws.numel(), _stream(k_src)))
     return out_k, out_v, w_k, w_v, d, g, hbar, acc
+
+
+# --------------------------------------------------------------------- paged pools
+
+POOL_FORMATS = {"bf16": 0, "e4m3": 1, "int4": 2}
+
+
+class Pool(NamedTuple):
+    """A paged pool's planes (or some consecutive layers of them).
+    format    "bf16", "e4m3" or "int4"
+    k, v      bf16: bfloat16 [layers][slots][heads][dim]; e4m3: uint8 of that shape;
+              int4: uint8 [layers][slots][heads][dim/2]
+    *_scales  bf16: None; e4m3: uint8 [layers][heads][slots]; int4: bfloat16
+              [layers][heads][slots][dim/32][2] (scale, zero)"""
+    format: str
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor | None = None
+    v_scales: torch.Tensor | None = None
+
+    def layer(self, i: int) -> "Pool":
+        """The pool's layer i alone, as shared_attend takes it (views)."""
+        one = lambda t: None if t is None else t[i:i + 1]  # noqa: E731
+        return Pool(self.format, self.k[i:i + 1], self.v[i:i + 1], one(self.k_scales), one(self.v_scales))
+
+
+def pool_empty(format: str, layers: int, slots: int, kv_heads: int, head_dim: int, device="cuda") -> Pool:
+    """A pool of `slots` rows per layer, its contents zero."""
+    if format not in POOL_FORMATS:
+        raise ValueError(f"unknown pool format {format!r}")
+    z = lambda *shape, dtype: torch.zeros(*shape, dtype=dtype, device=device)  # noqa: E731
+
+    def plane():
+        if format == "bf16":
+            return z(layers, slots, kv_heads, head_dim, dtype=torch.bfloat16), None
+        if format == "e4m3":
+            return (z(layers, slots, kv_heads, head_dim, dtype=torch.uint8),
+                    z(layers, kv_heads, slots, dtype=torch.uint8))
+        return (z(layers, slots, kv_heads, head_dim // 2, dtype=torch.uint8),
+                z(layers, kv_heads, slots, head_dim // 32, 2, dtype=torch.bfloat16))
+
+    (k, ks), (v, vs) = plane(), plane()
+    return Pool(format, k, v, ks, vs)
+
+
+def pool_desc(pool: Pool) -> PoolDesc:
+    """Descriptor of a pool; checks dtypes, devices, shapes and strides."""
+    fmt = POOL_FORMATS.get(pool.format)
+    if fmt is None:
+        raise ValueError(f"unknown pool format {pool.format!r}")
+    code = torch.bfloat16 if fmt == 0 else torch.uint8
+    k, v = pool.k, pool.v
+    if k.dtype != code or v.dtype != code or not k.is_cuda or k.device != v.device:
+        raise TypeError(f"pool planes of a {pool.format} pool must be CUDA {code} tensors on one device")
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("pool planes must be [layers][slots][heads][width], of one shape and strides")
+    L, n, H, W = k.shape
+    sl, ss, sh, sw = k.stride()
+    if (sw != 1 or sh != W) and H * W > 1:
+        raise ValueError("a pool slot's heads must be contiguous")
+    size = k.element_size()
+    dim = 2 * W if fmt == 2 else W
+    if fmt:
+        want = (L, H, n) if fmt == 1 else (L, H, n, dim // 32, 2)
+        kind = torch.uint8 if fmt == 1 else torch.bfloat16
+        for s in (pool.k_scales, pool.v_scales):
+            if s is None or s.dtype != kind or s.shape != want or not s.is_contiguous() or s.device != k.device:
+                raise TypeError(f"scales of this {pool.format} pool must be contiguous {kind} tensors {want} "
+                                "on the planes' device")
+    return PoolDesc(fmt, L, n, H, dim, sl * size if L > 1 else 0, ss * size if n > 1 else H * W * size,
+                    k.data_ptr(), v.data_ptr(), pool.k_scales.data_ptr() if fmt else None,
+                    pool.v_scales.data_ptr() if fmt else None)
+
+
+def _pool_rows(k, v, slot_mapping, delta):
+    _bf16(k, "k")
+    _bf16(v, "v")
+    _i32(slot_mapping, "slot_mapping")
+    if delta is not None:
+        _i32(delta, "delta")
+    d = plane_desc(k)
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have the same shape and strides")
+    if slot_mapping.numel() != d.chunks * d.tokens:
+        raise ValueError(f"slot_mapping must hold {d.chunks} x {d.tokens} slots")
+    if delta is not None and delta.numel() != d.chunks:
+        raise ValueError(f"delta must hold {d.chunks} shifts")
+    return d
+
+
+def pool_write(pool: Pool, k, v, slot_mapping, delta=None, rope_base: float = 0.0):
+    """Write rows k, v [C][L][n][H][D] (L, H, D the pool's) to pool rows slot_mapping [C][n]
+    (< 0: not kept), in the pool's format, keys rotated by delta [C] first (None: as they are)."""
+    d = _pool_rows(k, v, slot_mapping, delta)
+    _check(lib.kvfix_pool_write(_ptr(k), _ptr(v), d, _ptr(delta), float(rope_base), _ptr(slot_mapping),
+                                pool_desc(pool), _stream(k)))
+
+
+def pool_read(pool: Pool, slot_mapping, delta=None, rope_base: float = 0.0, k_out=None, v_out=None):
+    """The values of pool rows slot_mapping [C][n] as bf16 planes [C][L][n][H][D], keys rotated
+    by delta [C] (None: as stored).  Rows with a negative slot keep what the outputs held (zero
+    in outputs allocated here)."""
+    pd = pool_desc(pool)
+    if k_out is None or v_out is None:
+        if slot_mapping.dim() != 2:
+            raise ValueError("slot_mapping must be [chunks][tokens]")
+        shape = (slot_mapping.shape[0], pd.layers, slot_mapping.shape[1], pd.kv_heads, pd.head_dim)
+        new = lambda: torch.zeros(shape, dtype=torch.bfloat16, device=pool.k.device)  # noqa: E731
+        k_out, v_out = new() if k_out is None else k_out, new() if v_out is None else v_out
+    d = _pool_rows(k_out, v_out, slot_mapping, delta)
+    _check(lib.kvfix_pool_read(pd, _ptr(slot_mapping), _ptr(delta), float(rope_base), _ptr(k_out), _ptr(v_out), d,
+                               _stream(k_out)))
+    return k_out, v_out

@@ -575,6 +575,82 @@ KVFIX_API kvfix_status kvfix_anchor_gate_correct(
     kvfix_kv_desc out, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Paged pools.  A pool holds `slots` rows per layer; row (layer, slot, head) stores head_dim
+ * values of a key and of a value in one of three forms:
+ *   KVFIX_POOL_BF16  the values, 2 head_dim bytes; no scales.
+ *   KVFIX_POOL_E4M3  head_dim e4m3 codes (one byte each, in order) and one scale byte b:
+ *                    value = e4m3(code) * 2^(b - 127).  With A the largest finite magnitude
+ *                    of the row, 2^(b-127) is the least power of two with
+ *                    A <= 448 * 2^(b-127), kept within [2^-110, 2^119]; codes are
+ *                    x / 2^(b-127) rounded to nearest even; infinities saturate to the
+ *                    largest code, a NaN stays a NaN.  Every stored value is exactly a bf16
+ *                    value.
+ *   KVFIX_POOL_INT4  head_dim/2 bytes: each 32-bit word (little endian) holds 8 codes 0..15,
+ *                    value 2i in bits [4i, 4i+4) and value 2i+1 in bits [16+4i, 20+4i).
+ *                    Groups of 32 values share a bf16 scale and a bf16 zero (one 32-bit
+ *                    word, scale in the low half): value = bf16(scale * code + zero).  Over
+ *                    the group's finite values: zero = min, scale = bf16((max - min) / 15)
+ *                    (float division; 0 if below 2^-120; a range beyond the largest float
+ *                    counts as that), code = rint((x - zero) * (1 / scale)) in float, kept
+ *                    within 0..15 (0 if the scale is 0).  Infinities saturate, a NaN takes
+ *                    code 0 (the form has no NaN); a group with no finite value is all zero.
+ *
+ * kvfix_pool describes a pool (or some consecutive layers of one):
+ *   code bytes of (l, slot, h): k + l*stride_layer + slot*stride_slot + h*B with B = 2 D,
+ *       D or D/2 (strides in BYTES, multiples of 16; stride_slot >= kv_heads*B; 16-byte
+ *       aligned bases);
+ *   scales: contiguous [layers][kv_heads][slots] bytes (e4m3), or
+ *       [layers][kv_heads][slots][D/32] 32-bit words, 4-byte aligned (int4); NULL for bf16.
+ * head_dim D is 64 or 128.  The heads-major scales put the scales of one head's consecutive
+ * slots side by side, as attention reads them.
+ */
+typedef enum { KVFIX_POOL_BF16 = 0, KVFIX_POOL_E4M3 = 1, KVFIX_POOL_INT4 = 2 } kvfix_pool_format;
+typedef struct {
+    int32_t format; /* kvfix_pool_format */
+    int32_t layers;
+    int32_t slots;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int64_t stride_layer; /* bytes */
+    int64_t stride_slot;  /* bytes */
+    void* k;
+    void* v;
+    void* k_scales;
+    void* v_scales;
+} kvfix_pool;
+
+/*
+ * kvfix_pool_write -- write cached rows into a pool, quantised as they are written.  [TD]
+ * section 4.4, Algorithm 1 (re-aligned rows written to the paged cache through the slot
+ * mapping); [AKS] combines reuse with caches kept in 2 to 4 bits, which this form serves.
+ *
+ * Token t of chunk c goes, in every layer, to pool row slot_mapping[c*tokens + t], in the
+ * pool's format.  Keys are first rotated by delta[c] as kvfix_rerope does (the same bf16
+ * bits); delta NULL, or 0, writes them as they are; values are not rotated.  A negative slot
+ * means the token is not kept; a slot >= pool.slots is skipped and flagged (KVFIX_EDEVICE in
+ * kvfix_check_status).  Rows no slot names are left unchanged.  Slots must be distinct (two
+ * tokens naming one row race).
+ * k, v         : `src` planes (any chunks and tokens, layers and heads of the pool).
+ * slot_mapping : device int32[chunks][tokens].
+ * delta        : device int32[chunks], or NULL.  rope_base: as for kvfix_rerope (ignored,
+ *                and unchecked, without delta).
+ */
+KVFIX_API kvfix_status kvfix_pool_write(const kvfix_bf16* k, const kvfix_bf16* v, kvfix_kv_desc src,
+                                        const int32_t* delta, double rope_base,
+                                        const int32_t* slot_mapping, kvfix_pool pool, void* stream);
+
+/*
+ * kvfix_pool_read -- read pool rows back as bf16 rows, keys re-aligned on the way: the
+ * inverse gather of kvfix_pool_write.  Row t of chunk c of the outputs gets the values that
+ * pool row slot_mapping[c*tokens + t] stands for, keys rotated by delta[c] (as kvfix_rerope
+ * of those bf16 values).  Rows with a negative slot are left unchanged; a slot >= pool.slots
+ * leaves its row unchanged and is flagged.  A token may be read any number of times.
+ */
+KVFIX_API kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapping, const int32_t* delta,
+                                       double rope_base, kvfix_bf16* k, kvfix_bf16* v, kvfix_kv_desc out,
+                                       void* stream);
+
+/*
  * kvfix_selftest_wait -- exercise the bounded wait that every pipelined kernel uses, with
  * no hang: one warp waits on a barrier phase that never completes and then on the device
  * int32 *flag (optional; 0 = not set), each for at most limit_cycles SM clocks, and records
