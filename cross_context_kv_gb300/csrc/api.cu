@@ -7,6 +7,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "attend.h"
 #include "internal.h"
 
 namespace kvfix {
@@ -164,7 +165,8 @@ kvfix_status kvfix_check_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "kvfix_check_status: stream synchronize");
     unsigned bits = read_status_repair(s) | read_status_diff(s) | read_status_draft(s) | read_status_lowrank(s) |
                     read_status_anchor(s) | read_status_layout(s) | read_status_selftest(s) |
-                    read_status_lowrank_draft(s) | read_status_pool(s);
+                    read_status_lowrank_draft(s) | read_status_pool(s) |
+                    read_status_attend(s);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "kvfix_check_status: status read");
     if (bits & 8u) return fail(KVFIX_EDEVICE, "a kernel's shared-memory layout check failed; its work was skipped");
@@ -961,6 +963,84 @@ kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapping, const
     if (overlaps(k, out, v, out)) return fail(KVFIX_EINVAL, "%s: k and v overlap", fn);
     RopeTheta th = make_theta(delta ? rope_base : 2.0, out.head_dim);
     return launched(launch_pool_read(pool, slot_mapping, delta, th, k, v, out, (cudaStream_t)stream), fn);
+}
+
+size_t kvfix_shared_attend_workspace_bytes(int32_t agents, int32_t new_tokens, int32_t q_heads, int32_t kv_heads,
+                                           int32_t head_dim, int32_t groups) {
+    if (agents < 0 || new_tokens < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || groups < 0 ||
+        (head_dim != 64 && head_dim != 128) || (double)agents * new_tokens * q_heads >= 134217728.0)
+        return 0;
+    return attend_workspace_bytes(agents, new_tokens, q_heads, kv_heads, head_dim, groups);
+}
+
+kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_pool pool, int32_t page_tokens,
+                                 const int32_t* prefix_pages, int32_t max_prefix_pages, const int32_t* prefix_len,
+                                 const int32_t* group_begin, int32_t groups, const int32_t* suffix_pages,
+                                 int32_t max_suffix_pages, const int32_t* suffix_len, double scale, kvfix_bf16* out,
+                                 kvfix_kv_desc od, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "kvfix_shared_attend";
+    kvfix_status st;
+    if ((st = check_plane(q, qd, "kvfix_shared_attend: q")) != KVFIX_OK) return st;
+    if ((st = check_plane(out, od, "kvfix_shared_attend: out")) != KVFIX_OK) return st;
+    if ((st = check_pool(pool, fn)) != KVFIX_OK) return st;
+    if (!same_shape(qd, od) || qd.chunks != od.chunks) return fail(KVFIX_EINVAL, "%s: q and out shapes differ", fn);
+    if (qd.layers != 1 || pool.layers != 1) return fail(KVFIX_EINVAL, "%s: q, out and the pool must have one layer", fn);
+    if (qd.head_dim != pool.head_dim || qd.kv_heads % pool.kv_heads)
+        return fail(KVFIX_EINVAL, "%s: the query heads must be a multiple of the pool's heads, with its head_dim", fn);
+    if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128)
+        return fail(KVFIX_EINVAL, "%s: page_tokens must be 16, 32, 64 or 128 (got %d)", fn, page_tokens);
+    if (pool.slots % page_tokens)
+        return fail(KVFIX_EINVAL, "%s: the pool's slots must be a multiple of page_tokens", fn);
+    if (pool.format != KVFIX_POOL_BF16 && (!aligned16(pool.k_scales) || !aligned16(pool.v_scales)))
+        return fail(KVFIX_EINVAL, "%s: the pool's scales must be 16-byte aligned", fn);
+    const int agents = qd.chunks, T = qd.tokens;
+    if ((double)agents * T * qd.kv_heads >= 134217728.0)
+        return fail(KVFIX_EINVAL, "%s: agents * new tokens * query heads must be below 2^27", fn);
+    if (groups < 0 || groups > agents + 65536)
+        return fail(KVFIX_EINVAL, "%s: groups must be in [0, agents + 65536]", fn);
+    if (max_prefix_pages < 0 || max_suffix_pages < 0 ||
+        ((double)max_prefix_pages + max_suffix_pages) * page_tokens >= 1073741824.0)
+        return fail(KVFIX_EINVAL, "%s: the page lists must cover fewer than 2^30 keys", fn);
+    if (groups > 0 && (!prefix_len || !group_begin || (max_prefix_pages > 0 && !prefix_pages)))
+        return fail(KVFIX_EINVAL, "%s: prefix_pages, prefix_len and group_begin are required with groups", fn);
+    if (agents > 0 && (!suffix_len || (max_suffix_pages > 0 && !suffix_pages)))
+        return fail(KVFIX_EINVAL, "%s: suffix_pages and suffix_len are required", fn);
+    if (!(scale > 0.0) || !isfinite(scale)) return fail(KVFIX_EINVAL, "%s: scale must be finite and > 0", fn);
+    const size_t need = kvfix_shared_attend_workspace_bytes(agents, T, qd.kv_heads, pool.kv_heads, pool.head_dim, groups);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+        return fail(KVFIX_EINVAL, "%s: workspace needs %zu bytes, 16-byte aligned (got %zu)", fn, need, workspace_bytes);
+    const size_t lse_bytes = lse ? 4 * (size_t)agents * (size_t)T * (size_t)qd.kv_heads : 0;
+    uintptr_t o0, o1, q0, q1;
+    extent(out, od, &o0, &o1);
+    extent(q, qd, &q0, &q1);
+    if (overlaps(out, od, q, qd) || pool_meets_plane(pool, out, od) || pool_meets(pool, lse, lse_bytes) ||
+        pool_meets(pool, workspace, need) || overlaps_bytes(lse, lse_bytes, (const void*)o0, o1 - o0) ||
+        overlaps_bytes(lse, lse_bytes, (const void*)q0, q1 - q0) ||
+        overlaps_bytes(workspace, need, (const void*)o0, o1 - o0) ||
+        overlaps_bytes(workspace, need, (const void*)q0, q1 - q0) || overlaps_bytes(workspace, need, lse, lse_bytes))
+        return fail(KVFIX_EINVAL, "%s: out, lse and workspace must not overlap each other, q or the pool", fn);
+    AttendArgs a = {};
+    a.q = q;
+    a.qp = plane_of(qd);
+    a.out = out;
+    a.op = plane_of(od);
+    a.lse = lse;
+    a.pool = view_of(pool);
+    a.agents = agents;
+    a.new_tokens = T;
+    a.q_heads = qd.kv_heads;
+    a.groups = groups;
+    a.page = page_tokens;
+    a.max_prefix_pages = max_prefix_pages;
+    a.max_suffix_pages = max_suffix_pages;
+    a.prefix_pages = prefix_pages;
+    a.prefix_len = prefix_len;
+    a.group_begin = group_begin;
+    a.suffix_pages = suffix_pages;
+    a.suffix_len = suffix_len;
+    a.scale_log2 = (float)(scale * 1.4426950408889634);
+    a.workspace = workspace;
+    return launched(launch_attend(a, (cudaStream_t)stream), fn);
 }
 
 kvfix_status kvfix_selftest_wait(int64_t limit_cycles, const int32_t* flag, void* stream) {

@@ -166,6 +166,9 @@ cudaError_t launch_pool_write(const uint16_t* k, const uint16_t* v, const kvfix_
 cudaError_t launch_pool_read(const kvfix_pool& pool, const int32_t* slots, const int32_t* delta, const RopeTheta& th,
                              uint16_t* k, uint16_t* v, const kvfix_kv_desc& d, cudaStream_t s);
 
+// Shared-prefix attention (attend.h).
+unsigned read_status_attend(cudaStream_t stream);
+
 // Bounded-wait self test.
 unsigned read_status_selftest(cudaStream_t stream);
 cudaError_t launch_selftest_wait(long long limit_cycles, const int* flag, cudaStream_t s);

@@ -75,6 +75,8 @@ SIGNATURES = {
                                                 P]),
     "kvfix_pool_write": (ctypes.c_int, [P, P, D, P, F64, P, PD, P]),
     "kvfix_pool_read": (ctypes.c_int, [PD, P, P, F64, P, P, D, P]),
+    "kvfix_shared_attend_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
+    "kvfix_shared_attend": (ctypes.c_int, [P, D, PD, I32, P, I32, P, P, I32, P, I32, P, F64, P, D, P, P, SZ, P]),
     "kvfix_repair_rows": (ctypes.c_int, [P, P, D, P, P, D, P, I32, P, P]),
     "kvfix_anchor_gate_workspace_bytes": (SZ, [D, I32, I32]),
     "kvfix_anchor_gate": (ctypes.c_int, [P, D, P, P, I32, I32, I32, F64, F64, P, P, P, P, P, SZ, P]),
@@ -695,3 +697,49 @@ def pool_read(pool: Pool, slot_mapping, delta=None, rope_base: float = 0.0, k_ou
     _check(lib.kvfix_pool_read(pd, _ptr(slot_mapping), _ptr(delta), float(rope_base), _ptr(k_out), _ptr(v_out), d,
                                _stream(k_out)))
     return k_out, v_out
+
+
+def shared_attend_workspace_bytes(q, pool: Pool, groups: int) -> int:
+    A, T, Hq, D = q.shape
+    return int(lib.kvfix_shared_attend_workspace_bytes(A, T, Hq, pool.k.shape[2], D, groups))
+
+
+def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, prefix_pages=None, prefix_len=None,
+                  group_begin=None, scale: float | None = None, out=None, return_lse: bool = False, workspace=None):
+    """Attention of queries q [agents][T][q_heads][dim] over one layer of a pool (pool.layer(i)):
+    agent a's keys are its group's prefix (the first prefix_len[g] keys on prefix_pages[g]), then
+    the first suffix_len[a] on suffix_pages[a], the T newest of them its own queries' places.
+    Groups are the runs of agents group_begin[g] .. group_begin[g+1].  scale: dim^-1/2 if None.
+    Returns out, shaped like q, or (out, lse [agents][T][q_heads])."""
+    _bf16(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [agents][new tokens][heads][dim]")
+    qd, pd = plane_desc(q), pool_desc(pool)
+    A, T, Hq, Dh = q.shape
+    groups = 0 if prefix_len is None else prefix_len.numel()
+    for t, nm, count in ((suffix_pages, "suffix_pages", None), (suffix_len, "suffix_len", A),
+                         (prefix_pages, "prefix_pages", None), (prefix_len, "prefix_len", groups),
+                         (group_begin, "group_begin", groups + 1)):
+        if t is None:
+            if groups or nm.startswith("suffix"):
+                raise ValueError(f"{nm} is required")
+            continue
+        _i32(t, nm)
+        if count is not None and t.numel() != count:
+            raise ValueError(f"{nm} must hold {count} values (got {t.numel()})")
+    if suffix_pages.dim() != 2 or suffix_pages.shape[0] != A:
+        raise ValueError(f"suffix_pages must be [{A}][pages]")
+    if groups and (prefix_pages.dim() != 2 or prefix_pages.shape[0] != groups):
+        raise ValueError(f"prefix_pages must be [{groups}][pages]")
+    out = torch.empty(A, T, Hq, Dh, dtype=torch.bfloat16, device=q.device) if out is None else out
+    _bf16(out, "out")
+    lse = torch.empty(A, T, Hq, dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        workspace = torch.empty(shared_attend_workspace_bytes(q, pool, groups), dtype=torch.uint8, device=q.device)
+    _check(lib.kvfix_shared_attend(
+        _ptr(q), qd, pd, int(page_tokens), _ptr(prefix_pages) if groups else None,
+        prefix_pages.shape[1] if groups else 0, _ptr(prefix_len) if groups else None,
+        _ptr(group_begin) if groups else None, groups, _ptr(suffix_pages), suffix_pages.shape[1], _ptr(suffix_len),
+        float(Dh ** -0.5 if scale is None else scale), _ptr(out), plane_desc(out), _ptr(lse), _ptr(workspace),
+        workspace.numel(), _stream(q)))
+    return (out, lse) if return_lse else out

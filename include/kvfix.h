@@ -651,6 +651,61 @@ KVFIX_API kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapp
                                        void* stream);
 
 /*
+ * kvfix_shared_attend -- attention of the agents of a round over the context they share and
+ * their own tokens, read from one layer of a paged pool.  [TD] section 2.1 (a round's prompts
+ * hold the same blocks) and section 4.4 (attention over the restored paged cache); [BCR] App.
+ * B, Algorithm 2 (grouped-query keys expanded to query heads).
+ *
+ * The agents of group g, group_begin[g] <= a < group_begin[g+1], share the prefix of
+ * prefix_len[g] keys on the pages prefix_pages[g]; agent a's own suffix_len[a] keys lie on
+ * suffix_pages[a].  An agent outside every group has no prefix.  Key i of a page list is pool
+ * row pages[i / page_tokens] * page_tokens + i % page_tokens.  The sequence of an agent is
+ * its prefix, then its suffix; its new_tokens = q.tokens queries stand at the last new_tokens
+ * places of it (their keys and values are already in the pool), so query t sees the first
+ *     N_t = prefix_len + suffix_len - new_tokens + 1 + t
+ * keys (none if that is not positive).  With z_j = scale * q[a][t][h] . k[j][h / (q_heads /
+ * kv_heads)] over the keys it sees:
+ *     out[a][t][h] = sum_j exp(z_j) v[j] / sum_j exp(z_j),   lse[a][t][h] = log sum_j exp(z_j)
+ * and out = 0, lse = -inf for a query that sees no key.  A group's shared keys are read once
+ * for all its agents.  One new token per agent is a decode step; more are drafts or a message
+ * that every agent receives.
+ * q, out       : planes with chunks = agents, layers = 1, tokens = new tokens, kv_heads =
+ *                query heads (a multiple of the pool's), head_dim the pool's.
+ * pool         : one layer (layers == 1), any format; slots a multiple of page_tokens; scales
+ *                16-byte aligned.
+ * page_tokens  : 16, 32, 64 or 128.
+ * prefix_pages : device int32[groups][max_prefix_pages]; prefix_len: device int32[groups];
+ *                group_begin: device int32[groups + 1], ascending within 0..agents.  groups
+ *                may be 0 (all three NULL).
+ * suffix_pages : device int32[agents][max_suffix_pages]; suffix_len: device int32[agents].
+ * scale        : finite, > 0 (usually head_dim^-1/2).
+ * lse          : device float[agents][new tokens][q_heads], or NULL.
+ * workspace    : device buffer of kvfix_shared_attend_workspace_bytes(agents, new tokens,
+ *                q_heads, kv_heads, head_dim, groups) bytes, 16-byte aligned, contents
+ *                irrelevant on entry.
+ * Pages, lengths and groups are read on the device, so a captured call follows them as they
+ * change.  A page out of range counts as absent (its keys are not seen), a length outside its
+ * page list and a group boundary out of order are clamped; each is flagged (KVFIX_EDEVICE in
+ * kvfix_check_status).  Page entries past a length are not read.
+ * Limits: (max_prefix_pages + max_suffix_pages) * page_tokens < 2^30 and agents * new tokens *
+ * q_heads < 2^27.
+ * Arithmetic: bf16 tensor-core products with float accumulation (stored values are bf16
+ * values, so no operand is rounded but the softmax weights, to bf16 before their product with
+ * the values); maxima, sums and lse in float; one rounding of out to bf16.  The same inputs
+ * give the same bits on every run; the order of sums depends on the lengths.
+ */
+KVFIX_API size_t kvfix_shared_attend_workspace_bytes(int32_t agents, int32_t new_tokens, int32_t q_heads,
+                                                     int32_t kv_heads, int32_t head_dim, int32_t groups);
+KVFIX_API kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc q_desc, kvfix_pool pool,
+                                           int32_t page_tokens, const int32_t* prefix_pages,
+                                           int32_t max_prefix_pages, const int32_t* prefix_len,
+                                           const int32_t* group_begin, int32_t groups,
+                                           const int32_t* suffix_pages, int32_t max_suffix_pages,
+                                           const int32_t* suffix_len, double scale, kvfix_bf16* out,
+                                           kvfix_kv_desc out_desc, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/*
  * kvfix_selftest_wait -- exercise the bounded wait that every pipelined kernel uses, with
  * no hang: one warp waits on a barrier phase that never completes and then on the device
  * int32 *flag (optional; 0 = not set), each for at most limit_cycles SM clocks, and records

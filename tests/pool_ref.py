@@ -78,10 +78,10 @@ def int4_encode(x):
 def int4_decode(codes, sz):
     w = np.ascontiguousarray(codes).view("<u4")
     at = np.array([0, 16, 4, 20, 8, 24, 12, 28], np.uint32)
-    c = ((w[..., None] >> at) & 15).astype(np.float64).reshape(*codes.shape[:-1], -1, GROUP)
+    c = ((w[..., None] >> at) & 15).astype(np.float64).reshape(*codes.shape[:-1], sz.shape[-2], GROUP)
     s, z = of_bf16(sz[..., 0])[..., None], of_bf16(sz[..., 1])[..., None]
     v = c * s + z                                             # exact in float32 (see the range note)
-    return of_bf16(bf16_of(v)).reshape(*codes.shape[:-1], -1)
+    return of_bf16(bf16_of(v)).reshape(*codes.shape[:-1], 2 * codes.shape[-1])
 
 
 def encode(fmt, words):
