@@ -989,8 +989,8 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
         return fail(KVFIX_EINVAL, "%s: the query heads must be a multiple of the pool's heads, with its head_dim", fn);
     if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128)
         return fail(KVFIX_EINVAL, "%s: page_tokens must be 16, 32, 64 or 128 (got %d)", fn, page_tokens);
-    if (pool.slots % page_tokens)
-        return fail(KVFIX_EINVAL, "%s: the pool's slots must be a multiple of page_tokens", fn);
+    if (pool.slots < page_tokens || pool.slots % page_tokens)
+        return fail(KVFIX_EINVAL, "%s: the pool's slots must be a positive multiple of page_tokens", fn);
     if (pool.format != KVFIX_POOL_BF16 && (!aligned16(pool.k_scales) || !aligned16(pool.v_scales)))
         return fail(KVFIX_EINVAL, "%s: the pool's scales must be 16-byte aligned", fn);
     const int agents = qd.chunks, T = qd.tokens;

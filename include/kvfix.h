@@ -671,8 +671,8 @@ KVFIX_API kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapp
  * that every agent receives.
  * q, out       : planes with chunks = agents, layers = 1, tokens = new tokens, kv_heads =
  *                query heads (a multiple of the pool's), head_dim the pool's.
- * pool         : one layer (layers == 1), any format; slots a multiple of page_tokens; scales
- *                16-byte aligned.
+ * pool         : one layer (layers == 1), any format; slots a positive multiple of page_tokens;
+ *                scales 16-byte aligned.
  * page_tokens  : 16, 32, 64 or 128.
  * prefix_pages : device int32[groups][max_prefix_pages]; prefix_len: device int32[groups];
  *                group_begin: device int32[groups + 1], ascending within 0..agents.  groups
