@@ -55,41 +55,36 @@ constexpr int kAtBlock = 256;     // rows per entry
 constexpr int kAtMaxCtas = 256;   // bound of the persistent grid
 
 // ------------------------------------------------------------------ plan
-// The line of units.  Entries of a segment are its 256-row blocks in order; segments are the
-// groups' prefixes, then the agents' suffixes.  Unit (entry e, head h) begins at
-// begin + h * (tiles + 1).
+// A segment's rows are cut into blocks of 256; a block of more than 128 rows is a pair (both
+// softmax groups share its tiles), the last one may be a single.  Pairs and singles lie on a
+// line of their own: unit (entry e, head h) begins at begin + h * (tiles + 1).  The pairs'
+// line is cut into one piece per CTA, the singles' into two (one per softmax group).
 struct __align__(16) AtEntry {
     long long begin;  // position of head 0 on the line
-    long long prow;   // part rows of head 0
-    int tiles, rows, row0, seg;
-    int keys;         // keys of the segment that some row of the block may see
-    int agent0;       // the segment's first agent
-    int prefix;       // 1: a group's prefix
-    int pad;
+    int tiles, rows;
+    int row0, seg, keys, agent0;  // keys: those that some row of the block may see
 };
 
 struct AtPlan {
-    long long total;  // length of the line
-    int entries, pad;
-    int start[kAtMaxCtas];  // the entry in which a CTA's piece begins
+    long long total[2], chunk[2];  // pairs, singles: length of the line, of a piece
+    int count[2];                  // entries
+    int pad[2];
+    int start[3][kAtMaxCtas];      // the entry in which a piece begins: pairs, singles of group 0, 1
 };
 
 struct AtLayout {
-    size_t plan, first, bounds, entries, ml, o, bytes;
+    size_t plan, first, bounds, entries[2], ml, o, bytes;
     long long own_rows;
 };
 
-// Part rows: each unit's first part has its own rows (two sets where both softmax groups hold
-// the same rows), a part that continues a unit from an earlier CTA has its CTA's 256 rows.
+// Part rows.  The first part of a unit has its rows' own places (prefix rows, then suffix
+// rows: [head][agent][token, query head]); a part that continues a unit from an earlier piece
+// has its CTA's: 256 rows for a pair, 2 x 128 for singles.
 static AtLayout at_layout(int agents, int T, int q_heads, int kv_heads, int head_dim, int groups) {
     const long long tg = (long long)T * (q_heads / kv_heads), all = (long long)agents * tg;
-    const long long small = tg < kAtRows ? tg : kAtRows;
-    const long long entries = groups + all / kAtBlock + (long long)agents * ((tg + kAtBlock - 1) / kAtBlock) + 1;
-    long long extra = (long long)kAtRows * groups;
-    if (extra > all) extra = all;
     AtLayout l;
-    l.own_rows = kv_heads * (all + extra + agents * (tg + small));
-    const long long rows = l.own_rows + (long long)kAtMaxCtas * kAtBlock;
+    l.own_rows = 2 * kv_heads * all;
+    const long long rows = l.own_rows + (long long)kAtMaxCtas * 2 * kAtBlock;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -97,9 +92,10 @@ static AtLayout at_layout(int agents, int T, int q_heads, int kv_heads, int head
         return here;
     };
     l.plan = take(sizeof(AtPlan));
-    l.first = take(4 * ((size_t)groups + agents));
+    l.first = take(8 * ((size_t)groups + agents));
     l.bounds = take(4 * ((size_t)groups + 1));
-    l.entries = take(sizeof(AtEntry) * (size_t)entries);
+    l.entries[0] = take(sizeof(AtEntry) * (size_t)(2 * all / kAtRows + 2));
+    l.entries[1] = take(sizeof(AtEntry) * ((size_t)groups + agents + 1));
     l.ml = take(8 * (size_t)rows);
     l.o = take(4 * (size_t)rows * head_dim);
     l.bytes = at;
@@ -112,70 +108,79 @@ size_t attend_workspace_bytes(int agents, int T, int q_heads, int kv_heads, int 
 
 struct AtWork {
     AtPlan* plan;
-    int* first;   // [groups + agents]: a segment's first entry
-    int* bounds;  // [groups + 1]: the groups' agents, clamped and ascending
-    AtEntry* entries;
-    float2* ml;   // part rows: (max in base-2 units, sum)
-    float* o;     // part rows x D
+    int2* first;          // [groups + agents]: a segment's first pair and its single
+    int* bounds;          // [groups + 1]: the groups' agents, clamped and ascending
+    AtEntry* entries[2];  // pairs, singles
+    float2* ml;           // part rows: (max in base-2 units, sum)
+    float* o;             // part rows x D
     long long own_rows;
     int ctas;
 };
-
-// The piece of the line that CTA i of n takes.
-__host__ __device__ __forceinline__ long long piece(long long total, int i, int n) {
-    return total / n * i + total % n * i / n;
-}
 
 __device__ __forceinline__ int clamp_len(int n, long long most, bool& bad) {
     if (n < 0 || n > most) bad = true;
     return (int)min(max((long long)n, 0ll), most);
 }
 
-constexpr int kPlanThreads = 512;
+// A quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division takes
+// about a hundred instructions).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return (x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
+}
 
-// Exclusive scan over the block of three sums and an (inclusive) running maximum.
+constexpr int kPlanThreads = 256;
+
 struct PlanSums {
-    long long entries, line, rows;
+    int n[2];
+    long long line[2];
 };
-__device__ __forceinline__ PlanSums plan_scan(PlanSums x, PlanSums* warp_sums, PlanSums* total) {
+// Exclusive scan over the block, and the totals.
+__device__ __forceinline__ PlanSums plan_scan(const PlanSums& x, PlanSums* warp_sums, PlanSums* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PlanSums inc = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long a = __shfl_up_sync(0xffffffffu, inc.entries, o);
-        const long long b = __shfl_up_sync(0xffffffffu, inc.line, o);
-        const long long c = __shfl_up_sync(0xffffffffu, inc.rows, o);
-        if (lane >= o) {
-            inc.entries += a;
-            inc.line += b;
-            inc.rows += c;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int a = __shfl_up_sync(0xffffffffu, inc.n[k], o);
+            const long long b = __shfl_up_sync(0xffffffffu, inc.line[k], o);
+            if (lane >= o) {
+                inc.n[k] += a;
+                inc.line[k] += b;
+            }
         }
-    }
     if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
-    PlanSums before = {0, 0, 0}, all = {0, 0, 0};
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const PlanSums s = warp_sums[w];
-        if (w < warp) {
-            before.entries += s.entries;
-            before.line += s.line;
-            before.rows += s.rows;
-        }
-        all.entries += s.entries;
-        all.line += s.line;
-        all.rows += s.rows;
+    PlanSums ex, all = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        ex.n[k] = inc.n[k] - x.n[k];
+        ex.line[k] = inc.line[k] - x.line[k];
     }
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int a = warp_sums[w].n[k];
+            const long long b = warp_sums[w].line[k];
+            if (w < warp) {
+                ex.n[k] += a;
+                ex.line[k] += b;
+            }
+            all.n[k] += a;
+            all.line[k] += b;
+        }
     *total = all;
-    PlanSums ex;
-    ex.entries = before.entries + inc.entries - x.entries;
-    ex.line = before.line + inc.line - x.line;
-    ex.rows = before.rows + inc.rows - x.rows;
     return ex;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendArgs a, AtWork w) {
+constexpr int kPlanKept = 1024;  // entries of a line whose places stay in shared memory
+
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendArgs a,
+                                                                   const __grid_constant__ AtWork w) {
     __shared__ PlanSums warp_sums[kPlanThreads / 32];
     __shared__ int warp_max[kPlanThreads / 32];
+    __shared__ long long kept[2][kPlanKept];
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G, H = a.pool.heads;
@@ -184,12 +189,15 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     const int s0 = min(segs, tid * per), s1 = min(segs, s0 + per);
     const long long most_p = (long long)a.max_prefix_pages * a.page, most_s = (long long)a.max_suffix_pages * a.page;
     bool bad = false;
+    // the first segment's length is on its way while the bounds are worked out
+    int len0 = 0;
+    if (s0 < s1) len0 = s0 < a.groups ? __ldg(a.prefix_len + s0) : __ldg(a.suffix_len + s0 - a.groups);
     // group bounds: the running maximum of the given ones, kept within 0..agents
     if (a.groups > 0) {
         const int n = a.groups + 1, each = (n + kPlanThreads - 1) / kPlanThreads;
         const int g0 = min(n, tid * each), g1 = min(n, g0 + each);
         int mine = 0;
-        for (int g = g0; g < g1; ++g) mine = max(mine, min(max(a.group_begin[g], 0), a.agents));
+        for (int g = g0; g < g1; ++g) mine = max(mine, min(max(__ldg(a.group_begin + g), 0), a.agents));
         int inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -203,19 +211,20 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         const int left = __shfl_up_sync(0xffffffffu, inc, 1);
         if (lane > 0) run = max(run, left);
         for (int g = g0; g < g1; ++g) {
-            const int b = a.group_begin[g];
+            const int b = __ldg(a.group_begin + g);
             if (b < run || b > a.agents) bad = true;
             run = max(run, min(max(b, 0), a.agents));
             w.bounds[g] = run;
         }
         __syncthreads();
     }
-    // one segment: rows, keys; its blocks in turn
+    // a segment's blocks in turn
     auto each_block = [&](int s, auto&& f) {
         const bool prefix = s < a.groups;
         const int agent0 = prefix ? w.bounds[s] : s - a.groups;
         const int count = prefix ? w.bounds[s + 1] - agent0 : 1;
-        const int n = prefix ? clamp_len(a.prefix_len[s], most_p, bad) : clamp_len(a.suffix_len[agent0], most_s, bad);
+        const int given = s == s0 ? len0 : prefix ? __ldg(a.prefix_len + s) : __ldg(a.suffix_len + agent0);
+        const int n = clamp_len(given, prefix ? most_p : most_s, bad);
         const int rows = count * TG;
         for (int r0 = 0; r0 < rows; r0 += kAtBlock) {
             AtEntry e;
@@ -223,113 +232,127 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             e.row0 = r0;
             e.seg = s;
             e.agent0 = agent0;
-            e.prefix = prefix;
             // own keys are seen up to the place of the block's last row
             e.keys = prefix ? n : max(0, n - T + 1 + (r0 + e.rows - 1) / G);
             e.tiles = (e.keys + kAtKeys - 1) / kAtKeys;
-            e.pad = 0;
-            f(e);
+            f(e, e.rows > kAtRows ? 0 : 1);
         }
     };
-    auto set_rows = [](const AtEntry& e) { return e.rows > kAtRows ? e.rows : 2 * e.rows; };
     auto cost = [&](const AtEntry& e) { return e.tiles > 0 ? (long long)H * (e.tiles + 1) : 0ll; };
-    PlanSums mine = {0, 0, 0};
+    PlanSums mine = {};
     for (int s = s0; s < s1; ++s)
-        each_block(s, [&](const AtEntry& e) {
-            mine.entries += 1;
-            mine.line += cost(e);
-            mine.rows += (long long)H * set_rows(e);
+        each_block(s, [&](const AtEntry& e, int k) {
+            if (k == 0) {
+                mine.n[0] += 1;
+                mine.line[0] += cost(e);
+            } else {
+                mine.n[1] += 1;
+                mine.line[1] += cost(e);
+            }
         });
     PlanSums total;
     PlanSums at = plan_scan(mine, warp_sums, &total);
     for (int s = s0; s < s1; ++s) {
-        w.first[s] = (int)at.entries;
-        each_block(s, [&](AtEntry e) {
-            e.begin = at.line;
-            e.prow = at.rows;
+        w.first[s] = make_int2(at.n[0], at.n[1]);
+        each_block(s, [&](AtEntry e, int k) {
             const long long c = cost(e);
-            w.entries[at.entries] = e;
-            // the CTAs whose pieces begin inside this entry
-            if (c > 0) {
-                long long i = total.line ? at.line * w.ctas / total.line : 0;
-                while (i > 0 && piece(total.line, (int)i, w.ctas) >= at.line) --i;
-                while (i < w.ctas && piece(total.line, (int)i, w.ctas) < at.line) ++i;
-                for (; i < w.ctas && piece(total.line, (int)i, w.ctas) < at.line + c; ++i) w.plan->start[i] = (int)at.entries;
+            if (k == 0) {
+                e.begin = at.line[0];
+                w.entries[0][at.n[0]] = e;
+                if (at.n[0] < kPlanKept) kept[0][at.n[0]] = e.begin;
+                at.n[0] += 1;
+                at.line[0] += c;
+            } else {
+                e.begin = at.line[1];
+                w.entries[1][at.n[1]] = e;
+                if (at.n[1] < kPlanKept) kept[1][at.n[1]] = e.begin;
+                at.n[1] += 1;
+                at.line[1] += c;
             }
-            at.entries += 1;
-            at.line += c;
-            at.rows += (long long)H * set_rows(e);
         });
     }
-    if (tid == 0) {
-        w.plan->total = total.line;
-        w.plan->entries = (int)total.entries;
+    __syncthreads();
+    const long long chunk[2] = {max(1ll, quotient(total.line[0] + w.ctas - 1, w.ctas)),
+                                max(1ll, quotient(total.line[1] + 2 * w.ctas - 1, 2 * w.ctas))};
+    // the last entry that begins at or before a piece does
+    for (int i = tid; i < 3 * w.ctas; i += kPlanThreads) {
+        const int cta = i % w.ctas, set = i / w.ctas, k = set > 0;
+        const long long lo = chunk[k] * (set == 2 ? cta + w.ctas : cta);
+        if (lo >= total.line[k]) continue;
+        int x = 0, y = total.n[k];  // begin[x] <= lo < begin[y]
+        while (y - x > 1) {
+            const int m = (x + y) / 2;
+            const long long b = total.n[k] <= kPlanKept ? kept[k][m] : w.entries[k][m].begin;
+            if (b <= lo) x = m;
+            else y = m;
+        }
+        w.plan->start[set][cta] = x;
+    }
+    if (tid < 2) {
+        w.plan->total[tid] = total.line[tid];
+        w.plan->chunk[tid] = chunk[tid];
+        w.plan->count[tid] = total.n[tid];
     }
     if (bad) atomicOr(&g_status_attend, FLAG_BOUNDS);
 }
 
-// A CTA's units in order.
-struct AtUnit {
-    int e, head, t0, nt, rows, row0, seg, keys, agent0, prefix;
-    long long part;  // first part row
+// ------------------------------------------------------------------ a CTA's work
+// One tile of a softmax group's work, as the scheduling warp hands it to the others.
+struct __align__(16) AtItem {
+    int head, tile, flags, keys;        // tile: running number of the CTA's tiles (ring places); keys in the tile
+    int key0, rows, row0, agent0;       // first key of the tile in its segment; the group's rows
+    int sees0, absent;                  // see the softmax; 16-key parts of the tile that are not there
+    long long part;                     // first part row
+    int page[8];                        // pool pages, -1: not read
 };
+enum : int { kFirst = 1, kLast = 2, kPair = 4, kPrefix = 8, kEnd = 16 };
+constexpr int kItems = 4;  // items ahead per group
 
+// Pieces of a line in order of units.
 struct AtWalk {
     const AtEntry* ent;
-    const AtEntry* end;
-    long long lo, hi, cta_part, own;
-    int H, e, h;
+    long long lo, hi;
+    int e, n, h, H;
     AtEntry rec;
     bool have;
 
-    __device__ __forceinline__ void open(const AtWork& w, int heads, int cta) {
-        const long long total = w.plan->total;
-        lo = piece(total, cta, w.ctas);
-        hi = piece(total, cta + 1, w.ctas);
-        ent = w.entries;
+    __device__ __forceinline__ void open(const AtWork& w, int k, int piece, int start, int heads) {
+        const long long total = w.plan->total[k], chunk = w.plan->chunk[k];
+        lo = min(total, chunk * piece);
+        hi = min(total, lo + chunk);
+        ent = w.entries[k];
+        n = w.plan->count[k];
         H = heads;
-        e = lo < hi ? w.plan->start[cta] : 0;
+        h = 0;
+        e = start;
         have = lo < hi;
         if (have) {
             rec = ent[e];
-            h = (int)((lo - rec.begin) / (rec.tiles + 1));
+            // entries without tiles take no room: of several at one place the last was found,
+            // and it has the piece's first unit
+            h = rec.tiles > 0 ? (int)quotient(lo - rec.begin, rec.tiles + 1) : H;
         }
-        end = ent + w.plan->entries;
-        cta_part = w.own_rows + (long long)cta * kAtBlock;
     }
 
-    __device__ __forceinline__ bool next(AtUnit& u) {
+    // The next unit's tiles [t0, t1) of head `head` in this piece.
+    __device__ __forceinline__ bool next(int& head, int& t0, int& t1) {
         while (have) {
-            const long long c = rec.tiles + 1, base = rec.begin + (long long)h * c;
             if (rec.tiles == 0 || h >= H) {
                 ++e;
                 h = 0;
-                if (ent + e >= end) have = false;
-                else {
-                    rec = ent[e];
-                    if (rec.tiles > 0 && rec.begin >= hi) have = false;
-                }
+                have = e < n;
+                if (have) rec = ent[e];
                 continue;
             }
+            const long long base = rec.begin + (long long)h * (rec.tiles + 1);
             if (base >= hi) {
                 have = false;
-                continue;
+                break;
             }
-            const int t0 = (int)max(0ll, lo - base), t1 = (int)min((long long)rec.tiles, hi - base);
-            const int head = h++;
-            if (t0 >= t1) continue;
-            u.e = e;
-            u.head = head;
-            u.t0 = t0;
-            u.nt = t1 - t0;
-            u.rows = rec.rows;
-            u.row0 = rec.row0;
-            u.seg = rec.seg;
-            u.keys = rec.keys;
-            u.agent0 = rec.agent0;
-            u.prefix = rec.prefix;
-            u.part = t0 == 0 ? rec.prow + (long long)head * (rec.rows > kAtRows ? rec.rows : 2 * rec.rows) : cta_part;
-            return true;
+            t0 = (int)max(0ll, lo - base);
+            t1 = (int)min((long long)rec.tiles, hi - base);
+            head = h++;
+            if (t0 < t1) return true;
         }
         return false;
     }
@@ -364,7 +387,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 template <int F, int D>
 struct AtCfg {
     static constexpr bool kQuant = F != KVFIX_POOL_BF16;
-    static constexpr int kThreads = kQuant ? 512 : 384;
+    static constexpr int kConvWarps = 4;
+    static constexpr int kThreads = kQuant ? 384 + 32 * kConvWarps : 384;
     static constexpr int kRegsSoftmax = kQuant ? 168 : 208;
     static constexpr int kRegsOther = 88;
     static constexpr int kTile = kAtKeys * D * 2;   // a K or V tile as bf16
@@ -374,9 +398,9 @@ struct AtCfg {
     static constexpr int kCodeRow = pool_head_bytes(F, D);
     static constexpr int kScaleRow = F == KVFIX_POOL_E4M3 ? 1 : F == KVFIX_POOL_INT4 ? D / 8 : 0;
     static constexpr int kRaw = kQuant ? kAtKeys * (kCodeRow + kScaleRow) : 0;
-    static constexpr int kRawStages = kQuant ? (F == KVFIX_POOL_E4M3 ? 4 : 6) : 1;
+    static constexpr int kRawStages = kQuant ? (F == KVFIX_POOL_E4M3 && D == 128 ? 3 : 6) : 1;
     static constexpr int kSmem = 1024 + kStages * kTile + 2 * kQ + (kQuant ? kRawStages * kRaw : 0);
-    static_assert(kSmem <= 231 * 1024, "shared memory");
+    static_assert(kSmem <= 227 * 1024 - 1536, "shared memory, with the barriers and items");
 };
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -393,14 +417,14 @@ __device__ __forceinline__ void regs_dec() {
 // their 16-byte chunks puts the eight threads of a store phase on different banks.
 template <int F, int D, int N>
 __device__ __forceinline__ void convert_tile(const unsigned char* raw, unsigned char* tile, int tid, int in_tile,
-                                             unsigned absent, int page_shift) {
+                                             unsigned absent) {
     using C = AtCfg<F, D>;
     constexpr int V = C::kCodeRow / 16;  // vectors per row
     const unsigned char* scales = raw + kAtKeys * C::kCodeRow;
 #pragma unroll 4
     for (int i = tid; i < kAtKeys * V; i += N) {
         const int r = i / V, v = i % V;
-        const bool gone = r >= in_tile || ((absent >> (r >> (4 + page_shift))) & 1u);
+        const bool gone = r >= in_tile || ((absent >> (r >> 4)) & 1u);
         const uint4 x = *reinterpret_cast<const uint4*>(raw + 16 * i);
         const unsigned c[4] = {x.x, x.y, x.z, x.w};
         if (F == KVFIX_POOL_E4M3) {
@@ -444,6 +468,23 @@ __device__ __forceinline__ void convert_tile(const unsigned char* raw, unsigned 
 // than this many powers of two: weights stay below 2^8, and bf16 keeps 8 bits of any of them.
 constexpr float kAtSlack = 8.f;
 
+// Two floats at once (packed 32-bit arithmetic).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return d;
+}
+
 template <int F, int D>
 __global__ void __launch_bounds__(AtCfg<F, D>::kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -451,8 +492,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     using C = AtCfg<F, D>;
     constexpr int S = C::kStages, R = C::kRawStages;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], q_ready[2], s_full[2], p_ready[2], o_full[2];
-    __shared__ __align__(8) uint64_t raw_full[R], raw_empty[R];
+    __shared__ __align__(8) uint64_t full[S], empty[S], raw_full[R], raw_empty[R];
+    __shared__ __align__(8) uint64_t q_ready[2], q_free[2], s_full[2], p_ready[2], o_full[2];
+    __shared__ __align__(8) uint64_t item_full[2][kItems], item_free[2][kItems];
+    __shared__ AtItem items[2][kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -461,18 +504,24 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], C::kQuant ? 128 : 1);
+            mbar_init(&full[i], C::kQuant ? 32 * C::kConvWarps : 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < R; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 128);
+            mbar_init(&raw_empty[i], C::kQuant ? 32 * C::kConvWarps : 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_ready[i], 128);
+            mbar_init(&q_ready[i], 32);
+            mbar_init(&q_free[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 128);
             mbar_init(&o_full[i], 1);
+            for (int k = 0; k < kItems; ++k) {
+                mbar_init(&item_full[i][k], 1);
+                // readers: producer, MMA, queries, four softmax warps, converters
+                mbar_init(&item_free[i][k], 7 + (C::kQuant ? C::kConvWarps : 0));
+            }
         }
         fence_mbar_init();
         abort_flag = 0;
@@ -489,336 +538,502 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     const uint32_t tmem = tmem_slot;
     pdl_wait();
     pdl_trigger();
-    const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
-    AtWalk walk;
-    walk.open(w, a.pool.heads, blockIdx.x);
-    AtUnit u;
-    const int ppt = kAtKeys / a.page;  // pages per tile
-    const int pool_pages = a.pool.slots / a.page;
-    const int page_shift = 31 - __clz(a.page / 16);
+    const int page_log = 31 - __clz(a.page);
 
-    auto page_list = [&](const AtUnit& x) {
-        return x.prefix ? a.prefix_pages + (long long)x.seg * a.max_prefix_pages
-                        : a.suffix_pages + (long long)x.agent0 * a.max_suffix_pages;
+    // Items of group g in order.  The roles that serve both groups take them in turn, group 0
+    // then 1, an ended group left out; `at` counts a group's items.
+    auto item_wait = [&](int g, unsigned at) {
+        return __all_sync(__activemask(), mbar_wait(&item_full[g][at % kItems], (at / kItems) & 1u));
     };
-    // lanes of a warp look at a tile's pages: which of those that hold keys are not there
-    auto page_ok = [&](const AtUnit& x, const int32_t* pages, int tile) {
-        const int i = tile * ppt + lane;
-        if (lane >= ppt || i >= (x.keys + a.page - 1) / a.page) return true;
-        const int p = __ldg(pages + i);
-        return p >= 0 && p < pool_pages;
-    };
+    auto item_done = [&](int g, unsigned at) { mbar_arrive(&item_free[g][at % kItems]); };
 
     if (warp >= 8) {
-    regs_dec<C::kRegsOther>();
-    if (warp == 8) {
-        // ---------------------------------------------------------------- producer
-        // a lane per copy: its page of the tile, and its 64-column half (bf16), or codes and
-        // scales (stored forms)
-        uint64_t* const ring_full = C::kQuant ? raw_full : full;
-        uint64_t* const ring_empty = C::kQuant ? raw_empty : empty;
-        constexpr int N = C::kQuant ? R : S;
-        const int my = lane % ppt, part = lane / ppt;
-        const bool live = part < (C::kQuant ? 2 : D / 64);
-        const unsigned page_bytes = (unsigned)a.page * (C::kQuant ? C::kCodeRow + C::kScaleRow : 2 * D);
-        bool ok = true, bad = false;
-        unsigned item = 0;  // tiles issued (K and V of a tile are two)
-        while (ok && walk.next(u)) {
-            const int32_t* pages = page_list(u);
-            const int used = (u.keys + a.page - 1) / a.page;  // page entries that hold keys
-            auto page_of = [&](int tile) {
-                const int i = tile * ppt + my;
-                return live && i < used ? __ldg(pages + i) : -2;
+        regs_dec<C::kRegsOther>();
+        if (warp == 10) {
+            // ------------------------------------------------------------ schedule
+            bool ok = true, bad = false;
+            unsigned put[2] = {0, 0};
+            int tile_no = 0;
+            const int ppt = kAtKeys >> page_log, pool_pages = a.pool.slots >> page_log;
+            const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
+            const long long all = (long long)a.agents * TG;
+            struct Feed {
+                AtWalk walk;
+                int head, t, t1;   // the unit's tiles left
+                int page;          // this lane's page of tile t
+                bool first, live;
             };
-            int page = page_of(u.t0);
-            for (int t = 0; t < u.nt && ok; ++t) {
-                const int ahead = t + 1 < u.nt ? page_of(u.t0 + t + 1) : -2;
-                const bool good = page >= 0 && page < pool_pages;
-                if (page != -2 && !good) bad = true;
-                const int boxes = __popc(__ballot_sync(0xffffffffu, good && part == 0));
-#pragma unroll
-                for (int p = 0; p < 2 && ok; ++p, ++item) {
-                    const int st = item % N;
-                    if (item >= N) ok = mbar_wait(&ring_empty[st], (item / N - 1) & 1u);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&ring_full[st], (unsigned)boxes * page_bytes);
-                    __syncwarp();
-                    if (good) {
-                        if (!C::kQuant) {
-                            tma_load_2d(smem + st * C::kTile + part * (kAtKeys * 128) + my * a.page * 128,
-                                        p ? &tm_v : &tm_k, u.head * D + 64 * part, page * a.page, &ring_full[st]);
-                        } else if (part == 0) {
-                            tma_load_2d(rawsm + st * C::kRaw + my * a.page * C::kCodeRow, p ? &tm_v : &tm_k,
-                                        u.head * C::kCodeRow, page * a.page, &ring_full[st]);
-                        } else {
-                            bulk_g2s(rawsm + st * C::kRaw + kAtKeys * C::kCodeRow + my * a.page * C::kScaleRow,
-                                     a.pool.plane[p].scales +
-                                         ((long long)u.head * a.pool.slots + (long long)page * a.page) * C::kScaleRow,
-                                     (unsigned)a.page * C::kScaleRow, &ring_full[st]);
-                        }
+            auto fetch = [&](Feed& f) {
+                const bool prefix = f.walk.rec.seg < a.groups;
+                const int32_t* pages = prefix ? a.prefix_pages + (long long)f.walk.rec.seg * a.max_prefix_pages
+                                              : a.suffix_pages + (long long)f.walk.rec.agent0 * a.max_suffix_pages;
+                const int i = f.t * ppt + lane;
+                const bool used = lane < ppt && i < (f.walk.rec.keys + a.page - 1) >> page_log;
+                f.page = used ? __ldg(pages + i) : -2;
+            };
+            auto advance = [&](Feed& f) {
+                f.live = f.walk.next(f.head, f.t, f.t1);
+                f.first = true;
+                if (f.live) fetch(f);
+            };
+            // hands tile f.t, or the end, to group g
+            auto push = [&](const Feed& f, int g, bool pair) {
+                const int slot = put[g] % kItems;
+                if (put[g] >= kItems) ok = mbar_wait(&item_free[g][slot], (put[g] / kItems - 1) & 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                AtItem* it = &items[g][slot];
+                if (!f.live) {
+                    if (lane == 0) {
+                        it->flags = kEnd;
+                        mbar_arrive(&item_full[g][slot]);
+                    }
+                    ++put[g];
+                    return;
+                }
+                const AtEntry& e = f.walk.rec;
+                const bool there = f.page >= 0 && f.page < pool_pages;
+                const unsigned gone = __ballot_sync(0xffffffffu, f.page != -2 && !there);
+                if (gone) bad = true;
+                if (lane < 8) it->page[lane] = there ? f.page : -1;
+                if (lane == 0) {
+                    unsigned absent = 0;  // by 16 keys
+                    for (int b = 0; b < 8; ++b) absent |= ((gone >> (b >> (page_log - 4))) & 1u) << b;
+                    const bool prefix = e.seg < a.groups;
+                    const int r0 = pair ? kAtRows * g : 0;
+                    it->head = f.head;
+                    it->tile = tile_no;
+                    it->flags = (f.first ? kFirst : 0) | (f.t + 1 == f.t1 ? kLast : 0) | (pair ? kPair : 0) | (prefix ? kPrefix : 0);
+                    it->keys = min(kAtKeys, e.keys - f.t * kAtKeys);
+                    it->key0 = f.t * kAtKeys;
+                    it->rows = min(kAtRows, e.rows - r0);
+                    it->row0 = e.row0 + r0;
+                    it->agent0 = e.agent0;
+                    // prefix: its keys; suffix: a row of new token t sees sees0 + t keys
+                    it->sees0 = prefix ? e.keys : e.keys - (e.row0 + e.rows - 1) / G;
+                    it->absent = (int)absent;
+                    // a unit's first part lies in its rows' own places, a continued one in the CTA's
+                    const bool own = f.walk.rec.begin + (long long)f.head * (e.tiles + 1) >= f.walk.lo;
+                    it->part = own ? ((prefix ? 0 : a.pool.heads) + (long long)f.head) * all + (long long)e.agent0 * TG + e.row0 + r0
+                                   : w.own_rows + (long long)blockIdx.x * (2 * kAtBlock) + (pair ? 0 : kAtBlock) + kAtRows * g;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&item_full[g][slot]);
+                ++put[g];
+            };
+            auto step = [&](Feed& f) {
+                f.first = false;
+                if (++f.t < f.t1) fetch(f);
+                else advance(f);
+            };
+            Feed f0, f1;
+            f0.walk.open(w, 0, blockIdx.x, w.plan->start[0][blockIdx.x], a.pool.heads);
+            advance(f0);
+            while (ok && f0.live) {
+                push(f0, 0, true);
+                if (ok) push(f0, 1, true);
+                ++tile_no;
+                step(f0);
+            }
+            f0.walk.open(w, 1, blockIdx.x, w.plan->start[1][blockIdx.x], a.pool.heads);
+            f1.walk.open(w, 1, blockIdx.x + w.ctas, w.plan->start[2][blockIdx.x], a.pool.heads);
+            advance(f0);
+            advance(f1);
+            // a group that is done says so at its next turn: the other roles wait for that turn
+            bool open0 = true, open1 = true;
+            while (ok && (open0 || open1)) {
+                if (open0) {
+                    open0 = f0.live;
+                    push(f0, 0, false);
+                    if (open0) {
+                        ++tile_no;
+                        step(f0);
                     }
                 }
-                page = ahead;
-            }
-        }
-        if (!ok) {
-            // the copies in flight land before this block gives up its shared memory
-            for (unsigned i = item > N ? item - N : 0; i < item; ++i) mbar_wait(&ring_full[i % N], (i / N) & 1u);
-            if (lane == 0) atomicOr(&abort_flag, 1);
-        }
-        if (bad) atomicOr(&g_status_attend, FLAG_BOUNDS);
-    } else if (C::kQuant && warp >= 12) {
-        // ---------------------------------------------------------------- conversion
-        bool ok = true;
-        unsigned item = 0;
-        while (ok && walk.next(u)) {
-            const int32_t* pages = page_list(u);
-            bool pg = page_ok(u, pages, u.t0);
-            for (int t = 0; t < u.nt && ok; ++t) {
-                const unsigned absent = ~__ballot_sync(0xffffffffu, pg);
-                if (t + 1 < u.nt) pg = page_ok(u, pages, u.t0 + t + 1);
-                const int in_tile = min(kAtKeys, u.keys - (u.t0 + t) * kAtKeys);
-                for (int p = 0; p < 2; ++p, ++item) {
-                    const int rs = item % R, st = item % S;
-                    ok = mbar_wait(&raw_full[rs], (item / R) & 1u);
-                    if (ok && item >= S) ok = mbar_wait(&empty[st], (item / S - 1) & 1u);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    convert_tile<F, D, 128>(rawsm + rs * C::kRaw, smem + st * C::kTile, threadIdx.x - 384, in_tile, absent,
-                                            page_shift);
-                    mbar_arrive(&raw_empty[rs]);
-                    fence_proxy_async_smem();
-                    mbar_arrive(&full[st]);
+                if (ok && open1) {
+                    open1 = f1.live;
+                    push(f1, 1, false);
+                    if (open1) {
+                        ++tile_no;
+                        step(f1);
+                    }
                 }
             }
-        }
-        if (!ok && lane == 0) atomicOr(&abort_flag, 1);
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t id_qk = tc_idesc_bf16(kAtRows, kAtKeys), id_pv = at_idesc_pv(D);
-            // descriptors of the first query block and the first stage (as keys, K-major, and as
-            // values, N-major: 64-column halves 16 KB apart, 8-key groups 1 KB apart); an offset
-            // adds to the address field, which all of shared memory fits
-            const uint64_t q_desc = tc_smem_desc(qsm, 16, 1024, 2), t_desc = tc_smem_desc(smem, 16, 1024, 2);
-            const uint64_t v_desc = tc_smem_desc(smem, kAtKeys * 128, 1024, 2);
-            bool ok = true;
-            unsigned item = 0, nq = 0, np = 0;  // phase bits by group
-            while (ok && walk.next(u)) {
-                const bool two = u.rows > kAtRows;
-                const int jobs = two ? 2 * u.nt : u.nt;
-                for (int j = 0; j <= jobs && ok; ++j) {
-                    if (j < jobs) {
-                        const int g = j & 1, tile = two ? j >> 1 : j;
-                        const unsigned it = item + 2 * tile, st = it % S;
-                        if (j < 2) {
-                            ok = mbar_wait(&q_ready[g], (nq >> g) & 1u);
-                            nq ^= 1u << g;
+            if (!ok && lane == 0) atomicOr(&abort_flag, 1);
+            if (bad && lane == 0) atomicOr(&g_status_attend, FLAG_BOUNDS);
+        } else if (warp == 8) {
+            // ------------------------------------------------------------ producer
+            // a lane per copy: its page of the tile, and its 64-column half (bf16), or codes
+            // and scales (stored forms)
+            uint64_t* const ring_full = C::kQuant ? raw_full : full;
+            uint64_t* const ring_empty = C::kQuant ? raw_empty : empty;
+            constexpr int N = C::kQuant ? R : S;
+            const int ppt = kAtKeys >> page_log, my = lane & (ppt - 1), part = lane >> (7 - page_log);
+            const bool mine = part < (C::kQuant ? 2 : D / 64);
+            const unsigned page_bytes = (unsigned)a.page * (C::kQuant ? C::kCodeRow + C::kScaleRow : 2 * D);
+            bool ok = true, live[2] = {true, true};
+            unsigned at[2] = {0, 0}, item = 0;
+            while (ok && (live[0] || live[1])) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!ok || !live[g]) continue;
+                    ok = item_wait(g, at[g]);
+                    if (!ok) break;
+                    const AtItem& it = items[g][at[g] % kItems];
+                    const int flags = it.flags, head = it.head;
+                    const int page = mine ? it.page[my] : -1;
+                    __syncwarp();
+                    if (lane == 0) item_done(g, at[g]);
+                    ++at[g];
+                    if (flags & kEnd) {
+                        live[g] = false;
+                        continue;
+                    }
+                    if ((flags & kPair) && g == 1) continue;  // the tile is loaded already
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0 && part == 0));
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int st = item % N;
+                        if (item >= N) ok = mbar_wait(&ring_empty[st], (item / N - 1) & 1u);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&ring_full[st], (unsigned)boxes * page_bytes);
+                        __syncwarp();
+                        if (page >= 0) {
+                            if (!C::kQuant) {
+                                tma_load_2d(smem + st * C::kTile + part * (kAtKeys * 128) + (my << page_log) * 128,
+                                            p ? &tm_v : &tm_k, head * D + 64 * part, page << page_log, &ring_full[st]);
+                            } else if (part == 0) {
+                                tma_load_2d(rawsm + st * C::kRaw + (my << page_log) * C::kCodeRow, p ? &tm_v : &tm_k,
+                                            head * C::kCodeRow, page << page_log, &ring_full[st]);
+                            } else {
+                                bulk_g2s(rawsm + st * C::kRaw + kAtKeys * C::kCodeRow + (my << page_log) * C::kScaleRow,
+                                         a.pool.plane[p].scales +
+                                             ((long long)head * a.pool.slots + (page << page_log)) * C::kScaleRow,
+                                         (unsigned)a.page * C::kScaleRow, &ring_full[st]);
+                            }
                         }
-                        if (ok && (!two || g == 0)) ok = mbar_wait(&full[st], (it / S) & 1u);
+                        ++item;
+                    }
+                }
+            }
+            if (!ok) {
+                // the copies in flight land before this block gives up its shared memory
+                for (unsigned i = item > N ? item - N : 0; i < item; ++i) mbar_wait(&ring_full[i % N], (i / N) & 1u);
+                if (lane == 0) atomicOr(&abort_flag, 1);
+            }
+        } else if (warp == 11) {
+            // ------------------------------------------------------------ queries
+            // a unit's query rows, K-major with the 128-byte swizzle, once the last product
+            // with the rows before them is done; rows past the unit's keep what they hold (a
+            // row of a product depends on its own operand row alone)
+            constexpr int V = D / 8;  // 16-byte vectors per row
+            const int cv = lane % V;
+            bool ok = true, live[2] = {true, true};
+            unsigned at[2] = {0, 0}, units[2] = {0, 0};
+            const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
+            while (ok && (live[0] || live[1])) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!ok || !live[g]) continue;
+                    ok = item_wait(g, at[g]);
+                    if (!ok) break;
+                    const AtItem& it = items[g][at[g] % kItems];
+                    const int flags = it.flags, head = it.head, rows = it.rows, row0 = it.row0, agent0 = it.agent0;
+                    __syncwarp();
+                    if (lane == 0) item_done(g, at[g]);
+                    ++at[g];
+                    if (flags & kEnd) live[g] = false;
+                    if (!(flags & kFirst) || (flags & kEnd)) continue;
+                    if (units[g] > 0) ok = mbar_wait(&q_free[g], (units[g] - 1) & 1u);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    ++units[g];
+                    unsigned char* qt = qsm + g * C::kQ + (cv / 8) * (kAtRows * 128);
+                    int r = lane / V;
+                    int ag = (row0 + r) / TG, t = (row0 + r - ag * TG) / G, m = row0 + r - ag * TG - t * G;
+                    for (; r < rows; r += 32 / V) {
+                        cp_async16(qt + r * 128 + (((cv % 8) ^ (r & 7)) << 4),
+                                   a.q + a.qp.row(agent0 + ag, 0, t) + (long long)(head * G + m) * D + 8 * cv);
+                        for (m += 32 / V; m >= G;) {
+                            m -= G;
+                            if (++t == T) {
+                                t = 0;
+                                ++ag;
+                            }
+                        }
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    mbar_arrive(&q_ready[g]);
+                }
+            }
+            if (!ok && lane == 0) atomicOr(&abort_flag, 1);
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ MMA issue
+            if (lane == 0) {
+                constexpr uint32_t id_qk = tc_idesc_bf16(kAtRows, kAtKeys), id_pv = at_idesc_pv(D);
+                // descriptors of the first query block and the first stage (as keys, K-major,
+                // and as values, N-major: 64-column halves 16 KB apart, 8-key groups 1 KB
+                // apart); an offset adds to the address field, which all of shared memory fits
+                const uint64_t q_desc = tc_smem_desc(qsm, 16, 1024, 2), t_desc = tc_smem_desc(smem, 16, 1024, 2);
+                const uint64_t v_desc = tc_smem_desc(smem, kAtKeys * 128, 1024, 2);
+                bool ok = true, live[2] = {true, true};
+                unsigned at[2] = {0, 0};
+                unsigned q_phase = 0, p_phase = 0;  // by group
+                int pend_g = -1, pend_flags = 0, pend_tile = 0;
+                // O += P V of the item whose S was issued last
+                auto values = [&]() {
+                    const int g = pend_g;
+                    const unsigned i = 2u * pend_tile + 1, st = i % S;
+                    ok = mbar_wait(&p_ready[g], (p_phase >> g) & 1u);
+                    p_phase ^= 1u << g;
+                    if (ok) ok = mbar_wait(&full[st], (i / S) & 1u);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t bd = v_desc + st * (uint32_t)(C::kTile >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kAtKeys / 16; ++kk)
+                        tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4),
+                                       id_pv, kk > 0 || !(pend_flags & kFirst) ? 1u : 0u);
+                    if (!(pend_flags & kPair) || g == 1) tc_commit(&empty[st]);
+                    if (pend_flags & kLast) tc_commit(&o_full[g]);
+                    pend_g = -1;
+                };
+                while (ok && (live[0] || live[1])) {
+#pragma unroll 1
+                    for (int g = 0; g < 2; ++g) {
+                        if (!ok || !live[g]) continue;
+                        const unsigned n = at[g];
+                        ok = mbar_wait(&item_full[g][n % kItems], (n / kItems) & 1u);
+                        if (!ok) break;
+                        const int flags = items[g][n % kItems].flags, tile = items[g][n % kItems].tile;
+                        item_done(g, n);
+                        at[g] = n + 1;
+                        if (flags & kEnd) {
+                            live[g] = false;
+                            continue;
+                        }
+                        if (pend_g == g) {  // one group alone: its weights lie where S goes
+                            values();
+                            if (!ok) break;
+                        }
+                        const unsigned i = 2u * tile, st = i % S;
+                        if (flags & kFirst) {
+                            ok = mbar_wait(&q_ready[g], (q_phase >> g) & 1u);
+                            q_phase ^= 1u << g;
+                        }
+                        if (ok) ok = mbar_wait(&full[st], (i / S) & 1u);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t ad = q_desc + (uint32_t)(g * C::kQ >> 4), bd = t_desc + st * (uint32_t)(C::kTile >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t at = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
-                            tc_mma_bf16(tmem + 128 * g, ad + at, bd + at, id_qk, kk > 0 ? 1u : 0u);
+                            const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
+                            tc_mma_bf16(tmem + 128 * g, ad + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
                         }
-                        if (!two || g == 1) tc_commit(&empty[st]);
                         tc_commit(&s_full[g]);
-                    }
-                    if (j > 0) {
-                        const int i = j - 1, g = i & 1, tile = two ? i >> 1 : i;
-                        const unsigned it = item + 2 * tile + 1, st = it % S;
-                        ok = mbar_wait(&p_ready[g], (np >> g) & 1u);
-                        np ^= 1u << g;
-                        if (ok && (!two || g == 0)) ok = mbar_wait(&full[st], (it / S) & 1u);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t bd = v_desc + st * (uint32_t)(C::kTile >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < kAtKeys / 16; ++kk)
-                            tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4),
-                                           id_pv, (i > 1 || kk > 0) ? 1u : 0u);
-                        if (!two || g == 1) tc_commit(&empty[st]);
-                        if (i + 2 >= jobs) tc_commit(&o_full[g]);
+                        if (!(flags & kPair) || g == 1) tc_commit(&empty[st]);
+                        if (flags & kLast) tc_commit(&q_free[g]);
+                        if (pend_g >= 0) values();
+                        pend_g = g;
+                        pend_flags = flags;
+                        pend_tile = tile;
                     }
                 }
-                item += 2 * u.nt;
+                if (ok && pend_g >= 0) values();
+                if (!ok) atomicOr(&abort_flag, 1);
             }
-            if (!ok) atomicOr(&abort_flag, 1);
+        } else if (C::kQuant) {
+            // ------------------------------------------------------------ conversion
+            constexpr int N = 32 * C::kConvWarps;
+            bool ok = true, live[2] = {true, true};
+            unsigned at[2] = {0, 0}, item = 0;
+            while (ok && (live[0] || live[1])) {
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    if (!ok || !live[g]) continue;
+                    ok = item_wait(g, at[g]);
+                    if (!ok) break;
+                    const AtItem& it = items[g][at[g] % kItems];
+                    const int flags = it.flags, keys = it.keys;
+                    const unsigned absent = it.absent;
+                    __syncwarp();
+                    if (lane == 0) item_done(g, at[g]);
+                    ++at[g];
+                    if (flags & kEnd) {
+                        live[g] = false;
+                        continue;
+                    }
+                    if ((flags & kPair) && g == 1) continue;
+#pragma unroll 1
+                    for (int p = 0; p < 2; ++p, ++item) {
+                        const int rs = item % R, st = item % S;
+                        ok = mbar_wait(&raw_full[rs], (item / R) & 1u);
+                        if (ok && item >= S) ok = mbar_wait(&empty[st], (item / S - 1) & 1u);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        convert_tile<F, D, N>(rawsm + rs * C::kRaw, smem + st * C::kTile, threadIdx.x - 384, keys, absent);
+                        mbar_arrive(&raw_empty[rs]);
+                        fence_proxy_async_smem();
+                        mbar_arrive(&full[st]);
+                    }
+                }
+            }
+            if (!ok && lane == 0) atomicOr(&abort_flag, 1);
         }
-    }
     } else {
         regs_inc<C::kRegsSoftmax>();
         // ---------------------------------------------------------------- softmax
         const int g = warp >> 2, wq = warp & 3, row = 32 * wq + lane;  // group, TMEM lane quarter, row
         const uint32_t lanes = (uint32_t)(32 * wq) << 16;
         const uint32_t s_at = tmem + lanes + 128 * g, o_at = tmem + lanes + 256 + 128 * g;
-        unsigned char* qt = qsm + g * C::kQ;
         const float c = a.scale_log2;
+        const float2 c2 = make_float2(c, c);
         bool ok = true;
-        unsigned item = 0, ns = 0, no = 0;
-        while (ok && walk.next(u)) {
-            const bool two = u.rows > kAtRows;
-            const int r0 = two ? kAtRows * g : 0;                    // the group's rows of the block
-            const int rows = min(kAtRows, u.rows - r0);
-            const int jobs = two ? u.nt : (u.nt + 1 - g) / 2;        // tiles of this group
-            const long long part = u.part + (two ? r0 : g * u.rows);
-            if (jobs == 0) {
-                if (row < rows) w.ml[part + row] = make_float2(-INFINITY, 0.f);
-                item += 2 * u.nt;
-                continue;
-            }
-            // the group's queries, K-major with the 128-byte swizzle
-            {
-                constexpr int V = D / 8;  // 16-byte vectors per row
-                const int tg = threadIdx.x & 127, cv = tg % V;
-#pragma unroll 8
-                for (int i = 0; i < V; ++i) {
-                    const int r = tg / V + i * (128 / V);
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows) {
-                        const int at = u.row0 + r0 + r, ag = at / TG, in = at - ag * TG, t = in / G;
-                        x = __ldg(reinterpret_cast<const uint4*>(
-                            a.q + a.qp.row(u.agent0 + ag, 0, t) + (long long)(u.head * G + in - t * G) * D + 8 * cv));
+        unsigned at = 0, units = 0;
+        int rows = 0, sees = 0;   // of the unit: the group's rows; keys this row sees
+        float m = -INFINITY, l = 0.f;
+        while (true) {
+            ok = item_wait(g, at);
+            if (!ok) break;
+            const AtItem& it = items[g][at % kItems];
+            const int flags = it.flags;
+            if (flags & kEnd) break;
+            const int keys = it.keys, key0 = it.key0, tile = it.tile;
+            const unsigned absent = it.absent;
+            if (flags & kFirst) {
+                rows = it.rows;
+                m = -INFINITY;
+                l = 0.f;
+                sees = 0;
+                if (row < rows) {
+                    const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
+                    const int x = it.row0 + row, ag = x / TG, t = (x - ag * TG) / G;
+                    if (flags & kPrefix) {
+                        // the new tokens stand at the end of the sequence: with fewer own keys
+                        // than new tokens the first ones miss part of the prefix
+                        bool ignore = false;
+                        const int own = clamp_len(__ldg(a.suffix_len + it.agent0 + ag), (long long)a.max_suffix_pages * a.page, ignore);
+                        sees = max(0, min(it.sees0, it.sees0 + own - T + 1 + t));
+                    } else {
+                        sees = max(0, it.sees0 + t);
                     }
-                    *reinterpret_cast<uint4*>(qt + (cv / 8) * (kAtRows * 128) + r * 128 + (((cv % 8) ^ (r & 7)) << 4)) = x;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&q_ready[g]);
-            }
-            // keys this thread's row sees, from the segment's first
-            int sees = 0;
-            if (row < rows) {
-                const int at = u.row0 + r0 + row, ag = at / TG, t = (at - ag * TG) / G;
-                const int place = t + 1 - T;
-                if (u.prefix) {
-                    bool ignore = false;
-                    const int own = clamp_len(a.suffix_len[u.agent0 + ag], (long long)a.max_suffix_pages * a.page, ignore);
-                    sees = max(0, min(u.keys, u.keys + own + place));
-                } else {
-                    // u.keys holds the places seen by the block's last row
-                    sees = max(0, u.keys + t - (u.row0 + u.rows - 1) / G);
                 }
             }
             const bool warp_live = 32 * wq < rows;
-            const int32_t* pages = page_list(u);
-            const int step = two ? 1 : 2;
-            bool pg = page_ok(u, pages, u.t0 + (two ? 0 : g));
-            float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < jobs; ++j) {
-                const int tl = two ? j : 2 * j + g, tile = u.t0 + tl;
-                const unsigned absent = ~__ballot_sync(0xffffffffu, pg);  // pages of the tile that are not there
-                if (j + 1 < jobs) pg = page_ok(u, pages, tile + step);
-                const int in_tile = min(kAtKeys, u.keys - tile * kAtKeys);  // keys of the segment in the tile
-                const bool whole = absent == 0u && in_tile == kAtKeys;
-                ok = mbar_wait(&s_full[g], ns++ & 1u);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (!C::kQuant && !whole) {
-                    // value rows that hold no key read as zero: a weight of 0 times what lies
-                    // there (anything, NaN too) would not be 0
-                    const unsigned it = item + 2 * tl + 1, st = it % S;
-                    ok = mbar_wait(&full[st], (it / S) & 1u);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (row >= in_tile || ((absent >> (row / a.page)) & 1u)) {
-                        unsigned char* vt = smem + st * C::kTile + row * 128;
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4*>(vt + h * (kAtKeys * 128) + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                }
-                if (warp_live) {
-                    uint32_t sv[128];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, sv + 32 * i);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_wait_ld32(sv + 32 * i);
-                    const int nv = sees - tile * kAtKeys;  // columns this row sees
-                    if (!whole || __any_sync(0xffffffffu, nv < kAtKeys)) {
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {  // 16 columns: part of one page
-                            const int n = (absent >> (b >> page_shift)) & 1u ? 0 : nv - 16 * b;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (i >= n) sv[16 * b + i] = 0xff800000u;  // -inf
-                        }
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(sv[i]);
-#pragma unroll
-                    for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sv[i]));
-                    const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    const bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float f = raise ? ex2(m - z) : 1.f;  // m = -inf: 0
-                        if (raise) {
-                            m = z;
-                            l *= f;
-                        }
-                        if (j > 0) {
-#pragma unroll
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t o[32];
-                                tmem_ld32(o_at + 32 * i, o);
-                                tmem_wait_ld32(o);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                tmem_st32(o_at + 32 * i, o);
-                            }
-                        }
-                    }
-                    const float off = m == -INFINITY ? 0.f : -m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float x = ex2(__fmaf_rn(__uint_as_float(sv[64 * i + 2 * k]), c, off));
-                            const float y = ex2(__fmaf_rn(__uint_as_float(sv[64 * i + 2 * k + 1]), c, off));
-                            sum[(2 * k) & 3] += x;
-                            sum[(2 * k + 1) & 3] += y;
-                            pk[k] = pack_bf16(x, y);
-                        }
-                        tmem_st32(s_at + 32 * i, pk);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_wait_st();
-                }
-                tc_fence_before();
-                mbar_arrive(&p_ready[g]);
-            }
-            if (!ok) break;
-            ok = mbar_wait(&o_full[g], no++ & 1u);
-            ok = __all_sync(0xffffffffu, ok);
+            const int nv = sees - key0;  // columns this row sees
+            const bool whole = absent == 0u && keys == kAtKeys;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], at & 1u));
             if (!ok) break;
             tc_fence_after();
-            if (warp_live) {
-                float* out = w.o + (part + row) * D;
+            if (!C::kQuant && !whole) {
+                // value rows that hold no key read as zero: a weight of 0 times what lies there
+                // (anything, NaN too) would not be 0
+                const unsigned i = 2u * tile + 1, st = i % S;
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / S) & 1u));
+                if (!ok) break;
+                if (row >= keys || ((absent >> (row >> 4)) & 1u)) {
+                    unsigned char* vt = smem + st * C::kTile + row * 128;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t o[32];
-                    tmem_ld32(o_at + 32 * i, o);
-                    tmem_wait_ld32(o);
-                    if (row < rows)
+                    for (int h = 0; h < D / 64; ++h)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<uint4*>(out + 32 * i + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            *reinterpret_cast<uint4*>(vt + h * (kAtKeys * 128) + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (row < rows) w.ml[part + row] = make_float2(m, l);
-                tc_fence_before();
+                fence_proxy_async_smem();
             }
-            item += 2 * u.nt;
+            if (warp_live) {
+                uint32_t sv[128];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, sv + 32 * i);
+                tmem_wait_ld32(sv);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) tmem_wait_ld32(sv + 32 * i);
+                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys)) {
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                        const int n = (absent >> b) & 1u ? 0 : nv - 16 * b;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i >= n) sv[16 * b + i] = 0xff800000u;  // -inf
+                    }
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[i + 4]));
+#pragma unroll
+                for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx[k] = fmaxf(fmaxf(__uint_as_float(sv[i + k]), __uint_as_float(sv[i + 4 + k])), mx[k]);
+                const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? ex2(m - z) : 1.f;  // m = -inf: 0
+                    if (raise) {
+                        m = z;
+                        l *= f;
+                    }
+                    if (!(flags & kFirst)) {
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            uint32_t o[32];
+                            tmem_ld32(o_at + 32 * i, o);
+                            tmem_wait_ld32(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st32(o_at + 32 * i, o);
+                        }
+                    }
+                }
+                const float off = m == -INFINITY ? 0.f : -m;
+                const float2 off2 = make_float2(off, off);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        float2 x = fma2(make_float2(__uint_as_float(sv[64 * i + 2 * k]), __uint_as_float(sv[64 * i + 2 * k + 1])), c2, off2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[k & 1] = add2(sum[k & 1], x);
+                        pk[k] = pack_bf16(x.x, x.y);
+                    }
+                    tmem_st32(s_at + 32 * i, pk);
+                }
+                l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            mbar_arrive(&p_ready[g]);
+            if (flags & kLast) {
+                const long long part = it.part;
+                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[g], units & 1u));
+                if (!ok) break;
+                ++units;
+                tc_fence_after();
+                if (warp_live) {
+                    float* out = w.o + (part + row) * D;
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + 32 * i, o);
+                        tmem_wait_ld32(o);
+                        if (row < rows)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                *reinterpret_cast<uint4*>(out + 32 * i + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                    if (row < rows) w.ml[part + row] = make_float2(m, l);
+                    tc_fence_before();
+                }
+            }
+            __syncwarp();
+            if (lane == 0) item_done(g, at);
+            ++at;
         }
         if (!ok && lane == 0) atomicOr(&abort_flag, 1);
     }
@@ -830,20 +1045,24 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ join
-// One warp per query row: its prefix's parts, then its suffix's, in the order of the line.
-template <int D>
+// WPR warps per query row: its prefix's parts, then its suffix's; a warp takes every WPR-th
+// part, its lanes first read 32 parts' (max, sum) at once, then each part's O row.  With few
+// rows several warps per row shorten the chain of parts (a long prefix has as many as there
+// are pieces in its head's share of the line); with many rows each has few parts.
+template <int D, int WPR>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a,
                                                           const __grid_constant__ AtWork w) {
     constexpr int V = D / 32;  // values per lane
-    const int lane = threadIdx.x & 31;
-    const long long id = (long long)blockIdx.x * 4 + threadIdx.x / 32;
-    pdl_wait();
-    if (id >= (long long)a.agents * a.new_tokens * a.q_heads) return;
+    __shared__ float sh_m[4], sh_l[4], sh_acc[4][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+    const long long id = (long long)blockIdx.x * (4 / WPR) + warp / WPR;
+    const bool live = id < (long long)a.agents * a.new_tokens * a.q_heads;
     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
-    const int qh = (int)(id % a.q_heads), t = (int)(id / a.q_heads % T);
-    const int agent = (int)(id / ((long long)a.q_heads * T));
+    const int qh = (int)(id % a.q_heads), t = (int)(id / a.q_heads) % T;
+    const int agent = live ? (int)(id / ((long long)a.q_heads * T)) : 0;
     const int head = qh / G, in = t * G + qh % G;
-    const long long total = w.plan->total;
+    const long long all = (long long)a.agents * TG;
+    pdl_wait();
     int group = -1;
     if (a.groups > 0 && agent >= w.bounds[0] && agent < w.bounds[a.groups]) {
         int lo = 0, hi = a.groups;  // bounds[lo] <= agent < bounds[hi]
@@ -857,58 +1076,94 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
     for (int s = 0; s < 2; ++s) {
-        if (s == 0 && group < 0) continue;
+        if (!live || (s == 0 && group < 0)) continue;
         const int seg = s == 0 ? group : a.groups + agent;
-        const int r = s == 0 ? (agent - w.bounds[group]) * TG + in : in;
-        const AtEntry e = w.entries[w.first[seg] + r / kAtBlock];
+        const int agent0 = s == 0 ? w.bounds[group] : agent;
+        const int seg_rows = s == 0 ? (w.bounds[group + 1] - agent0) * TG : TG;
+        const int r = (agent - agent0) * TG + in, block = r / kAtBlock;
+        const bool pair = seg_rows - block * kAtBlock > kAtRows;
+        const int k = pair ? 0 : 1;
+        const int2 first = w.first[seg];
+        const AtEntry e = w.entries[k][pair ? first.x + block : first.y];
         if (e.tiles == 0) continue;
+        const long long chunk = w.plan->chunk[k];
         const long long base = e.begin + (long long)head * (e.tiles + 1), stop = base + e.tiles;
-        const bool two = e.rows > kAtRows;
-        const int sets = two ? 1 : 2, rr = r - e.row0;
-        const long long own = e.prow + (long long)head * (two ? e.rows : 2 * e.rows);
-        // the first CTA whose piece reaches past base
-        long long i0 = base * w.ctas / total;
-        while (i0 > 0 && piece(total, (int)i0, w.ctas) > base) --i0;
-        while (piece(total, (int)i0 + 1, w.ctas) <= base) ++i0;
-        for (long long first = i0 * sets;; first += 32) {
-            // lane k: part first + k (CTA, set)
-            const long long k = first + lane;
-            const int cta = (int)(k / sets), set = (int)(k % sets);
-            const long long lo = cta < w.ctas ? piece(total, cta, w.ctas) : total;
-            const long long hi = cta < w.ctas ? piece(total, cta + 1, w.ctas) : total;
-            const bool in_unit = cta < w.ctas && lo < stop && hi > lo && max(lo, base) < min(hi, stop);
-            const long long part = (lo <= base ? own : w.own_rows + (long long)cta * kAtBlock) + set * e.rows + rr;
+        const long long own = (s * a.pool.heads + (long long)head) * all + (long long)agent0 * TG + r;
+        const long long i0 = quotient(base, chunk), n = quotient(stop - 1, chunk) - i0 + 1;  // pieces that hold tiles
+        for (long long j0 = sub; j0 < n; j0 += 32 * WPR) {
+            const long long j = j0 + (long long)lane * WPR;
+            const bool in_unit = j < n;
+            const long long i = i0 + j;
+            long long part = own;
+            if (j > 0 && in_unit) {
+                const int half = !pair && i >= w.ctas ? 1 : 0, cta = (int)i - half * w.ctas;
+                part = w.own_rows + (long long)cta * (2 * kAtBlock) + (pair ? 0 : kAtBlock + kAtRows * half) + (r - e.row0);
+            }
             float2 ml = make_float2(-INFINITY, 0.f);
             if (in_unit) ml = w.ml[part];
             float top = ml.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float N = fmaxf(M, top);
-            const float f = M == -INFINITY ? 0.f : ex2(M - N);
-            const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - N);
-            // a part with NaN logits keeps m but has l = NaN: it must reach the result
-            const bool counts = !(ml.y == 0.f);
-            float sum = counts ? (ml.x == -INFINITY ? ml.y : ml.y * wt) : 0.f;
+            const float f = M == -INFINITY ? 0.f : exp2f(M - N);
+            const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - N);
+            // (a row with a NaN logit has l = NaN and must keep it)
+            float sum = ml.y == 0.f ? 0.f : ml.y * (ml.x == -INFINITY ? 1.f : wt);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             L = L * f + sum;
             M = N;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] *= f;
-            unsigned live = __ballot_sync(0xffffffffu, in_unit && counts);
-            while (live) {
-                const int b = __ffs(live) - 1;
-                live &= live - 1;
-                const long long p = __shfl_sync(0xffffffffu, part, b);
-                const float x = __shfl_sync(0xffffffffu, wt, b);
-                const float* o = w.o + p * D + V * lane;
+            for (int q = 0; q < V; ++q) acc[q] *= f;
+            const unsigned has = __ballot_sync(0xffffffffu, in_unit && !(ml.y == 0.f));
+            const int count = 32 - __clz(has);
+#pragma unroll 1
+            for (int b0 = 0; b0 < count; b0 += 8) {
+                float x[8][V], wb[8];
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], x, acc[i]);
+                for (int b = 0; b < 8; ++b) {
+                    const long long p = __shfl_sync(0xffffffffu, part, (b0 + b) & 31);
+                    wb[b] = __shfl_sync(0xffffffffu, wt, (b0 + b) & 31);
+                    const bool there = b0 + b < count && ((has >> (b0 + b)) & 1u);
+                    if (!there) wb[b] = 0.f;
+#pragma unroll
+                    for (int q = 0; q < V; ++q) x[b][q] = there ? __ldcg(w.o + p * D + V * lane + q) : 0.f;
+                }
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) acc[q] = fmaf(x[b][q], wb[b], acc[q]);
             }
-            if (__all_sync(0xffffffffu, true) && __shfl_sync(0xffffffffu, (int)(cta + 1 >= w.ctas || hi >= stop), 31)) break;
         }
     }
+    if (WPR > 1) {
+        if (lane == 0) {
+            sh_m[warp] = M;
+            sh_l[warp] = L;
+        }
+#pragma unroll
+        for (int q = 0; q < V; ++q) sh_acc[warp][V * lane + q] = acc[q];
+        __syncthreads();
+        if (sub != 0) return;
+        float N = M;
+#pragma unroll
+        for (int x = 1; x < WPR; ++x) N = fmaxf(N, sh_m[warp + x]);
+        const float f = M == -INFINITY ? 1.f : exp2f(M - N);  // (M = -inf: L is 0, or NaN)
+        L *= f;
+#pragma unroll
+        for (int q = 0; q < V; ++q) acc[q] *= f;
+#pragma unroll
+        for (int x = 1; x < WPR; ++x) {
+            const float mx = sh_m[warp + x], fx = mx == -INFINITY ? 1.f : exp2f(mx - N);
+            L += sh_l[warp + x] * fx;
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[q] = fmaf(sh_acc[warp + x][V * lane + q], fx, acc[q]);
+        }
+        M = N;
+    }
+    if (!live) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const long long oo = a.op.row(agent, 0, t) + (long long)qh * D + V * lane;
     if (V == 4)
@@ -945,7 +1200,9 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, cuda
     if ((e = launch_chained(attend_kernel<F, D>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w)) != cudaSuccess)
         return e;
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;
-    return launch_chained(attend_join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, w);
+    // four warps per row while that leaves them all resident at once
+    if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
+    return launch_chained(attend_join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, w);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
@@ -958,9 +1215,10 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
     unsigned char* base = (unsigned char*)a.workspace;
     AtWork w;
     w.plan = (AtPlan*)(base + l.plan);
-    w.first = (int*)(base + l.first);
+    w.first = (int2*)(base + l.first);
     w.bounds = (int*)(base + l.bounds);
-    w.entries = (AtEntry*)(base + l.entries);
+    w.entries[0] = (AtEntry*)(base + l.entries[0]);
+    w.entries[1] = (AtEntry*)(base + l.entries[1]);
     w.ml = (float2*)(base + l.ml);
     w.o = (float*)(base + l.o);
     w.own_rows = l.own_rows;

@@ -141,6 +141,9 @@ CASES = {
     "many_rows": (1, 8, 128, 16, 1, [700], [0, 40], [3 * i for i in range(40)]),
     "message": (1, 2, 128, 64, 150, [130], [0, 2], [150, 400]),
     "long": (1, 3, 64, 16, 1, [3001], [0, 2], [2, 900]),
+    # more tiles than the work in flight on an SM, halves of an SM that end far apart
+    "uneven": (8, 1, 64, 16, 1, [40000], [0, 8], [0, 3000, 5, 1, 2000, 0, 64, 1300]),
+    "uneven_pairs": (4, 40, 64, 64, 4, [9000], [0, 2], [4, 2500]),
     "seven_heads": (3, 7, 64, 16, 4, [31], [0, 3], [4, 5, 77]),
 }
 
