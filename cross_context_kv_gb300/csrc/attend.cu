@@ -23,8 +23,8 @@
 //                   smaller blocks give both groups the same rows and alternate tiles.  A
 //                   thread owns a row (a TMEM lane): no cross-lane reduction.
 //   warp 8          TMA producer: pages of K and V tiles (128 keys x D) into a ring.
-//   warps 12-15     (stored forms) converters: code tiles and their scales, loaded as they lie,
-//                   to bf16 tiles for the MMA.
+//   warps 12-19     (stored forms) converters: code tiles and their scales, loaded as they lie,
+//                   to bf16 tiles for the MMA; four warps for keys, four for values.
 //   warp 9          one thread issues tcgen05.mma: S = Q K^T (both K-major in shared memory)
 //                   and O += P V with P from tensor memory and V read N-major as it lies.
 // S occupies 128 TMEM columns per group, P (bf16) overwrites the first half of S, O takes D.
@@ -377,20 +377,29 @@ __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem,
 // B N-major (bit 16): keys are the contraction, a value row is contiguous along N.
 __host__ __device__ constexpr uint32_t at_idesc_pv(int N) { return tc_idesc_bf16(kAtRows, N) | (1u << 16); }
 
+// 16 consecutive 32-bit columns of this warp's 32 TMEM lanes from registers.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Registers move from the issuing and converting warpgroups to the softmax ones, whose threads
-// hold a row of logits (setmaxnreg: the shares add up to what the block launches with).
+// Registers move from the other warpgroups to the softmax ones (setmaxnreg: the shares add up
+// to no more than what the block launches with).
 template <int F, int D>
 struct AtCfg {
     static constexpr bool kQuant = F != KVFIX_POOL_BF16;
-    static constexpr int kConvWarps = 4;
-    static constexpr int kThreads = kQuant ? 384 + 32 * kConvWarps : 384;
-    static constexpr int kRegsSoftmax = kQuant ? 168 : 208;
-    static constexpr int kRegsOther = 88;
+    static constexpr int kConvWarps = 4;  // per converting team: one for keys, one for values
+    static constexpr int kThreads = kQuant ? 384 + 64 * kConvWarps : 384;
+    static constexpr int kRegsSoftmax = kQuant ? 120 : 208;
+    static constexpr int kRegsOther = kQuant ? 80 : 88;
     static constexpr int kTile = kAtKeys * D * 2;   // a K or V tile as bf16
     static constexpr int kQ = kAtRows * D * 2;
     static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
@@ -401,6 +410,7 @@ struct AtCfg {
     static constexpr int kRawStages = kQuant ? (F == KVFIX_POOL_E4M3 && D == 128 ? 3 : 6) : 1;
     static constexpr int kSmem = 1024 + kStages * kTile + 2 * kQ + (kQuant ? kRawStages * kRaw : 0);
     static_assert(kSmem <= 227 * 1024 - 1536, "shared memory, with the barriers and items");
+    static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (65536 / kThreads / 8 * 8), "registers");
 };
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -520,7 +530,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             for (int k = 0; k < kItems; ++k) {
                 mbar_init(&item_full[i][k], 1);
                 // readers: producer, MMA, queries, four softmax warps, converters
-                mbar_init(&item_free[i][k], 7 + (C::kQuant ? C::kConvWarps : 0));
+                mbar_init(&item_free[i][k], 7 + (C::kQuant ? 2 * C::kConvWarps : 0));
             }
         }
         fence_mbar_init();
@@ -847,9 +857,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             }
         } else if (C::kQuant) {
             // ------------------------------------------------------------ conversion
+            // one team of warps converts the key tiles, another the value tiles
             constexpr int N = 32 * C::kConvWarps;
+            const int p = (int)(threadIdx.x - 384) / N, tid = (int)(threadIdx.x - 384) % N;
             bool ok = true, live[2] = {true, true};
-            unsigned at[2] = {0, 0}, item = 0;
+            unsigned at[2] = {0, 0}, item = p;
             while (ok && (live[0] || live[1])) {
 #pragma unroll 1
                 for (int g = 0; g < 2; ++g) {
@@ -867,18 +879,16 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         continue;
                     }
                     if ((flags & kPair) && g == 1) continue;
-#pragma unroll 1
-                    for (int p = 0; p < 2; ++p, ++item) {
-                        const int rs = item % R, st = item % S;
-                        ok = mbar_wait(&raw_full[rs], (item / R) & 1u);
-                        if (ok && item >= S) ok = mbar_wait(&empty[st], (item / S - 1) & 1u);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        convert_tile<F, D, N>(rawsm + rs * C::kRaw, smem + st * C::kTile, threadIdx.x - 384, keys, absent);
-                        mbar_arrive(&raw_empty[rs]);
-                        fence_proxy_async_smem();
-                        mbar_arrive(&full[st]);
-                    }
+                    const int rs = item % R, st = item % S;
+                    ok = mbar_wait(&raw_full[rs], (item / R) & 1u);
+                    if (ok && item >= S) ok = mbar_wait(&empty[st], (item / S - 1) & 1u);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    convert_tile<F, D, N>(rawsm + rs * C::kRaw, smem + st * C::kTile, tid, keys, absent);
+                    mbar_arrive(&raw_empty[rs]);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&full[st]);
+                    item += 2;
                 }
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
@@ -945,30 +955,43 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 fence_proxy_async_smem();
             }
             if (warp_live) {
-                uint32_t sv[128];
+                // two sweeps over the row in 32-column pieces, the next piece on its way while
+                // one is worked on: the maximum, then the weights
+                uint32_t x[2][32];
+                const bool masked = __any_sync(0xffffffffu, absent != 0u || nv < kAtKeys);
+                float mx = -INFINITY;
+                tmem_ld32(s_at, x[0]);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, sv + 32 * i);
-                tmem_wait_ld32(sv);
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_wait_ld32(x[k]);
+                        const int at32 = 64 * h + 32 * k;
+                        if (at32 < 96) tmem_ld32(s_at + at32 + 32, x[1 - k]);
+                        if (masked) {
 #pragma unroll
-                for (int i = 1; i < 4; ++i) tmem_wait_ld32(sv + 32 * i);
-                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys)) {
+                            for (int b = 0; b < 2; ++b) {
+                                const int n = (absent >> (at32 / 16 + b)) & 1u ? 0 : nv - at32 - 16 * b;
 #pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        const int n = (absent >> b) & 1u ? 0 : nv - 16 * b;
+                                for (int i = 0; i < 16; ++i)
+                                    if (i >= n) x[k][16 * b + i] = 0xff800000u;  // -inf
+                            }
+                            tmem_st32(s_at + at32, x[k]);
+                        }
+                        float m4[4];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i >= n) sv[16 * b + i] = 0xff800000u;  // -inf
+                        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(x[k][i]), __uint_as_float(x[k][i + 4]));
+#pragma unroll
+                        for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                m4[q] = fmaxf(fmaxf(__uint_as_float(x[k][i + q]), __uint_as_float(x[k][i + 4 + q])), m4[q]);
+                        mx = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mx);
                     }
                 }
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[i + 4]));
-#pragma unroll
-                for (int i = 8; i < 128; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx[k] = fmaxf(fmaxf(__uint_as_float(sv[i + k]), __uint_as_float(sv[i + 4 + k])), mx[k]);
-                const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                if (masked) tmem_wait_st();
+                tmem_ld32(s_at, x[0]);
+                const float z = mx * c;
                 const bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m - z) : 1.f;  // m = -inf: 0
@@ -977,32 +1000,38 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         l *= f;
                     }
                     if (!(flags & kFirst)) {
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 32) {
+                            tmem_ld32(o_at + i, x[1]);
+                            tmem_wait_ld32(x[1]);
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            uint32_t o[32];
-                            tmem_ld32(o_at + 32 * i, o);
-                            tmem_wait_ld32(o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st32(o_at + 32 * i, o);
+                            for (int k = 0; k < 32; ++k) x[1][k] = __float_as_uint(__uint_as_float(x[1][k]) * f);
+                            tmem_st32(o_at + i, x[1]);
                         }
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : -m;
                 const float2 off2 = make_float2(off, off);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t pk[32];
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_wait_ld32(x[k]);
+                        const int at32 = 64 * h + 32 * k;
+                        if (at32 < 96) tmem_ld32(s_at + at32 + 32, x[1 - k]);
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        float2 x = fma2(make_float2(__uint_as_float(sv[64 * i + 2 * k]), __uint_as_float(sv[64 * i + 2 * k + 1])), c2, off2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        sum[k & 1] = add2(sum[k & 1], x);
-                        pk[k] = pack_bf16(x.x, x.y);
+                        for (int i = 0; i < 16; ++i) {
+                            float2 y = fma2(make_float2(__uint_as_float(x[k][2 * i]), __uint_as_float(x[k][2 * i + 1])), c2, off2);
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            sum[i & 1] = add2(sum[i & 1], y);
+                            pk[i] = pack_bf16(y.x, y.y);
+                        }
+                        // over logits of this piece or an earlier one
+                        tmem_st16(s_at + at32 / 2, pk);
                     }
-                    tmem_st32(s_at + 32 * i, pk);
                 }
                 l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 tmem_wait_st();
@@ -1017,7 +1046,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 tc_fence_after();
                 if (warp_live) {
                     float* out = w.o + (part + row) * D;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < D / 32; ++i) {
                         uint32_t o[32];
                         tmem_ld32(o_at + 32 * i, o);
