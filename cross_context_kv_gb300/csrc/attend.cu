@@ -22,11 +22,14 @@
 //                   128 rows give each group its half of the rows and both use every tile;
 //                   smaller blocks give both groups the same rows and alternate tiles.  A
 //                   thread owns a row (a TMEM lane): no cross-lane reduction.
-//   warp 8          TMA producer: pages of K and V tiles (128 keys x D) into a ring.
+//   warp 10         scheduler: walks the CTA's pieces of the line, reads the page lists and hands
+//                   each tile of either group to the other roles.
+//   warp 8          TMA producer: pages of K and V tiles (128 keys x D) into their rings.
+//   warps 9, 11     one per softmax group: loads a unit's queries and issues tcgen05.mma,
+//                   S = Q K^T (both K-major in shared memory), and O += P V with P from tensor
+//                   memory and V read N-major as it lies.
 //   warps 12-19     (stored forms) converters: code tiles and their scales, loaded as they lie,
 //                   to bf16 tiles for the MMA; four warps for keys, four for values.
-//   warp 9          one thread issues tcgen05.mma: S = Q K^T (both K-major in shared memory)
-//                   and O += P V with P from tensor memory and V read N-major as it lies.
 // S occupies 128 TMEM columns per group, P (bf16) overwrites the first half of S, O takes D.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -305,7 +308,7 @@ struct __align__(16) AtItem {
     long long part;                     // first part row
     int page[8];                        // pool pages, -1: not read
 };
-enum : int { kFirst = 1, kLast = 2, kPair = 4, kPrefix = 8, kEnd = 16 };
+enum : int { kFirst = 1, kLast = 2, kPair = 4, kPrefix = 8, kEnd = 16, kKeyTurn = 32, kValueTurn = 64 };
 constexpr int kItems = 4;  // items ahead per group
 
 // Pieces of a line in order of units.
@@ -316,12 +319,12 @@ struct AtWalk {
     AtEntry rec;
     bool have;
 
-    __device__ __forceinline__ void open(const AtWork& w, int k, int piece, int start, int heads) {
-        const long long total = w.plan->total[k], chunk = w.plan->chunk[k];
+    __device__ __forceinline__ void open(const AtWork& w, int k, long long total, long long chunk, int count, int piece,
+                                         int start, int heads) {
         lo = min(total, chunk * piece);
         hi = min(total, lo + chunk);
         ent = w.entries[k];
-        n = w.plan->count[k];
+        n = count;
         H = heads;
         h = 0;
         e = start;
@@ -402,12 +405,15 @@ struct AtCfg {
     static constexpr int kRegsOther = kQuant ? 80 : 88;
     static constexpr int kTile = kAtKeys * D * 2;   // a K or V tile as bf16
     static constexpr int kQ = kAtRows * D * 2;
-    static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    // rings of bf16 tiles: keys are free once their product is done, values wait for the weights
+    static constexpr int kKeyStages = D == 128 ? (kQuant ? 1 : 2) : (kQuant ? 3 : 4);
+    static constexpr int kValueStages = D == 128 ? (kQuant ? 2 : 3) : (kQuant ? 3 : 4);
+    static constexpr int kStages = kKeyStages + kValueStages;
     // stored tiles before conversion: codes, then scales
     static constexpr int kCodeRow = pool_head_bytes(F, D);
     static constexpr int kScaleRow = F == KVFIX_POOL_E4M3 ? 1 : F == KVFIX_POOL_INT4 ? D / 8 : 0;
     static constexpr int kRaw = kQuant ? kAtKeys * (kCodeRow + kScaleRow) : 0;
-    static constexpr int kRawStages = kQuant ? (F == KVFIX_POOL_E4M3 && D == 128 ? 3 : 6) : 1;
+    static constexpr int kRawStages = kQuant ? 2 * (F == KVFIX_POOL_E4M3 && D == 128 ? 2 : 3) : 2;  // half for keys
     static constexpr int kSmem = 1024 + kStages * kTile + 2 * kQ + (kQuant ? kRawStages * kRaw : 0);
     static_assert(kSmem <= 227 * 1024 - 1536, "shared memory, with the barriers and items");
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (65536 / kThreads / 8 * 8), "registers");
@@ -500,37 +506,36 @@ __global__ void __launch_bounds__(AtCfg<F, D>::kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ AttendArgs a, const __grid_constant__ AtWork w) {
     using C = AtCfg<F, D>;
-    constexpr int S = C::kStages, R = C::kRawStages;
+    constexpr int SK = C::kKeyStages, SV = C::kValueStages, R = C::kRawStages / 2;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], raw_full[R], raw_empty[R];
-    __shared__ __align__(8) uint64_t q_ready[2], q_free[2], s_full[2], p_ready[2], o_full[2];
+    __shared__ __align__(8) uint64_t full[3][SK + SV], empty[SK + SV], raw_full[2 * R], raw_empty[2 * R];
+    __shared__ __align__(8) uint64_t q_free[2], s_full[2], p_ready[2], o_full[2];
     __shared__ __align__(8) uint64_t item_full[2][kItems], item_free[2][kItems];
     __shared__ AtItem items[2][kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* qsm = smem + S * C::kTile;
+    unsigned char* qsm = smem + (SK + SV) * C::kTile;
     unsigned char* rawsm = qsm + 2 * C::kQ;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], C::kQuant ? 32 * C::kConvWarps : 1);
-            mbar_init(&empty[i], 1);
+        for (int i = 0; i < SK + SV; ++i) {
+            for (int f = 0; f < 3; ++f) mbar_init(&full[f][i], C::kQuant ? 32 * C::kConvWarps : 1);
+            mbar_init(&empty[i], 2);  // one release per softmax group (a group alone releases twice)
         }
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < 2 * R; ++i) {
             mbar_init(&raw_full[i], 1);
             mbar_init(&raw_empty[i], C::kQuant ? 32 * C::kConvWarps : 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_ready[i], 32);
             mbar_init(&q_free[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 128);
             mbar_init(&o_full[i], 1);
             for (int k = 0; k < kItems; ++k) {
                 mbar_init(&item_full[i][k], 1);
-                // readers: producer, MMA, queries, four softmax warps, converters
-                mbar_init(&item_free[i][k], 7 + (C::kQuant ? 2 * C::kConvWarps : 0));
+                // readers: producer, MMA, four softmax warps, converters
+                mbar_init(&item_free[i][k], 6 + (C::kQuant ? 2 * C::kConvWarps : 0));
             }
         }
         fence_mbar_init();
@@ -538,6 +543,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
+    // Ring place of tile n's keys (p = 0) or values (1).  Who fills a place waits for each of its
+    // releases in turn; who reads it sees only its own tiles, and a parity tells a barrier's
+    // last phase from the one before, no more: so a place has a full barrier per reader (group
+    // 0, group 1, both), whose phases that reader sees one by one, and the item says which
+    // parity its tile's phase has.
+    auto place = [](int p, int n) { return p ? SK + n % SV : n % SK; };
+    auto reader = [](int flags, int g) { return flags & kPair ? 2 : g; };
+    auto released = [](int p, int n) { return (unsigned)((p ? n / SV : n / SK) - 1) & 1u; };  // its use before n's
     if (warp == 9) {
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
@@ -563,6 +576,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // ------------------------------------------------------------ schedule
             bool ok = true, bad = false;
             unsigned put[2] = {0, 0};
+            unsigned turns[3] = {0, 0, 0};  // by reader: the parities of the places' next phases
             int tile_no = 0;
             const int ppt = kAtKeys >> page_log, pool_pages = a.pool.slots >> page_log;
             const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
@@ -613,7 +627,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     const int r0 = pair ? kAtRows * g : 0;
                     it->head = f.head;
                     it->tile = tile_no;
-                    it->flags = (f.first ? kFirst : 0) | (f.t + 1 == f.t1 ? kLast : 0) | (pair ? kPair : 0) | (prefix ? kPrefix : 0);
+                    const unsigned bits = pair ? turns[2] : g ? turns[1] : turns[0];
+                    it->flags = (f.first ? kFirst : 0) | (f.t + 1 == f.t1 ? kLast : 0) | (pair ? kPair : 0) |
+                                (prefix ? kPrefix : 0) | ((bits >> place(0, tile_no)) & 1u ? kKeyTurn : 0) |
+                                ((bits >> place(1, tile_no)) & 1u ? kValueTurn : 0);
                     it->keys = min(kAtKeys, e.keys - f.t * kAtKeys);
                     it->key0 = f.t * kAtKeys;
                     it->rows = min(kAtRows, e.rows - r0);
@@ -631,22 +648,29 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (lane == 0) mbar_arrive(&item_full[g][slot]);
                 ++put[g];
             };
-            auto step = [&](Feed& f) {
+            auto step = [&](Feed& f, unsigned& reader_turns) {
+                reader_turns ^= (1u << place(0, tile_no)) | (1u << place(1, tile_no));
+                ++tile_no;
                 f.first = false;
                 if (++f.t < f.t1) fetch(f);
                 else advance(f);
             };
             Feed f0, f1;
-            f0.walk.open(w, 0, blockIdx.x, w.plan->start[0][blockIdx.x], a.pool.heads);
+            // the plan's head in one round of loads
+            const long long total0 = __ldcg(&w.plan->total[0]), total1 = __ldcg(&w.plan->total[1]);
+            const long long chunk0 = __ldcg(&w.plan->chunk[0]), chunk1 = __ldcg(&w.plan->chunk[1]);
+            const int count0 = __ldcg(&w.plan->count[0]), count1 = __ldcg(&w.plan->count[1]);
+            const int start0 = __ldcg(&w.plan->start[0][blockIdx.x]), start1 = __ldcg(&w.plan->start[1][blockIdx.x]),
+                      start2 = __ldcg(&w.plan->start[2][blockIdx.x]);
+            f0.walk.open(w, 0, total0, chunk0, count0, blockIdx.x, start0, a.pool.heads);
             advance(f0);
             while (ok && f0.live) {
                 push(f0, 0, true);
                 if (ok) push(f0, 1, true);
-                ++tile_no;
-                step(f0);
+                step(f0, turns[2]);
             }
-            f0.walk.open(w, 1, blockIdx.x, w.plan->start[1][blockIdx.x], a.pool.heads);
-            f1.walk.open(w, 1, blockIdx.x + w.ctas, w.plan->start[2][blockIdx.x], a.pool.heads);
+            f0.walk.open(w, 1, total1, chunk1, count1, blockIdx.x, start1, a.pool.heads);
+            f1.walk.open(w, 1, total1, chunk1, count1, blockIdx.x + w.ctas, start2, a.pool.heads);
             advance(f0);
             advance(f1);
             // a group that is done says so at its next turn: the other roles wait for that turn
@@ -655,18 +679,12 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (open0) {
                     open0 = f0.live;
                     push(f0, 0, false);
-                    if (open0) {
-                        ++tile_no;
-                        step(f0);
-                    }
+                    if (open0) step(f0, turns[0]);
                 }
                 if (ok && open1) {
                     open1 = f1.live;
                     push(f1, 1, false);
-                    if (open1) {
-                        ++tile_no;
-                        step(f1);
-                    }
+                    if (open1) step(f1, turns[1]);
                 }
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
@@ -675,14 +693,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // ------------------------------------------------------------ producer
             // a lane per copy: its page of the tile, and its 64-column half (bf16), or codes
             // and scales (stored forms)
-            uint64_t* const ring_full = C::kQuant ? raw_full : full;
-            uint64_t* const ring_empty = C::kQuant ? raw_empty : empty;
-            constexpr int N = C::kQuant ? R : S;
             const int ppt = kAtKeys >> page_log, my = lane & (ppt - 1), part = lane >> (7 - page_log);
             const bool mine = part < (C::kQuant ? 2 : D / 64);
             const unsigned page_bytes = (unsigned)a.page * (C::kQuant ? C::kCodeRow + C::kScaleRow : 2 * D);
             bool ok = true, live[2] = {true, true};
-            unsigned at[2] = {0, 0}, item = 0;
+            unsigned at[2] = {0, 0};
+            int n = 0;
+            uint64_t* last_bar[C::kQuant ? 2 * R : SK + SV] = {};  // of each place's last copy, with its parity
+            unsigned last_turn = 0;
             while (ok && (live[0] || live[1])) {
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -703,165 +721,155 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0 && part == 0));
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const int st = item % N;
-                        if (item >= N) ok = mbar_wait(&ring_empty[st], (item / N - 1) & 1u);
+                        const int st = C::kQuant ? p * R + n % R : place(p, n);
+                        uint64_t* const bar = C::kQuant ? &raw_full[st] : &full[reader(flags, g)][st];
+                        if (C::kQuant) {
+                            if (n >= R) ok = mbar_wait(&raw_empty[st], (unsigned)(n / R - 1) & 1u);
+                        } else if (n >= (p ? SV : SK)) {
+                            ok = mbar_wait(&empty[st], released(p, n));
+                        }
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&ring_full[st], (unsigned)boxes * page_bytes);
+                        if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)boxes * page_bytes);
                         __syncwarp();
                         if (page >= 0) {
                             if (!C::kQuant) {
                                 tma_load_2d(smem + st * C::kTile + part * (kAtKeys * 128) + (my << page_log) * 128,
-                                            p ? &tm_v : &tm_k, head * D + 64 * part, page << page_log, &ring_full[st]);
+                                            p ? &tm_v : &tm_k, head * D + 64 * part, page << page_log, bar);
                             } else if (part == 0) {
                                 tma_load_2d(rawsm + st * C::kRaw + (my << page_log) * C::kCodeRow, p ? &tm_v : &tm_k,
-                                            head * C::kCodeRow, page << page_log, &ring_full[st]);
+                                            head * C::kCodeRow, page << page_log, bar);
                             } else {
                                 bulk_g2s(rawsm + st * C::kRaw + kAtKeys * C::kCodeRow + (my << page_log) * C::kScaleRow,
                                          a.pool.plane[p].scales +
                                              ((long long)head * a.pool.slots + (page << page_log)) * C::kScaleRow,
-                                         (unsigned)a.page * C::kScaleRow, &ring_full[st]);
+                                         (unsigned)a.page * C::kScaleRow, bar);
                             }
                         }
-                        ++item;
+                        const unsigned t = C::kQuant ? (unsigned)(n / R) & 1u : flags & (p ? kValueTurn : kKeyTurn) ? 1u : 0u;
+#pragma unroll
+                        for (int i = 0; i < (C::kQuant ? 2 * R : SK + SV); ++i)
+                            if (i == st) last_bar[i] = bar;
+                        last_turn = (last_turn & ~(1u << st)) | (t << st);
                     }
+                    ++n;
                 }
             }
             if (!ok) {
-                // the copies in flight land before this block gives up its shared memory
-                for (unsigned i = item > N ? item - N : 0; i < item; ++i) mbar_wait(&ring_full[i % N], (i / N) & 1u);
+                // the copies in flight land before this block gives up its shared memory: each
+                // place's last one
+                for (int st = 0; st < (C::kQuant ? 2 * R : SK + SV); ++st)
+                    if (last_bar[st]) mbar_wait(last_bar[st], last_turn >> st & 1u);
                 if (lane == 0) atomicOr(&abort_flag, 1);
             }
-        } else if (warp == 11) {
-            // ------------------------------------------------------------ queries
-            // a unit's query rows, K-major with the 128-byte swizzle, once the last product
-            // with the rows before them is done; rows past the unit's keep what they hold (a
-            // row of a product depends on its own operand row alone)
-            constexpr int V = D / 8;  // 16-byte vectors per row
-            const int cv = lane % V;
-            bool ok = true, live[2] = {true, true};
-            unsigned at[2] = {0, 0}, units[2] = {0, 0};
+        } else if (warp == 9 || warp == 11) {
+            // ------------------------------------------------------------ queries and MMA issue
+            // One warp per softmax group: S = Q K^T, then, once the weights are in tensor
+            // memory, O += P V.  While the group works on a tile's weights the warp looks at its
+            // next tile and, where that begins a unit, brings the unit's queries.
+            const int g = warp == 9 ? 0 : 1;
+            constexpr uint32_t id_qk = tc_idesc_bf16(kAtRows, kAtKeys), id_pv = at_idesc_pv(D);
+            // descriptors of the group's queries and of the first stage (as keys, K-major, and as
+            // values, N-major: 64-column halves 16 KB apart, 8-key groups 1 KB apart); an offset
+            // adds to the address field, which all of shared memory fits
+            unsigned char* const qt = qsm + g * C::kQ;
+            const uint64_t q_desc = tc_smem_desc(qt, 16, 1024, 2), t_desc = tc_smem_desc(smem, 16, 1024, 2);
+            const uint64_t v_desc = tc_smem_desc(smem, kAtKeys * 128, 1024, 2);
             const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
-            while (ok && (live[0] || live[1])) {
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (!ok || !live[g]) continue;
-                    ok = item_wait(g, at[g]);
-                    if (!ok) break;
-                    const AtItem& it = items[g][at[g] % kItems];
-                    const int flags = it.flags, head = it.head, rows = it.rows, row0 = it.row0, agent0 = it.agent0;
-                    __syncwarp();
-                    if (lane == 0) item_done(g, at[g]);
-                    ++at[g];
-                    if (flags & kEnd) live[g] = false;
-                    if (!(flags & kFirst) || (flags & kEnd)) continue;
-                    if (units[g] > 0) ok = mbar_wait(&q_free[g], (units[g] - 1) & 1u);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    ++units[g];
-                    unsigned char* qt = qsm + g * C::kQ + (cv / 8) * (kAtRows * 128);
-                    int r = lane / V;
-                    int ag = (row0 + r) / TG, t = (row0 + r - ag * TG) / G, m = row0 + r - ag * TG - t * G;
-                    for (; r < rows; r += 32 / V) {
-                        cp_async16(qt + r * 128 + (((cv % 8) ^ (r & 7)) << 4),
-                                   a.q + a.qp.row(agent0 + ag, 0, t) + (long long)(head * G + m) * D + 8 * cv);
-                        for (m += 32 / V; m >= G;) {
-                            m -= G;
-                            if (++t == T) {
-                                t = 0;
-                                ++ag;
-                            }
-                        }
+            bool ok = true;
+            unsigned at = 0, units = 0, p_phase = 0;
+            int flags = 0, tile = 0;
+            // Reads the next item; begins to load its queries where it opens a unit, K-major
+            // with the 128-byte swizzle, once the last product with the rows before them is
+            // done.  Rows past the unit's keep what they hold (a row of a product depends on its
+            // own operand row alone).
+            auto open_item = [&]() {
+                ok = item_wait(g, at);
+                if (!ok) return;
+                const AtItem& it = items[g][at % kItems];
+                flags = it.flags;
+                tile = it.tile;
+                const int head = it.head, rows = it.rows, row0 = it.row0, agent0 = it.agent0;
+                __syncwarp();
+                if (lane == 0) item_done(g, at);
+                ++at;
+                if ((flags & kEnd) || !(flags & kFirst)) return;
+                if (units > 0) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[g], (units - 1) & 1u));
+                ++units;
+                if (!ok) return;
+                constexpr int V = D / 8, P = 32 / V;  // 16-byte vectors per row, rows per step
+                const int cv = lane % V;
+                unsigned char* const dst = qt + (cv / 8) * (kAtRows * 128);
+#pragma unroll 1
+                for (int r32 = 0; r32 < rows; r32 += 32) {
+                    // a lane finds one row's place; then P rows a step
+                    const int x = row0 + min(r32 + lane, rows - 1), ag = x / TG, t = (x - ag * TG) / G, m = x - ag * TG - t * G;
+                    const long long off = a.qp.row(agent0 + ag, 0, t) + (long long)(head * G + m) * D;
+#pragma unroll 4
+                    for (int i = 0; i < 32; i += P) {
+                        const int k = i + lane / V, r = r32 + k;
+                        const long long o = __shfl_sync(0xffffffffu, off, k);
+                        if (r < rows) cp_async16(dst + r * 128 + (((cv % 8) ^ (r & 7)) << 4), a.q + o + 8 * cv);
                     }
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    fence_proxy_async_smem();
-                    mbar_arrive(&q_ready[g]);
                 }
-            }
-            if (!ok && lane == 0) atomicOr(&abort_flag, 1);
-        } else if (warp == 9) {
-            // ------------------------------------------------------------ MMA issue
-            if (lane == 0) {
-                constexpr uint32_t id_qk = tc_idesc_bf16(kAtRows, kAtKeys), id_pv = at_idesc_pv(D);
-                // descriptors of the first query block and the first stage (as keys, K-major,
-                // and as values, N-major: 64-column halves 16 KB apart, 8-key groups 1 KB
-                // apart); an offset adds to the address field, which all of shared memory fits
-                const uint64_t q_desc = tc_smem_desc(qsm, 16, 1024, 2), t_desc = tc_smem_desc(smem, 16, 1024, 2);
-                const uint64_t v_desc = tc_smem_desc(smem, kAtKeys * 128, 1024, 2);
-                bool ok = true, live[2] = {true, true};
-                unsigned at[2] = {0, 0};
-                unsigned q_phase = 0, p_phase = 0;  // by group
-                int pend_g = -1, pend_flags = 0, pend_tile = 0;
-                // O += P V of the item whose S was issued last
-                auto values = [&]() {
-                    const int g = pend_g;
-                    const unsigned i = 2u * pend_tile + 1, st = i % S;
-                    ok = mbar_wait(&p_ready[g], (p_phase >> g) & 1u);
-                    p_phase ^= 1u << g;
-                    if (ok) ok = mbar_wait(&full[st], (i / S) & 1u);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t bd = v_desc + st * (uint32_t)(C::kTile >> 4);
+                cp_async_commit();
+            };
+            auto queries_here = [&]() {
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            open_item();
+            if (ok && !(flags & kEnd)) queries_here();
+            while (ok && !(flags & kEnd)) {
+                const int now = flags, n = tile;
+                const int ks = place(0, n), vs = place(1, n);
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[reader(now, g)][ks], now & kKeyTurn ? 1u : 0u));
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t bd = t_desc + (uint32_t)ks * (uint32_t)(C::kTile >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
+                        tc_mma_bf16(tmem + 128 * g, q_desc + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&s_full[g]);
+                    tc_commit(&empty[ks]);
+                    if (!(now & kPair)) tc_commit(&empty[ks]);
+                    if (now & kLast) tc_commit(&q_free[g]);
+                }
+                __syncwarp();
+                open_item();
+                if (!ok) break;
+                ok = mbar_wait(&p_ready[g], p_phase & 1u);
+                p_phase ^= 1u;
+                if (ok) ok = mbar_wait(&full[reader(now, g)][vs], now & kValueTurn ? 1u : 0u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t bd = v_desc + (uint32_t)vs * (uint32_t)(C::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kAtKeys / 16; ++kk)
                         tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4),
-                                       id_pv, kk > 0 || !(pend_flags & kFirst) ? 1u : 0u);
-                    if (!(pend_flags & kPair) || g == 1) tc_commit(&empty[st]);
-                    if (pend_flags & kLast) tc_commit(&o_full[g]);
-                    pend_g = -1;
-                };
-                while (ok && (live[0] || live[1])) {
-#pragma unroll 1
-                    for (int g = 0; g < 2; ++g) {
-                        if (!ok || !live[g]) continue;
-                        const unsigned n = at[g];
-                        ok = mbar_wait(&item_full[g][n % kItems], (n / kItems) & 1u);
-                        if (!ok) break;
-                        const int flags = items[g][n % kItems].flags, tile = items[g][n % kItems].tile;
-                        item_done(g, n);
-                        at[g] = n + 1;
-                        if (flags & kEnd) {
-                            live[g] = false;
-                            continue;
-                        }
-                        if (pend_g == g) {  // one group alone: its weights lie where S goes
-                            values();
-                            if (!ok) break;
-                        }
-                        const unsigned i = 2u * tile, st = i % S;
-                        if (flags & kFirst) {
-                            ok = mbar_wait(&q_ready[g], (q_phase >> g) & 1u);
-                            q_phase ^= 1u << g;
-                        }
-                        if (ok) ok = mbar_wait(&full[st], (i / S) & 1u);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t ad = q_desc + (uint32_t)(g * C::kQ >> 4), bd = t_desc + st * (uint32_t)(C::kTile >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
-                            tc_mma_bf16(tmem + 128 * g, ad + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
-                        }
-                        tc_commit(&s_full[g]);
-                        if (!(flags & kPair) || g == 1) tc_commit(&empty[st]);
-                        if (flags & kLast) tc_commit(&q_free[g]);
-                        if (pend_g >= 0) values();
-                        pend_g = g;
-                        pend_flags = flags;
-                        pend_tile = tile;
-                    }
+                                       id_pv, kk > 0 || !(now & kFirst) ? 1u : 0u);
+                    tc_commit(&empty[vs]);
+                    if (!(now & kPair)) tc_commit(&empty[vs]);
+                    if (now & kLast) tc_commit(&o_full[g]);
                 }
-                if (ok && pend_g >= 0) values();
-                if (!ok) atomicOr(&abort_flag, 1);
+                __syncwarp();
+                if ((flags & kFirst) && !(flags & kEnd)) queries_here();
             }
+            if (!ok && lane == 0) atomicOr(&abort_flag, 1);
         } else if (C::kQuant) {
             // ------------------------------------------------------------ conversion
             // one team of warps converts the key tiles, another the value tiles
             constexpr int N = 32 * C::kConvWarps;
             const int p = (int)(threadIdx.x - 384) / N, tid = (int)(threadIdx.x - 384) % N;
             bool ok = true, live[2] = {true, true};
-            unsigned at[2] = {0, 0}, item = p;
+            unsigned at[2] = {0, 0};
+            int n = 0;
             while (ok && (live[0] || live[1])) {
 #pragma unroll 1
                 for (int g = 0; g < 2; ++g) {
@@ -879,16 +887,16 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         continue;
                     }
                     if ((flags & kPair) && g == 1) continue;
-                    const int rs = item % R, st = item % S;
-                    ok = mbar_wait(&raw_full[rs], (item / R) & 1u);
-                    if (ok && item >= S) ok = mbar_wait(&empty[st], (item / S - 1) & 1u);
+                    const int rs = p * R + n % R, st = place(p, n);
+                    ok = mbar_wait(&raw_full[rs], (unsigned)(n / R) & 1u);
+                    if (ok && n >= (p ? SV : SK)) ok = mbar_wait(&empty[st], released(p, n));
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     convert_tile<F, D, N>(rawsm + rs * C::kRaw, smem + st * C::kTile, tid, keys, absent);
                     mbar_arrive(&raw_empty[rs]);
                     fence_proxy_async_smem();
-                    mbar_arrive(&full[st]);
-                    item += 2;
+                    mbar_arrive(&full[reader(flags, g)][st]);
+                    ++n;
                 }
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
@@ -941,8 +949,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if (!C::kQuant && !whole) {
                 // value rows that hold no key read as zero: a weight of 0 times what lies there
                 // (anything, NaN too) would not be 0
-                const unsigned i = 2u * tile + 1, st = i % S;
-                ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / S) & 1u));
+                const int st = place(1, tile);
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[reader(flags, g)][st], flags & kValueTurn ? 1u : 0u));
                 if (!ok) break;
                 if (row >= keys || ((absent >> (row >> 4)) & 1u)) {
                     unsigned char* vt = smem + st * C::kTile + row * 128;
