@@ -368,6 +368,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// One lane of a converged warp, by elect.sync: in a branch on it the compiler knows that one
+// lane runs, and keeps the operands of tensor instructions in uniform registers.  (Behind
+// `lane == 0` every operand of every product moves through a vector register: 95 cycles a
+// product with four busy warps beside it, against the tensor pipe's 64.)
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
 // D[tmem] (+)= A[tmem] * B[smem], bf16, B as the instruction descriptor says.
 __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
@@ -513,7 +522,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     __shared__ __align__(8) uint64_t item_full[2][kItems], item_free[2][kItems];
     __shared__ AtItem items[2][kItems];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, mma_lock;
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* qsm = smem + (SK + SV) * C::kTile;
     unsigned char* rawsm = qsm + 2 * C::kQ;
@@ -540,6 +549,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         fence_mbar_init();
         abort_flag = 0;
+        mma_lock = 0;
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
@@ -566,7 +576,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     // Items of group g in order.  The roles that serve both groups take them in turn, group 0
     // then 1, an ended group left out; `at` counts a group's items.
     auto item_wait = [&](int g, unsigned at) {
-        return __all_sync(__activemask(), mbar_wait(&item_full[g][at % kItems], (at / kItems) & 1u));
+        return __all_sync(0xffffffffu, mbar_wait(&item_full[g][at % kItems], (at / kItems) & 1u));
     };
     auto item_done = [&](int g, unsigned at) { mbar_arrive(&item_free[g][at % kItems]); };
 
@@ -787,8 +797,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 ok = item_wait(g, at);
                 if (!ok) return;
                 const AtItem& it = items[g][at % kItems];
-                flags = it.flags;
-                tile = it.tile;
+                flags = __shfl_sync(0xffffffffu, it.flags, 0);
+                tile = __shfl_sync(0xffffffffu, it.tile, 0);
                 const int head = it.head, rows = it.rows, row0 = it.row0, agent0 = it.agent0;
                 __syncwarp();
                 if (lane == 0) item_done(g, at);
@@ -819,47 +829,78 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            open_item();
-            if (ok && !(flags & kEnd)) queries_here();
-            while (ok && !(flags & kEnd)) {
-                const int now = flags, n = tile;
-                const int ks = place(0, n), vs = place(1, n);
-                ok = __all_sync(0xffffffffu, mbar_wait(&full[reader(now, g)][ks], now & kKeyTurn ? 1u : 0u));
-                if (!ok) break;
-                tc_fence_after();
+            // The tensor pipe takes products in the order of issue.  A group's O += P V and next
+            // S = Q K^T go in one piece, so that its softmax waits for those alone and the other
+            // group's follow while it works: the two groups settle half a turn apart.
+            auto take_pipe = [&]() {
                 if (lane == 0) {
-                    const uint64_t bd = t_desc + (uint32_t)ks * (uint32_t)(C::kTile >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
-                        tc_mma_bf16(tmem + 128 * g, q_desc + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit(&s_full[g]);
-                    tc_commit(&empty[ks]);
-                    if (!(now & kPair)) tc_commit(&empty[ks]);
-                    if (now & kLast) tc_commit(&q_free[g]);
+                    const long long t0 = clock64();
+                    while (ok && atomicCAS_block(&mma_lock, 0, 1) != 0) ok = clock64() - t0 < kWaitCycles;
                 }
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            auto leave_pipe = [&]() {
+                if (lane == 0) atomicExch_block(&mma_lock, 0);
                 __syncwarp();
+            };
+            auto keys_here = [&]() {
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[reader(flags, g)][place(0, tile)], flags & kKeyTurn ? 1u : 0u));
+            };
+            // S of the open item (one lane)
+            auto logits = [&]() {
+                const int ks = place(0, tile);
+                const uint64_t bd = t_desc + (uint32_t)ks * (uint32_t)(C::kTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
+                    tc_mma_bf16(tmem + 128 * g, q_desc + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(&s_full[g]);
+                tc_commit(&empty[ks]);
+                if (!(flags & kPair)) tc_commit(&empty[ks]);
+                if (flags & kLast) tc_commit(&q_free[g]);
+            };
+            open_item();
+            if (ok && !(flags & kEnd)) {
+                queries_here();
+                keys_here();
+                if (ok) {
+                    tc_fence_after();
+                    if (elect_lane()) logits();
+                    __syncwarp();
+                }
+            }
+            while (ok && !(flags & kEnd)) {
+                const int now = flags, vs = place(1, tile);
                 open_item();
                 if (!ok) break;
+                const bool more = !(flags & kEnd);
                 ok = mbar_wait(&p_ready[g], p_phase & 1u);
                 p_phase ^= 1u;
                 if (ok) ok = mbar_wait(&full[reader(now, g)][vs], now & kValueTurn ? 1u : 0u);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                if (more) {
+                    if (flags & kFirst) queries_here();
+                    keys_here();
+                    if (!ok) break;
+                }
+                take_pipe();
+                if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_lane()) {
                     const uint64_t bd = v_desc + (uint32_t)vs * (uint32_t)(C::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kAtKeys / 16; ++kk)
-                        tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4),
-                                       id_pv, kk > 0 || !(now & kFirst) ? 1u : 0u);
+                        tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4), id_pv,
+                                       kk > 0 || !(now & kFirst) ? 1u : 0u);
                     tc_commit(&empty[vs]);
                     if (!(now & kPair)) tc_commit(&empty[vs]);
                     if (now & kLast) tc_commit(&o_full[g]);
+                    if (more) logits();
                 }
                 __syncwarp();
-                if ((flags & kFirst) && !(flags & kEnd)) queries_here();
+                leave_pipe();
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
         } else if (C::kQuant) {
@@ -1074,32 +1115,41 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         if (!ok && lane == 0) atomicOr(&abort_flag, 1);
     }
+    // The roles end in their own ways: a barrier that counts threads, not warps, for the one that
+    // stands before the tensor memory goes (a warp that reached an aligned barrier in two parts
+    // would count twice, and the memory would go under a group still reading it).
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    asm volatile("barrier.sync 0;" ::: "memory");
+    __syncwarp();
     tc_fence_after();
     if (abort_flag && threadIdx.x == 0) atomicOr(&g_status_attend, FLAG_TIMEOUT);
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ join
-// WPR warps per query row: its prefix's parts, then its suffix's; a warp takes every WPR-th
-// part, its lanes first read 32 parts' (max, sum) at once, then each part's O row.  With few
-// rows several warps per row shorten the chain of parts (a long prefix has as many as there
-// are pieces in its head's share of the line); with many rows each has few parts.
-template <int D, int WPR>
+// A warp takes RPW consecutive rows (new token, query head) of an agent's KV head, whose parts
+// lie side by side: their prefix's parts, then their suffix's; its lanes first read up to 32
+// parts' (max, sum), then each part's O rows.  With few rows WPR warps share the parts of one
+// row (a long prefix has as many as there are pieces in its head's share of the line); with
+// many rows each has few parts, and several rows per warp share the look-ups.
+template <int D, int WPR, int RPW>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a,
                                                           const __grid_constant__ AtWork w) {
+    static_assert(WPR == 1 || RPW == 1, "shared parts or shared rows");
     constexpr int V = D / 32;  // values per lane
     __shared__ float sh_m[4], sh_l[4], sh_acc[4][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+    const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G, H = a.pool.heads;
+    const int chunks = (TG + RPW - 1) / RPW;
     const long long id = (long long)blockIdx.x * (4 / WPR) + warp / WPR;
-    const bool live = id < (long long)a.agents * a.new_tokens * a.q_heads;
-    const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
-    const int qh = (int)(id % a.q_heads), t = (int)(id / a.q_heads) % T;
-    const int agent = live ? (int)(id / ((long long)a.q_heads * T)) : 0;
-    const int head = qh / G, in = t * G + qh % G;
+    const bool live = id < (long long)a.agents * H * chunks;
+    const long long ah = live ? quotient(id, chunks) : 0;
+    const int in0 = live ? (int)(id - ah * chunks) * RPW : 0, rows = min(RPW, TG - in0);
+    const int agent = (int)quotient(ah, H), head = (int)(ah - (long long)agent * H);
     const long long all = (long long)a.agents * TG;
-    pdl_wait();
+    // The plan lies ready before this kernel can start (the attention kernel lets it start only
+    // after its own wait for the plan); only the parts need the wait below.
     int group = -1;
     if (a.groups > 0 && agent >= w.bounds[0] && agent < w.bounds[a.groups]) {
         int lo = 0, hi = a.groups;  // bounds[lo] <= agent < bounds[hi]
@@ -1110,105 +1160,168 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
         }
         group = lo;
     }
-    float M = -INFINITY, L = 0.f, acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    // where the parts of row r of a segment (block-wise the same for its neighbours) lie
+    struct Place {
+        long long own;  // part row of the segment's row 0, first part
+        long long i0;   // first piece
+        int n, pair, row0;
+    };
+    auto find = [&](int s, int r, int seg, int agent0, int seg_rows) {
+        Place p = {0, 0, 0, 0, 0};
+        const int block = r / kAtBlock;
+        p.pair = seg_rows - block * kAtBlock > kAtRows;
+        const int k = p.pair ? 0 : 1;
+        const int2 first = w.first[seg];
+        const AtEntry e = w.entries[k][p.pair ? first.x + block : first.y];
+        if (e.tiles == 0) return p;
+        const long long chunk = w.plan->chunk[k];
+        const long long base = e.begin + (long long)head * (e.tiles + 1);
+        p.own = (s * H + (long long)head) * all + (long long)agent0 * TG;
+        p.i0 = quotient(base, chunk);
+        p.n = (int)(quotient(base + e.tiles - 1, chunk) - p.i0) + 1;  // pieces that hold tiles
+        p.row0 = e.row0;
+        return p;
+    };
+    int seg[2] = {group, a.groups + agent}, agent0[2] = {agent, agent}, seg_rows[2] = {0, TG};
+    Place at[2] = {};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         if (!live || (s == 0 && group < 0)) continue;
-        const int seg = s == 0 ? group : a.groups + agent;
-        const int agent0 = s == 0 ? w.bounds[group] : agent;
-        const int seg_rows = s == 0 ? (w.bounds[group + 1] - agent0) * TG : TG;
-        const int r = (agent - agent0) * TG + in, block = r / kAtBlock;
-        const bool pair = seg_rows - block * kAtBlock > kAtRows;
-        const int k = pair ? 0 : 1;
-        const int2 first = w.first[seg];
-        const AtEntry e = w.entries[k][pair ? first.x + block : first.y];
-        if (e.tiles == 0) continue;
-        const long long chunk = w.plan->chunk[k];
-        const long long base = e.begin + (long long)head * (e.tiles + 1), stop = base + e.tiles;
-        const long long own = (s * a.pool.heads + (long long)head) * all + (long long)agent0 * TG + r;
-        const long long i0 = quotient(base, chunk), n = quotient(stop - 1, chunk) - i0 + 1;  // pieces that hold tiles
-        for (long long j0 = sub; j0 < n; j0 += 32 * WPR) {
-            const long long j = j0 + (long long)lane * WPR;
-            const bool in_unit = j < n;
-            const long long i = i0 + j;
-            long long part = own;
-            if (j > 0 && in_unit) {
-                const int half = !pair && i >= w.ctas ? 1 : 0, cta = (int)i - half * w.ctas;
-                part = w.own_rows + (long long)cta * (2 * kAtBlock) + (pair ? 0 : kAtBlock + kAtRows * half) + (r - e.row0);
-            }
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (in_unit) ml = w.ml[part];
-            float top = ml.x;
+        if (s == 0) {
+            agent0[0] = w.bounds[group];
+            seg_rows[0] = (w.bounds[group + 1] - agent0[0]) * TG;
+        }
+        at[s] = find(s, (agent - agent0[s]) * TG + in0, seg[s], agent0[s], seg_rows[s]);
+    }
+    pdl_wait();
+    float M[RPW], L[RPW], acc[RPW][V];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float N = fmaxf(M, top);
-            const float f = M == -INFINITY ? 0.f : exp2f(M - N);
-            const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - N);
-            // (a row with a NaN logit has l = NaN and must keep it)
-            float sum = ml.y == 0.f ? 0.f : ml.y * (ml.x == -INFINITY ? 1.f : wt);
+    for (int q = 0; q < RPW; ++q) {
+        M[q] = -INFINITY;
+        L[q] = 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            L = L * f + sum;
-            M = N;
+        for (int i = 0; i < V; ++i) acc[q][i] = 0.f;
+    }
 #pragma unroll
-            for (int q = 0; q < V; ++q) acc[q] *= f;
-            const unsigned has = __ballot_sync(0xffffffffu, in_unit && !(ml.y == 0.f));
-            const int count = 32 - __clz(has);
-#pragma unroll 1
-            for (int b0 = 0; b0 < count; b0 += 8) {
-                float x[8][V], wb[8];
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    const long long p = __shfl_sync(0xffffffffu, part, (b0 + b) & 31);
-                    wb[b] = __shfl_sync(0xffffffffu, wt, (b0 + b) & 31);
-                    const bool there = b0 + b < count && ((has >> (b0 + b)) & 1u);
-                    if (!there) wb[b] = 0.f;
-#pragma unroll
-                    for (int q = 0; q < V; ++q) x[b][q] = there ? __ldcg(w.o + p * D + V * lane + q) : 0.f;
+    for (int s = 0; s < 2; ++s) {
+        if (!live || (s == 0 && group < 0)) continue;
+        const int r0 = (agent - agent0[s]) * TG + in0;
+        for (int q0 = 0; q0 < rows;) {  // once, or twice where the rows straddle two blocks
+            const int q1 = min(rows, (r0 + q0) / kAtBlock * kAtBlock + kAtBlock - r0);
+            Place p = at[s];
+            if (q0 > 0) p = find(s, r0 + q0, seg[s], agent0[s], seg_rows[s]);
+            for (int j0 = sub; j0 < p.n; j0 += 32 * WPR) {
+                const int j = j0 + lane * WPR;
+                const bool in_unit = j < p.n;
+                long long part = p.own + r0;
+                if (j > 0 && in_unit) {
+                    const long long i = p.i0 + j;
+                    const int half = !p.pair && i >= w.ctas ? 1 : 0, cta = (int)i - half * w.ctas;
+                    part = w.own_rows + (long long)cta * (2 * kAtBlock) + (p.pair ? 0 : kAtBlock + kAtRows * half) + (r0 - p.row0);
                 }
+                float wt[RPW];
+                unsigned has[RPW], any = 0;
 #pragma unroll
-                for (int b = 0; b < 8; ++b)
+                for (int q = 0; q < RPW; ++q) {
+                    float2 ml = make_float2(-INFINITY, 0.f);
+                    if (in_unit && q >= q0 && q < q1) ml = __ldcg(w.ml + part + q);
+                    float top = ml.x;
 #pragma unroll
-                    for (int q = 0; q < V; ++q) acc[q] = fmaf(x[b][q], wb[b], acc[q]);
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float N = fmaxf(M[q], top);
+                    const float f = M[q] == -INFINITY ? 0.f : exp2f(M[q] - N);
+                    wt[q] = ml.x == -INFINITY ? 0.f : exp2f(ml.x - N);
+                    // (a row with a NaN logit has l = NaN and must keep it)
+                    float sum = ml.y == 0.f ? 0.f : ml.y * (ml.x == -INFINITY ? 1.f : wt[q]);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (top != -INFINITY || !(sum == 0.f)) {
+                        L[q] = L[q] * (M[q] == -INFINITY ? (L[q] == 0.f ? 0.f : 1.f) : f) + sum;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[q][i] *= f;
+                        M[q] = N;
+                    }
+                    has[q] = __ballot_sync(0xffffffffu, !(ml.y == 0.f));
+                    any |= has[q];
+                }
+                const int count = 32 - __clz(any);
+                constexpr int B = RPW > 1 ? 2 : 8;  // parts whose rows are on their way at once
+#pragma unroll 1
+                for (int b0 = 0; b0 < count; b0 += B) {
+                    float x[B][RPW][V], wb[B][RPW];
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        const long long row = __shfl_sync(0xffffffffu, part, (b0 + b) & 31);
+#pragma unroll
+                        for (int q = 0; q < RPW; ++q) {
+                            const bool there = b0 + b < count && ((has[q] >> ((b0 + b) & 31)) & 1u);
+                            wb[b][q] = __shfl_sync(0xffffffffu, wt[q], (b0 + b) & 31);
+                            if (!there) wb[b][q] = 0.f;
+                            const float* src = w.o + (row + q) * D + V * lane;
+                            if (V == 4) {
+                                const float4 v = there ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                x[b][q][0] = v.x;
+                                x[b][q][1] = v.y;
+                                x[b][q][V - 2] = v.z;
+                                x[b][q][V - 1] = v.w;
+                            } else {
+                                const float2 v = there ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+                                x[b][q][0] = v.x;
+                                x[b][q][1] = v.y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < B; ++b)
+#pragma unroll
+                        for (int q = 0; q < RPW; ++q)
+#pragma unroll
+                            for (int i = 0; i < V; ++i) acc[q][i] = fmaf(x[b][q][i], wb[b][q], acc[q][i]);
+                }
             }
+            q0 = q1;
         }
     }
     if (WPR > 1) {
         if (lane == 0) {
-            sh_m[warp] = M;
-            sh_l[warp] = L;
+            sh_m[warp] = M[0];
+            sh_l[warp] = L[0];
         }
 #pragma unroll
-        for (int q = 0; q < V; ++q) sh_acc[warp][V * lane + q] = acc[q];
+        for (int i = 0; i < V; ++i) sh_acc[warp][V * lane + i] = acc[0][i];
         __syncthreads();
         if (sub != 0) return;
-        float N = M;
+        float N = M[0];
 #pragma unroll
         for (int x = 1; x < WPR; ++x) N = fmaxf(N, sh_m[warp + x]);
-        const float f = M == -INFINITY ? 1.f : exp2f(M - N);  // (M = -inf: L is 0, or NaN)
-        L *= f;
+        const float f = M[0] == -INFINITY ? 1.f : exp2f(M[0] - N);  // (M = -inf: L is 0, or NaN)
+        L[0] *= f;
 #pragma unroll
-        for (int q = 0; q < V; ++q) acc[q] *= f;
+        for (int i = 0; i < V; ++i) acc[0][i] *= f;
 #pragma unroll
         for (int x = 1; x < WPR; ++x) {
             const float mx = sh_m[warp + x], fx = mx == -INFINITY ? 1.f : exp2f(mx - N);
-            L += sh_l[warp + x] * fx;
+            L[0] += sh_l[warp + x] * fx;
 #pragma unroll
-            for (int q = 0; q < V; ++q) acc[q] = fmaf(sh_acc[warp + x][V * lane + q], fx, acc[q]);
+            for (int i = 0; i < V; ++i) acc[0][i] = fmaf(sh_acc[warp + x][V * lane + i], fx, acc[0][i]);
         }
-        M = N;
+        M[0] = N;
     }
     if (!live) return;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const long long oo = a.op.row(agent, 0, t) + (long long)qh * D + V * lane;
-    if (V == 4)
-        *reinterpret_cast<uint2*>(a.out + oo) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
-                                                           pack_bf16(acc[V - 2] * inv, acc[V - 1] * inv));
-    else
-        *reinterpret_cast<uint32_t*>(a.out + oo) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (a.lse && lane == 0) a.lse[id] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+#pragma unroll
+    for (int q = 0; q < RPW; ++q) {
+        if (q >= rows) continue;
+        const int in = in0 + q, t = in / G, qh = head * G + in - t * G;
+        const float inv = L[q] == 0.f ? 0.f : 1.f / L[q];
+        const long long oo = a.op.row(agent, 0, t) + (long long)qh * D + V * lane;
+        if (V == 4)
+            *reinterpret_cast<uint2*>(a.out + oo) = make_uint2(pack_bf16(acc[q][0] * inv, acc[q][1] * inv),
+                                                               pack_bf16(acc[q][V - 2] * inv, acc[q][V - 1] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(a.out + oo) = pack_bf16(acc[q][0] * inv, acc[q][1] * inv);
+        if (a.lse && lane == 0)
+            a.lse[((long long)agent * T + t) * a.q_heads + qh] = L[q] == 0.f ? -INFINITY : (M[q] + log2f(L[q])) * 0.69314718055994531f;
+    }
 }
 
 // ------------------------------------------------------------------ host
@@ -1238,8 +1351,13 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, cuda
         return e;
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;
     // four warps per row while that leaves them all resident at once
-    if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
-    return launch_chained(attend_join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, w);
+    if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
+    const int tg = a.new_tokens * (a.q_heads / a.pool.heads);
+    if (tg >= 4) {
+        const long long warps = (long long)a.agents * a.pool.heads * ((tg + 3) / 4);
+        return launch_chained(attend_join_kernel<D, 1, 4>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a, w);
+    }
+    return launch_chained(attend_join_kernel<D, 1, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, w);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
