@@ -68,11 +68,16 @@ struct __align__(16) AtEntry {
     int row0, seg, keys, agent0;  // keys: those that some row of the block may see
 };
 
+// Where a piece of a line begins, all that its walk needs in one round of loads.
+struct __align__(16) AtStart {
+    AtEntry rec;        // the entry
+    long long lo, hi;   // the piece
+    int e, h, n, have;  // the entry's index, the head, the line's entries; whether there is a piece
+};
+
 struct AtPlan {
-    long long total[2], chunk[2];  // pairs, singles: length of the line, of a piece
-    int count[2];                  // entries
-    int pad[2];
-    int start[3][kAtMaxCtas];      // the entry in which a piece begins: pairs, singles of group 0, 1
+    long long chunk[2];               // pairs, singles: length of a piece of the line
+    AtStart start[3][kAtMaxCtas];     // pairs, singles of group 0, of group 1
 };
 
 struct AtLayout {
@@ -177,13 +182,14 @@ __device__ __forceinline__ PlanSums plan_scan(const PlanSums& x, PlanSums* warp_
     return ex;
 }
 
-constexpr int kPlanKept = 1024;  // entries of a line whose places stay in shared memory
+constexpr int kPlanKept = 256;  // entries of a line that stay in shared memory
 
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendArgs a,
                                                                    const __grid_constant__ AtWork w) {
     __shared__ PlanSums warp_sums[kPlanThreads / 32];
     __shared__ int warp_max[kPlanThreads / 32];
-    __shared__ long long kept[2][kPlanKept];
+    __shared__ AtEntry kept[2][kPlanKept];
+    pdl_wait();  // the lengths may be the work of the kernel before
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G, H = a.pool.heads;
@@ -262,13 +268,13 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             if (k == 0) {
                 e.begin = at.line[0];
                 w.entries[0][at.n[0]] = e;
-                if (at.n[0] < kPlanKept) kept[0][at.n[0]] = e.begin;
+                if (at.n[0] < kPlanKept) kept[0][at.n[0]] = e;
                 at.n[0] += 1;
                 at.line[0] += c;
             } else {
                 e.begin = at.line[1];
                 w.entries[1][at.n[1]] = e;
-                if (at.n[1] < kPlanKept) kept[1][at.n[1]] = e.begin;
+                if (at.n[1] < kPlanKept) kept[1][at.n[1]] = e;
                 at.n[1] += 1;
                 at.line[1] += c;
             }
@@ -277,25 +283,35 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     __syncthreads();
     const long long chunk[2] = {max(1ll, quotient(total.line[0] + w.ctas - 1, w.ctas)),
                                 max(1ll, quotient(total.line[1] + 2 * w.ctas - 1, 2 * w.ctas))};
-    // the last entry that begins at or before a piece does
     for (int i = tid; i < 3 * w.ctas; i += kPlanThreads) {
         const int cta = i % w.ctas, set = i / w.ctas, k = set > 0;
+        AtStart* st = &w.plan->start[set][cta];
         const long long lo = chunk[k] * (set == 2 ? cta + w.ctas : cta);
-        if (lo >= total.line[k]) continue;
+        if (lo >= total.line[k]) {
+            st->have = 0;
+            continue;
+        }
+        // The last entry that begins at or before the piece does: entries without tiles take no
+        // room, and of several at one place the last has it.
         int x = 0, y = total.n[k];  // begin[x] <= lo < begin[y]
+        const bool here = total.n[k] <= kPlanKept;
         while (y - x > 1) {
             const int m = (x + y) / 2;
-            const long long b = total.n[k] <= kPlanKept ? kept[k][m] : w.entries[k][m].begin;
+            const long long b = here ? kept[k][m].begin : w.entries[k][m].begin;
             if (b <= lo) x = m;
             else y = m;
         }
-        w.plan->start[set][cta] = x;
+        AtStart r;
+        r.rec = here ? kept[k][x] : w.entries[k][x];
+        r.lo = lo;
+        r.hi = min(total.line[k], lo + chunk[k]);
+        r.e = x;
+        r.h = (int)quotient(lo - r.rec.begin, r.rec.tiles + 1);
+        r.n = total.n[k];
+        r.have = 1;
+        *st = r;
     }
-    if (tid < 2) {
-        w.plan->total[tid] = total.line[tid];
-        w.plan->chunk[tid] = chunk[tid];
-        w.plan->count[tid] = total.n[tid];
-    }
+    if (tid < 2) w.plan->chunk[tid] = tid ? chunk[1] : chunk[0];
     if (bad) atomicOr(&g_status_attend, FLAG_BOUNDS);
 }
 
@@ -319,22 +335,16 @@ struct AtWalk {
     AtEntry rec;
     bool have;
 
-    __device__ __forceinline__ void open(const AtWork& w, int k, long long total, long long chunk, int count, int piece,
-                                         int start, int heads) {
-        lo = min(total, chunk * piece);
-        hi = min(total, lo + chunk);
-        ent = w.entries[k];
-        n = count;
+    __device__ __forceinline__ void open(const AtStart& s, const AtEntry* entries, int heads) {
+        rec = s.rec;
+        lo = s.lo;
+        hi = s.hi;
+        e = s.e;
+        h = s.h;
+        n = s.n;
+        have = s.have != 0;
+        ent = entries;
         H = heads;
-        h = 0;
-        e = start;
-        have = lo < hi;
-        if (have) {
-            rec = ent[e];
-            // entries without tiles take no room: of several at one place the last was found,
-            // and it has the piece's first unit
-            h = rec.tiles > 0 ? (int)quotient(lo - rec.begin, rec.tiles + 1) : H;
-        }
     }
 
     // The next unit's tiles [t0, t1) of head `head` in this piece.
@@ -444,47 +454,59 @@ template <int F, int D, int N>
 __device__ __forceinline__ void convert_tile(const unsigned char* raw, unsigned char* tile, int tid, int in_tile,
                                              unsigned absent) {
     using C = AtCfg<F, D>;
-    constexpr int V = C::kCodeRow / 16;  // vectors per row
+    constexpr int V = C::kCodeRow / 16;       // vectors per row
+    constexpr int P = kAtKeys * V / N;        // vectors per thread
+    constexpr int B = P < 4 ? P : 4;          // on their way at once
     const unsigned char* scales = raw + kAtKeys * C::kCodeRow;
-#pragma unroll 4
-    for (int i = tid; i < kAtKeys * V; i += N) {
-        const int r = i / V, v = i % V;
-        const bool gone = r >= in_tile || ((absent >> (r >> 4)) & 1u);
-        const uint4 x = *reinterpret_cast<const uint4*>(raw + 16 * i);
-        const unsigned c[4] = {x.x, x.y, x.z, x.w};
-        if (F == KVFIX_POOL_E4M3) {
-            const E4m3Scale sc = e4m3_scale(min(max((int)scales[r] - 127, kE4m3MinExp), kE4m3MaxExp));
-            uint2 w[4];
+    const int r0 = tid / V, v = tid % V;
+    const bool partial = in_tile < kAtKeys || absent != 0u;
+#pragma unroll 1
+    for (int k0 = 0; k0 < P; k0 += B) {
+        uint4 x[B];
+        unsigned sc[B];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = e4m3x4_to_bf16(c[k], sc);
-            unsigned nan = 0;
+        for (int k = 0; k < B; ++k) {
+            const int r = r0 + (k0 + k) * (N / V);
+            x[k] = *reinterpret_cast<const uint4*>(raw + 16 * (tid + (k0 + k) * N));
+            if (F == KVFIX_POOL_E4M3) sc[k] = scales[r];
+            else sc[k] = *reinterpret_cast<const unsigned*>(scales + r * C::kScaleRow + 4 * v);
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) nan |= ((c[k] & 0x7f7f7f7fu) + 0x01010101u);
-            if (nan & 0x80808080u)
+        for (int k = 0; k < B; ++k) {
+            const int r = r0 + (k0 + k) * (N / V);
+            const bool gone = partial && (r >= in_tile || ((absent >> (r >> 4)) & 1u));
+            const unsigned c[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            if (F == KVFIX_POOL_E4M3) {
+                const E4m3Scale es = e4m3_scale_byte(sc[k]);
+                uint2 w[4];
+                unsigned nan = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = e4m3x4_nan(c[k], w[k]);
-            uint4 o[2] = {make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), make_uint4(w[2].x, w[2].y, w[3].x, w[3].y)};
-            if (gone) o[0] = o[1] = make_uint4(0u, 0u, 0u, 0u);
-            unsigned char* dst = tile + (v / 4) * (kAtKeys * 128) + r * 128;
-            const int first = (v / 4) & 1;
-            const int c0 = 2 * (v % 4);
-            *reinterpret_cast<uint4*>(dst + (((c0 + first) ^ (r & 7)) << 4)) = first ? o[1] : o[0];
-            *reinterpret_cast<uint4*>(dst + (((c0 + 1 - first) ^ (r & 7)) << 4)) = first ? o[0] : o[1];
-        } else {
-            const unsigned sz = *reinterpret_cast<const unsigned*>(scales + r * C::kScaleRow + 4 * v);
-            const unsigned ss = __byte_perm(sz, 0u, 0x1010), zz = __byte_perm(sz, 0u, 0x3232);
-            unsigned char* dst = tile + (v / 2) * (kAtKeys * 128) + r * 128;
-            uint4 o[4];
+                for (int q = 0; q < 4; ++q) {
+                    w[q] = e4m3x4_to_bf16(c[q], es);
+                    nan |= (c[q] & 0x7f7f7f7fu) + 0x01010101u;
+                }
+                if (nan & 0x80808080u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                o[k] = int4x8_to_bf16(c[k], *reinterpret_cast<const __nv_bfloat162*>(&ss),
-                                      *reinterpret_cast<const __nv_bfloat162*>(&zz));
-                if (gone) o[k] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int q = 0; q < 4; ++q) w[q] = e4m3x4_nan(c[q], w[q]);
+                uint4 o0 = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), o1 = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+                if (gone) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
+                unsigned char* dst = tile + (v / 4) * (kAtKeys * 128) + r * 128;
+                const int c0 = 2 * (v % 4), sw = (v / 4) & 1;  // the upper half's odd chunk first
+                const int a0 = ((c0 ^ (r & 7)) << 4), a1 = (((c0 + 1) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4*>(dst + (sw ? a1 : a0)) = sw ? o1 : o0;
+                *reinterpret_cast<uint4*>(dst + (sw ? a0 : a1)) = sw ? o0 : o1;
+            } else {
+                const unsigned ss = __byte_perm(sc[k], 0u, 0x1010), zz = __byte_perm(sc[k], 0u, 0x3232);
+                unsigned char* dst = tile + (v / 2) * (kAtKeys * 128) + r * 128;
+                const int sw = ((v / 2) & 1) ? 2 : 0;  // the upper half's chunks in the order 2 3 0 1
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint4 o = int4x8_to_bf16(sw ? c[q ^ 2] : c[q], *reinterpret_cast<const __nv_bfloat162*>(&ss),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&zz));
+                    if (gone) o = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(dst + (((4 * (v % 2) + (q ^ sw)) ^ (r & 7)) << 4)) = o;
+                }
             }
-            const bool swap = (v / 2) & 1;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(dst + (((4 * (v % 2) + (swap ? k ^ 2 : k)) ^ (r & 7)) << 4)) = swap ? o[k ^ 2] : o[k];
         }
     }
 }
@@ -666,21 +688,17 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 else advance(f);
             };
             Feed f0, f1;
-            // the plan's head in one round of loads
-            const long long total0 = __ldcg(&w.plan->total[0]), total1 = __ldcg(&w.plan->total[1]);
-            const long long chunk0 = __ldcg(&w.plan->chunk[0]), chunk1 = __ldcg(&w.plan->chunk[1]);
-            const int count0 = __ldcg(&w.plan->count[0]), count1 = __ldcg(&w.plan->count[1]);
-            const int start0 = __ldcg(&w.plan->start[0][blockIdx.x]), start1 = __ldcg(&w.plan->start[1][blockIdx.x]),
-                      start2 = __ldcg(&w.plan->start[2][blockIdx.x]);
-            f0.walk.open(w, 0, total0, chunk0, count0, blockIdx.x, start0, a.pool.heads);
+            const AtStart s0 = w.plan->start[0][blockIdx.x], s1 = w.plan->start[1][blockIdx.x],
+                          s2 = w.plan->start[2][blockIdx.x];
+            f0.walk.open(s0, w.entries[0], a.pool.heads);
             advance(f0);
             while (ok && f0.live) {
                 push(f0, 0, true);
                 if (ok) push(f0, 1, true);
                 step(f0, turns[2]);
             }
-            f0.walk.open(w, 1, total1, chunk1, count1, blockIdx.x, start1, a.pool.heads);
-            f1.walk.open(w, 1, total1, chunk1, count1, blockIdx.x + w.ctas, start2, a.pool.heads);
+            f0.walk.open(s1, w.entries[1], a.pool.heads);
+            f1.walk.open(s2, w.entries[1], a.pool.heads);
             advance(f0);
             advance(f1);
             // a group that is done says so at its next turn: the other roles wait for that turn
@@ -875,16 +893,17 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 open_item();
                 if (!ok) break;
                 const bool more = !(flags & kEnd);
-                ok = mbar_wait(&p_ready[g], p_phase & 1u);
-                p_phase ^= 1u;
-                if (ok) ok = mbar_wait(&full[reader(now, g)][vs], now & kValueTurn ? 1u : 0u);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                // all that the two products read, the weights last
                 if (more) {
                     if (flags & kFirst) queries_here();
                     keys_here();
                     if (!ok) break;
                 }
+                ok = mbar_wait(&full[reader(now, g)][vs], now & kValueTurn ? 1u : 0u);
+                if (ok) ok = mbar_wait(&p_ready[g], p_phase & 1u);
+                p_phase ^= 1u;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 take_pipe();
                 if (!ok) break;
                 tc_fence_after();
@@ -1345,8 +1364,7 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, cuda
     if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(attend_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    attend_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, w);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_chained(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
     if ((e = launch_chained(attend_kernel<F, D>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w)) != cudaSuccess)
         return e;
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;

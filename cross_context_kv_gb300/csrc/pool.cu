@@ -326,7 +326,7 @@ pool_read_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Rop
             for (int p = 0; p < 2; ++p) {
                 uint4 vx = x[u][p], vy = y[u][p];
                 if (F == KVFIX_POOL_E4M3) {
-                    const E4m3Scale s = e4m3_scale(min(max((int)sx[u][p] - 127, kE4m3MinExp), kE4m3MaxExp));
+                    const E4m3Scale s = e4m3_scale_byte(sx[u][p]);
                     const unsigned c[4] = {vx.x, vx.y, vy.x, vy.y};
                     uint2 w[4];
 #pragma unroll

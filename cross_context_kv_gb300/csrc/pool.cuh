@@ -64,13 +64,15 @@ struct E4m3Scale {
     bool two;
 };
 
-__device__ __forceinline__ E4m3Scale e4m3_scale(int k) {
+// From a stored scale byte b (k = b - 127), kept within the format's limits.
+__device__ __forceinline__ E4m3Scale e4m3_scale_byte(unsigned b) {
     E4m3Scale s;
-    const unsigned a = (unsigned)(min(k, 7) + 120 + 127) << 7, b = (unsigned)(max(k - 7, 0) + 127) << 7;
-    const unsigned aa = a | (a << 16), bb = b | (b << 16);
+    b = min(max(b, (unsigned)(kE4m3MinExp + 127)), (unsigned)(kE4m3MaxExp + 127));
+    // a bf16 power of two in both halves: (exponent field) * (2^7 + 2^23)
+    const unsigned aa = (min(b, 134u) + 120u) * 0x00800080u, bb = (max(b, 134u) - 134u + 127u) * 0x00800080u;
     s.a = *reinterpret_cast<const __nv_bfloat162*>(&aa);
     s.b = *reinterpret_cast<const __nv_bfloat162*>(&bb);
-    s.two = k > 7;
+    s.two = b > 134u;
     return s;
 }
 
