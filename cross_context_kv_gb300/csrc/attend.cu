@@ -408,6 +408,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
         : "memory");
 }
 
+// 16 TMEM lanes x 64 32-bit columns: v[4k], v[4k+1] are columns 8k + 2 (lane % 4) + {0, 1} of
+// row lane / 4, v[4k+2], v[4k+3] those of the row 8 below.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -1113,16 +1127,22 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 ++units;
                 tc_fence_after();
                 if (warp_live) {
-                    float* out = w.o + (part + row) * D;
+                    // 16 rows x 64 columns a load, 8 bytes of a row per lane: a store writes eight
+                    // rows' 32-byte sectors (a lane per row would write 32 rows' 16 bytes: 15000
+                    // cycles for the 128 rows against 3000)
+                    const int pair_col = 2 * (lane & 3);
 #pragma unroll 1
-                    for (int i = 0; i < D / 32; ++i) {
+                    for (int i = 0; i < 2 * (D / 64); ++i) {
+                        const int r = 32 * wq + 16 * (i & 1) + lane / 4, c0 = 64 * (i / 2) + pair_col;
                         uint32_t o[32];
-                        tmem_ld32(o_at + 32 * i, o);
+                        tmem_ld_16x64(o_at + ((uint32_t)(16 * (i & 1)) << 16) + 64 * (i / 2), o);
                         tmem_wait_ld32(o);
-                        if (row < rows)
+                        float* out = w.o + (part + r) * D + c0;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                *reinterpret_cast<uint4*>(out + 32 * i + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        for (int k = 0; k < 8; ++k) {
+                            if (r < rows) *reinterpret_cast<uint2*>(out + 8 * k) = make_uint2(o[4 * k], o[4 * k + 1]);
+                            if (r + 8 < rows) *reinterpret_cast<uint2*>(out + 8 * D + 8 * k) = make_uint2(o[4 * k + 2], o[4 * k + 3]);
+                        }
                     }
                     if (row < rows) w.ml[part + row] = make_float2(m, l);
                     tc_fence_before();
