@@ -439,14 +439,14 @@ struct AtCfg {
     static constexpr int kTile = kAtKeys * D * 2;   // a K or V tile as bf16
     static constexpr int kQ = kAtRows * D * 2;
     // rings of bf16 tiles: keys are free once their product is done, values wait for the weights
-    static constexpr int kKeyStages = D == 128 ? (kQuant ? 1 : 2) : (kQuant ? 3 : 4);
-    static constexpr int kValueStages = D == 128 ? (kQuant ? 2 : 3) : (kQuant ? 3 : 4);
+    static constexpr int kKeyStages = D == 128 ? 2 : 4;
+    static constexpr int kValueStages = D == 128 ? (kQuant ? 2 : 3) : 4;
     static constexpr int kStages = kKeyStages + kValueStages;
     // stored tiles before conversion: codes, then scales
     static constexpr int kCodeRow = pool_head_bytes(F, D);
     static constexpr int kScaleRow = F == KVFIX_POOL_E4M3 ? 1 : F == KVFIX_POOL_INT4 ? D / 8 : 0;
     static constexpr int kRaw = kQuant ? kAtKeys * (kCodeRow + kScaleRow) : 0;
-    static constexpr int kRawStages = kQuant ? 2 * (F == KVFIX_POOL_E4M3 && D == 128 ? 2 : 3) : 2;  // half for keys
+    static constexpr int kRawStages = kQuant && D == 64 ? 4 : 2;  // half for keys
     static constexpr int kSmem = 1024 + kStages * kTile + 2 * kQ + (kQuant ? kRawStages * kRaw : 0);
     static_assert(kSmem <= 227 * 1024 - 1536, "shared memory, with the barriers and items");
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (65536 / kThreads / 8 * 8), "registers");
@@ -461,69 +461,65 @@ __device__ __forceinline__ void regs_dec() {
 }
 
 // One stored tile (codes [128][kCodeRow], scales [128][kScaleRow]) to the bf16 tile the MMA
-// reads: rows of 128 bytes per 64-column half, 128-byte swizzle.  Rows that hold no key
-// (`gone`) become zero.  A thread takes 16 code bytes at a time; the order in which it writes
-// their 16-byte chunks puts the eight threads of a store phase on different banks.
+// reads: rows of 128 bytes per 64-column half, 128-byte swizzle.  Rows that hold no key become
+// zero.  A team of N threads first takes the whole stored tile into registers, so that the
+// next one can be on its way while this one is converted; a thread has 16 code bytes of a row
+// at a time, and the order in which it writes their 16-byte chunks puts the eight threads of a
+// store phase on different banks.
 template <int F, int D, int N>
-__device__ __forceinline__ void convert_tile(const unsigned char* raw, unsigned char* tile, int tid, int in_tile,
-                                             unsigned absent) {
+struct StoredTile {
     using C = AtCfg<F, D>;
-    constexpr int V = C::kCodeRow / 16;       // vectors per row
-    constexpr int P = kAtKeys * V / N;        // vectors per thread
-    constexpr int B = P < 4 ? P : 4;          // on their way at once
-    const unsigned char* scales = raw + kAtKeys * C::kCodeRow;
-    const int r0 = tid / V, v = tid % V;
-    const bool partial = in_tile < kAtKeys || absent != 0u;
-#pragma unroll 1
-    for (int k0 = 0; k0 < P; k0 += B) {
-        uint4 x[B];
-        unsigned sc[B];
+    static constexpr int V = C::kCodeRow / 16;  // vectors per row
+    static constexpr int P = kAtKeys * V / N;   // vectors per thread
+    uint4 x[P];
+    unsigned sc[P];
+
+    __device__ __forceinline__ void take(const unsigned char* raw, int tid) {
+        const unsigned char* scales = raw + kAtKeys * C::kCodeRow;
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const int r = r0 + (k0 + k) * (N / V);
-            x[k] = *reinterpret_cast<const uint4*>(raw + 16 * (tid + (k0 + k) * N));
+        for (int k = 0; k < P; ++k) {
+            const int r = tid / V + k * (N / V);
+            x[k] = *reinterpret_cast<const uint4*>(raw + 16 * (tid + k * N));
             if (F == KVFIX_POOL_E4M3) sc[k] = scales[r];
-            else sc[k] = *reinterpret_cast<const unsigned*>(scales + r * C::kScaleRow + 4 * v);
+            else sc[k] = *reinterpret_cast<const unsigned*>(scales + r * C::kScaleRow + 4 * (tid % V));
         }
+    }
+
+    __device__ __forceinline__ void put(unsigned char* tile, int tid, int in_tile, unsigned absent) const {
+        const int r0 = tid / V, v = tid % V;
+        const bool partial = in_tile < kAtKeys || absent != 0u;
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const int r = r0 + (k0 + k) * (N / V);
+        for (int k = 0; k < P; ++k) {
+            const int r = r0 + k * (N / V);
             const bool gone = partial && (r >= in_tile || ((absent >> (r >> 4)) & 1u));
             const unsigned c[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             if (F == KVFIX_POOL_E4M3) {
-                const E4m3Scale es = e4m3_scale_byte(sc[k]);
+                E4m3Scale es = e4m3_scale_byte(sc[k]);
+                if (gone) es.a = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
                 uint2 w[4];
-                unsigned nan = 0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    w[q] = e4m3x4_to_bf16(c[q], es);
-                    nan |= (c[q] & 0x7f7f7f7fu) + 0x01010101u;
-                }
-                if (nan & 0x80808080u)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) w[q] = e4m3x4_nan(c[q], w[q]);
-                uint4 o0 = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), o1 = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
-                if (gone) o0 = o1 = make_uint4(0u, 0u, 0u, 0u);
+                for (int q = 0; q < 4; ++q) w[q] = e4m3x4_to_bf16(c[q], es);
+                const uint4 o0 = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), o1 = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
                 unsigned char* dst = tile + (v / 4) * (kAtKeys * 128) + r * 128;
                 const int c0 = 2 * (v % 4), sw = (v / 4) & 1;  // the upper half's odd chunk first
                 const int a0 = ((c0 ^ (r & 7)) << 4), a1 = (((c0 + 1) ^ (r & 7)) << 4);
                 *reinterpret_cast<uint4*>(dst + (sw ? a1 : a0)) = sw ? o1 : o0;
                 *reinterpret_cast<uint4*>(dst + (sw ? a0 : a1)) = sw ? o0 : o1;
             } else {
-                const unsigned ss = __byte_perm(sc[k], 0u, 0x1010), zz = __byte_perm(sc[k], 0u, 0x3232);
+                const unsigned sz = gone ? 0u : sc[k];
+                const unsigned ss = __byte_perm(sz, 0u, 0x1010), zz = __byte_perm(sz, 0u, 0x3232);
                 unsigned char* dst = tile + (v / 2) * (kAtKeys * 128) + r * 128;
                 const int sw = ((v / 2) & 1) ? 2 : 0;  // the upper half's chunks in the order 2 3 0 1
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint4 o = int4x8_to_bf16(sw ? c[q ^ 2] : c[q], *reinterpret_cast<const __nv_bfloat162*>(&ss),
-                                             *reinterpret_cast<const __nv_bfloat162*>(&zz));
-                    if (gone) o = make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 o = int4x8_to_bf16(sw ? c[q ^ 2] : c[q], *reinterpret_cast<const __nv_bfloat162*>(&ss),
+                                                   *reinterpret_cast<const __nv_bfloat162*>(&zz));
                     *reinterpret_cast<uint4*>(dst + (((4 * (v % 2) + (q ^ sw)) ^ (r & 7)) << 4)) = o;
                 }
             }
         }
     }
-}
+};
 
 // A row's maximum is raised (and its accumulator rescaled) once a logit passes it by more
 // than this many powers of two: weights stay below 2^8, and bf16 keeps 8 bits of any of them.
@@ -962,12 +958,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     }
                     if ((flags & kPair) && g == 1) continue;
                     const int rs = p * R + n % R, st = place(p, n);
-                    ok = mbar_wait(&raw_full[rs], (unsigned)(n / R) & 1u);
-                    if (ok && n >= (p ? SV : SK)) ok = mbar_wait(&empty[st], released(p, n));
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], (unsigned)(n / R) & 1u));
                     if (!ok) break;
-                    convert_tile<F, D, N>(rawsm + rs * C::kRaw, smem + st * C::kTile, tid, keys, absent);
+                    StoredTile<F, D, N> stored;
+                    stored.take(rawsm + rs * C::kRaw, tid);
                     mbar_arrive(&raw_empty[rs]);
+                    if (n >= (p ? SV : SK)) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], released(p, n)));
+                    if (!ok) break;
+                    stored.put(smem + st * C::kTile, tid, keys, absent);
                     fence_proxy_async_smem();
                     mbar_arrive(&full[reader(flags, g)][st]);
                     ++n;

@@ -68,6 +68,8 @@ __device__ __forceinline__ int e4m3_exponent(unsigned a) {
     return min(max(k, kE4m3MinExp), kE4m3MaxExp);
 }
 
+constexpr unsigned kNanRow = 0xffffu;
+
 __device__ __forceinline__ uint2 to_e4m3(const uint4& v, float inv) {
     float f[8];
     unpack8(v, f);
@@ -233,13 +235,16 @@ pool_write_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Ro
                         *reinterpret_cast<uint4*>(codes + at + D + 16 * j) = y;
                     }
                 } else if (F == KVFIX_POOL_E4M3) {
+                    // the largest finite magnitude; above them all, a mark that the row has a NaN
                     unsigned m = abs_max16(x, y);
-                    if (m >= 0x7f80u) m = max(finite_abs_max8(x), finite_abs_max8(y));
+                    if (m > 0x7f80u) m = kNanRow;
+                    else if (m == 0x7f80u) m = max(finite_abs_max8(x), finite_abs_max8(y));
 #pragma unroll
                     for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    const int k = e4m3_exponent(m);
-                    const float inv = pow2f(-k);
-                    const uint2 cx = to_e4m3(x, inv), cy = to_e4m3(y, inv);
+                    const int k = m == kNanRow ? (int)kE4m3NanByte - 127 : e4m3_exponent(m);
+                    const float inv = pow2f(-min(k, kE4m3MaxExp));
+                    uint2 cx = to_e4m3(x, inv), cy = to_e4m3(y, inv);
+                    if (m == kNanRow) cx = cy = make_uint2(0u, 0u);
                     if (slot[u] >= 0) {
                         *reinterpret_cast<uint2*>(codes + at + 8 * j) = cx;
                         *reinterpret_cast<uint2*>(codes + at + D / 2 + 8 * j) = cy;
@@ -330,10 +335,7 @@ pool_read_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Rop
                     const unsigned c[4] = {vx.x, vx.y, vy.x, vy.y};
                     uint2 w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = e4m3x4_to_bf16(c[i], s);
-                        if (e4m3x4_has_nan(c[i])) w[i] = e4m3x4_nan(c[i], w[i]);
-                    }
+                    for (int i = 0; i < 4; ++i) w[i] = e4m3x4_to_bf16(c[i], s);
                     vx = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
                     vy = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
                 } else if (F == KVFIX_POOL_INT4) {

@@ -2,7 +2,8 @@
 // that write, read and attend over a pool.
 //
 //   bf16  the values.
-//   e4m3  one byte per value and one byte b per (slot, head): value = e4m3(code) 2^(b-127).
+//   e4m3  one byte per value and one byte b per (slot, head): value = e4m3(code) 2^(b-127),
+//         or NaN throughout for b = 255 (a row that held a NaN).
 //         The scale is a power of two, so scaling a value to its code's range is exact, and
 //         every stored value is exactly a bf16 value (4 significant bits, an exponent within
 //         [-110-9, 119+8]): nothing is lost when rows are read back or become bf16
@@ -58,30 +59,34 @@ __device__ __forceinline__ float pow2f(int k) { return __uint_as_float((unsigned
 // ------------------------------------------------------------- e4m3 -> bf16, exactly
 // A code s eeee mmm moved to the bf16 fields s 0000eeee mmm0000 is the value times 2^-120
 // (subnormal codes included, as bf16 subnormals), so one or two exact multiplications by
-// powers of two give the stored value: mul holds (2^(120+min(k,7)), 2^max(k-7,0)) as pairs.
+// powers of two give the stored value: pairs of 2^(120+min(k,7)) and 2^max(k-7,0), k = b - 127.
 struct E4m3Scale {
     __nv_bfloat162 a, b;
     bool two;
 };
 
-// From a stored scale byte b (k = b - 127), kept within the format's limits.
-__device__ __forceinline__ E4m3Scale e4m3_scale_byte(unsigned b) {
+constexpr unsigned kE4m3NanByte = 255;  // the scale byte of a row that holds a NaN: all of it reads NaN
+
+// From a stored scale byte, kept within the format's limits.
+__device__ __forceinline__ E4m3Scale e4m3_scale_byte(unsigned byte) {
     E4m3Scale s;
-    b = min(max(b, (unsigned)(kE4m3MinExp + 127)), (unsigned)(kE4m3MaxExp + 127));
+    const unsigned b = min(max(byte, (unsigned)(kE4m3MinExp + 127)), (unsigned)(kE4m3MaxExp + 127));
     // a bf16 power of two in both halves: (exponent field) * (2^7 + 2^23)
-    const unsigned aa = (min(b, 134u) + 120u) * 0x00800080u, bb = (max(b, 134u) - 134u + 127u) * 0x00800080u;
+    unsigned aa = (min(b, 134u) + 120u) * 0x00800080u;
+    const unsigned bb = (max(b, 134u) - 134u + 127u) * 0x00800080u;
+    if (byte == kE4m3NanByte) aa = 0x7fff7fffu;
     s.a = *reinterpret_cast<const __nv_bfloat162*>(&aa);
     s.b = *reinterpret_cast<const __nv_bfloat162*>(&bb);
     s.two = b > 134u;
     return s;
 }
 
-// Four codes (bytes in order) to two bf16 pairs.  The code 0x7f (NaN) would read as 480:
-// it is replaced by bf16 NaN.
+// Four codes (bytes in order) to two bf16 pairs: the nibbles of every code at their places in
+// the high and the low bytes of the results, then the bytes side by side.
 __device__ __forceinline__ uint2 e4m3x4_to_bf16(unsigned codes, const E4m3Scale& s) {
-    const unsigned y0 = __byte_perm(codes, 0u, 0x1404), y1 = __byte_perm(codes, 0u, 0x3424);
-    unsigned r0 = (y0 & 0x80008000u) | ((y0 >> 4) & 0x07f007f0u);
-    unsigned r1 = (y1 & 0x80008000u) | ((y1 >> 4) & 0x07f007f0u);
+    const unsigned hi = ((codes >> 4) & 0x07070707u) | (codes & 0x80808080u);
+    const unsigned lo = (codes << 4) & 0xf0f0f0f0u;
+    unsigned r0 = __byte_perm(lo, hi, 0x5140), r1 = __byte_perm(lo, hi, 0x7362);
     __nv_bfloat162 p0 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r0), s.a);
     __nv_bfloat162 p1 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r1), s.a);
     if (s.two) {
@@ -89,22 +94,6 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(unsigned codes, const E4m3Scale&
         p1 = __hmul2(p1, s.b);
     }
     return make_uint2(*reinterpret_cast<unsigned*>(&p0), *reinterpret_cast<unsigned*>(&p1));
-}
-
-// Whether one of four codes is NaN (0x7f or 0xff).
-__device__ __forceinline__ bool e4m3x4_has_nan(unsigned codes) {
-    const unsigned m = (codes & 0x7f7f7f7fu) + 0x01010101u;  // a byte's top bit: its code is 0x7f
-    return (m & 0x80808080u) != 0u;
-}
-
-__device__ __forceinline__ uint2 e4m3x4_nan(unsigned codes, uint2 v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (((codes >> (8 * i)) & 0x7fu) == 0x7fu) {
-            unsigned& w = i < 2 ? v.x : v.y;
-            w = (i & 1) ? (w & 0xffffu) | 0x7fff0000u : (w & 0xffff0000u) | 0x7fffu;
-        }
-    return v;
 }
 
 // ------------------------------------------------------------- int4 -> bf16

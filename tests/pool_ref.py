@@ -26,8 +26,10 @@ def e4m3_values():
     c = np.arange(256)
     e, m = (c >> 3) & 15, (c & 7).astype(np.float64)
     v = np.where(e > 0, (8 + m) * 2.0 ** (e - 10.0), m * 2.0 ** -9)
-    v[(c & 127) == 127] = np.nan
     return np.where(c > 127, -v, v)
+
+
+NAN_ROW = 255  # the scale byte of a row that holds a NaN
 
 
 def e4m3_encode(x):
@@ -45,12 +47,15 @@ def e4m3_encode(x):
     up = np.clip(np.searchsorted(grid, y), 1, 126)
     lo, hi = grid[up - 1], grid[up]
     pick = np.where((y - lo < hi - y) | ((y - lo == hi - y) & ((up - 1) % 2 == 0)), up - 1, up)
-    code = np.where(np.isnan(x), 127, pick) | np.where(np.signbit(x) & ~np.isnan(x), 128, 0)
-    return code.astype(np.uint8), (k + 127).astype(np.uint8)
+    code = pick | np.where(np.signbit(x), 128, 0)
+    bad = np.isnan(x).any(-1)
+    code[bad] &= 128  # (the sign of a zero code means nothing)
+    return code.astype(np.uint8), np.where(bad, NAN_ROW, k + 127).astype(np.uint8)
 
 
 def e4m3_decode(codes, scale):
-    return e4m3_values()[codes] * 2.0 ** (scale.astype(np.float64) - 127)[..., None]
+    v = e4m3_values()[codes] * 2.0 ** (scale.astype(np.float64) - 127)[..., None]
+    return np.where((scale == NAN_ROW)[..., None], np.nan, v)
 
 
 def int4_encode(x):

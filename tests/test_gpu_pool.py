@@ -61,8 +61,8 @@ def assert_same_rows(fmt, got, want):
         assert np.array_equal(gc, wc)
         return
     if fmt == "e4m3":
-        gc, wc = (np.where((c & 127) == 127, 127, c) for c in (gc, wc))
         assert np.array_equal(gs, ws)
+        gc, wc = (np.where((s == ref.NAN_ROW)[..., None], c & 127, c) for c, s in ((gc, gs), (wc, ws)))
     else:
         assert np.array_equal(ref.of_bf16(gs), ref.of_bf16(ws))  # -0 and +0 zeros are the same zero
     assert np.array_equal(gc, wc)
@@ -199,12 +199,14 @@ def test_odd_values(kvfix, fmt, dim):
 
 @gpu
 def test_every_e4m3_code_at_every_scale_reads_exactly(kvfix):
-    """All 256 codes at the 230 scales the format allows."""
+    """All 254 codes that are written at the 230 scales the format allows, and the NaN scale."""
     dim, n = 128, 2 * 230
     pool = kvfix.pool_empty("e4m3", 1, n, 1, dim)
     codes = np.arange(256, dtype=np.uint8).reshape(2, 128)
+    codes[codes & 127 == 127] = 0
     pool.k.copy_(torch.from_numpy(np.tile(codes, (230, 1)).reshape(1, n, 1, dim)))
     scale = np.repeat(np.arange(-110, 120) + 127, 2).astype(np.uint8)
+    scale[100] = ref.NAN_ROW
     pool.k_scales.copy_(torch.from_numpy(scale.reshape(1, 1, n)))
     k, _ = kvfix.pool_read(pool, torch.arange(n, dtype=torch.int32, device="cuda").view(1, n))
     got = ref.of_bf16(words_of(k)).reshape(n, dim)
@@ -350,6 +352,7 @@ def test_the_restatement_itself():
     half a step of its form."""
     v = ref.e4m3_values()
     codes = np.array([c for c in range(256) if c & 127 != 127], np.uint8)
+    assert v[126] == 448 and v[1] == 2.0 ** -9 and v[8] == 2.0 ** -6 and v[0x38] == 1.0
     row = np.concatenate((v[codes], [448.0, 0.0]))           # the largest code fixes the scale at 1
     got, k = ref.e4m3_encode(row)
     assert k == 127 and np.array_equal(v[got], row)
