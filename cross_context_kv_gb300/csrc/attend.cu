@@ -496,10 +496,8 @@ struct StoredTile {
             if (F == KVFIX_POOL_E4M3) {
                 E4m3Scale es = e4m3_scale_byte(sc[k]);
                 if (gone) es.a = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
-                uint2 w[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = e4m3x4_to_bf16(c[q], es);
-                const uint4 o0 = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), o1 = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+                uint4 o0, o1;
+                e4m3x16_to_bf16(x[k], es, o0, o1);
                 unsigned char* dst = tile + (v / 4) * (kAtKeys * 128) + r * 128;
                 const int c0 = 2 * (v % 4), sw = (v / 4) & 1;  // the upper half's odd chunk first
                 const int a0 = ((c0 ^ (r & 7)) << 4), a1 = (((c0 + 1) ^ (r & 7)) << 4);

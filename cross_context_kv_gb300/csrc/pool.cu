@@ -332,12 +332,7 @@ pool_read_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Rop
                 uint4 vx = x[u][p], vy = y[u][p];
                 if (F == KVFIX_POOL_E4M3) {
                     const E4m3Scale s = e4m3_scale_byte(sx[u][p]);
-                    const unsigned c[4] = {vx.x, vx.y, vy.x, vy.y};
-                    uint2 w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = e4m3x4_to_bf16(c[i], s);
-                    vx = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
-                    vy = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+                    e4m3x16_to_bf16(make_uint4(vx.x, vx.y, vy.x, vy.y), s, vx, vy);
                 } else if (F == KVFIX_POOL_INT4) {
                     const unsigned a0 = __byte_perm(sx[u][p], 0u, 0x1010), z0 = __byte_perm(sx[u][p], 0u, 0x3232);
                     const unsigned a1 = __byte_perm(sy[u][p], 0u, 0x1010), z1 = __byte_perm(sy[u][p], 0u, 0x3232);

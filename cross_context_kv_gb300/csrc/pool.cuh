@@ -83,17 +83,29 @@ __device__ __forceinline__ E4m3Scale e4m3_scale_byte(unsigned byte) {
 
 // Four codes (bytes in order) to two bf16 pairs: the nibbles of every code at their places in
 // the high and the low bytes of the results, then the bytes side by side.
-__device__ __forceinline__ uint2 e4m3x4_to_bf16(unsigned codes, const E4m3Scale& s) {
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(unsigned codes, __nv_bfloat162 a) {
     const unsigned hi = ((codes >> 4) & 0x07070707u) | (codes & 0x80808080u);
     const unsigned lo = (codes << 4) & 0xf0f0f0f0u;
     unsigned r0 = __byte_perm(lo, hi, 0x5140), r1 = __byte_perm(lo, hi, 0x7362);
-    __nv_bfloat162 p0 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r0), s.a);
-    __nv_bfloat162 p1 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r1), s.a);
+    const __nv_bfloat162 p0 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r0), a);
+    const __nv_bfloat162 p1 = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r1), a);
+    return make_uint2(*reinterpret_cast<const unsigned*>(&p0), *reinterpret_cast<const unsigned*>(&p1));
+}
+
+// Sixteen codes to eight pairs.  Scales above 2^7 (values beyond 57344) are rare.
+__device__ __forceinline__ void e4m3x16_to_bf16(const uint4& codes, const E4m3Scale& s, uint4& o0, uint4& o1) {
+    const uint2 w0 = e4m3x4_to_bf16(codes.x, s.a), w1 = e4m3x4_to_bf16(codes.y, s.a);
+    const uint2 w2 = e4m3x4_to_bf16(codes.z, s.a), w3 = e4m3x4_to_bf16(codes.w, s.a);
+    unsigned w[8] = {w0.x, w0.y, w1.x, w1.y, w2.x, w2.y, w3.x, w3.y};
     if (s.two) {
-        p0 = __hmul2(p0, s.b);
-        p1 = __hmul2(p1, s.b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), s.b);
+            w[k] = *reinterpret_cast<const unsigned*>(&p);
+        }
     }
-    return make_uint2(*reinterpret_cast<unsigned*>(&p0), *reinterpret_cast<unsigned*>(&p1));
+    o0 = make_uint4(w[0], w[1], w[2], w[3]);
+    o1 = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // ------------------------------------------------------------- int4 -> bf16
