@@ -33,6 +33,15 @@ RopeTheta make_theta(double base, int head_dim) {
     return t;
 }
 
+// The frequencies of a call that may not rotate (delta null): D/2 powers are a few
+// microseconds of a small call, so none are taken then.
+static RopeTheta theta_if(const int32_t* delta, double base, int head_dim) {
+    if (delta) return make_theta(base, head_dim);
+    RopeTheta t;
+    memset(&t, 0, sizeof t);
+    return t;
+}
+
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Checks one plane descriptor and its pointer.  `what` names the argument.
@@ -951,7 +960,7 @@ kvfix_status kvfix_pool_write(const kvfix_bf16* k, const kvfix_bf16* v, kvfix_kv
     kvfix_status st = check_pool_rows(fn, k, v, src, delta, rope_base, slot_mapping, pool);
     if (st != KVFIX_OK) return st;
     if (pool_meets_itself(pool)) return fail(KVFIX_EINVAL, "%s: the pool's buffers overlap each other", fn);
-    RopeTheta th = make_theta(delta ? rope_base : 2.0, src.head_dim);
+    RopeTheta th = theta_if(delta, rope_base, src.head_dim);
     return launched(launch_pool_write(k, v, src, delta, th, slot_mapping, pool, (cudaStream_t)stream), fn);
 }
 
@@ -961,7 +970,7 @@ kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapping, const
     kvfix_status st = check_pool_rows(fn, k, v, out, delta, rope_base, slot_mapping, pool);
     if (st != KVFIX_OK) return st;
     if (overlaps(k, out, v, out)) return fail(KVFIX_EINVAL, "%s: k and v overlap", fn);
-    RopeTheta th = make_theta(delta ? rope_base : 2.0, out.head_dim);
+    RopeTheta th = theta_if(delta, rope_base, out.head_dim);
     return launched(launch_pool_read(pool, slot_mapping, delta, th, k, v, out, (cudaStream_t)stream), fn);
 }
 

@@ -36,6 +36,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "attend.h"
 #include "pool.cuh"
 #include "tc.cuh"
@@ -1374,12 +1376,18 @@ static bool pool_map(CUtensorMap* m, const PoolView& p, int plane, int page) {
 }
 
 template <int F, int D>
-static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, cudaStream_t s) {
+static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
     using C = AtCfg<F, D>;
     CUtensorMap mk, mv;
     if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use the shared memory
+    const unsigned long long bit = 1ull << (device & 63);
+    if (!(ready.load(std::memory_order_acquire) & bit) || device > 63) {
+        e = cudaFuncSetAttribute(attend_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
     if ((e = launch_chained(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
     if ((e = launch_chained(attend_kernel<F, D>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w)) != cudaSuccess)
         return e;
@@ -1413,12 +1421,12 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
     w.own_rows = l.own_rows;
     w.ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
     switch (a.pool.format * 2 + (a.pool.dim == 128)) {
-        case KVFIX_POOL_BF16 * 2: return launch_attend_form<KVFIX_POOL_BF16, 64>(a, w, s);
-        case KVFIX_POOL_BF16 * 2 + 1: return launch_attend_form<KVFIX_POOL_BF16, 128>(a, w, s);
-        case KVFIX_POOL_E4M3 * 2: return launch_attend_form<KVFIX_POOL_E4M3, 64>(a, w, s);
-        case KVFIX_POOL_E4M3 * 2 + 1: return launch_attend_form<KVFIX_POOL_E4M3, 128>(a, w, s);
-        case KVFIX_POOL_INT4 * 2: return launch_attend_form<KVFIX_POOL_INT4, 64>(a, w, s);
-        default: return launch_attend_form<KVFIX_POOL_INT4, 128>(a, w, s);
+        case KVFIX_POOL_BF16 * 2: return launch_attend_form<KVFIX_POOL_BF16, 64>(a, w, dev, s);
+        case KVFIX_POOL_BF16 * 2 + 1: return launch_attend_form<KVFIX_POOL_BF16, 128>(a, w, dev, s);
+        case KVFIX_POOL_E4M3 * 2: return launch_attend_form<KVFIX_POOL_E4M3, 64>(a, w, dev, s);
+        case KVFIX_POOL_E4M3 * 2 + 1: return launch_attend_form<KVFIX_POOL_E4M3, 128>(a, w, dev, s);
+        case KVFIX_POOL_INT4 * 2: return launch_attend_form<KVFIX_POOL_INT4, 64>(a, w, dev, s);
+        default: return launch_attend_form<KVFIX_POOL_INT4, 128>(a, w, dev, s);
     }
 }
 

@@ -629,57 +629,86 @@ def pool_empty(format: str, layers: int, slots: int, kv_heads: int, head_dim: in
     return Pool(format, k, v, ks, vs)
 
 
+def _raw_stream(t) -> int:
+    """The current stream of a CUDA tensor's device, as an address (no Stream object on the way)."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
 def pool_desc(pool: Pool) -> PoolDesc:
     """Descriptor of a pool; checks dtypes, devices, shapes and strides."""
-    fmt = POOL_FORMATS.get(pool.format)
+    format, k, v, ks, vs = pool
+    fmt = POOL_FORMATS.get(format)
     if fmt is None:
-        raise ValueError(f"unknown pool format {pool.format!r}")
-    code = torch.bfloat16 if fmt == 0 else torch.uint8
-    k, v = pool.k, pool.v
-    if k.dtype != code or v.dtype != code or not k.is_cuda or k.device != v.device:
-        raise TypeError(f"pool planes of a {pool.format} pool must be CUDA {code} tensors on one device")
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError(f"unknown pool format {format!r}")
+    code = torch.uint8 if fmt else torch.bfloat16
+    dev = k.device
+    if k.dtype != code or v.dtype != code or not k.is_cuda or dev != v.device:
+        raise TypeError(f"pool planes of a {format} pool must be CUDA {code} tensors on one device")
+    shape, stride = k.shape, k.stride()
+    if len(shape) != 4 or shape != v.shape or stride != v.stride():
         raise ValueError("pool planes must be [layers][slots][heads][width], of one shape and strides")
-    L, n, H, W = k.shape
-    sl, ss, sh, sw = k.stride()
+    L, n, H, W = shape
+    sl, ss, sh, sw = stride
     if (sw != 1 or sh != W) and H * W > 1:
         raise ValueError("a pool slot's heads must be contiguous")
-    size = k.element_size()
+    if not fmt:
+        return PoolDesc(0, L, n, H, W, 2 * sl if L > 1 else 0, 2 * ss if n > 1 else 2 * H * W,
+                        k.data_ptr(), v.data_ptr(), None, None)
     dim = 2 * W if fmt == 2 else W
-    if fmt:
-        want = (L, H, n) if fmt == 1 else (L, H, n, dim // 32, 2)
-        kind = torch.uint8 if fmt == 1 else torch.bfloat16
-        for s in (pool.k_scales, pool.v_scales):
-            if s is None or s.dtype != kind or s.shape != want or not s.is_contiguous() or s.device != k.device:
-                raise TypeError(f"scales of this {pool.format} pool must be contiguous {kind} tensors {want} "
-                                "on the planes' device")
-    return PoolDesc(fmt, L, n, H, dim, sl * size if L > 1 else 0, ss * size if n > 1 else H * W * size,
-                    k.data_ptr(), v.data_ptr(), pool.k_scales.data_ptr() if fmt else None,
-                    pool.v_scales.data_ptr() if fmt else None)
+    want, kind = ((L, H, n), torch.uint8) if fmt == 1 else ((L, H, n, dim // 32, 2), torch.bfloat16)
+    for s in (ks, vs):
+        if s is None or s.dtype != kind or s.shape != want or not s.is_contiguous() or s.device != dev:
+            raise TypeError(f"scales of this {format} pool must be contiguous {kind} tensors {want} "
+                            "on the planes' device")
+    return PoolDesc(fmt, L, n, H, dim, sl if L > 1 else 0, ss if n > 1 else H * W,
+                    k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
 
-def _pool_rows(k, v, slot_mapping, delta):
-    _bf16(k, "k")
-    _bf16(v, "v")
-    _i32(slot_mapping, "slot_mapping")
-    if delta is not None:
-        _i32(delta, "delta")
-    d = plane_desc(k)
+def _rows_desc(t: torch.Tensor, name: str) -> KvDesc:
+    """plane_desc of a CUDA bf16 tensor (one layer if 4-D), without a view on the way."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor (got {t.dtype} on {t.device})")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 5:
+        C, L, n, H, Dh = shape
+        sc, sl, st, sh, sd = stride
+    elif len(shape) == 4:
+        C, n, H, Dh = shape
+        sc, st, sh, sd = stride
+        L, sl = 1, 0
+    else:
+        raise ValueError(f"{name} must be 4-D or 5-D, got shape {tuple(shape)}")
+    if (sd != 1 or sh != Dh) and H * Dh > 1:
+        raise ValueError(f"{name} needs contiguous heads and dims (stride(-1) == 1, stride(-2) == head_dim)")
+    return KvDesc(C, L, n, H, Dh, sc if C > 1 else 0, sl if L > 1 else 0, st if n > 1 else H * Dh)
+
+
+def _pool_rows(k, v, slot_mapping, delta, pool):
+    d = _rows_desc(k, "k")
+    if v.dtype != torch.bfloat16 or not v.is_cuda:
+        raise TypeError(f"v must be a CUDA bfloat16 tensor (got {v.dtype} on {v.device})")
     if k.shape != v.shape or k.stride() != v.stride():
         raise ValueError("k and v must have the same shape and strides")
+    _i32(slot_mapping, "slot_mapping")
     if slot_mapping.numel() != d.chunks * d.tokens:
         raise ValueError(f"slot_mapping must hold {d.chunks} x {d.tokens} slots")
-    if delta is not None and delta.numel() != d.chunks:
-        raise ValueError(f"delta must hold {d.chunks} shifts")
+    if delta is not None:
+        _i32(delta, "delta")
+        if delta.numel() != d.chunks:
+            raise ValueError(f"delta must hold {d.chunks} shifts")
+    if k.device != pool.k.device or v.device != k.device or slot_mapping.device != k.device or \
+            (delta is not None and delta.device != k.device):
+        raise ValueError("the pool, the rows, slot_mapping and delta must be on one device")
     return d
 
 
 def pool_write(pool: Pool, k, v, slot_mapping, delta=None, rope_base: float = 0.0):
     """Write rows k, v [C][L][n][H][D] (L, H, D the pool's) to pool rows slot_mapping [C][n]
     (< 0: not kept), in the pool's format, keys rotated by delta [C] first (None: as they are)."""
-    d = _pool_rows(k, v, slot_mapping, delta)
-    _check(lib.kvfix_pool_write(_ptr(k), _ptr(v), d, _ptr(delta), float(rope_base), _ptr(slot_mapping),
-                                pool_desc(pool), _stream(k)))
+    pd = pool_desc(pool)
+    d = _pool_rows(k, v, slot_mapping, delta, pool)
+    _check(lib.kvfix_pool_write(k.data_ptr(), v.data_ptr(), d, None if delta is None else delta.data_ptr(),
+                                float(rope_base), slot_mapping.data_ptr(), pd, _raw_stream(k)))
 
 
 def pool_read(pool: Pool, slot_mapping, delta=None, rope_base: float = 0.0, k_out=None, v_out=None):
@@ -693,9 +722,9 @@ def pool_read(pool: Pool, slot_mapping, delta=None, rope_base: float = 0.0, k_ou
         shape = (slot_mapping.shape[0], pd.layers, slot_mapping.shape[1], pd.kv_heads, pd.head_dim)
         new = lambda: torch.zeros(shape, dtype=torch.bfloat16, device=pool.k.device)  # noqa: E731
         k_out, v_out = new() if k_out is None else k_out, new() if v_out is None else v_out
-    d = _pool_rows(k_out, v_out, slot_mapping, delta)
-    _check(lib.kvfix_pool_read(pd, _ptr(slot_mapping), _ptr(delta), float(rope_base), _ptr(k_out), _ptr(v_out), d,
-                               _stream(k_out)))
+    d = _pool_rows(k_out, v_out, slot_mapping, delta, pool)
+    _check(lib.kvfix_pool_read(pd, slot_mapping.data_ptr(), None if delta is None else delta.data_ptr(),
+                               float(rope_base), k_out.data_ptr(), v_out.data_ptr(), d, _raw_stream(k_out)))
     return k_out, v_out
 
 
@@ -711,35 +740,41 @@ def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, pre
     the first suffix_len[a] on suffix_pages[a], the T newest of them its own queries' places.
     Groups are the runs of agents group_begin[g] .. group_begin[g+1].  scale: dim^-1/2 if None.
     Returns out, shaped like q, or (out, lse [agents][T][q_heads])."""
-    _bf16(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [agents][new tokens][heads][dim]")
-    qd, pd = plane_desc(q), pool_desc(pool)
+    qd, pd, dev = _rows_desc(q, "q"), pool_desc(pool), q.device
     A, T, Hq, Dh = q.shape
     groups = 0 if prefix_len is None else prefix_len.numel()
-    for t, nm, count in ((suffix_pages, "suffix_pages", None), (suffix_len, "suffix_len", A),
-                         (prefix_pages, "prefix_pages", None), (prefix_len, "prefix_len", groups),
-                         (group_begin, "group_begin", groups + 1)):
-        if t is None:
-            if groups or nm.startswith("suffix"):
-                raise ValueError(f"{nm} is required")
-            continue
-        _i32(t, nm)
-        if count is not None and t.numel() != count:
-            raise ValueError(f"{nm} must hold {count} values (got {t.numel()})")
-    if suffix_pages.dim() != 2 or suffix_pages.shape[0] != A:
-        raise ValueError(f"suffix_pages must be [{A}][pages]")
-    if groups and (prefix_pages.dim() != 2 or prefix_pages.shape[0] != groups):
-        raise ValueError(f"prefix_pages must be [{groups}][pages]")
-    out = torch.empty(A, T, Hq, Dh, dtype=torch.bfloat16, device=q.device) if out is None else out
-    _bf16(out, "out")
-    lse = torch.empty(A, T, Hq, dtype=torch.float32, device=q.device) if return_lse else None
+    _i32(suffix_pages, "suffix_pages")
+    _i32(suffix_len, "suffix_len")
+    if suffix_pages.dim() != 2 or suffix_pages.shape[0] != A or suffix_len.numel() != A:
+        raise ValueError(f"suffix_pages must be [{A}][pages] and suffix_len hold {A} lengths")
+    if pool.k.device != dev or suffix_pages.device != dev or suffix_len.device != dev:
+        raise ValueError("q, the pool, pages and lengths must be on one device")
+    shared = (None, 0, None, None)
+    if groups:
+        if prefix_pages is None or group_begin is None:
+            raise ValueError("prefix_pages and group_begin are required with prefix_len")
+        _i32(prefix_pages, "prefix_pages")
+        _i32(prefix_len, "prefix_len")
+        _i32(group_begin, "group_begin")
+        if prefix_pages.dim() != 2 or prefix_pages.shape[0] != groups or group_begin.numel() != groups + 1:
+            raise ValueError(f"prefix_pages must be [{groups}][pages] and group_begin hold {groups + 1} bounds")
+        if prefix_pages.device != dev or prefix_len.device != dev or group_begin.device != dev:
+            raise ValueError("q, the pool, pages and lengths must be on one device")
+        shared = (prefix_pages.data_ptr(), prefix_pages.shape[1], prefix_len.data_ptr(), group_begin.data_ptr())
+    if out is None:
+        out = torch.empty((A, T, Hq, Dh), dtype=torch.bfloat16, device=dev)
+    od = _rows_desc(out, "out")
+    lse = torch.empty((A, T, Hq), dtype=torch.float32, device=dev) if return_lse else None
     if workspace is None:
-        workspace = torch.empty(shared_attend_workspace_bytes(q, pool, groups), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(lib.kvfix_shared_attend_workspace_bytes(A, T, Hq, pd.kv_heads, Dh, groups),
+                                dtype=torch.uint8, device=dev)
+    if out.device != dev or workspace.device != dev:
+        raise ValueError("out and workspace must be on q's device")
     _check(lib.kvfix_shared_attend(
-        _ptr(q), qd, pd, int(page_tokens), _ptr(prefix_pages) if groups else None,
-        prefix_pages.shape[1] if groups else 0, _ptr(prefix_len) if groups else None,
-        _ptr(group_begin) if groups else None, groups, _ptr(suffix_pages), suffix_pages.shape[1], _ptr(suffix_len),
-        float(Dh ** -0.5 if scale is None else scale), _ptr(out), plane_desc(out), _ptr(lse), _ptr(workspace),
-        workspace.numel(), _stream(q)))
+        q.data_ptr(), qd, pd, int(page_tokens), *shared, groups, suffix_pages.data_ptr(), suffix_pages.shape[1],
+        suffix_len.data_ptr(), Dh ** -0.5 if scale is None else float(scale), out.data_ptr(), od,
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _raw_stream(q)))
     return (out, lse) if return_lse else out
