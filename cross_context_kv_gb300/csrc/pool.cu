@@ -28,7 +28,9 @@ unsigned read_status_pool(cudaStream_t stream) {
 }
 
 constexpr int kPoolThreads = 256;
-constexpr int kPoolUnroll = 2;  // (token, head) rows in flight per lane, both planes each
+// (token, head) rows in flight per lane, both planes each.  Writing int4 takes one: its
+// arithmetic (20 instructions a value) wants warps more than loads in flight.
+constexpr int pool_unroll(int format, bool write) { return format == KVFIX_POOL_INT4 && write ? 1 : 2; }
 
 struct PoolArgs {
     const uint16_t* in[2];  // write: the source planes
@@ -80,19 +82,31 @@ __device__ __forceinline__ uint2 to_e4m3(const uint4& v, float inv) {
     return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
+// Eight codes (as 2^23 + code in float, whose low byte is the code) to their word: value 2i in
+// nibble i, value 2i+1 in nibble i + 4.
+__device__ __forceinline__ unsigned int4_word(const float* t) {
+    unsigned w = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i)
+        w = w * 16u + __byte_perm(__float_as_uint(t[2 * i]), __float_as_uint(t[2 * i + 1]), 0x5410);
+    return w;
+}
+
 // Eight values against their group's zero and 1/scale -> one word of codes.  Adding 2^23
-// rounds to the nearest integer, ties to even; the maximum with 0 takes a NaN to code 0.
+// rounds to the nearest integer, ties to even.  Values below 2^127 lie within their group's
+// range, and the rounded scale takes its end to at most 15 (1 + 2^-8), so they need no bounds;
+// infinities and clipped ranges do, and the maximum with 0 takes a NaN to code 0.
+template <bool kTame>
 __device__ __forceinline__ unsigned to_int4(const uint4& v, float zero, float inv) {
     float f[8];
     unpack8(v, f);
-    unsigned w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = fminf(fmaxf((f[i] - zero) * inv, 0.f), 15.f) + 8388608.f;
-        const int at = 4 * (i / 2) + 16 * (i & 1);
-        w |= (__float_as_uint(t) & 15u) << at;
+        float t = __fmul_rn(__fsub_rn(f[i], zero), inv);
+        if (!kTame) t = fminf(fmaxf(t, 0.f), 15.f);
+        f[i] = __fadd_rn(t, 8388608.f);
     }
-    return w;
+    return int4_word(f);
 }
 
 struct Int4Group {
@@ -101,34 +115,56 @@ struct Int4Group {
 };
 
 // Scale and zero of the group of 32 values whose 4 lanes each hold 8 of them.
+// Smallest and largest values go through the lanes as one pair of bf16, (min, -max).
+template <bool kTame>
 __device__ __forceinline__ Int4Group int4_group(const uint4& v) {
-    float f[8];
-    unpack8(v, f);
-    float lo = INFINITY, hi = -INFINITY;
+    __nv_bfloat162 ends;
+    if (kTame) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+        const __nv_bfloat162 lo = __hmin2(__hmin2(h[0], h[1]), __hmin2(h[2], h[3]));
+        const __nv_bfloat162 hi = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        ends = __halves2bfloat162(__hmin(__low2bfloat16(lo), __high2bfloat16(lo)),
+                                  __hneg(__hmax(__low2bfloat16(hi), __high2bfloat16(hi))));
+    } else {
+        float f[8], lo = INFINITY, hi = -INFINITY;
+        unpack8(v, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool fine = fabsf(f[i]) < INFINITY;  // false for NaN too
-        lo = fine ? fminf(lo, f[i]) : lo;
-        hi = fine ? fmaxf(hi, f[i]) : hi;
+        for (int i = 0; i < 8; ++i) {
+            const bool fine = fabsf(f[i]) < INFINITY;  // false for NaN too
+            lo = fine ? fminf(lo, f[i]) : lo;
+            hi = fine ? fmaxf(hi, f[i]) : hi;
+        }
+        ends = __floats2bfloat162_rn(lo, -hi);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        const unsigned other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const unsigned*>(&ends), o);
+        ends = __hmin2(ends, *reinterpret_cast<const __nv_bfloat162*>(&other));
     }
-    if (lo > hi) lo = hi = 0.f;  // no finite value
+    float lo = __low2float(ends), hi = -__high2float(ends);
+    if (!kTame && lo > hi) lo = hi = 0.f;  // no finite value
     const float range = fminf(__fsub_rn(hi, lo), 3.402823466e38f);
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.f));
-    float s = __bfloat162float(sb);
+    float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.f)));
     if (s < pow2f(-120)) s = 0.f;
     Int4Group g;
-    // -0 and +0 compare equal: the zero of a group with both is +0 or -0 by the lanes' order,
-    // which decides no value (0 code + -0 and 0 code + 0 compare equal)
+    // (-0 and +0 compare equal: which of them a group that has both keeps as its zero decides
+    // no value)
     g.zero = lo;
-    g.inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-    const __nv_bfloat16 z = __float2bfloat16_rn(lo), sc = __float2bfloat16_rn(s);
-    g.word = (unsigned)__bfloat16_as_ushort(sc) | ((unsigned)__bfloat16_as_ushort(z) << 16);
+    g.inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    const __nv_bfloat162 w = __floats2bfloat162_rn(s, lo);
+    g.word = *reinterpret_cast<const unsigned*>(&w);
     return g;
+}
+
+// Both halves of a lane's row: codes and their groups' words.
+template <bool kTame>
+__device__ __forceinline__ void int4_rows(const uint4& x, const uint4& y, unsigned& cx, unsigned& cy, unsigned& wx,
+                                          unsigned& wy) {
+    const Int4Group gx = int4_group<kTame>(x), gy = int4_group<kTame>(y);
+    cx = to_int4<kTame>(x, gx.zero, gx.inv);
+    cy = to_int4<kTame>(y, gy.zero, gy.inv);
+    wx = gx.word;
+    wy = gy.word;
 }
 
 struct PairAngles {
@@ -178,11 +214,11 @@ __device__ __forceinline__ Run run_of(const PoolArgs& a) {
 }
 
 template <int F, int D>
-__global__ void __launch_bounds__(kPoolThreads)
+__global__ void __launch_bounds__(kPoolThreads, F == KVFIX_POOL_INT4 ? 4 : 3)
 pool_write_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ RopeTheta th) {
     constexpr int kLanes = D / 16;                 // lanes per (token, head)
     constexpr int kRows = kPoolThreads / kLanes;   // (token, head) rows per step of the CTA
-    constexpr int HB = pool_head_bytes(F, D);
+    constexpr int HB = pool_head_bytes(F, D), kU = pool_unroll(F, true);
     const Run r = run_of(a);
     const int j = threadIdx.x % kLanes;
     const int d = a.delta ? __ldg(a.delta + r.c) : 0;
@@ -194,11 +230,11 @@ pool_write_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Ro
     const int items = (r.t1 - r.t0) * H;
     bool bad = false;
     // every lane of a warp runs the same number of steps (the reductions are warp-wide)
-    for (int i0 = 0; i0 < items; i0 += kPoolUnroll * kRows) {
-        uint4 lo[kPoolUnroll][2], hi[kPoolUnroll][2];
-        int slot[kPoolUnroll], head[kPoolUnroll];
+    for (int i0 = 0; i0 < items; i0 += kU * kRows) {
+        uint4 lo[kU][2], hi[kU][2];
+        int slot[kU], head[kU];
 #pragma unroll
-        for (int u = 0; u < kPoolUnroll; ++u) {
+        for (int u = 0; u < kU; ++u) {
             const int i = i0 + u * kRows + (int)threadIdx.x / kLanes;
             slot[u] = -1;
             head[u] = 0;
@@ -221,7 +257,7 @@ pool_write_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Ro
             }
         }
 #pragma unroll
-        for (int u = 0; u < kPoolUnroll; ++u) {
+        for (int u = 0; u < kU; ++u) {
             if (d != 0) turn(lo[u][0], hi[u][0], ang);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -251,15 +287,17 @@ pool_write_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Ro
                         if (j == 0) a.pool.plane[p].scales[row] = (unsigned char)(k + 127);
                     }
                 } else {
-                    const Int4Group gx = int4_group(x), gy = int4_group(y);
-                    const unsigned cx = to_int4(x, gx.zero, gx.inv), cy = to_int4(y, gy.zero, gy.inv);
+                    unsigned cx, cy, wx, wy;
+                    // (2^127 and above: infinities, NaN, and ranges past the largest float)
+                    if (__any_sync(0xffffffffu, abs_max16(x, y) >= 0x7f00u)) int4_rows<false>(x, y, cx, cy, wx, wy);
+                    else int4_rows<true>(x, y, cx, cy, wx, wy);
                     if (slot[u] >= 0) {
                         *reinterpret_cast<unsigned*>(codes + at + 4 * j) = cx;
                         *reinterpret_cast<unsigned*>(codes + at + D / 4 + 4 * j) = cy;
                         if (j % 4 == 0) {
                             unsigned* sc = reinterpret_cast<unsigned*>(a.pool.plane[p].scales) + row * (D / kQGroup);
-                            sc[j / 4] = gx.word;
-                            sc[j / 4 + D / (2 * kQGroup)] = gy.word;
+                            sc[j / 4] = wx;
+                            sc[j / 4 + D / (2 * kQGroup)] = wy;
                         }
                     }
                 }
@@ -274,7 +312,7 @@ __global__ void __launch_bounds__(kPoolThreads)
 pool_read_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ RopeTheta th) {
     constexpr int kLanes = D / 16;
     constexpr int kRows = kPoolThreads / kLanes;
-    constexpr int HB = pool_head_bytes(F, D);
+    constexpr int HB = pool_head_bytes(F, D), kU = pool_unroll(F, false);
     const Run r = run_of(a);
     const int j = threadIdx.x % kLanes;
     const int d = a.delta ? __ldg(a.delta + r.c) : 0;
@@ -285,12 +323,12 @@ pool_read_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Rop
     const int32_t* slots = a.slots + (long long)r.c * a.p.tokens + r.t0;
     const int items = (r.t1 - r.t0) * H;
     bool bad = false;
-    for (int i0 = threadIdx.x / kLanes; i0 < items; i0 += kPoolUnroll * kRows) {
-        uint4 x[kPoolUnroll][2], y[kPoolUnroll][2];  // codes (in part), then values
-        unsigned sx[kPoolUnroll][2], sy[kPoolUnroll][2];
-        long long off[kPoolUnroll];
+    for (int i0 = threadIdx.x / kLanes; i0 < items; i0 += kU * kRows) {
+        uint4 x[kU][2], y[kU][2];  // codes (in part), then values
+        unsigned sx[kU][2], sy[kU][2];
+        long long off[kU];
 #pragma unroll
-        for (int u = 0; u < kPoolUnroll; ++u) {
+        for (int u = 0; u < kU; ++u) {
             const int i = i0 + u * kRows;
             off[u] = -1;
             if (i >= items) continue;
@@ -325,7 +363,7 @@ pool_read_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Rop
             }
         }
 #pragma unroll
-        for (int u = 0; u < kPoolUnroll; ++u) {
+        for (int u = 0; u < kU; ++u) {
             if (off[u] < 0) continue;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -354,12 +392,15 @@ pool_read_kernel(const __grid_constant__ PoolArgs a, const __grid_constant__ Rop
 // rotation table (one double-precision angle per pair) is a small part of its work.
 constexpr int kPoolCtas = 152 * 8;
 
-static void plan_runs(PoolArgs& a) {
+static void plan_runs(PoolArgs& a, bool write) {
     const long long cl = (long long)a.p.chunks * a.p.layers;
     const int rows = kPoolThreads / (a.p.dim / 16);
     const long long per = (cl * a.p.tokens + kPoolCtas - 1) / kPoolCtas;  // tokens per CTA
-    const long long least = (kPoolUnroll * rows + a.p.heads - 1) / a.p.heads;  // one full step
-    long long run = per > least ? per : least;
+    // whole steps of the CTA: a step more for a few rows would cost as much as a full one
+    const int step = pool_unroll(a.pool.format, write) * rows;
+    const long long steps = (per * a.p.heads + step / 2) / step;
+    long long run = (steps > 1 ? steps : 1) * step / a.p.heads;
+    if (run < 1) run = 1;
     if (run > a.p.tokens) run = a.p.tokens;
     while ((a.p.tokens + run - 1) / run * cl > 0x7fffffffll) run *= 2;  // grid.x limit
     a.run = (int)run;
@@ -378,7 +419,7 @@ static cudaError_t launch_pool_form(const PoolArgs& a, const RopeTheta& th, bool
 
 static cudaError_t launch_pool(PoolArgs& a, const RopeTheta& th, bool write, cudaStream_t s) {
     if (a.p.chunks == 0 || a.p.layers == 0 || a.p.tokens == 0) return cudaSuccess;
-    plan_runs(a);
+    plan_runs(a, write);
     switch (a.pool.format * 2 + (a.p.dim == 128)) {
         case KVFIX_POOL_BF16 * 2: return launch_pool_form<KVFIX_POOL_BF16, 64>(a, th, write, s);
         case KVFIX_POOL_BF16 * 2 + 1: return launch_pool_form<KVFIX_POOL_BF16, 128>(a, th, write, s);
