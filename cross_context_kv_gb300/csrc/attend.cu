@@ -487,11 +487,30 @@ struct StoredTile {
         }
     }
 
-    __device__ __forceinline__ void put(unsigned char* tile, int tid, int in_tile, unsigned absent) const {
-        const int r0 = tid / V, v = tid % V;
+    // In rounds of four vectors, the rest moving down between them: with all eight unrolled the
+    // roles' code outgrows the instruction caches (a quarter of the stalls were for
+    // instructions).
+    __device__ __forceinline__ void put(unsigned char* tile, int tid, int in_tile, unsigned absent) {
+        constexpr int B = P < 4 ? P : 4;
+        int r0 = tid / V;
+        const int v = tid % V;
         const bool partial = in_tile < kAtKeys || absent != 0u;
+#pragma unroll 1
+        for (int k0 = 0; k0 < P; k0 += B, r0 += B * (N / V)) {
+            put_some<B>(tile, r0, v, partial, in_tile, absent);
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
+            for (int k = 0; k + B < P; ++k) {
+                x[k] = x[k + B];
+                sc[k] = sc[k + B];
+            }
+        }
+    }
+
+    template <int B>
+    __device__ __forceinline__ void put_some(unsigned char* tile, int r0, int v, bool partial, int in_tile,
+                                             unsigned absent) const {
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
             const int r = r0 + k * (N / V);
             const bool gone = partial && (r >= in_tile || ((absent >> (r >> 4)) & 1u));
             const unsigned c[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
