@@ -487,11 +487,11 @@ struct StoredTile {
         }
     }
 
-    // In rounds of four vectors, the rest moving down between them: with all eight unrolled the
+    // In rounds of two vectors, the rest moving down between them: with all eight unrolled the
     // roles' code outgrows the instruction caches (a quarter of the stalls were for
     // instructions).
     __device__ __forceinline__ void put(unsigned char* tile, int tid, int in_tile, unsigned absent) {
-        constexpr int B = P < 4 ? P : 4;
+        constexpr int B = P < 2 ? P : 2;
         int r0 = tid / V;
         const int v = tid % V;
         const bool partial = in_tile < kAtKeys || absent != 0u;
@@ -1057,8 +1057,25 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 // two sweeps over the row in 32-column pieces, the next piece on its way while
                 // one is worked on: the maximum, then the weights
                 uint32_t x[2][32];
-                const bool masked = __any_sync(0xffffffffu, absent != 0u || nv < kAtKeys);
                 float mx = -INFINITY;
+                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys)) {
+                    // columns that hold no key, or none that this row sees: -inf (on the side, so
+                    // that the sweeps' code stays small)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kAtKeys; c0 += 32) {
+                        tmem_ld32(s_at + c0, x[0]);
+                        tmem_wait_ld32(x[0]);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const int n = (absent >> (c0 / 16 + b)) & 1u ? 0 : nv - c0 - 16 * b;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (i >= n) x[0][16 * b + i] = 0xff800000u;
+                        }
+                        tmem_st32(s_at + c0, x[0]);
+                    }
+                    tmem_wait_st();
+                }
                 tmem_ld32(s_at, x[0]);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -1067,16 +1084,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         tmem_wait_ld32(x[k]);
                         const int at32 = 64 * h + 32 * k;
                         if (at32 < 96) tmem_ld32(s_at + at32 + 32, x[1 - k]);
-                        if (masked) {
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const int n = (absent >> (at32 / 16 + b)) & 1u ? 0 : nv - at32 - 16 * b;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (i >= n) x[k][16 * b + i] = 0xff800000u;  // -inf
-                            }
-                            tmem_st32(s_at + at32, x[k]);
-                        }
                         float m4[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(x[k][i]), __uint_as_float(x[k][i + 4]));
@@ -1088,7 +1095,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         mx = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mx);
                     }
                 }
-                if (masked) tmem_wait_st();
                 tmem_ld32(s_at, x[0]);
                 const float z = mx * c;
                 const bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
