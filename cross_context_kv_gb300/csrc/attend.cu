@@ -10,7 +10,7 @@
 // anywhere.
 //
 // Work.  An entry is a block of up to 256 rows of a segment; a unit is an entry and a KV
-// head; its work is ceil(keys / 128) tiles of 128 keys (causally trimmed), plus one for its
+// head; its work is ceil(keys / 128) tiles of 128 keys (causally trimmed), plus a few for its
 // fixed cost.  One plan kernel lays all units on a line; CTA i of the persistent grid takes
 // the i-th equal piece of it, whole units and parts of units alike, and writes one part per
 // unit it touches; the join kernel finds a row's parts from the same line.  Everything
@@ -62,8 +62,13 @@ constexpr int kAtMaxCtas = 256;   // bound of the persistent grid
 // ------------------------------------------------------------------ plan
 // A segment's rows are cut into blocks of 256; a block of more than 128 rows is a pair (both
 // softmax groups share its tiles), the last one may be a single.  Pairs and singles lie on a
-// line of their own: unit (entry e, head h) begins at begin + h * (tiles + 1).  The pairs'
+// line of their own: unit (entry e, head h) begins at begin + h * (tiles + at_pad).  The pairs'
 // line is cut into one piece per CTA, the singles' into two (one per softmax group).
+// What a unit costs beside its tiles (queries in, masks, its part out), in tiles: measured on
+// pairs of short own segments, 17000 cycles a unit against 4000 a tile; with 1 there, the CTAs
+// that had those units ran 1.7 times as long as the others.
+__host__ __device__ constexpr int at_pad(bool single) { return single ? 1 : 4; }
+
 struct __align__(16) AtEntry {
     long long begin;  // position of head 0 on the line
     int tiles, rows;
@@ -249,7 +254,9 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             f(e, e.rows > kAtRows ? 0 : 1);
         }
     };
-    auto cost = [&](const AtEntry& e) { return e.tiles > 0 ? (long long)H * (e.tiles + 1) : 0ll; };
+    auto cost = [&](const AtEntry& e) {
+        return e.tiles > 0 ? (long long)H * (e.tiles + at_pad(e.rows <= kAtRows)) : 0ll;
+    };
     PlanSums mine = {};
     for (int s = s0; s < s1; ++s)
         each_block(s, [&](const AtEntry& e, int k) {
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         r.lo = lo;
         r.hi = min(total.line[k], lo + chunk[k]);
         r.e = x;
-        r.h = (int)quotient(lo - r.rec.begin, r.rec.tiles + 1);
+        r.h = (int)quotient(lo - r.rec.begin, r.rec.tiles + at_pad(k == 1));
         r.n = total.n[k];
         r.have = 1;
         *st = r;
@@ -359,7 +366,7 @@ struct AtWalk {
                 if (have) rec = ent[e];
                 continue;
             }
-            const long long base = rec.begin + (long long)h * (rec.tiles + 1);
+            const long long base = rec.begin + (long long)h * (rec.tiles + at_pad(rec.rows <= kAtRows));
             if (base >= hi) {
                 have = false;
                 break;
@@ -701,7 +708,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     it->sees0 = prefix ? e.keys : e.keys - (e.row0 + e.rows - 1) / G;
                     it->absent = (int)absent;
                     // a unit's first part lies in its rows' own places, a continued one in the CTA's
-                    const bool own = f.walk.rec.begin + (long long)f.head * (e.tiles + 1) >= f.walk.lo;
+                    const bool own = e.begin + (long long)f.head * (e.tiles + at_pad(!pair)) >= f.walk.lo;
                     it->part = own ? ((prefix ? 0 : a.pool.heads) + (long long)f.head) * all + (long long)e.agent0 * TG + e.row0 + r0
                                    : w.own_rows + (long long)blockIdx.x * (2 * kAtBlock) + (pair ? 0 : kAtBlock) + kAtRows * g;
                 }
@@ -1237,7 +1244,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
         const AtEntry e = w.entries[k][p.pair ? first.x + block : first.y];
         if (e.tiles == 0) return p;
         const long long chunk = w.plan->chunk[k];
-        const long long base = e.begin + (long long)head * (e.tiles + 1);
+        const long long base = e.begin + (long long)head * (e.tiles + at_pad(!p.pair));
         p.own = (s * H + (long long)head) * all + (long long)agent0 * TG;
         p.i0 = quotient(base, chunk);
         p.n = (int)(quotient(base + e.tiles - 1, chunk) - p.i0) + 1;  // pieces that hold tiles
