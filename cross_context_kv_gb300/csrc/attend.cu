@@ -885,7 +885,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             };
             // The tensor pipe takes products in the order of issue.  A group's O += P V and next
             // S = Q K^T go in one piece, so that its softmax waits for those alone and the other
-            // group's follow while it works: the two groups settle half a turn apart.
+            // group's follow while it works: the two groups settle half a turn apart.  (Pairs: the
+            // tensor pipe is what they wait for; 329 against 377 us on 8 x 256 new tokens over
+            // 8192 keys.  Units alone wait for memory, and save the lock.)
             auto take_pipe = [&]() {
                 if (lane == 0) {
                     const long long t0 = clock64();
@@ -940,7 +942,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 p_phase ^= 1u;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                take_pipe();
+                if (now & kPair) take_pipe();
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_lane()) {
@@ -955,7 +957,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     if (more) logits();
                 }
                 __syncwarp();
-                leave_pipe();
+                if (now & kPair) leave_pipe();
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
         } else if (C::kQuant) {
