@@ -32,6 +32,7 @@
 //                   to bf16 tiles for the MMA; four warps for keys, four for values.
 // S occupies 128 TMEM columns per group, P (bf16) overwrites the first half of S, O takes D.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -405,8 +406,29 @@ __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem,
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// B N-major (bit 16): keys are the contraction, a value row is contiguous along N.
-__host__ __device__ constexpr uint32_t at_idesc_pv(int N) { return tc_idesc_bf16(kAtRows, N) | (1u << 16); }
+// The same products of e4m3 operands (32 along the contraction a step), float accumulator.
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptors: e4m3 operands (format 0); B N-major: keys are the contraction, a
+// value row is contiguous along N.
+__host__ __device__ constexpr uint32_t at_idesc_e4m3(int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kAtRows >> 4) << 24);
+}
+constexpr uint32_t kNMajorB = 1u << 16;
 
 // 16 consecutive 32-bit columns of this warp's 32 TMEM lanes from registers.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
@@ -440,25 +462,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // to no more than what the block launches with).
 template <int F, int D>
 struct AtCfg {
-    static constexpr bool kQuant = F != KVFIX_POOL_BF16;
+    static constexpr bool kE4m3 = F == KVFIX_POOL_E4M3;  // e4m3 products, scales beside them
+    static constexpr bool kConv = F == KVFIX_POOL_INT4;  // converted to bf16 tiles
     static constexpr int kConvWarps = 4;  // per converting team: one for keys, one for values
-    static constexpr int kThreads = kQuant ? 384 + 64 * kConvWarps : 384;
-    static constexpr int kRegsSoftmax = kQuant ? 120 : 208;
-    static constexpr int kRegsOther = kQuant ? 80 : 88;
-    static constexpr int kTile = kAtKeys * D * 2;   // a K or V tile as bf16
-    static constexpr int kQ = kAtRows * D * 2;
-    // rings of bf16 tiles: keys are free once their product is done, values wait for the weights
-    static constexpr int kKeyStages = D == 128 ? 2 : 4;
-    static constexpr int kValueStages = D == 128 ? (kQuant ? 2 : 3) : 4;
+    static constexpr int kThreads = kConv ? 384 + 64 * kConvWarps : kE4m3 ? 512 : 384;
+    static constexpr int kRegsSoftmax = kConv ? 120 : kE4m3 ? 168 : 208;
+    static constexpr int kRegsOther = kConv ? 80 : 88;
+    static constexpr int kRow = kE4m3 ? D : 2 * D;  // bytes of an operand row (a key, a value, a query piece)
+    static constexpr int kTile = kAtKeys * kRow;    // a K or V tile as the MMA reads it
+    static constexpr int kQ = kAtRows * D * 2;      // a group's queries: bf16, or two e4m3 pieces
+    // rings of tiles: keys are free once their product is done, values wait for the weights
+    static constexpr int kKeyStages = kE4m3 || D == 64 ? 4 : 2;
+    static constexpr int kValueStages = kE4m3 ? 5 : D == 64 ? 4 : kConv ? 2 : 3;
     static constexpr int kStages = kKeyStages + kValueStages;
     // stored tiles before conversion: codes, then scales
     static constexpr int kCodeRow = pool_head_bytes(F, D);
     static constexpr int kScaleRow = F == KVFIX_POOL_E4M3 ? 1 : F == KVFIX_POOL_INT4 ? D / 8 : 0;
-    static constexpr int kRaw = kQuant ? kAtKeys * (kCodeRow + kScaleRow) : 0;
-    static constexpr int kRawStages = kQuant && D == 64 ? 4 : 2;  // half for keys
-    static constexpr int kSmem = 1024 + kStages * kTile + 2 * kQ + (kQuant ? kRawStages * kRaw : 0);
+    static constexpr int kRaw = kConv ? kAtKeys * (kCodeRow + kScaleRow) : 0;
+    static constexpr int kRawStages = kConv && D == 64 ? 4 : 2;  // half for keys
+    // e4m3: per value place a tile's scale bytes (keys, values), what the weights need of every
+    // key (four floats) and which keys are NaN; per group two units' query row scales
+    static constexpr int kScaleBytes = kE4m3 ? kValueStages * 2 * kAtKeys : 0;
+    static constexpr int kScaleFloats = kE4m3 ? kValueStages * (4 * kAtKeys + 4) * 4 + 2 * 2 * kAtRows * 4 : 0;
+    static constexpr int kSmem =
+        1024 + kStages * kTile + 2 * kQ + (kConv ? kRawStages * kRaw : 0) + kScaleBytes + kScaleFloats;
     static_assert(kSmem <= 227 * 1024 - 1536, "shared memory, with the barriers and items");
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (65536 / kThreads / 8 * 8), "registers");
+    // operand rows of 128 or 64 bytes: the swizzle of a tile and the bytes from 8 rows to the next 8
+    static constexpr int kSwizzle = kRow == 64 ? 4 : 2, kRows8 = kRow == 64 ? 512 : 1024;
 };
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -489,8 +520,7 @@ struct StoredTile {
         for (int k = 0; k < P; ++k) {
             const int r = tid / V + k * (N / V);
             x[k] = *reinterpret_cast<const uint4*>(raw + 16 * (tid + k * N));
-            if (F == KVFIX_POOL_E4M3) sc[k] = scales[r];
-            else sc[k] = *reinterpret_cast<const unsigned*>(scales + r * C::kScaleRow + 4 * (tid % V));
+            sc[k] = *reinterpret_cast<const unsigned*>(scales + r * C::kScaleRow + 4 * (tid % V));
         }
     }
 
@@ -521,17 +551,7 @@ struct StoredTile {
             const int r = r0 + k * (N / V);
             const bool gone = partial && (r >= in_tile || ((absent >> (r >> 4)) & 1u));
             const unsigned c[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            if (F == KVFIX_POOL_E4M3) {
-                E4m3Scale es = e4m3_scale_byte(sc[k]);
-                if (gone) es.a = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
-                uint4 o0, o1;
-                e4m3x16_to_bf16(x[k], es, o0, o1);
-                unsigned char* dst = tile + (v / 4) * (kAtKeys * 128) + r * 128;
-                const int c0 = 2 * (v % 4), sw = (v / 4) & 1;  // the upper half's odd chunk first
-                const int a0 = ((c0 ^ (r & 7)) << 4), a1 = (((c0 + 1) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4*>(dst + (sw ? a1 : a0)) = sw ? o1 : o0;
-                *reinterpret_cast<uint4*>(dst + (sw ? a0 : a1)) = sw ? o0 : o1;
-            } else {
+            {
                 const unsigned sz = gone ? 0u : sc[k];
                 const unsigned ss = __byte_perm(sz, 0u, 0x1010), zz = __byte_perm(sz, 0u, 0x3232);
                 unsigned char* dst = tile + (v / 2) * (kAtKeys * 128) + r * 128;
@@ -567,6 +587,99 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
     return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return d;
+}
+
+// ------------------------------------------------------------------ e4m3 pools
+// The stored codes are the operands themselves.  With q = 2^e (q1 + q2), q1 the e4m3 value
+// nearest q / 2^e and q2 the e4m3 value nearest the rest, a bf16 query is exact but for bits
+// below 2^-18 of its row's largest (8 bits in two pieces of 4), and with key j's scale 2^(kj),
+//     z_j = scale log2 e 2^e 2^(kj) (q1 + q2) . code_j.
+// A value is 2^(vj) code: the weight that meets its code is w_j = 2^(z_j + vj - m) with
+// m = max (z_j + vj), split in two pieces likewise (8 bits, as bf16 has, down to 2^-16 of the
+// largest), and the sum of softmax weights is sum w_j 2^(-vj).  Two products of half the
+// operand bytes take the time of one in bf16, and no tile is converted: converting them held
+// this kernel to 170 us on 131072 keys, where the cache is read in 42.
+constexpr float kAtBaseE4m3 = 6.f;   // the largest weight is 2^6 when a maximum is set,
+constexpr float kAtSlackE4m3 = 2.f;  // and at most 2^8 before it is raised (e4m3 ends at 448)
+// Values of rows below 448 2^-80 do not lower the maximum further: their weights lose pieces,
+// and the sum of weights stays finite.
+constexpr int kAtLeastShift = -80;
+
+__device__ __forceinline__ int e4m3_scale_exp(unsigned byte) {
+    return min(max((int)byte - 127, kE4m3MinExp), kE4m3MaxExp);
+}
+
+// e4m3 pieces of four weights: the word of the nearest, and in `rest` that of what is left.
+__device__ __forceinline__ uint32_t split_e4m3(float2 u, float2 v, uint32_t& rest) {
+    unsigned short a, b, c, d;
+    uint32_t ha, hb;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(a) : "f"(u.x), "f"(u.y));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(b) : "f"(v.x), "f"(v.y));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(ha) : "h"(a));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hb) : "h"(b));
+    const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
+    const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
+    const float2 ru = add2(u, make_float2(-fa.x, -fa.y)), rv = add2(v, make_float2(-fb.x, -fb.y));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(ru.x), "f"(ru.y));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(d) : "f"(rv.x), "f"(rv.y));
+    rest = (uint32_t)c | ((uint32_t)d << 16);
+    return (uint32_t)a | ((uint32_t)b << 16);
+}
+
+// A unit's query rows as two e4m3 pieces (K-major, swizzled like the keys), and 2^e per row
+// (NaN where a row is not finite).  D/8 lanes per row, eight values each.
+template <int D>
+__device__ __forceinline__ void split_queries(const AttendArgs& a, unsigned char* qt, float* scales, int lane, int head,
+                                              int rows, int row0, int agent0, int TG, int G) {
+    constexpr int L = D / 8, P = 32 / L, B = 4;  // lanes per row, rows per step, steps at a time
+    const int cv = lane % L;
+#pragma unroll 1
+    for (int r32 = 0; r32 < rows; r32 += 32) {
+        // a lane finds one row's place
+        const int x = row0 + min(r32 + lane, rows - 1), ag = x / TG, t = (x - ag * TG) / G, m = x - ag * TG - t * G;
+        const long long off = a.qp.row(agent0 + ag, 0, t) + (long long)(head * G + m) * D;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 && r32 + i0 < rows; i0 += B * P) {
+            uint4 v[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int k = (i0 + b * P + lane / L) & 31;
+                v[b] = __ldg(reinterpret_cast<const uint4*>(a.q + __shfl_sync(0xffffffffu, off, k) + 8 * cv));
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int r = r32 + i0 + b * P + lane / L;
+                const unsigned mask = 0x7fff7fffu;
+                const unsigned y = __vmaxu2(__vmaxu2(v[b].x & mask, v[b].y & mask), __vmaxu2(v[b].z & mask, v[b].w & mask));
+                unsigned top = max(y & 0xffffu, y >> 16);
+#pragma unroll
+                for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = e4m3_exponent(top);
+                const float inv = pow2f(-e);
+                float f[8];
+                unpack8(v[b], f);
+                uint32_t w[2], rest[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    w[h] = split_e4m3(make_float2(f[4 * h] * inv, f[4 * h + 1] * inv),
+                                      make_float2(f[4 * h + 2] * inv, f[4 * h + 3] * inv), rest[h]);
+                if (r < rows) {
+                    // rows of D bytes: 16-byte chunk c of row r at c ^ (r % 8), or c ^ (r / 2 % 4) for 64-byte rows
+                    const int at = r * D + (((cv / 2) ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4) + 8 * (cv & 1);
+                    *reinterpret_cast<uint2*>(qt + at) = make_uint2(w[0], w[1]);
+                    *reinterpret_cast<uint2*>(qt + kAtRows * D + at) = make_uint2(rest[0], rest[1]);
+                    if (cv == 0) scales[r] = top >= 0x7f80u ? NAN : pow2f(e);
+                }
+            }
+        }
+    }
+}
 
 template <int F, int D>
 __global__ void __launch_bounds__(AtCfg<F, D>::kThreads, 1)
@@ -577,6 +690,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t full[3][SK + SV], empty[SK + SV], raw_full[2 * R], raw_empty[2 * R];
     __shared__ __align__(8) uint64_t q_free[2], s_full[2], p_ready[2], o_full[2];
+    __shared__ __align__(8) uint64_t scales_full[C::kE4m3 ? 3 : 1][SV], q_scaled[2];
     __shared__ __align__(8) uint64_t item_full[2][kItems], item_free[2][kItems];
     __shared__ AtItem items[2][kItems];
     __shared__ uint32_t tmem_slot;
@@ -584,25 +698,33 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* qsm = smem + (SK + SV) * C::kTile;
     unsigned char* rawsm = qsm + 2 * C::kQ;
+    unsigned char* scale_bytes = rawsm + (C::kConv ? C::kRawStages * C::kRaw : 0);         // [SV][2][128]
+    float* scale_floats = reinterpret_cast<float*>(scale_bytes + C::kScaleBytes);          // [SV][4][128]
+    float* query_scales = scale_floats + (C::kE4m3 ? C::kValueStages * 4 * kAtKeys : 0);   // [2][2][128]
+    uint4* nan_keys = reinterpret_cast<uint4*>(query_scales + (C::kE4m3 ? 4 * kAtRows : 0)); // [SV]: a bit per key
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < SK + SV; ++i) {
-            for (int f = 0; f < 3; ++f) mbar_init(&full[f][i], C::kQuant ? 32 * C::kConvWarps : 1);
+            for (int f = 0; f < 3; ++f) mbar_init(&full[f][i], C::kConv ? 32 * C::kConvWarps : 1);
             mbar_init(&empty[i], 2);  // one release per softmax group (a group alone releases twice)
         }
+        if (C::kE4m3)
+            for (int i = 0; i < SV; ++i)
+                for (int f = 0; f < 3; ++f) mbar_init(&scales_full[f][i], 128);
         for (int i = 0; i < 2 * R; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], C::kQuant ? 32 * C::kConvWarps : 1);
+            mbar_init(&raw_empty[i], C::kConv ? 32 * C::kConvWarps : 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_free[i], 1);
+            mbar_init(&q_scaled[i], 32);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 128);
             mbar_init(&o_full[i], 1);
             for (int k = 0; k < kItems; ++k) {
                 mbar_init(&item_full[i][k], 1);
-                // readers: producer, MMA, four softmax warps, converters
-                mbar_init(&item_free[i][k], 6 + (C::kQuant ? 2 * C::kConvWarps : 0));
+                // readers: producer, MMA, four softmax warps, converters or scale warps
+                mbar_init(&item_free[i][k], 6 + (C::kConv ? 2 * C::kConvWarps : C::kE4m3 ? 4 : 0));
             }
         }
         fence_mbar_init();
@@ -758,12 +880,12 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // a lane per copy: its page of the tile, and its 64-column half (bf16), or codes
             // and scales (stored forms)
             const int ppt = kAtKeys >> page_log, my = lane & (ppt - 1), part = lane >> (7 - page_log);
-            const bool mine = part < (C::kQuant ? 2 : D / 64);
-            const unsigned page_bytes = (unsigned)a.page * (C::kQuant ? C::kCodeRow + C::kScaleRow : 2 * D);
+            const bool mine = part < (C::kConv || C::kE4m3 ? 2 : D / 64);
+            const unsigned page_bytes = (unsigned)a.page * (C::kE4m3 ? D : C::kCodeRow + C::kScaleRow);
             bool ok = true, live[2] = {true, true};
             unsigned at[2] = {0, 0};
             int n = 0;
-            uint64_t* last_bar[C::kQuant ? 2 * R : SK + SV] = {};  // of each place's last copy, with its parity
+            uint64_t* last_bar[C::kConv ? 2 * R : SK + SV] = {};  // of each place's last copy, with its parity
             unsigned last_turn = 0;
             while (ok && (live[0] || live[1])) {
 #pragma unroll
@@ -785,19 +907,31 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0 && part == 0));
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const int st = C::kQuant ? p * R + n % R : place(p, n);
-                        uint64_t* const bar = C::kQuant ? &raw_full[st] : &full[reader(flags, g)][st];
-                        if (C::kQuant) {
+                        const int st = C::kConv ? p * R + n % R : place(p, n);
+                        uint64_t* const bar = C::kConv ? &raw_full[st] : &full[reader(flags, g)][st];
+                        if (C::kConv) {
                             if (n >= R) ok = mbar_wait(&raw_empty[st], (unsigned)(n / R - 1) & 1u);
                         } else if (n >= (p ? SV : SK)) {
                             ok = mbar_wait(&empty[st], released(p, n));
                         }
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)boxes * page_bytes);
+                        if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)boxes * (page_bytes + (C::kE4m3 && p ? 2u * (unsigned)a.page : 0u)));
                         __syncwarp();
                         if (page >= 0) {
-                            if (!C::kQuant) {
+                            if (C::kE4m3) {
+                                if (part == 0)
+                                    tma_load_2d(smem + st * C::kTile + (my << page_log) * C::kRow, p ? &tm_v : &tm_k, head * D,
+                                                page << page_log, bar);
+                                else if (p == 1)
+                                    // both planes' scale bytes come with the values: their place is
+                                    // kept until the weights are done
+                                    for (int q = 0; q < 2; ++q)
+                                        bulk_g2s(scale_bytes + (2 * (st - SK) + q) * kAtKeys + (my << page_log),
+                                                 a.pool.plane[q].scales +
+                                                     ((long long)head * a.pool.slots + (page << page_log)),
+                                                 (unsigned)a.page, bar);
+                            } else if (!C::kConv) {
                                 tma_load_2d(smem + st * C::kTile + part * (kAtKeys * 128) + (my << page_log) * 128,
                                             p ? &tm_v : &tm_k, head * D + 64 * part, page << page_log, bar);
                             } else if (part == 0) {
@@ -810,9 +944,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                          (unsigned)a.page * C::kScaleRow, bar);
                             }
                         }
-                        const unsigned t = C::kQuant ? (unsigned)(n / R) & 1u : flags & (p ? kValueTurn : kKeyTurn) ? 1u : 0u;
+                        const unsigned t = C::kConv ? (unsigned)(n / R) & 1u : flags & (p ? kValueTurn : kKeyTurn) ? 1u : 0u;
 #pragma unroll
-                        for (int i = 0; i < (C::kQuant ? 2 * R : SK + SV); ++i)
+                        for (int i = 0; i < (C::kConv ? 2 * R : SK + SV); ++i)
                             if (i == st) last_bar[i] = bar;
                         last_turn = (last_turn & ~(1u << st)) | (t << st);
                     }
@@ -822,7 +956,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if (!ok) {
                 // the copies in flight land before this block gives up its shared memory: each
                 // place's last one
-                for (int st = 0; st < (C::kQuant ? 2 * R : SK + SV); ++st)
+                for (int st = 0; st < (C::kConv ? 2 * R : SK + SV); ++st)
                     if (last_bar[st]) mbar_wait(last_bar[st], last_turn >> st & 1u);
                 if (lane == 0) atomicOr(&abort_flag, 1);
             }
@@ -832,13 +966,15 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // memory, O += P V.  While the group works on a tile's weights the warp looks at its
             // next tile and, where that begins a unit, brings the unit's queries.
             const int g = warp == 9 ? 0 : 1;
-            constexpr uint32_t id_qk = tc_idesc_bf16(kAtRows, kAtKeys), id_pv = at_idesc_pv(D);
+            constexpr uint32_t id_qk = C::kE4m3 ? at_idesc_e4m3(kAtKeys) : tc_idesc_bf16(kAtRows, kAtKeys);
+            constexpr uint32_t id_pv = (C::kE4m3 ? at_idesc_e4m3(D) : tc_idesc_bf16(kAtRows, D)) | kNMajorB;
             // descriptors of the group's queries and of the first stage (as keys, K-major, and as
             // values, N-major: 64-column halves 16 KB apart, 8-key groups 1 KB apart); an offset
             // adds to the address field, which all of shared memory fits
             unsigned char* const qt = qsm + g * C::kQ;
-            const uint64_t q_desc = tc_smem_desc(qt, 16, 1024, 2), t_desc = tc_smem_desc(smem, 16, 1024, 2);
-            const uint64_t v_desc = tc_smem_desc(smem, kAtKeys * 128, 1024, 2);
+            const uint64_t q_desc = tc_smem_desc(qt, 16, C::kRows8, C::kSwizzle);
+            const uint64_t t_desc = tc_smem_desc(smem, 16, C::kRows8, C::kSwizzle);
+            const uint64_t v_desc = tc_smem_desc(smem, kAtKeys * 128, C::kRows8, C::kSwizzle);
             const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
             bool ok = true;
             unsigned at = 0, units = 0, p_phase = 0;
@@ -861,6 +997,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (units > 0) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[g], (units - 1) & 1u));
                 ++units;
                 if (!ok) return;
+                if constexpr (C::kE4m3) {
+                    split_queries<D>(a, qt, query_scales + (2 * g + (units & 1)) * kAtRows, lane, head, rows, row0, agent0, TG, G);
+                    return;
+                }
                 constexpr int V = D / 8, P = 32 / V;  // 16-byte vectors per row, rows per step
                 const int cv = lane % V;
                 unsigned char* const dst = qt + (cv / 8) * (kAtRows * 128);
@@ -879,8 +1019,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 cp_async_commit();
             };
             auto queries_here = [&]() {
-                cp_async_wait<0>();
+                if (!C::kE4m3) cp_async_wait<0>();
                 fence_proxy_async_smem();
+                if (C::kE4m3) mbar_arrive(&q_scaled[g]);
                 __syncwarp();
             };
             // The tensor pipe takes products in the order of issue.  A group's O += P V and next
@@ -906,10 +1047,19 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             auto logits = [&]() {
                 const int ks = place(0, tile);
                 const uint64_t bd = t_desc + (uint32_t)ks * (uint32_t)(C::kTile >> 4);
+                if (C::kE4m3) {
+                    // both pieces of the queries against the same keys
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
-                    tc_mma_bf16(tmem + 128 * g, q_desc + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 2 * (D / 32); ++kk) {
+                        const uint32_t off = 32 * (kk % (D / 32)) >> 4, piece = (kk / (D / 32)) * (kAtRows * D) >> 4;
+                        mma_e4m3_ss(tmem + 128 * g, q_desc + piece + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
+                    }
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
+                        tc_mma_bf16(tmem + 128 * g, q_desc + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
+                    }
                 }
                 tc_commit(&s_full[g]);
                 tc_commit(&empty[ks]);
@@ -947,10 +1097,19 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 tc_fence_after();
                 if (elect_lane()) {
                     const uint64_t bd = v_desc + (uint32_t)vs * (uint32_t)(C::kTile >> 4);
+                    if (C::kE4m3) {
+                        // 32 keys at a time, both pieces of their weights
 #pragma unroll
-                    for (int kk = 0; kk < kAtKeys / 16; ++kk)
-                        tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4), id_pv,
-                                       kk > 0 || !(now & kFirst) ? 1u : 0u);
+                        for (int kk = 0; kk < 2 * (kAtKeys / 32); ++kk)
+                            mma_e4m3_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk,
+                                        bd + (uint32_t)((kk / 2) * 32 * C::kRow >> 4), id_pv,
+                                        kk > 0 || !(now & kFirst) ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < kAtKeys / 16; ++kk)
+                            tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4),
+                                           id_pv, kk > 0 || !(now & kFirst) ? 1u : 0u);
+                    }
                     tc_commit(&empty[vs]);
                     if (!(now & kPair)) tc_commit(&empty[vs]);
                     if (now & kLast) tc_commit(&o_full[g]);
@@ -960,7 +1119,67 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (now & kPair) leave_pipe();
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
-        } else if (C::kQuant) {
+        } else if (C::kE4m3 && warp >= 12) {
+            // ------------------------------------------------------------ scales
+            // A thread per key: what its weight needs beside the product, and its value row set
+            // to zero where no key lies, or to NaN where the row's scale says so.
+            bool ok = true, live[2] = {true, true};
+            unsigned at[2] = {0, 0};
+            const int r = threadIdx.x - 384;
+            while (ok && (live[0] || live[1])) {
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    if (!ok || !live[g]) continue;
+                    ok = item_wait(g, at[g]);
+                    if (!ok) break;
+                    const AtItem& it = items[g][at[g] % kItems];
+                    const int flags = it.flags, keys = it.keys, tile = it.tile;
+                    const unsigned absent = it.absent;
+                    __syncwarp();
+                    if (lane == 0) item_done(g, at[g]);
+                    ++at[g];
+                    if (flags & kEnd) {
+                        live[g] = false;
+                        continue;
+                    }
+                    if ((flags & kPair) && g == 1) continue;
+                    const int vs = place(1, tile), f = reader(flags, g);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full[f][vs], flags & kValueTurn ? 1u : 0u));
+                    if (!ok) break;
+                    const bool there = r < keys && !((absent >> (r >> 4)) & 1u);
+                    const unsigned kb = scale_bytes[2 * (vs - SK) * kAtKeys + r];
+                    const unsigned vb = scale_bytes[(2 * (vs - SK) + 1) * kAtKeys + r];
+                    // (a NaN key makes its logits NaN where a row sees it: the softmax is told which)
+                    const bool nan_key = there && kb == kE4m3NanByte;
+                    const unsigned nans = __ballot_sync(0xffffffffu, nan_key);
+                    if (lane == 0) reinterpret_cast<unsigned*>(nan_keys + (vs - SK))[r >> 5] = nans;
+                    float factor = a.scale_log2, top = 0.f, shift = 0.f, back = 1.f;
+                    if (there) {
+                        if (!nan_key) factor = a.scale_log2 * pow2f(e4m3_scale_exp(kb));
+                        if (vb != kE4m3NanByte) {
+                            const int k = e4m3_scale_exp(vb);
+                            top = (float)max(k, kAtLeastShift);
+                            shift = (float)k;
+                            back = pow2f(-k);
+                        }
+                    }
+                    float* out = scale_floats + (vs - SK) * 4 * kAtKeys + r;
+                    out[0] = factor;
+                    out[kAtKeys] = top;
+                    out[2 * kAtKeys] = shift;
+                    out[3 * kAtKeys] = back;
+                    if (!there || vb == kE4m3NanByte) {
+                        const unsigned fill = there ? 0x7f7f7f7fu : 0u;
+                        uint4* row = reinterpret_cast<uint4*>(smem + vs * C::kTile + r * C::kRow);
+#pragma unroll
+                        for (int i = 0; i < C::kRow / 16; ++i) row[i] = make_uint4(fill, fill, fill, fill);
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&scales_full[f][vs - SK]);
+                }
+            }
+            if (!ok && lane == 0) atomicOr(&abort_flag, 1);
+        } else if (C::kConv) {
             // ------------------------------------------------------------ conversion
             // one team of warps converts the key tiles, another the value tiles
             constexpr int N = 32 * C::kConvWarps;
@@ -1012,6 +1231,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         bool ok = true;
         unsigned at = 0, units = 0;
         int rows = 0, sees = 0;   // of the unit: the group's rows; keys this row sees
+        float q_scale = 1.f;      // e4m3: of this row's queries
         float m = -INFINITY, l = 0.f;
         while (true) {
             ok = item_wait(g, at);
@@ -1046,7 +1266,16 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], at & 1u));
             if (!ok) break;
             tc_fence_after();
-            if (!C::kQuant && !whole) {
+            if (C::kE4m3) {
+                ok = mbar_wait(&scales_full[reader(flags, g)][place(1, tile) - SK], flags & kValueTurn ? 1u : 0u);
+                if (ok && (flags & kFirst)) {
+                    ok = mbar_wait(&q_scaled[g], units & 1u);
+                    q_scale = query_scales[(2 * g + ((units + 1) & 1)) * kAtRows + row];
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+            if (F == KVFIX_POOL_BF16 && !whole) {
                 // value rows that hold no key read as zero: a weight of 0 times what lies there
                 // (anything, NaN too) would not be 0
                 const int st = place(1, tile);
@@ -1067,13 +1296,21 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 // one is worked on: the maximum, then the weights
                 uint32_t x[2][32];
                 float mx = -INFINITY;
-                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys)) {
+                uint4 nans = make_uint4(0u, 0u, 0u, 0u);
+                if (C::kE4m3) nans = nan_keys[place(1, tile) - SK];
+                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys || (nans.x | nans.y | nans.z | nans.w) != 0u)) {
                     // columns that hold no key, or none that this row sees: -inf (on the side, so
                     // that the sweeps' code stays small)
 #pragma unroll 1
                     for (int c0 = 0; c0 < kAtKeys; c0 += 32) {
                         tmem_ld32(s_at + c0, x[0]);
                         tmem_wait_ld32(x[0]);
+                        if (C::kE4m3) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if ((nans.x >> i) & 1u) x[0][i] = 0x7fffffffu;
+                            nans = make_uint4(nans.y, nans.z, nans.w, 0u);
+                        }
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int n = (absent >> (c0 / 16 + b)) & 1u ? 0 : nv - c0 - 16 * b;
@@ -1085,6 +1322,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     }
                     tmem_wait_st();
                 }
+                // e4m3: a key's factor, and the exponents of its value's scale (for the maximum, for
+                // the weight, and its inverse)
+                const float4* key_scales =
+                    reinterpret_cast<const float4*>(scale_floats + (C::kE4m3 ? (place(1, tile) - SK) * 4 * kAtKeys : 0));
+                const float2 qs2 = make_float2(q_scale, q_scale);
                 tmem_ld32(s_at, x[0]);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -1093,6 +1335,21 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         tmem_wait_ld32(x[k]);
                         const int at32 = 64 * h + 32 * k;
                         if (at32 < 96) tmem_ld32(s_at + at32 + 32, x[1 - k]);
+                        if constexpr (C::kE4m3) {
+                            float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 fa = key_scales[at32 / 4 + i], ta = key_scales[kAtKeys / 4 + at32 / 4 + i];
+                                const float2 u = fma2(mul2(make_float2(__uint_as_float(x[k][4 * i]), __uint_as_float(x[k][4 * i + 1])), qs2),
+                                                      make_float2(fa.x, fa.y), make_float2(ta.x, ta.y));
+                                const float2 v = fma2(mul2(make_float2(__uint_as_float(x[k][4 * i + 2]), __uint_as_float(x[k][4 * i + 3])), qs2),
+                                                      make_float2(fa.z, fa.w), make_float2(ta.z, ta.w));
+                                m4[i & 1] = fmaxf(fmaxf(u.x, u.y), m4[i & 1]);
+                                m4[2 + (i & 1)] = fmaxf(fmaxf(v.x, v.y), m4[2 + (i & 1)]);
+                            }
+                            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            continue;
+                        }
                         float m4[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(x[k][i]), __uint_as_float(x[k][i + 4]));
@@ -1105,8 +1362,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     }
                 }
                 tmem_ld32(s_at, x[0]);
-                const float z = mx * c;
-                const bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
+                const float z = C::kE4m3 ? mx : mx * c;
+                const bool raise = z > m + (C::kE4m3 ? kAtSlackE4m3 : kAtSlack) || (m == -INFINITY && z > m);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m - z) : 1.f;  // m = -inf: 0
                     if (raise) {
@@ -1124,7 +1381,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         }
                     }
                 }
-                const float off = m == -INFINITY ? 0.f : -m;
+                const float off = m == -INFINITY ? 0.f : C::kE4m3 ? kAtBaseE4m3 - m : -m;
                 const float2 off2 = make_float2(off, off);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -1135,6 +1392,27 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         const int at32 = 64 * h + 32 * k;
                         if (at32 < 96) tmem_ld32(s_at + at32 + 32, x[1 - k]);
                         uint32_t pk[16];
+                        if constexpr (C::kE4m3) {
+                            // two e4m3 pieces of every weight: 8 words of the first, 8 of the second
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 fa = key_scales[at32 / 4 + i], sh = key_scales[2 * (kAtKeys / 4) + at32 / 4 + i];
+                                const float4 bk = key_scales[3 * (kAtKeys / 4) + at32 / 4 + i];
+                                float2 u = fma2(mul2(make_float2(__uint_as_float(x[k][4 * i]), __uint_as_float(x[k][4 * i + 1])), qs2),
+                                                make_float2(fa.x, fa.y), add2(make_float2(sh.x, sh.y), off2));
+                                float2 v = fma2(mul2(make_float2(__uint_as_float(x[k][4 * i + 2]), __uint_as_float(x[k][4 * i + 3])), qs2),
+                                                make_float2(fa.z, fa.w), add2(make_float2(sh.z, sh.w), off2));
+                                u.x = ex2(u.x);
+                                u.y = ex2(u.y);
+                                v.x = ex2(v.x);
+                                v.y = ex2(v.y);
+                                sum[0] = fma2(u, make_float2(bk.x, bk.y), sum[0]);
+                                sum[1] = fma2(v, make_float2(bk.z, bk.w), sum[1]);
+                                pk[i] = split_e4m3(u, v, pk[8 + i]);
+                            }
+                            tmem_st16(s_at + at32 / 2, pk);
+                            continue;
+                        }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float2 y = fma2(make_float2(__uint_as_float(x[k][2 * i]), __uint_as_float(x[k][2 * i + 1])), c2, off2);
@@ -1176,7 +1454,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                             if (r + 8 < rows) *reinterpret_cast<uint2*>(out + 8 * D + 8 * k) = make_uint2(o[4 * k + 2], o[4 * k + 3]);
                         }
                     }
-                    if (row < rows) w.ml[part + row] = make_float2(m, l);
+                    if (row < rows) w.ml[part + row] = make_float2(C::kE4m3 ? m - kAtBaseE4m3 : m, l);
                     tc_fence_before();
                 }
             }
@@ -1399,13 +1677,14 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 template <int F, int D>
 static bool pool_map(CUtensorMap* m, const PoolView& p, int plane, int page) {
     using C = AtCfg<F, D>;
-    const cuuint64_t dims[2] = {(cuuint64_t)p.heads * (C::kQuant ? C::kCodeRow : D), (cuuint64_t)p.slots};
+    constexpr bool bf16 = F == KVFIX_POOL_BF16;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.heads * (bf16 ? D : C::kCodeRow), (cuuint64_t)p.slots};
     const cuuint64_t strides[1] = {(cuuint64_t)(p.slots > 1 ? p.ss : (long long)p.heads * C::kCodeRow)};
-    const cuuint32_t box[2] = {(cuuint32_t)(C::kQuant ? C::kCodeRow : 64), (cuuint32_t)page}, one[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)(bf16 ? 64 : C::kCodeRow), (cuuint32_t)page}, one[2] = {1, 1};
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    return enc && enc(m, C::kQuant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                      p.plane[plane].codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      C::kQuant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+    return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.plane[plane].codes,
+                      dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      C::kConv ? CU_TENSOR_MAP_SWIZZLE_NONE : swizzle_for(bf16 ? 128 : C::kRow),
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
