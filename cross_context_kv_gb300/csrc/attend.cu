@@ -32,7 +32,6 @@
 //                   to bf16 tiles for the MMA; four warps for keys, four for values.
 // S occupies 128 TMEM columns per group, P (bf16) overwrites the first half of S, O takes D.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -334,7 +333,7 @@ struct __align__(16) AtItem {
     long long part;                     // first part row
     int page[8];                        // pool pages, -1: not read
 };
-enum : int { kFirst = 1, kLast = 2, kPair = 4, kPrefix = 8, kEnd = 16, kKeyTurn = 32, kValueTurn = 64, kFactorTurn = 128 };
+enum : int { kFirst = 1, kLast = 2, kPair = 4, kPrefix = 8, kEnd = 16, kKeyTurn = 32, kValueTurn = 64 };
 constexpr int kItems = 4;  // items ahead per group
 
 // Pieces of a line in order of units.
@@ -406,21 +405,8 @@ __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem,
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The same products of e4m3 operands (32 along the contraction a step), float accumulator.
-__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Instruction descriptors: e4m3 operands (format 0); B N-major: keys are the contraction, a
-// value row is contiguous along N.
-__host__ __device__ constexpr uint32_t at_idesc_e4m3(int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kAtRows >> 4) << 24);
-}
-constexpr uint32_t kNMajorB = 1u << 16;
+// B N-major (bit 16): keys are the contraction, a value row is contiguous along N.
+__host__ __device__ constexpr uint32_t at_idesc_pv(int N) { return tc_idesc_bf16(kAtRows, N) | (1u << 16); }
 
 // 16 consecutive 32-bit columns of this warp's 32 TMEM lanes from registers.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
@@ -454,34 +440,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // to no more than what the block launches with).
 template <int F, int D>
 struct AtCfg {
-    static constexpr bool kE4m3 = F == KVFIX_POOL_E4M3;      // key codes are operands as they lie
-    static constexpr bool kConvKeys = F == KVFIX_POOL_INT4;  // keys, values converted to bf16 tiles
-    static constexpr bool kConv = F != KVFIX_POOL_BF16;
-    static constexpr int kConvWarps = 4;  // per converting team: int4: keys and values; e4m3: values of every second tile
-    static constexpr int kThreads = kConv ? 384 + 64 * kConvWarps : 384;
-    static constexpr int kRegsSoftmax = kConv ? 120 : 208;
-    static constexpr int kRegsOther = kConv ? 80 : 88;
-    static constexpr int kKeyRow = kE4m3 ? D : 2 * D;  // bytes of a key (and of a query piece) as the MMA reads it
-    static constexpr int kKeyTile = kAtKeys * kKeyRow, kValueTile = kAtKeys * 2 * D;
-    static constexpr int kQ = kAtRows * D * 2;         // a group's queries: bf16, or two e4m3 pieces
-    // rings of tiles: keys are free once their product is done, values wait for the weights
-    static constexpr int kKeyStages = D == 64 ? 4 : kE4m3 ? 3 : 2;
-    static constexpr int kValueStages = D == 64 ? 4 : kConv ? 2 : 3;
-    static constexpr int kTiles = kKeyStages * kKeyTile + kValueStages * kValueTile;
-    // stored tiles before conversion: codes, their scales, and (e4m3) the keys' scales
+    static constexpr bool kQuant = F != KVFIX_POOL_BF16;
+    static constexpr int kConvWarps = 4;  // per converting team: one for keys, one for values
+    static constexpr int kThreads = kQuant ? 384 + 64 * kConvWarps : 384;
+    static constexpr int kRegsSoftmax = kQuant ? 120 : 208;
+    static constexpr int kRegsOther = kQuant ? 80 : 88;
+    static constexpr int kTile = kAtKeys * D * 2;   // a K or V tile as bf16
+    static constexpr int kQ = kAtRows * D * 2;
+    // rings of bf16 tiles: keys are free once their product is done, values wait for the weights
+    static constexpr int kKeyStages = D == 128 ? 2 : 4;
+    static constexpr int kValueStages = D == 128 ? (kQuant ? 2 : 3) : 4;
+    static constexpr int kStages = kKeyStages + kValueStages;
+    // stored tiles before conversion: codes, then scales
     static constexpr int kCodeRow = pool_head_bytes(F, D);
     static constexpr int kScaleRow = F == KVFIX_POOL_E4M3 ? 1 : F == KVFIX_POOL_INT4 ? D / 8 : 0;
-    static constexpr int kRaw = kConv ? kAtKeys * (kCodeRow + kScaleRow + (kE4m3 ? 1 : 0)) : 0;
-    static constexpr int kRawStages = kConvKeys && D == 64 ? 4 : 2;  // int4: half for keys
-    // e4m3: a ring of tiles' key factors (and which keys are NaN), longer than conversion can run
-    // ahead of the weights; two units' query row scales per group
-    static constexpr int kFactorSlots = kE4m3 ? 8 : 0;
-    static constexpr int kFloats = kE4m3 ? kFactorSlots * (kAtKeys + 4) * 4 + 2 * 2 * kAtRows * 4 : 0;
-    static constexpr int kSmem = 1024 + kTiles + 2 * kQ + (kConv ? kRawStages * kRaw : 0) + kFloats;
+    static constexpr int kRaw = kQuant ? kAtKeys * (kCodeRow + kScaleRow) : 0;
+    static constexpr int kRawStages = kQuant && D == 64 ? 4 : 2;  // half for keys
+    static constexpr int kSmem = 1024 + kStages * kTile + 2 * kQ + (kQuant ? kRawStages * kRaw : 0);
     static_assert(kSmem <= 227 * 1024 - 1536, "shared memory, with the barriers and items");
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (65536 / kThreads / 8 * 8), "registers");
-    // key rows of 128 or 64 bytes: the swizzle of a tile and the bytes from 8 rows to the next 8
-    static constexpr int kSwizzle = kKeyRow == 64 ? 4 : 2, kRows8 = kKeyRow == 64 ? 512 : 1024;
 };
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -590,174 +567,42 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
     return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-    return d;
-}
-
-// ------------------------------------------------------------------ e4m3 pools
-// Key codes are tensor operands as they lie.  With q = 2^e (q1 + q2), q1 the e4m3 value nearest
-// q / 2^e and q2 the e4m3 value nearest the rest, a bf16 query is exact but for bits below
-// 2^-18 of its row's largest (8 bits in two pieces of 4), and with key j's scale 2^(kj),
-//     q . k_j = 2^e 2^(kj) (q1 + q2) . code_j:
-// two products over half the operand bytes take the time of one in bf16, and the scales come in
-// as the softmax reads the logits.  Values become bf16 tiles (a value's scale would meet the
-// weights key by key: with e4m3 weights in two pieces the softmax took 6000 cycles a tile, with
-// bf16 weights 2300), so half a cache is converted: 170 us with both halves on 131072 keys.
-__device__ __forceinline__ int e4m3_scale_exp(unsigned byte) {
-    return min(max((int)byte - 127, kE4m3MinExp), kE4m3MaxExp);
-}
-
-// e4m3 pieces of four values: the word of the nearest, and in `rest` that of what is left.
-__device__ __forceinline__ uint32_t split_e4m3(float2 u, float2 v, uint32_t& rest) {
-    unsigned short a, b, c, d;
-    uint32_t ha, hb;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(a) : "f"(u.x), "f"(u.y));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(b) : "f"(v.x), "f"(v.y));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(ha) : "h"(a));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hb) : "h"(b));
-    const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
-    const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
-    const float2 ru = add2(u, make_float2(-fa.x, -fa.y)), rv = add2(v, make_float2(-fb.x, -fb.y));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(ru.x), "f"(ru.y));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(d) : "f"(rv.x), "f"(rv.y));
-    rest = (uint32_t)c | ((uint32_t)d << 16);
-    return (uint32_t)a | ((uint32_t)b << 16);
-}
-
-constexpr int kSplitRows = 32;  // query rows that one warp splits; more are split a thread per row
-
-// One query row in two e4m3 pieces by one thread; returns 2^e (NaN where the row is not finite).
-template <int D>
-__device__ __forceinline__ float split_row(const uint16_t* q, unsigned char* qt, int r) {
-    uint4 v[D / 8];
-    unsigned top = 0;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(q + 8 * i));
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        const unsigned mask = 0x7fff7fffu;
-        const unsigned y = __vmaxu2(__vmaxu2(v[i].x & mask, v[i].y & mask), __vmaxu2(v[i].z & mask, v[i].w & mask));
-        top = max(top, max(y & 0xffffu, y >> 16));
-    }
-    const int e = e4m3_exponent(top);
-    const float inv = pow2f(-e);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        float f[16];
-        unpack8(v[2 * i], f);
-        unpack8(v[2 * i + 1], f + 8);
-        uint32_t w[4], rest[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-            w[h] = split_e4m3(make_float2(f[4 * h] * inv, f[4 * h + 1] * inv),
-                              make_float2(f[4 * h + 2] * inv, f[4 * h + 3] * inv), rest[h]);
-        const int at = r * D + ((i ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
-        *reinterpret_cast<uint4*>(qt + at) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(qt + kAtRows * D + at) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-    }
-    return top >= 0x7f80u ? NAN : pow2f(e);
-}
-
-// A unit's query rows as two e4m3 pieces (K-major, swizzled like the keys), and 2^e per row
-// (NaN where a row is not finite).  D/8 lanes per row, eight values each.
-template <int D>
-__device__ __forceinline__ void split_queries(const AttendArgs& a, unsigned char* qt, float* scales, int lane, int head,
-                                              int rows, int row0, int agent0, int TG, int G) {
-    constexpr int L = D / 8, P = 32 / L, B = 4;  // lanes per row, rows per step, steps at a time
-    const int cv = lane % L;
-#pragma unroll 1
-    for (int r32 = 0; r32 < rows; r32 += 32) {
-        // a lane finds one row's place
-        const int x = row0 + min(r32 + lane, rows - 1), ag = x / TG, t = (x - ag * TG) / G, m = x - ag * TG - t * G;
-        const long long off = a.qp.row(agent0 + ag, 0, t) + (long long)(head * G + m) * D;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32 && r32 + i0 < rows; i0 += B * P) {
-            uint4 v[B];
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int k = (i0 + b * P + lane / L) & 31;
-                v[b] = __ldg(reinterpret_cast<const uint4*>(a.q + __shfl_sync(0xffffffffu, off, k) + 8 * cv));
-            }
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int r = r32 + i0 + b * P + lane / L;
-                const unsigned mask = 0x7fff7fffu;
-                const unsigned y = __vmaxu2(__vmaxu2(v[b].x & mask, v[b].y & mask), __vmaxu2(v[b].z & mask, v[b].w & mask));
-                unsigned top = max(y & 0xffffu, y >> 16);
-#pragma unroll
-                for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int e = e4m3_exponent(top);
-                const float inv = pow2f(-e);
-                float f[8];
-                unpack8(v[b], f);
-                uint32_t w[2], rest[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    w[h] = split_e4m3(make_float2(f[4 * h] * inv, f[4 * h + 1] * inv),
-                                      make_float2(f[4 * h + 2] * inv, f[4 * h + 3] * inv), rest[h]);
-                if (r < rows) {
-                    // rows of D bytes: 16-byte chunk c of row r at c ^ (r % 8), or c ^ (r / 2 % 4) for 64-byte rows
-                    const int at = r * D + (((cv / 2) ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4) + 8 * (cv & 1);
-                    *reinterpret_cast<uint2*>(qt + at) = make_uint2(w[0], w[1]);
-                    *reinterpret_cast<uint2*>(qt + kAtRows * D + at) = make_uint2(rest[0], rest[1]);
-                    if (cv == 0) scales[r] = top >= 0x7f80u ? NAN : pow2f(e);
-                }
-            }
-        }
-    }
-}
 
 template <int F, int D>
 __global__ void __launch_bounds__(AtCfg<F, D>::kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ AttendArgs a, const __grid_constant__ AtWork w) {
     using C = AtCfg<F, D>;
-    constexpr int SK = C::kKeyStages, SV = C::kValueStages;
-    constexpr int R = C::kConvKeys ? C::kRawStages / 2 : C::kRawStages;  // stored tiles in flight, per plane that is converted
+    constexpr int SK = C::kKeyStages, SV = C::kValueStages, R = C::kRawStages / 2;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t full[3][SK + SV], empty[SK + SV], raw_full[C::kRawStages], raw_empty[C::kRawStages];
+    __shared__ __align__(8) uint64_t full[3][SK + SV], empty[SK + SV], raw_full[2 * R], raw_empty[2 * R];
     __shared__ __align__(8) uint64_t q_free[2], s_full[2], p_ready[2], o_full[2];
-    __shared__ __align__(8) uint64_t factors_full[C::kE4m3 ? 3 : 1][C::kE4m3 ? C::kFactorSlots : 1], q_scaled[2][2], q_rows[2];
     __shared__ __align__(8) uint64_t item_full[2][kItems], item_free[2][kItems];
     __shared__ AtItem items[2][kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, mma_lock;
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* values = smem + SK * C::kKeyTile;
-    unsigned char* qsm = smem + C::kTiles;
+    unsigned char* qsm = smem + (SK + SV) * C::kTile;
     unsigned char* rawsm = qsm + 2 * C::kQ;
-    float* factors = reinterpret_cast<float*>(rawsm + (C::kConv ? C::kRawStages * C::kRaw : 0));  // [slots][128]
-    float* query_scales = factors + C::kFactorSlots * kAtKeys;                                     // [2][2][128]
-    uint4* nan_keys = reinterpret_cast<uint4*>(query_scales + 4 * kAtRows);                        // [slots]: a bit per key
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < SK + SV; ++i) {
-            for (int f = 0; f < 3; ++f)
-                mbar_init(&full[f][i], (i < SK ? C::kConvKeys : C::kConv) ? 32 * C::kConvWarps : 1);
+            for (int f = 0; f < 3; ++f) mbar_init(&full[f][i], C::kQuant ? 32 * C::kConvWarps : 1);
             mbar_init(&empty[i], 2);  // one release per softmax group (a group alone releases twice)
         }
-        if (C::kE4m3)
-            for (int i = 0; i < C::kFactorSlots; ++i)
-                for (int f = 0; f < 3; ++f) mbar_init(&factors_full[f][i], 32 * C::kConvWarps);
-        for (int i = 0; i < C::kRawStages; ++i) {
+        for (int i = 0; i < 2 * R; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], C::kConv ? 32 * C::kConvWarps : 1);
+            mbar_init(&raw_empty[i], C::kQuant ? 32 * C::kConvWarps : 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_free[i], 1);
-            for (int k = 0; k < 2; ++k) mbar_init(&q_scaled[i][k], 32);
-            mbar_init(&q_rows[i], 128);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 128);
             mbar_init(&o_full[i], 1);
             for (int k = 0; k < kItems; ++k) {
                 mbar_init(&item_full[i][k], 1);
                 // readers: producer, MMA, four softmax warps, converters
-                mbar_init(&item_free[i][k], 6 + (C::kConv ? 2 * C::kConvWarps : 0));
+                mbar_init(&item_free[i][k], 6 + (C::kQuant ? 2 * C::kConvWarps : 0));
             }
         }
         fence_mbar_init();
@@ -772,7 +617,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     // 0, group 1, both), whose phases that reader sees one by one, and the item says which
     // parity its tile's phase has.
     auto place = [](int p, int n) { return p ? SK + n % SV : n % SK; };
-    auto factor_bit = [](int n) { return SK + SV + (C::kE4m3 ? n % C::kFactorSlots : 0); };
     auto reader = [](int flags, int g) { return flags & kPair ? 2 : g; };
     auto released = [](int p, int n) { return (unsigned)((p ? n / SV : n / SK) - 1) & 1u; };  // its use before n's
     if (warp == 9) {
@@ -854,8 +698,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     const unsigned bits = pair ? turns[2] : g ? turns[1] : turns[0];
                     it->flags = (f.first ? kFirst : 0) | (f.t + 1 == f.t1 ? kLast : 0) | (pair ? kPair : 0) |
                                 (prefix ? kPrefix : 0) | ((bits >> place(0, tile_no)) & 1u ? kKeyTurn : 0) |
-                                ((bits >> place(1, tile_no)) & 1u ? kValueTurn : 0) |
-                                ((bits >> factor_bit(tile_no)) & 1u ? kFactorTurn : 0);
+                                ((bits >> place(1, tile_no)) & 1u ? kValueTurn : 0);
                     it->keys = min(kAtKeys, e.keys - f.t * kAtKeys);
                     it->key0 = f.t * kAtKeys;
                     it->rows = min(kAtRows, e.rows - r0);
@@ -875,7 +718,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             };
             auto step = [&](Feed& f, unsigned& reader_turns) {
                 reader_turns ^= (1u << place(0, tile_no)) | (1u << place(1, tile_no));
-                if (C::kE4m3) reader_turns ^= 1u << factor_bit(tile_no);
                 ++tile_no;
                 f.first = false;
                 if (++f.t < f.t1) fetch(f);
@@ -916,12 +758,12 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // a lane per copy: its page of the tile, and its 64-column half (bf16), or codes
             // and scales (stored forms)
             const int ppt = kAtKeys >> page_log, my = lane & (ppt - 1), part = lane >> (7 - page_log);
-            const bool mine = part < (C::kConv ? 2 : D / 64);
-            const unsigned page = (unsigned)a.page;
+            const bool mine = part < (C::kQuant ? 2 : D / 64);
+            const unsigned page_bytes = (unsigned)a.page * (C::kQuant ? C::kCodeRow + C::kScaleRow : 2 * D);
             bool ok = true, live[2] = {true, true};
             unsigned at[2] = {0, 0};
             int n = 0;
-            uint64_t* last_bar[SK + SV + C::kRawStages] = {};  // of each place's last copy, with its parity
+            uint64_t* last_bar[C::kQuant ? 2 * R : SK + SV] = {};  // of each place's last copy, with its parity
             unsigned last_turn = 0;
             while (ok && (live[0] || live[1])) {
 #pragma unroll
@@ -931,7 +773,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     if (!ok) break;
                     const AtItem& it = items[g][at[g] % kItems];
                     const int flags = it.flags, head = it.head;
-                    const int row = mine ? it.page[my] << page_log : -1;  // this lane's page's first pool row
+                    const int page = mine ? it.page[my] : -1;
                     __syncwarp();
                     if (lane == 0) item_done(g, at[g]);
                     ++at[g];
@@ -940,46 +782,37 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         continue;
                     }
                     if ((flags & kPair) && g == 1) continue;  // the tile is loaded already
-                    const unsigned keys = page * (unsigned)__popc(__ballot_sync(0xffffffffu, row >= 0 && part == 0));
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0 && part == 0));
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        // a stored tile on its way to conversion, or an operand tile
-                        const bool raw = C::kConvKeys || (C::kConv && p == 1);
-                        const int rs = (C::kConvKeys ? p * R : 0) + n % R, st = raw ? SK + SV + rs : place(p, n);
-                        uint64_t* const bar = raw ? &raw_full[rs] : &full[reader(flags, g)][place(p, n)];
-                        if (raw) {
-                            if (n >= R) ok = mbar_wait(&raw_empty[rs], (unsigned)(n / R - 1) & 1u);
+                        const int st = C::kQuant ? p * R + n % R : place(p, n);
+                        uint64_t* const bar = C::kQuant ? &raw_full[st] : &full[reader(flags, g)][st];
+                        if (C::kQuant) {
+                            if (n >= R) ok = mbar_wait(&raw_empty[st], (unsigned)(n / R - 1) & 1u);
                         } else if (n >= (p ? SV : SK)) {
                             ok = mbar_wait(&empty[st], released(p, n));
                         }
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        const unsigned row_bytes = raw ? C::kRaw / kAtKeys : p ? 2u * D : C::kKeyRow;
-                        if (lane == 0) mbar_arrive_expect_tx(bar, keys * row_bytes);
+                        if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)boxes * page_bytes);
                         __syncwarp();
-                        if (row >= 0) {
-                            const int k0 = my << page_log;  // the page's first key in the tile
-                            if (raw) {
-                                unsigned char* const dst = rawsm + rs * C::kRaw;
-                                if (part == 0) {
-                                    tma_load_2d(dst + k0 * C::kCodeRow, p ? &tm_v : &tm_k, head * C::kCodeRow, row, bar);
-                                } else {
-                                    const long long at_row = (long long)head * a.pool.slots + row;
-                                    bulk_g2s(dst + kAtKeys * C::kCodeRow + k0 * C::kScaleRow,
-                                             a.pool.plane[p].scales + at_row * C::kScaleRow, page * C::kScaleRow, bar);
-                                    if (C::kE4m3)  // the keys' scales go with the stored values
-                                        bulk_g2s(dst + kAtKeys * (C::kCodeRow + 1) + k0, a.pool.plane[0].scales + at_row, page, bar);
-                                }
-                            } else if (C::kE4m3) {
-                                if (part == 0) tma_load_2d(smem + st * C::kKeyTile + k0 * D, &tm_k, head * D, row, bar);
+                        if (page >= 0) {
+                            if (!C::kQuant) {
+                                tma_load_2d(smem + st * C::kTile + part * (kAtKeys * 128) + (my << page_log) * 128,
+                                            p ? &tm_v : &tm_k, head * D + 64 * part, page << page_log, bar);
+                            } else if (part == 0) {
+                                tma_load_2d(rawsm + st * C::kRaw + (my << page_log) * C::kCodeRow, p ? &tm_v : &tm_k,
+                                            head * C::kCodeRow, page << page_log, bar);
                             } else {
-                                unsigned char* const dst = p ? values + (st - SK) * C::kValueTile : smem + st * C::kKeyTile;
-                                tma_load_2d(dst + part * (kAtKeys * 128) + k0 * 128, p ? &tm_v : &tm_k, head * D + 64 * part, row, bar);
+                                bulk_g2s(rawsm + st * C::kRaw + kAtKeys * C::kCodeRow + (my << page_log) * C::kScaleRow,
+                                         a.pool.plane[p].scales +
+                                             ((long long)head * a.pool.slots + (page << page_log)) * C::kScaleRow,
+                                         (unsigned)a.page * C::kScaleRow, bar);
                             }
                         }
-                        const unsigned t = raw ? (unsigned)(n / R) & 1u : flags & (p ? kValueTurn : kKeyTurn) ? 1u : 0u;
+                        const unsigned t = C::kQuant ? (unsigned)(n / R) & 1u : flags & (p ? kValueTurn : kKeyTurn) ? 1u : 0u;
 #pragma unroll
-                        for (int i = 0; i < SK + SV + C::kRawStages; ++i)
+                        for (int i = 0; i < (C::kQuant ? 2 * R : SK + SV); ++i)
                             if (i == st) last_bar[i] = bar;
                         last_turn = (last_turn & ~(1u << st)) | (t << st);
                     }
@@ -989,7 +822,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if (!ok) {
                 // the copies in flight land before this block gives up its shared memory: each
                 // place's last one
-                for (int st = 0; st < SK + SV + C::kRawStages; ++st)
+                for (int st = 0; st < (C::kQuant ? 2 * R : SK + SV); ++st)
                     if (last_bar[st]) mbar_wait(last_bar[st], last_turn >> st & 1u);
                 if (lane == 0) atomicOr(&abort_flag, 1);
             }
@@ -999,21 +832,17 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // memory, O += P V.  While the group works on a tile's weights the warp looks at its
             // next tile and, where that begins a unit, brings the unit's queries.
             const int g = warp == 9 ? 0 : 1;
-            constexpr uint32_t id_qk = C::kE4m3 ? at_idesc_e4m3(kAtKeys) : tc_idesc_bf16(kAtRows, kAtKeys);
-            constexpr uint32_t id_pv = tc_idesc_bf16(kAtRows, D) | kNMajorB;
+            constexpr uint32_t id_qk = tc_idesc_bf16(kAtRows, kAtKeys), id_pv = at_idesc_pv(D);
             // descriptors of the group's queries and of the first stage (as keys, K-major, and as
             // values, N-major: 64-column halves 16 KB apart, 8-key groups 1 KB apart); an offset
             // adds to the address field, which all of shared memory fits
             unsigned char* const qt = qsm + g * C::kQ;
-            const uint64_t q_desc = tc_smem_desc(qt, 16, C::kRows8, C::kSwizzle);
-            const uint64_t t_desc = tc_smem_desc(smem, 16, C::kRows8, C::kSwizzle);
-            const uint64_t v_desc = tc_smem_desc(values, kAtKeys * 128, 1024, 2);
+            const uint64_t q_desc = tc_smem_desc(qt, 16, 1024, 2), t_desc = tc_smem_desc(smem, 16, 1024, 2);
+            const uint64_t v_desc = tc_smem_desc(smem, kAtKeys * 128, 1024, 2);
             const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
             bool ok = true;
             unsigned at = 0, units = 0, p_phase = 0;
             int flags = 0, tile = 0;
-            bool wide = false;
-            unsigned wides = 0, narrows = 0;
             // Reads the next item; begins to load its queries where it opens a unit, K-major
             // with the 128-byte swizzle, once the last product with the rows before them is
             // done.  Rows past the unit's keep what they hold (a row of a product depends on its
@@ -1032,13 +861,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (units > 0) ok = __all_sync(0xffffffffu, mbar_wait(&q_free[g], (units - 1) & 1u));
                 ++units;
                 if (!ok) return;
-                if constexpr (C::kE4m3) {
-                    // (more rows than a warp has lanes: the softmax group's threads bring their own)
-                    wide = rows > kSplitRows;
-                    if (wide) return;
-                    split_queries<D>(a, qt, query_scales + (2 * g + (units & 1)) * kAtRows, lane, head, rows, row0, agent0, TG, G);
-                    return;
-                }
                 constexpr int V = D / 8, P = 32 / V;  // 16-byte vectors per row, rows per step
                 const int cv = lane % V;
                 unsigned char* const dst = qt + (cv / 8) * (kAtRows * 128);
@@ -1057,14 +879,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 cp_async_commit();
             };
             auto queries_here = [&]() {
-                if (C::kE4m3 && wide) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&q_rows[g], wides++ & 1u));
-                    return;
-                }
-                if (!C::kE4m3) cp_async_wait<0>();
+                cp_async_wait<0>();
                 fence_proxy_async_smem();
-                // (two barriers in turn: the next unit's queries may come before the softmax has looked)
-                if (C::kE4m3) mbar_arrive(&q_scaled[g][narrows++ & 1u]);
                 __syncwarp();
             };
             // The tensor pipe takes products in the order of issue.  A group's O += P V and next
@@ -1089,20 +905,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // S of the open item (one lane)
             auto logits = [&]() {
                 const int ks = place(0, tile);
-                const uint64_t bd = t_desc + (uint32_t)ks * (uint32_t)(C::kKeyTile >> 4);
-                if (C::kE4m3) {
-                    // both pieces of the queries against the same keys
+                const uint64_t bd = t_desc + (uint32_t)ks * (uint32_t)(C::kTile >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 2 * (D / 32); ++kk) {
-                        const uint32_t off = 32 * (kk % (D / 32)) >> 4, piece = (kk / (D / 32)) * (kAtRows * D) >> 4;
-                        mma_e4m3_ss(tmem + 128 * g, q_desc + piece + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
-                    }
-                } else {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
-                        tc_mma_bf16(tmem + 128 * g, q_desc + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
-                    }
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk / 4) * (kAtKeys * 128) + 32 * (kk % 4)) >> 4;
+                    tc_mma_bf16(tmem + 128 * g, q_desc + off, bd + off, id_qk, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(&s_full[g]);
                 tc_commit(&empty[ks]);
@@ -1112,7 +919,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             open_item();
             if (ok && !(flags & kEnd)) {
                 queries_here();
-                if (ok) keys_here();
+                keys_here();
                 if (ok) {
                     tc_fence_after();
                     if (elect_lane()) logits();
@@ -1124,12 +931,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 open_item();
                 if (!ok) break;
                 const bool more = !(flags & kEnd);
-                const bool late = C::kE4m3 && more && (flags & kFirst) && wide;
                 // all that the two products read, the weights last
                 if (more) {
-                    // (a wide unit's queries come from the group, which first needs its last tile's
-                    // products: they wait below)
-                    if ((flags & kFirst) && !wide) queries_here();
+                    if (flags & kFirst) queries_here();
                     keys_here();
                     if (!ok) break;
                 }
@@ -1142,7 +946,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_lane()) {
-                    const uint64_t bd = v_desc + (uint32_t)(vs - SK) * (uint32_t)(C::kValueTile >> 4);
+                    const uint64_t bd = v_desc + (uint32_t)vs * (uint32_t)(C::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kAtKeys / 16; ++kk)
                         tc_mma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, bd + (uint32_t)(2048 * kk >> 4), id_pv,
@@ -1150,29 +954,20 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     tc_commit(&empty[vs]);
                     if (!(now & kPair)) tc_commit(&empty[vs]);
                     if (now & kLast) tc_commit(&o_full[g]);
-                    if (more && !late) logits();
+                    if (more) logits();
                 }
                 __syncwarp();
                 if (now & kPair) leave_pipe();
-                if (late) {
-                    queries_here();
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_lane()) logits();
-                    __syncwarp();
-                }
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
-        } else if (C::kConv) {
+        } else if (C::kQuant) {
             // ------------------------------------------------------------ conversion
-            // two teams of warps: one for the key tiles and one for the value tiles (int4), or one
-            // for the values of even and one for those of odd tiles (e4m3)
+            // one team of warps converts the key tiles, another the value tiles
             constexpr int N = 32 * C::kConvWarps;
-            const int team = (int)(threadIdx.x - 384) / N, tid = (int)(threadIdx.x - 384) % N;
-            const int p = C::kConvKeys ? team : 1;
+            const int p = (int)(threadIdx.x - 384) / N, tid = (int)(threadIdx.x - 384) % N;
             bool ok = true, live[2] = {true, true};
             unsigned at[2] = {0, 0};
-            int n = -1;
+            int n = 0;
             while (ok && (live[0] || live[1])) {
 #pragma unroll 1
                 for (int g = 0; g < 2; ++g) {
@@ -1190,31 +985,18 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         continue;
                     }
                     if ((flags & kPair) && g == 1) continue;
-                    ++n;
-                    if (!C::kConvKeys && (n & 1) != team) continue;
-                    const int rs = (C::kConvKeys ? p * R : 0) + n % R, st = place(p, n);
+                    const int rs = p * R + n % R, st = place(p, n);
                     ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], (unsigned)(n / R) & 1u));
                     if (!ok) break;
                     StoredTile<F, D, N> stored;
-                    const unsigned char* const raw = rawsm + rs * C::kRaw;
-                    stored.take(raw, tid);
-                    if (C::kE4m3) {
-                        // a thread per key: its factor on the logits; a NaN key makes them NaN where a
-                        // row sees it, so the softmax is told which
-                        const unsigned kb = raw[kAtKeys * (C::kCodeRow + 1) + tid];
-                        const bool there = tid < keys && !((absent >> (tid >> 4)) & 1u), nan_key = there && kb == kE4m3NanByte;
-                        const int slot = n % (C::kE4m3 ? C::kFactorSlots : 1);
-                        factors[slot * kAtKeys + tid] = there && !nan_key ? pow2f(e4m3_scale_exp(kb)) : 1.f;
-                        const unsigned nans = __ballot_sync(0xffffffffu, nan_key);
-                        if (lane == 0) reinterpret_cast<unsigned*>(nan_keys + slot)[tid >> 5] = nans;
-                        mbar_arrive(&factors_full[reader(flags, g)][slot]);
-                    }
+                    stored.take(rawsm + rs * C::kRaw, tid);
                     mbar_arrive(&raw_empty[rs]);
                     if (n >= (p ? SV : SK)) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], released(p, n)));
                     if (!ok) break;
-                    stored.put(p ? values + (st - SK) * C::kValueTile : smem + st * C::kKeyTile, tid, keys, absent);
+                    stored.put(smem + st * C::kTile, tid, keys, absent);
                     fence_proxy_async_smem();
                     mbar_arrive(&full[reader(flags, g)][st]);
+                    ++n;
                 }
             }
             if (!ok && lane == 0) atomicOr(&abort_flag, 1);
@@ -1230,8 +1012,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         bool ok = true;
         unsigned at = 0, units = 0;
         int rows = 0, sees = 0;   // of the unit: the group's rows; keys this row sees
-        float q_scale = 1.f;      // e4m3: of this row's queries
-        unsigned narrows = 0;
         float m = -INFINITY, l = 0.f;
         while (true) {
             ok = item_wait(g, at);
@@ -1260,42 +1040,20 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     }
                 }
             }
-            if constexpr (C::kE4m3)
-                if ((flags & kFirst) && rows > kSplitRows) {
-                    // (this group's last product with the rows before is done: it has its logits)
-                    if (row < rows) {
-                        const int G = a.q_heads / a.pool.heads, TG = a.new_tokens * G;
-                        const int x = it.row0 + row, ag = x / TG, t = (x - ag * TG) / G, h = it.head * G + x - ag * TG - t * G;
-                        q_scale = split_row<D>(a.q + a.qp.row(it.agent0 + ag, 0, t) + (long long)h * D, qsm + g * C::kQ, row);
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(&q_rows[g]);
-                }
             const bool warp_live = 32 * wq < rows;
             const int nv = sees - key0;  // columns this row sees
             const bool whole = absent == 0u && keys == kAtKeys;
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], at & 1u));
             if (!ok) break;
             tc_fence_after();
-            const int slot = C::kE4m3 ? tile % C::kFactorSlots : 0;
-            if (C::kE4m3) {
-                ok = mbar_wait(&factors_full[reader(flags, g)][slot], flags & kFactorTurn ? 1u : 0u);
-                if (ok && (flags & kFirst) && rows <= kSplitRows) {
-                    ok = mbar_wait(&q_scaled[g][narrows & 1u], (narrows >> 1) & 1u);
-                    ++narrows;
-                    q_scale = query_scales[(2 * g + ((units + 1) & 1)) * kAtRows + row];
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-            }
-            if (F == KVFIX_POOL_BF16 && !whole) {
+            if (!C::kQuant && !whole) {
                 // value rows that hold no key read as zero: a weight of 0 times what lies there
                 // (anything, NaN too) would not be 0
                 const int st = place(1, tile);
                 ok = __all_sync(0xffffffffu, mbar_wait(&full[reader(flags, g)][st], flags & kValueTurn ? 1u : 0u));
                 if (!ok) break;
                 if (row >= keys || ((absent >> (row >> 4)) & 1u)) {
-                    unsigned char* vt = values + (st - SK) * C::kValueTile + row * 128;
+                    unsigned char* vt = smem + st * C::kTile + row * 128;
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h)
 #pragma unroll
@@ -1309,21 +1067,13 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 // one is worked on: the maximum, then the weights
                 uint32_t x[2][32];
                 float mx = -INFINITY;
-                uint4 nans = make_uint4(0u, 0u, 0u, 0u);
-                if (C::kE4m3) nans = nan_keys[slot];
-                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys || (nans.x | nans.y | nans.z | nans.w) != 0u)) {
+                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys)) {
                     // columns that hold no key, or none that this row sees: -inf (on the side, so
                     // that the sweeps' code stays small)
 #pragma unroll 1
                     for (int c0 = 0; c0 < kAtKeys; c0 += 32) {
                         tmem_ld32(s_at + c0, x[0]);
                         tmem_wait_ld32(x[0]);
-                        if (C::kE4m3) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if ((nans.x >> i) & 1u) x[0][i] = 0x7fffffffu;
-                            nans = make_uint4(nans.y, nans.z, nans.w, 0u);
-                        }
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int n = (absent >> (c0 / 16 + b)) & 1u ? 0 : nv - c0 - 16 * b;
@@ -1335,9 +1085,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     }
                     tmem_wait_st();
                 }
-                // e4m3: the row's and the keys' scales come in here, and the second sweep reads them in
-                const float4* key_factors = reinterpret_cast<const float4*>(factors + slot * kAtKeys);
-                const float2 qs2 = make_float2(q_scale, q_scale);
                 tmem_ld32(s_at, x[0]);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -1346,19 +1093,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         tmem_wait_ld32(x[k]);
                         const int at32 = 64 * h + 32 * k;
                         if (at32 < 96) tmem_ld32(s_at + at32 + 32, x[1 - k]);
-                        if (C::kE4m3) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 f = key_factors[at32 / 4 + i];
-                                const float2 u = mul2(mul2(make_float2(__uint_as_float(x[k][4 * i]), __uint_as_float(x[k][4 * i + 1])), qs2), make_float2(f.x, f.y));
-                                const float2 v = mul2(mul2(make_float2(__uint_as_float(x[k][4 * i + 2]), __uint_as_float(x[k][4 * i + 3])), qs2), make_float2(f.z, f.w));
-                                x[k][4 * i] = __float_as_uint(u.x);
-                                x[k][4 * i + 1] = __float_as_uint(u.y);
-                                x[k][4 * i + 2] = __float_as_uint(v.x);
-                                x[k][4 * i + 3] = __float_as_uint(v.y);
-                            }
-                            tmem_st32(s_at + at32, x[k]);
-                        }
                         float m4[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(x[k][i]), __uint_as_float(x[k][i + 4]));
@@ -1370,7 +1104,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         mx = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mx);
                     }
                 }
-                if (C::kE4m3) tmem_wait_st();
                 tmem_ld32(s_at, x[0]);
                 const float z = mx * c;
                 const bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
@@ -1663,22 +1396,17 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ host
-// A plane of the pool: bf16 in boxes of 64 columns, codes a head's row at a time, swizzled
-// where they are operands as they lie.
 template <int F, int D>
 static bool pool_map(CUtensorMap* m, const PoolView& p, int plane, int page) {
     using C = AtCfg<F, D>;
-    constexpr bool bf16 = F == KVFIX_POOL_BF16;
-    const cuuint64_t dims[2] = {(cuuint64_t)p.heads * (bf16 ? D : C::kCodeRow), (cuuint64_t)p.slots};
+    const cuuint64_t dims[2] = {(cuuint64_t)p.heads * (C::kQuant ? C::kCodeRow : D), (cuuint64_t)p.slots};
     const cuuint64_t strides[1] = {(cuuint64_t)(p.slots > 1 ? p.ss : (long long)p.heads * C::kCodeRow)};
-    const cuuint32_t box[2] = {(cuuint32_t)(bf16 ? 64 : C::kCodeRow), (cuuint32_t)page}, one[2] = {1, 1};
-    const CUtensorMapSwizzle swizzle = bf16                      ? CU_TENSOR_MAP_SWIZZLE_128B
-                                       : C::kE4m3 && plane == 0 ? swizzle_for(C::kKeyRow)
-                                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
+    const cuuint32_t box[2] = {(cuuint32_t)(C::kQuant ? C::kCodeRow : 64), (cuuint32_t)page}, one[2] = {1, 1};
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.plane[plane].codes,
-                      dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc && enc(m, C::kQuant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                      p.plane[plane].codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      C::kQuant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int F, int D>

@@ -63,6 +63,13 @@ __device__ __forceinline__ unsigned finite_abs_max8(const uint4& v) {
     return r;
 }
 
+// The e4m3 scale exponent of a row whose largest finite magnitude has bf16 bits `a`: the
+// least k with magnitude <= 448 2^k = 1.75 2^(k+8), within the format's limits.
+__device__ __forceinline__ int e4m3_exponent(unsigned a) {
+    const int k = (int)(a >> 7) - 127 - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
+    return min(max(k, kE4m3MinExp), kE4m3MaxExp);
+}
+
 constexpr unsigned kNanRow = 0xffffu;
 
 __device__ __forceinline__ uint2 to_e4m3(const uint4& v, float inv) {

@@ -108,13 +108,6 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4& codes, const E4m3Sc
     o1 = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// The e4m3 scale exponent of a row whose largest finite magnitude has bf16 bits `a`: the
-// least k with magnitude <= 448 2^k = 1.75 2^(k+8), within the format's limits.
-__device__ __forceinline__ int e4m3_exponent(unsigned a) {
-    const int k = (int)(a >> 7) - 127 - 8 + ((a & 0x7fu) > 0x60u ? 1 : 0);
-    return min(max(k, kE4m3MinExp), kE4m3MaxExp);
-}
-
 // ------------------------------------------------------------- int4 -> bf16
 // Eight codes to four bf16 pairs: 128 + code is exact in bf16, so is the difference, and one
 // fused multiply-add rounds once.
