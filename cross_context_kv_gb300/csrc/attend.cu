@@ -38,13 +38,11 @@
 
 #include <atomic>
 
-#include "attend.h"
-#include "pool.cuh"
+#include "attend_few.cuh"
+#include "attend_plan.cuh"
 #include "tc.cuh"
 
 namespace kvfix {
-
-static __device__ unsigned int g_status_attend;
 
 unsigned read_status_attend(cudaStream_t stream) {
     unsigned h = 0, zero = 0;
@@ -52,276 +50,6 @@ unsigned read_status_attend(cudaStream_t stream) {
     cudaMemcpyToSymbolAsync(g_status_attend, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, stream);
     cudaStreamSynchronize(stream);
     return h;
-}
-
-constexpr int kAtKeys = 128;      // keys per tile
-constexpr int kAtRows = 128;      // rows per accumulator (MMA M)
-constexpr int kAtBlock = 256;     // rows per entry
-constexpr int kAtMaxCtas = 256;   // bound of the persistent grid
-
-// ------------------------------------------------------------------ plan
-// A segment's rows are cut into blocks of 256; a block of more than 128 rows is a pair (both
-// softmax groups share its tiles), the last one may be a single.  Pairs and singles lie on a
-// line of their own: unit (entry e, head h) begins at begin + h * (tiles + at_pad).  The pairs'
-// line is cut into one piece per CTA, the singles' into two (one per softmax group).
-// What a unit costs beside its tiles (queries in, masks, its part out), in tiles: measured on
-// pairs of short own segments, 17000 cycles a unit against 4000 a tile; with 1 there, the CTAs
-// that had those units ran 1.7 times as long as the others.
-__host__ __device__ constexpr int at_pad(bool single) { return single ? 1 : 4; }
-
-struct __align__(16) AtEntry {
-    long long begin;  // position of head 0 on the line
-    int tiles, rows;
-    int row0, seg, keys, agent0;  // keys: those that some row of the block may see
-};
-
-// Where a piece of a line begins, all that its walk needs in one round of loads.
-struct __align__(16) AtStart {
-    AtEntry rec;        // the entry
-    long long lo, hi;   // the piece
-    int e, h, n, have;  // the entry's index, the head, the line's entries; whether there is a piece
-};
-
-struct AtPlan {
-    long long chunk[2];               // pairs, singles: length of a piece of the line
-    AtStart start[3][kAtMaxCtas];     // pairs, singles of group 0, of group 1
-};
-
-struct AtLayout {
-    size_t plan, first, bounds, entries[2], ml, o, bytes;
-    long long own_rows;
-};
-
-// Part rows.  The first part of a unit has its rows' own places (prefix rows, then suffix
-// rows: [head][agent][token, query head]); a part that continues a unit from an earlier piece
-// has its CTA's: 256 rows for a pair, 2 x 128 for singles.
-static AtLayout at_layout(int agents, int T, int q_heads, int kv_heads, int head_dim, int groups) {
-    const long long tg = (long long)T * (q_heads / kv_heads), all = (long long)agents * tg;
-    AtLayout l;
-    l.own_rows = 2 * kv_heads * all;
-    const long long rows = l.own_rows + (long long)kAtMaxCtas * 2 * kAtBlock;
-    size_t at = 0;
-    auto take = [&](size_t n) {
-        const size_t here = at;
-        at += (n + 255) / 256 * 256;
-        return here;
-    };
-    l.plan = take(sizeof(AtPlan));
-    l.first = take(8 * ((size_t)groups + agents));
-    l.bounds = take(4 * ((size_t)groups + 1));
-    l.entries[0] = take(sizeof(AtEntry) * (size_t)(2 * all / kAtRows + 2));
-    l.entries[1] = take(sizeof(AtEntry) * ((size_t)groups + agents + 1));
-    l.ml = take(8 * (size_t)rows);
-    l.o = take(4 * (size_t)rows * head_dim);
-    l.bytes = at;
-    return l;
-}
-
-size_t attend_workspace_bytes(int agents, int T, int q_heads, int kv_heads, int head_dim, int groups) {
-    return at_layout(agents, T, q_heads, kv_heads, head_dim, groups).bytes;
-}
-
-struct AtWork {
-    AtPlan* plan;
-    int2* first;          // [groups + agents]: a segment's first pair and its single
-    int* bounds;          // [groups + 1]: the groups' agents, clamped and ascending
-    AtEntry* entries[2];  // pairs, singles
-    float2* ml;           // part rows: (max in base-2 units, sum)
-    float* o;             // part rows x D
-    long long own_rows;
-    int ctas;
-};
-
-__device__ __forceinline__ int clamp_len(int n, long long most, bool& bad) {
-    if (n < 0 || n > most) bad = true;
-    return (int)min(max((long long)n, 0ll), most);
-}
-
-// A quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division takes
-// about a hundred instructions).
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-    return (x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
-}
-
-constexpr int kPlanThreads = 256;
-
-struct PlanSums {
-    int n[2];
-    long long line[2];
-};
-// Exclusive scan over the block, and the totals.
-__device__ __forceinline__ PlanSums plan_scan(const PlanSums& x, PlanSums* warp_sums, PlanSums* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    PlanSums inc = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int a = __shfl_up_sync(0xffffffffu, inc.n[k], o);
-            const long long b = __shfl_up_sync(0xffffffffu, inc.line[k], o);
-            if (lane >= o) {
-                inc.n[k] += a;
-                inc.line[k] += b;
-            }
-        }
-    if (lane == 31) warp_sums[warp] = inc;
-    __syncthreads();
-    PlanSums ex, all = {};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        ex.n[k] = inc.n[k] - x.n[k];
-        ex.line[k] = inc.line[k] - x.line[k];
-    }
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / 32; ++w)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int a = warp_sums[w].n[k];
-            const long long b = warp_sums[w].line[k];
-            if (w < warp) {
-                ex.n[k] += a;
-                ex.line[k] += b;
-            }
-            all.n[k] += a;
-            all.line[k] += b;
-        }
-    *total = all;
-    return ex;
-}
-
-constexpr int kPlanKept = 256;  // entries of a line that stay in shared memory
-
-__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendArgs a,
-                                                                   const __grid_constant__ AtWork w) {
-    __shared__ PlanSums warp_sums[kPlanThreads / 32];
-    __shared__ int warp_max[kPlanThreads / 32];
-    __shared__ AtEntry kept[2][kPlanKept];
-    pdl_wait();  // the lengths may be the work of the kernel before
-    pdl_trigger();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G, H = a.pool.heads;
-    const int segs = a.groups + a.agents;
-    const int per = (segs + kPlanThreads - 1) / kPlanThreads;
-    const int s0 = min(segs, tid * per), s1 = min(segs, s0 + per);
-    const long long most_p = (long long)a.max_prefix_pages * a.page, most_s = (long long)a.max_suffix_pages * a.page;
-    bool bad = false;
-    // the first segment's length is on its way while the bounds are worked out
-    int len0 = 0;
-    if (s0 < s1) len0 = s0 < a.groups ? __ldg(a.prefix_len + s0) : __ldg(a.suffix_len + s0 - a.groups);
-    // group bounds: the running maximum of the given ones, kept within 0..agents
-    if (a.groups > 0) {
-        const int n = a.groups + 1, each = (n + kPlanThreads - 1) / kPlanThreads;
-        const int g0 = min(n, tid * each), g1 = min(n, g0 + each);
-        int mine = 0;
-        for (int g = g0; g < g1; ++g) mine = max(mine, min(max(__ldg(a.group_begin + g), 0), a.agents));
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc = max(inc, y);
-        }
-        if (lane == 31) warp_max[warp] = inc;
-        __syncthreads();
-        int run = 0;
-        for (int x = 0; x < warp; ++x) run = max(run, warp_max[x]);
-        const int left = __shfl_up_sync(0xffffffffu, inc, 1);
-        if (lane > 0) run = max(run, left);
-        for (int g = g0; g < g1; ++g) {
-            const int b = __ldg(a.group_begin + g);
-            if (b < run || b > a.agents) bad = true;
-            run = max(run, min(max(b, 0), a.agents));
-            w.bounds[g] = run;
-        }
-        __syncthreads();
-    }
-    // a segment's blocks in turn
-    auto each_block = [&](int s, auto&& f) {
-        const bool prefix = s < a.groups;
-        const int agent0 = prefix ? w.bounds[s] : s - a.groups;
-        const int count = prefix ? w.bounds[s + 1] - agent0 : 1;
-        const int given = s == s0 ? len0 : prefix ? __ldg(a.prefix_len + s) : __ldg(a.suffix_len + agent0);
-        const int n = clamp_len(given, prefix ? most_p : most_s, bad);
-        const int rows = count * TG;
-        for (int r0 = 0; r0 < rows; r0 += kAtBlock) {
-            AtEntry e;
-            e.rows = min(kAtBlock, rows - r0);
-            e.row0 = r0;
-            e.seg = s;
-            e.agent0 = agent0;
-            // own keys are seen up to the place of the block's last row
-            e.keys = prefix ? n : max(0, n - T + 1 + (r0 + e.rows - 1) / G);
-            e.tiles = (e.keys + kAtKeys - 1) / kAtKeys;
-            f(e, e.rows > kAtRows ? 0 : 1);
-        }
-    };
-    auto cost = [&](const AtEntry& e) {
-        return e.tiles > 0 ? (long long)H * (e.tiles + at_pad(e.rows <= kAtRows)) : 0ll;
-    };
-    PlanSums mine = {};
-    for (int s = s0; s < s1; ++s)
-        each_block(s, [&](const AtEntry& e, int k) {
-            if (k == 0) {
-                mine.n[0] += 1;
-                mine.line[0] += cost(e);
-            } else {
-                mine.n[1] += 1;
-                mine.line[1] += cost(e);
-            }
-        });
-    PlanSums total;
-    PlanSums at = plan_scan(mine, warp_sums, &total);
-    for (int s = s0; s < s1; ++s) {
-        w.first[s] = make_int2(at.n[0], at.n[1]);
-        each_block(s, [&](AtEntry e, int k) {
-            const long long c = cost(e);
-            if (k == 0) {
-                e.begin = at.line[0];
-                w.entries[0][at.n[0]] = e;
-                if (at.n[0] < kPlanKept) kept[0][at.n[0]] = e;
-                at.n[0] += 1;
-                at.line[0] += c;
-            } else {
-                e.begin = at.line[1];
-                w.entries[1][at.n[1]] = e;
-                if (at.n[1] < kPlanKept) kept[1][at.n[1]] = e;
-                at.n[1] += 1;
-                at.line[1] += c;
-            }
-        });
-    }
-    __syncthreads();
-    const long long chunk[2] = {max(1ll, quotient(total.line[0] + w.ctas - 1, w.ctas)),
-                                max(1ll, quotient(total.line[1] + 2 * w.ctas - 1, 2 * w.ctas))};
-    for (int i = tid; i < 3 * w.ctas; i += kPlanThreads) {
-        const int cta = i % w.ctas, set = i / w.ctas, k = set > 0;
-        AtStart* st = &w.plan->start[set][cta];
-        const long long lo = chunk[k] * (set == 2 ? cta + w.ctas : cta);
-        if (lo >= total.line[k]) {
-            st->have = 0;
-            continue;
-        }
-        // The last entry that begins at or before the piece does: entries without tiles take no
-        // room, and of several at one place the last has it.
-        int x = 0, y = total.n[k];  // begin[x] <= lo < begin[y]
-        const bool here = total.n[k] <= kPlanKept;
-        while (y - x > 1) {
-            const int m = (x + y) / 2;
-            const long long b = here ? kept[k][m].begin : w.entries[k][m].begin;
-            if (b <= lo) x = m;
-            else y = m;
-        }
-        AtStart r;
-        r.rec = here ? kept[k][x] : w.entries[k][x];
-        r.lo = lo;
-        r.hi = min(total.line[k], lo + chunk[k]);
-        r.e = x;
-        r.h = (int)quotient(lo - r.rec.begin, r.rec.tiles + at_pad(k == 1));
-        r.n = total.n[k];
-        r.have = 1;
-        *st = r;
-    }
-    if (tid < 2) w.plan->chunk[tid] = tid ? chunk[1] : chunk[0];
-    if (bad) atomicOr(&g_status_attend, FLAG_BOUNDS);
 }
 
 // ------------------------------------------------------------------ a CTA's work
@@ -336,57 +64,7 @@ struct __align__(16) AtItem {
 enum : int { kFirst = 1, kLast = 2, kPair = 4, kPrefix = 8, kEnd = 16, kKeyTurn = 32, kValueTurn = 64 };
 constexpr int kItems = 4;  // items ahead per group
 
-// Pieces of a line in order of units.
-struct AtWalk {
-    const AtEntry* ent;
-    long long lo, hi;
-    int e, n, h, H;
-    AtEntry rec;
-    bool have;
-
-    __device__ __forceinline__ void open(const AtStart& s, const AtEntry* entries, int heads) {
-        rec = s.rec;
-        lo = s.lo;
-        hi = s.hi;
-        e = s.e;
-        h = s.h;
-        n = s.n;
-        have = s.have != 0;
-        ent = entries;
-        H = heads;
-    }
-
-    // The next unit's tiles [t0, t1) of head `head` in this piece.
-    __device__ __forceinline__ bool next(int& head, int& t0, int& t1) {
-        while (have) {
-            if (rec.tiles == 0 || h >= H) {
-                ++e;
-                h = 0;
-                have = e < n;
-                if (have) rec = ent[e];
-                continue;
-            }
-            const long long base = rec.begin + (long long)h * (rec.tiles + at_pad(rec.rows <= kAtRows));
-            if (base >= hi) {
-                have = false;
-                break;
-            }
-            t0 = (int)max(0ll, lo - base);
-            t1 = (int)min((long long)rec.tiles, hi - base);
-            head = h++;
-            if (t0 < t1) return true;
-        }
-        return false;
-    }
-};
-
 // ------------------------------------------------------------------ attention
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // One lane of a converged warp, by elect.sync: in a branch on it the compiler knows that one
 // lane runs, and keeps the operands of tensor instructions in uniform registers.  (Behind
 // `lane == 0` every operand of every product moves through a vector register: 95 cycles a
@@ -429,11 +107,6 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t* v) {
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr)
         : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // Registers move from the other warpgroups to the softmax ones (setmaxnreg: the shares add up
@@ -547,9 +220,6 @@ struct StoredTile {
     }
 };
 
-// A row's maximum is raised (and its accumulator rescaled) once a logit passes it by more
-// than this many powers of two: weights stay below 2^8, and bf16 keeps 8 bits of any of them.
-constexpr float kAtSlack = 8.f;
 
 // Two floats at once (packed 32-bit arithmetic).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -708,7 +378,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     it->sees0 = prefix ? e.keys : e.keys - (e.row0 + e.rows - 1) / G;
                     it->absent = (int)absent;
                     // a unit's first part lies in its rows' own places, a continued one in the CTA's
-                    const bool own = e.begin + (long long)f.head * (e.tiles + at_pad(!pair)) >= f.walk.lo;
+                    const bool own = e.begin + (long long)f.head * (e.tiles + at_pad(pair ? kPairs : kSingles)) >= f.walk.lo;
                     it->part = own ? ((prefix ? 0 : a.pool.heads) + (long long)f.head) * all + (long long)e.agent0 * TG + e.row0 + r0
                                    : w.own_rows + (long long)blockIdx.x * (2 * kAtBlock) + (pair ? 0 : kAtBlock) + kAtRows * g;
                 }
@@ -726,15 +396,15 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             Feed f0, f1;
             const AtStart s0 = w.plan->start[0][blockIdx.x], s1 = w.plan->start[1][blockIdx.x],
                           s2 = w.plan->start[2][blockIdx.x];
-            f0.walk.open(s0, w.entries[0], a.pool.heads);
+            f0.walk.open(s0, w.entries[kPairs], a.pool.heads, kPairs);
             advance(f0);
             while (ok && f0.live) {
                 push(f0, 0, true);
                 if (ok) push(f0, 1, true);
                 step(f0, turns[2]);
             }
-            f0.walk.open(s1, w.entries[1], a.pool.heads);
-            f1.walk.open(s2, w.entries[1], a.pool.heads);
+            f0.walk.open(s1, w.entries[kSingles], a.pool.heads, kSingles);
+            f1.walk.open(s2, w.entries[kSingles], a.pool.heads, kSingles);
             advance(f0);
             advance(f1);
             // a group that is done says so at its next turn: the other roles wait for that turn
@@ -1235,18 +905,18 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     struct Place {
         long long own;  // part row of the segment's row 0, first part
         long long i0;   // first piece
-        int n, pair, row0;
+        int n, kind, row0;
     };
     auto find = [&](int s, int r, int seg, int agent0, int seg_rows) {
         Place p = {0, 0, 0, 0, 0};
         const int block = r / kAtBlock;
-        p.pair = seg_rows - block * kAtBlock > kAtRows;
-        const int k = p.pair ? 0 : 1;
+        const int k = at_kind(seg_rows - block * kAtBlock, w.few);
+        p.kind = k;
         const int2 first = w.first[seg];
-        const AtEntry e = w.entries[k][p.pair ? first.x + block : first.y];
+        const AtEntry e = w.entries[k][k == kPairs ? first.x + block : first.y];
         if (e.tiles == 0) return p;
         const long long chunk = w.plan->chunk[k];
-        const long long base = e.begin + (long long)head * (e.tiles + at_pad(!p.pair));
+        const long long base = e.begin + (long long)head * (e.tiles + at_pad(k));
         p.own = (s * H + (long long)head) * all + (long long)agent0 * TG;
         p.i0 = quotient(base, chunk);
         p.n = (int)(quotient(base + e.tiles - 1, chunk) - p.i0) + 1;  // pieces that hold tiles
@@ -1287,8 +957,13 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
                 long long part = p.own + r0;
                 if (j > 0 && in_unit) {
                     const long long i = p.i0 + j;
-                    const int half = !p.pair && i >= w.ctas ? 1 : 0, cta = (int)i - half * w.ctas;
-                    part = w.own_rows + (long long)cta * (2 * kAtBlock) + (p.pair ? 0 : kAtBlock + kAtRows * half) + (r0 - p.row0);
+                    if (p.kind == kFew) {
+                        part = w.few_rows + i * w.few;
+                    } else {
+                        const int half = p.kind == kSingles && i >= w.ctas ? 1 : 0, cta = (int)i - half * w.ctas;
+                        part = w.own_rows + (long long)cta * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half);
+                    }
+                    part += r0 - p.row0;
                 }
                 float wt[RPW];
                 unsigned has[RPW], any = 0;
@@ -1396,6 +1071,10 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ host
+size_t attend_workspace_bytes(int agents, int T, int q_heads, int kv_heads, int head_dim, int groups) {
+    return at_layout(agents, T, q_heads, kv_heads, head_dim, groups).bytes;
+}
+
 template <int F, int D>
 static bool pool_map(CUtensorMap* m, const PoolView& p, int plane, int page) {
     using C = AtCfg<F, D>;
@@ -1410,21 +1089,31 @@ static bool pool_map(CUtensorMap* m, const PoolView& p, int plane, int page) {
 }
 
 template <int F, int D>
-static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
+static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& work, int device, cudaStream_t s) {
     using C = AtCfg<F, D>;
-    CUtensorMap mk, mv;
-    if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;
     cudaError_t e;
-    static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use the shared memory
-    const unsigned long long bit = 1ull << (device & 63);
-    if (!(ready.load(std::memory_order_acquire) & bit) || device > 63) {
-        e = cudaFuncSetAttribute(attend_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_release);
-    }
+    AtWork w = work;
+    w.few_warps = FewCfg<F, D>::warps(w.few == 16 ? 2 : 1);
     if ((e = launch_chained(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
-    if ((e = launch_chained(attend_kernel<F, D>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w)) != cudaSuccess)
-        return e;
+    if (w.many) {
+        CUtensorMap mk, mv;
+        if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;
+        static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use the shared memory
+        const unsigned long long bit = 1ull << (device & 63);
+        if (!(ready.load(std::memory_order_acquire) & bit) || device > 63) {
+            e = cudaFuncSetAttribute(attend_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+            if (e != cudaSuccess) return e;
+            ready.fetch_or(bit, std::memory_order_release);
+        }
+        e = launch_chained(attend_kernel<F, D>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w);
+        if (e != cudaSuccess) return e;
+    }
+    if (w.few > 0) {
+        const dim3 threads(32 * w.few_warps);
+        e = w.few == 8 ? launch_chained(attend_few_kernel<F, D, 1>, dim3(w.ctas), threads, 0, s, a, w)
+                       : launch_chained(attend_few_kernel<F, D, 2>, dim3(w.ctas), threads, 0, s, a, w);
+        if (e != cudaSuccess) return e;
+    }
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;
     // four warps per row while that leaves them all resident at once
     if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
@@ -1448,11 +1137,13 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
     w.plan = (AtPlan*)(base + l.plan);
     w.first = (int2*)(base + l.first);
     w.bounds = (int*)(base + l.bounds);
-    w.entries[0] = (AtEntry*)(base + l.entries[0]);
-    w.entries[1] = (AtEntry*)(base + l.entries[1]);
+    for (int k = 0; k < 3; ++k) w.entries[k] = (AtEntry*)(base + l.entries[k]);
     w.ml = (float2*)(base + l.ml);
     w.o = (float*)(base + l.o);
     w.own_rows = l.own_rows;
+    w.few_rows = l.few_rows;
+    w.few = l.few;
+    w.many = l.many;
     w.ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
     switch (a.pool.format * 2 + (a.pool.dim == 128)) {
         case KVFIX_POOL_BF16 * 2: return launch_attend_form<KVFIX_POOL_BF16, 64>(a, w, dev, s);
