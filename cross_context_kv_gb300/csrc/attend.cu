@@ -901,6 +901,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
         }
         group = lo;
     }
+    const int many_ctas = w.plan->many_ctas;
     // where the parts of row r of a segment (block-wise the same for its neighbours) lie
     struct Place {
         long long own;  // part row of the segment's row 0, first part
@@ -960,7 +961,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
                     if (p.kind == kFew) {
                         part = w.few_rows + i * w.few;
                     } else {
-                        const int half = p.kind == kSingles && i >= w.ctas ? 1 : 0, cta = (int)i - half * w.ctas;
+                        const int half = p.kind == kSingles && i >= many_ctas ? 1 : 0, cta = (int)i - half * many_ctas;
                         part = w.own_rows + (long long)cta * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half);
                     }
                     part += r0 - p.row0;
@@ -1115,10 +1116,10 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& work, i
         if (e != cudaSuccess) return e;
     }
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;
-    // four warps per row while that leaves them all resident at once
-    if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
+    // four warps per row while that leaves them all resident in two turns, one while rows are few
+    if (rows <= (long long)w.ctas * 16) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
     const int tg = a.new_tokens * (a.q_heads / a.pool.heads);
-    if (tg >= 4) {
+    if (tg >= 4 && rows > (long long)w.ctas * 128) {
         const long long warps = (long long)a.agents * a.pool.heads * ((tg + 3) / 4);
         return launch_chained(attend_join_kernel<D, 1, 4>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a, w);
     }

@@ -9,10 +9,10 @@
 // contraction's terms is free, so lane (g = lane / 4, t = lane % 4) loads 16 contiguous bytes of
 // key rows g and g + 8 and takes them as its own terms of consecutive instructions, and of value
 // rows 2t, 2t+1, 2t+8, 2t+9 the same D/8 values, which are its rows of consecutive instructions:
-// every load is as wide as the rows allow, and stored codes become bf16 in the registers that
-// feed the tensor cores.  A logit's key belongs to one lane, so both scales of an e4m3 row are
-// one multiplication each, on the logit and on the weight; maxima are lanes' own until a row's
-// has to be raised.  Weights go from the logits' layout to the operand's by movmatrix.
+// every load is as wide as the rows allow, and stored codes become operands in the registers that
+// feed the tensor cores: int4 as bf16, e4m3 as f16, which holds every code.  A logit's key belongs
+// to one lane, so an e4m3 row's scales are one multiplication of the logit and one exponent added
+// in the weight; maxima are lanes' own until a row's has to be raised.  Weights go from the logits' layout to the operand's by movmatrix.
 //
 // What bounds it: HBM (the next 16 keys' rows are on their way while these are worked on:
 // 4 to 8 KB per warp, 8 or 12 warps per SM), then the conversions of the stored forms.
@@ -22,12 +22,33 @@
 
 namespace kvfix {
 
+// C += A B, bf16 or f16 operands.
+template <bool HALF>
 __device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if constexpr (HALF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 codes to two f16 pairs: every code is an f16 value.
+__device__ __forceinline__ uint2 e4m3x4_to_f16(uint32_t codes) {
+    uint2 y;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+        : "=r"(y.x), "=r"(y.y)
+        : "r"(codes));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
@@ -71,6 +92,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
     using C = FewCfg<F, D>;
     constexpr bool kE4m3 = F == KVFIX_POOL_E4M3, kInt4 = F == KVFIX_POOL_INT4;
     constexpr int KW = C::kKeyBytes / 4, VW = C::kValBytes / 4;
+    constexpr int kScaleBytes = kInt4 ? D / 8 : 1;  // of a row
     constexpr int kSteps = D / 16;  // products of 16 along D; blocks of 16 values of the output
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
@@ -109,48 +131,45 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
             uint32_t s[kInt4 ? 4 : 2];
         } vr;
         int keys_k = 0, keys_v = 0;  // keys there are in the tiles that kr and vr hold
-        const unsigned char* const k0 = a.pool.plane[0].codes + (long long)head * C::kRow;
-        const unsigned char* const v0 = a.pool.plane[1].codes + (long long)head * C::kRow;
+        // this lane's places in a tile's first rows
+        const unsigned char* const k0 = a.pool.plane[0].codes + (long long)head * C::kRow + g * a.pool.ss + t * C::kKeyBytes;
+        const unsigned char* const v0 = a.pool.plane[1].codes + (long long)head * C::kRow + 2 * t * a.pool.ss + g * C::kValBytes;
+        const unsigned char* const ks0 = a.pool.plane[0].scales + ((long long)head * a.pool.slots + g) * kScaleBytes;
+        const unsigned char* const vs0 =
+            a.pool.plane[1].scales + ((long long)head * a.pool.slots + (kInt4 ? 2 * t : g)) * kScaleBytes;
         auto slot_of = [&](int tile, int page) { return (long long)page * a.page + ((tile * 16) & (a.page - 1)); };
         auto load_keys = [&](int tile, int page) {
             keys_k = page >= 0 && page < pool_pages ? min(16, e.keys - tile * 16) : 0;
             const long long slot = slot_of(tile, page);
+            const unsigned char* const p = k0 + slot * a.pool.ss;
+            const unsigned char* const ps = ks0 + slot * kScaleBytes;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int key = g + 8 * r;
-                const bool there = key < keys_k;
-                const unsigned char* p = k0 + (slot + key) * a.pool.ss + t * C::kKeyBytes;
+                const bool there = g + 8 * r < keys_k;
 #pragma unroll
-                for (int i = 0; i < C::kKeyLoads; ++i) load_words<C::kKeyBytes>(kr.x[r][i], p + i * 4 * C::kKeyBytes, there);
-                const long long at = (long long)head * a.pool.slots + slot + key;
-                if (kE4m3) kr.s[r] = there ? __ldg(a.pool.plane[0].scales + at) : 127u;
-                if (kInt4)
-                    kr.s[r] = there ? __ldg(reinterpret_cast<const uint32_t*>(a.pool.plane[0].scales) + at * (D / 32) +
-                                            t * C::kKeyVals / 32)
-                                    : 0u;
+                for (int i = 0; i < C::kKeyLoads; ++i)
+                    load_words<C::kKeyBytes>(kr.x[r][i], p + 8 * r * a.pool.ss + i * 4 * C::kKeyBytes, there);
+                if (kE4m3) kr.s[r] = there ? __ldg(ps + 8 * r) : 127u;
+                if (kInt4) load_words<4>(&kr.s[r], ps + 8 * r * kScaleBytes + t * C::kKeyVals / 32 * 4, there);
             }
         };
         auto load_values = [&](int tile, int page) {
             keys_v = page >= 0 && page < pool_pages ? min(16, e.keys - tile * 16) : 0;
             const long long slot = slot_of(tile, page);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int key = 2 * t + (r & 1) + 8 * (r >> 1);
-                const bool there = key < keys_v;
-                const unsigned char* p = v0 + (slot + key) * a.pool.ss + g * C::kValBytes;
-#pragma unroll
-                for (int i = 0; i < C::kValLoads; ++i) load_words<C::kValBytes>(vr.x[r][i], p + i * 8 * C::kValBytes, there);
-                if (kInt4)
-                    vr.s[r] = there ? __ldg(reinterpret_cast<const uint32_t*>(a.pool.plane[1].scales) +
-                                            ((long long)head * a.pool.slots + slot + key) * (D / 32) + g * C::kValVals / 32)
-                                    : 0u;
-            }
+            const unsigned char* const p = v0 + slot * a.pool.ss;
+            const unsigned char* const ps = vs0 + slot * kScaleBytes;
             if (kE4m3) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int key = g + 8 * r;
-                    vr.s[r] = key < keys_v ? __ldg(a.pool.plane[1].scales + (long long)head * a.pool.slots + slot + key) : 127u;
-                }
+                for (int r = 0; r < 2; ++r) vr.s[r] = g + 8 * r < keys_v ? __ldg(ps + 8 * r) : 127u;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = (r & 1) + 8 * (r >> 1);
+                const bool there = 2 * t + row < keys_v;
+#pragma unroll
+                for (int i = 0; i < C::kValLoads; ++i)
+                    load_words<C::kValBytes>(vr.x[r][i], p + row * a.pool.ss + i * 8 * C::kValBytes, there);
+                if (kInt4) load_words<4>(&vr.s[r], ps + row * kScaleBytes + g * C::kValVals / 32 * 4, there);
             }
         };
         int page = __shfl_sync(0xffffffffu, page_now, 0);
@@ -161,7 +180,9 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
         // queries, and how many keys each of this lane's columns sees
         uint32_t qf[NT][kSteps][2];
         int sees[NT][2];
-        float m[NT][2], l[NT][2], o[kSteps][NT][4];
+        // running maxima of the logits, and of the logits with the values' exponents (e4m3); sums
+        float m[NT][2], my[NT][2], l[NT][2], o[kSteps][NT][4];
+        float unit[NT][2];  // what a product of a query and a key's codes counts, in base-2 logits
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = 8 * n + g;
@@ -176,13 +197,37 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                 qf[n][s][0] = v.x;
                 qf[n][s][1] = v.y;
             }
+            if (kE4m3) {
+                // f16 has the codes exactly, and a query after division by its row's power of two:
+                // 2^12 at its largest, so all 8 bits down to 2^-26 of that, and never infinite
+                uint32_t top = 0;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) top = max(top, max(qf[n][s][x] & 0x7fffu, (qf[n][s][x] >> 16) & 0x7fffu));
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                // exponent field of the largest; an infinity or NaN stays one
+                const int ex = min(max((int)(top >> 7), 16), 254) - 127;
+                const float down0 = pow2f((12 - ex) / 2), down1 = pow2f((12 - ex) - (12 - ex) / 2);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        qf[n][s][x] = pack_f16(__uint_as_float(qf[n][s][x] << 16) * down0 * down1,
+                                               __uint_as_float(qf[n][s][x] & 0xffff0000u) * down0 * down1);
+                // (a column's lanes: its query's power lies in lanes 4 (2t + x) ...)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) unit[n][x] = c * pow2f(__shfl_sync(0xffffffffu, ex - 12, 4 * (2 * t + x)));
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int col = 8 * n + 2 * t + x, rc = e.row0 + col;
                 // a prefix is seen whole; new token i sees the keys up to its own
-                const int back = prefix ? 0 : (e.row0 + e.rows - 1) / G - rc / G;
-                sees[n][x] = col < e.rows ? e.keys - back : 0;
-                m[n][x] = -INFINITY;
+                const int unseen = prefix ? 0 : (e.row0 + e.rows - 1) / G - rc / G;
+                sees[n][x] = col < e.rows ? e.keys - unseen : 0;
+                m[n][x] = my[n][x] = -INFINITY;
+                if (!kE4m3) unit[n][x] = c;
                 l[n][x] = 0.f;
             }
 #pragma unroll
@@ -219,8 +264,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                     for (int r = 0; r < 2; ++r) {
                         const uint32_t word = kr.x[r][i][x];
                         if constexpr (kE4m3) {
-                            const unsigned up = 0x7b807b80u;  // 2^120; the row's scale comes with the logit
-                            const uint2 y = e4m3x4_to_bf16(word, *reinterpret_cast<const __nv_bfloat162*>(&up));
+                            const uint2 y = e4m3x4_to_f16(word);  // (the row's scale comes with the logit)
                             p[r][0] = y.x;
                             p[r][1] = y.y;
                         } else if constexpr (kInt4) {
@@ -240,7 +284,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                             const int st = (i * KW + x) / 2;
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                mma_16816(s[n], kr.x[0][i][x - 1], kr.x[1][i][x - 1], p[0][0], p[1][0], qf[n][st][0], qf[n][st][1]);
+                                mma_16816<kE4m3>(s[n], kr.x[0][i][x - 1], kr.x[1][i][x - 1], p[0][0], p[1][0], qf[n][st][0], qf[n][st][1]);
                         }
                     } else {
 #pragma unroll
@@ -248,32 +292,44 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                             const int st = ((i * KW + x) * kSub + y) / 2;
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                mma_16816(s[n], p[0][y], p[1][y], p[0][y + 1], p[1][y + 1], qf[n][st][0], qf[n][st][1]);
+                                mma_16816<kE4m3>(s[n], p[0][y], p[1][y], p[0][y + 1], p[1][y + 1], qf[n][st][0], qf[n][st][1]);
                         }
                     }
                 }
             const int keys_here = keys_k;
-            float kf[2] = {c, c};
+            float ke[2], ve[2];  // e4m3: the key's factor, the value's exponent
             if (kE4m3) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) kf[r] = kr.s[r] == kE4m3NanByte ? __int_as_float(0x7fffffff) : c * pow2f((int)kr.s[r] - 127);
+                for (int r = 0; r < 2; ++r) {
+                    ke[r] = kr.s[r] == kE4m3NanByte ? __int_as_float(0x7fffffff) : pow2f((int)kr.s[r] - 127);
+                    ve[r] = vr.s[r] == kE4m3NanByte ? __int_as_float(0x7fffffff) : (float)((int)vr.s[r] - 127);
+                }
             }
             if (more) load_keys(tile + 1, page);
             // ---- softmax: key g + 8 (x / 2), column 2t + x % 2
+            // e4m3: weights come with their value row's power of two, against a maximum of their own,
+            // so that the largest summand has f16's full precision whatever the rows' scales are
             bool raise = false;
-            float top[NT][2];
+            float top[NT][2], y[NT][4], top_y[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int key = g + 8 * (x >> 1);
+                    const int r = x >> 1, key = g + 8 * r;
                     const bool seen = key < keys_here && tile * 16 + key < sees[n][x & 1];
-                    s[n][x] = seen ? s[n][x] * kf[x >> 1] : -INFINITY;
+                    float z = s[n][x] * unit[n][x & 1];
+                    if (kE4m3) z *= ke[r];
+                    s[n][x] = seen ? z : -INFINITY;
+                    if (kE4m3) y[n][x] = seen ? z + ve[r] : -INFINITY;
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     top[n][x] = fmaxf(s[n][x], s[n][x + 2]);
                     raise |= top[n][x] > m[n][x] + kAtSlack;
+                    if (kE4m3) {
+                        top_y[n][x] = fmaxf(y[n][x], y[n][x + 2]);
+                        raise |= top_y[n][x] > my[n][x] + kAtSlack;
+                    }
                 }
             }
             if (__any_sync(0xffffffffu, raise)) {
@@ -281,25 +337,30 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        float y = top[n][x];
+                        float f = 1.f, hi = top[n][x], hi_y = kE4m3 ? top_y[n][x] : 0.f;
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-                        if (y > m[n][x]) {
-                            const float f = ex2(m[n][x] - y);  // (0 from -infinity)
-                            m[n][x] = y;
+                        for (int d = 4; d < 32; d <<= 1) {
+                            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+                            if (kE4m3) hi_y = fmaxf(hi_y, __shfl_xor_sync(0xffffffffu, hi_y, d));
+                        }
+                        if (hi > m[n][x]) {
+                            f = ex2(m[n][x] - hi);  // (0 from -infinity)
+                            m[n][x] = hi;
                             l[n][x] *= f;
-#pragma unroll
-                            for (int st = 0; st < kSteps; ++st) {
-                                o[st][n][x] *= f;
-                                o[st][n][x + 2] *= f;
+                        }
+                        if (kE4m3) {
+                            f = 1.f;
+                            if (hi_y > my[n][x]) {
+                                f = ex2(my[n][x] - hi_y);
+                                my[n][x] = hi_y;
                             }
                         }
-                    }
-            }
-            float vf[2] = {1.f, 1.f};
-            if (kE4m3) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) vf[r] = vr.s[r] == kE4m3NanByte ? __int_as_float(0x7fffffff) : pow2f((int)vr.s[r] - 127);
+                        for (int st = 0; st < kSteps; ++st) {
+                            o[st][n][x] *= f;
+                            o[st][n][x + 2] *= f;
+                        }
+                    }
             }
             uint32_t pf[NT][2];
 #pragma unroll
@@ -310,11 +371,12 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                     const float base = m[n][x & 1] == -INFINITY ? 0.f : m[n][x & 1];
                     p[x] = ex2(s[n][x] - base);
                     l[n][x & 1] += p[x];
-                    if (kE4m3 && p[x] != 0.f) p[x] *= vf[x >> 1];  // (a key without weight adds nothing, NaN or not)
+                    // (weights up to 2^8 before a maximum is raised: 2^15 here, of f16's 2^16)
+                    if (kE4m3) p[x] = ex2(y[n][x] - (my[n][x & 1] == -INFINITY ? 0.f : my[n][x & 1] - 7.f));
                 }
-                // bf16 weights: half a step of 2^-8 each, as the values themselves are held
-                pf[n][0] = transpose_8x8(pack_bf16(p[0], p[1]));
-                pf[n][1] = transpose_8x8(pack_bf16(p[2], p[3]));
+                // weights rounded to the operand's type: half a step, 2^-9 of each for bf16, 2^-12 for f16
+                pf[n][0] = transpose_8x8(kE4m3 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
+                pf[n][1] = transpose_8x8(kE4m3 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
             }
             // ---- values: blocks st of 16 rows, this lane's values 2 st and 2 st + 1
 #pragma unroll
@@ -323,15 +385,13 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                 for (int x = 0; x < VW; ++x) {
                     uint32_t w0 = vr.x[0][i][x], w1 = vr.x[1][i][x], w2 = vr.x[2][i][x], w3 = vr.x[3][i][x];
                     if constexpr (kE4m3) {
-                        const unsigned upw = 0x7b807b80u;
-                        const __nv_bfloat162 up = *reinterpret_cast<const __nv_bfloat162*>(&upw);
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             const int st = 2 * (i * VW + x) + y;
-                            const uint2 u = e4m3x4_to_bf16(__byte_perm(w0, w1, y ? 0x7362 : 0x5140), up);
-                            const uint2 v = e4m3x4_to_bf16(__byte_perm(w2, w3, y ? 0x7362 : 0x5140), up);
+                            const uint2 u = e4m3x4_to_f16(__byte_perm(w0, w1, y ? 0x7362 : 0x5140));
+                            const uint2 v = e4m3x4_to_f16(__byte_perm(w2, w3, y ? 0x7362 : 0x5140));
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_16816(o[st][n], u.x, u.y, v.x, v.y, pf[n][0], pf[n][1]);
+                            for (int n = 0; n < NT; ++n) mma_16816<kE4m3>(o[st][n], u.x, u.y, v.x, v.y, pf[n][0], pf[n][1]);
                         }
                     } else if constexpr (kInt4) {
                         uint4 y[4];
@@ -352,14 +412,14 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                             const uint32_t a0 = __byte_perm(p0, p1, 0x5410), a1 = __byte_perm(p0, p1, 0x7632);
                             const uint32_t a2 = __byte_perm(p2, p3, 0x5410), a3 = __byte_perm(p2, p3, 0x7632);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_16816(o[st][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                            for (int n = 0; n < NT; ++n) mma_16816<kE4m3>(o[st][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
                         }
                     } else {
                         const int st = i * VW + x;
                         const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
                         const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_16816(o[st][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                        for (int n = 0; n < NT; ++n) mma_16816<kE4m3>(o[st][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
                     }
                 }
             if (more) load_values(tile + 1, page);
@@ -378,6 +438,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                 for (int d = 4; d < 32; d <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], d);
                 if (col >= e.rows) continue;
                 if (g == 0) w.ml[part + col] = make_float2(m[n][x], l[n][x]);
+                const float f = !kE4m3 ? 1.f : my[n][x] == -INFINITY ? 1.f : ex2(my[n][x] - 7.f - m[n][x]);
                 float* dst = w.o + (part + col) * D + g * C::kValVals;
 #pragma unroll
                 for (int i = 0; i < C::kValLoads; ++i)
@@ -385,7 +446,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                     for (int v = 0; v < C::kValVals; v += 4) {
                         const int st = (i * C::kValVals + v) / 2;
                         *reinterpret_cast<float4*>(dst + i * 8 * C::kValVals + v) =
-                            make_float4(o[st][n][x], o[st][n][x + 2], o[st + 1][n][x], o[st + 1][n][x + 2]);
+                            make_float4(o[st][n][x] * f, o[st][n][x + 2] * f, o[st + 1][n][x] * f, o[st + 1][n][x + 2] * f);
                     }
             }
     }

@@ -53,6 +53,7 @@ struct __align__(16) AtStart {
 
 struct AtPlan {
     long long chunk[3];            // by kind: length of a piece of the line
+    int many_ctas;                 // CTAs that pairs and singles are cut for; the few-row blocks have the others
     AtStart start[4][kAtMaxCtas];  // pairs, singles of group 0, of group 1, few-row blocks
 };
 
@@ -261,16 +262,27 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         w.first[s] = first;
     }
     __syncthreads();
-    const int few_pieces = w.ctas * w.few_warps;
-    const long long chunk[3] = {max(1ll, quotient(total.line[0] + w.ctas - 1, w.ctas)),
-                                max(1ll, quotient(total.line[1] + 2 * w.ctas - 1, 2 * w.ctas)),
+    // The two kernels share the GPU: CTAs of the first that have no piece end at once, and the
+    // second's take their places.  128 keys cost a CTA of the first about as long as one of the
+    // second where both are bound by memory (bf16), twice that where it converts whole tiles.
+    const long long cost_many = (total.line[kPairs] + total.line[kSingles]) * (a.pool.format == KVFIX_POOL_BF16 ? 2 : 8);
+    const long long cost_few = 3 * total.line[kFew] / (kAtKeys / at_keys(kFew));
+    int nm = w.ctas, nf = w.ctas;
+    if (cost_many > 0 && total.line[kFew] > 0) {
+        nm = (int)((float)w.ctas * ((float)cost_many / (float)(cost_many + cost_few)) + 0.5f);
+        nm = min(max(nm, 1), w.ctas - 1);
+        nf = w.ctas - nm;
+    }
+    const int few_pieces = nf * w.few_warps;
+    const long long chunk[3] = {max(1ll, quotient(total.line[0] + nm - 1, nm)),
+                                max(1ll, quotient(total.line[1] + 2 * nm - 1, 2 * nm)),
                                 max(1ll, quotient(total.line[2] + few_pieces - 1, few_pieces))};
     // (a few-row CTA has its warps' pieces as one)
     for (int i = tid; i < 4 * w.ctas; i += kPlanThreads) {
         const int cta = i % w.ctas, set = i / w.ctas, k = set == 0 ? kPairs : set == 3 ? kFew : kSingles;
         AtStart* st = &w.plan->start[set][cta];
         const long long size = k == kFew ? chunk[kFew] * w.few_warps : k == kSingles ? chunk[kSingles] : chunk[kPairs];
-        const long long lo = size * (set == 2 ? cta + w.ctas : cta);
+        const long long lo = k != kFew && cta >= nm ? total.line[k] : size * (set == 2 ? cta + nm : cta);
         if (lo >= total.line[k]) {
             st->have = 0;
             continue;
@@ -296,6 +308,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         *st = r;
     }
     if (tid < 3) w.plan->chunk[tid] = tid == 0 ? chunk[0] : tid == 1 ? chunk[1] : chunk[2];
+    if (tid == 0) w.plan->many_ctas = nm;
     if (bad) atomicOr(&g_status_attend, FLAG_BOUNDS);
 }
 
