@@ -1089,30 +1089,41 @@ static bool pool_map(CUtensorMap* m, const PoolView& p, int plane, int page) {
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A kernel's dynamic shared memory, once per device (a form has one kernel of each K).
+template <int F, int D, int K, typename Kernel>
+static cudaError_t allow_smem(Kernel* kernel, int bytes, int device) {
+    static std::atomic<unsigned long long> ready{0};
+    const unsigned long long bit = 1ull << (device & 63);
+    if ((ready.load(std::memory_order_acquire) & bit) && device <= 63) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <int F, int D, int NT>
+static cudaError_t launch_few(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
+    using C = FewCfg<F, D, NT>;
+    const cudaError_t e = allow_smem<F, D, NT>(attend_few_kernel<F, D, NT>, C::kSmem, device);
+    if (e != cudaSuccess) return e;
+    return launch_chained(attend_few_kernel<F, D, NT>, dim3(w.ctas), dim3(32 * C::kWarps), C::kSmem, s, a, w);
+}
+
 template <int F, int D>
 static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& work, int device, cudaStream_t s) {
     using C = AtCfg<F, D>;
     cudaError_t e;
     AtWork w = work;
-    w.few_warps = FewCfg<F, D>::warps(w.few == 16 ? 2 : 1);
+    w.few_warps = w.few == 16 ? FewCfg<F, D, 2>::kWarps : FewCfg<F, D, 1>::kWarps;
     if ((e = launch_chained(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
     if (w.many) {
         CUtensorMap mk, mv;
         if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;
-        static std::atomic<unsigned long long> ready{0};  // devices whose kernel may use the shared memory
-        const unsigned long long bit = 1ull << (device & 63);
-        if (!(ready.load(std::memory_order_acquire) & bit) || device > 63) {
-            e = cudaFuncSetAttribute(attend_kernel<F, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-            if (e != cudaSuccess) return e;
-            ready.fetch_or(bit, std::memory_order_release);
-        }
+        if ((e = allow_smem<F, D, 0>(attend_kernel<F, D>, C::kSmem, device)) != cudaSuccess) return e;
         e = launch_chained(attend_kernel<F, D>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w);
         if (e != cudaSuccess) return e;
     }
     if (w.few > 0) {
-        const dim3 threads(32 * w.few_warps);
-        e = w.few == 8 ? launch_chained(attend_few_kernel<F, D, 1>, dim3(w.ctas), threads, 0, s, a, w)
-                       : launch_chained(attend_few_kernel<F, D, 2>, dim3(w.ctas), threads, 0, s, a, w);
+        e = w.few == 8 ? launch_few<F, D, 1>(a, w, device, s) : launch_few<F, D, 2>(a, w, device, s);
         if (e != cudaSuccess) return e;
     }
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;

@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
-template <int F, int D>
+template <int F, int D, int NT>
 struct FewCfg {
     static constexpr int kRow = F == KVFIX_POOL_BF16 ? 2 * D : F == KVFIX_POOL_E4M3 ? D : D / 2;  // bytes
     static constexpr int kKeyBytes = kRow / 4 < 16 ? kRow / 4 : 16;   // of one load of a key row
@@ -66,33 +66,51 @@ struct FewCfg {
     static constexpr int kValBytes = kRow / 8 < 16 ? kRow / 8 : 16;
     static constexpr int kValLoads = kRow / 8 / kValBytes;
     static constexpr int kValVals = kValBytes * D / kRow;
-    // Rows on their way take 64 registers a lane of bf16, at most 32 of the stored forms, and 16
-    // queries' output and operands twice those of 8: 8 warps where 12 do not fit the registers.
-    static constexpr int warps(int nt) { return F == KVFIX_POOL_BF16 || (nt == 2 && D == 128) ? 8 : kFewWarps; }
+    static constexpr int kScaleBytes = F == KVFIX_POOL_E4M3 ? 1 : F == KVFIX_POOL_INT4 ? D / 8 : 0;  // of a row
+    // A warp's ring of tiles on their way: codes as the lanes copied them, then scales by key.
+    static constexpr int kKeyPart = 16 * kRow, kScalePart = 16 * kScaleBytes;
+    static constexpr int kStage = 2 * kKeyPart + 2 * kScalePart;
+    static constexpr int kStages = F == KVFIX_POOL_BF16 && D == 128 ? 3 : 4;
+    // (16 queries' output and operands take twice the registers of 8)
+    static constexpr int kWarps = D == 128 && (F == KVFIX_POOL_BF16 || NT == 2) ? 8 : kFewWarps;
+    static constexpr int kSmem = kWarps * kStages * kStage;
 };
 
-// N (4, 8, 16) bytes as 32-bit words; nothing is read, and zeros come, where `there` is false.
+// N (4, 8, 16) bytes from global to shared memory; nothing is read, and zeros come, where `there`
+// is false.
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t* w, const unsigned char* p, bool there) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const unsigned char* src, bool there) {
+    const int n = there ? N : 0;
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void read_words(uint32_t* w, const unsigned char* p) {
     if constexpr (N == 16) {
-        const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else if constexpr (N == 8) {
-        const uint2 v = there ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
         w[0] = v.x, w[1] = v.y;
     } else {
-        w[0] = there ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
 }
 
 // NT: groups of 8 queries.
 template <int F, int D, int NT>
-__global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
+__global__ void __launch_bounds__(32 * FewCfg<F, D, NT>::kWarps, 1)
     attend_few_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ AtWork w) {
-    using C = FewCfg<F, D>;
+    using C = FewCfg<F, D, NT>;
     constexpr bool kE4m3 = F == KVFIX_POOL_E4M3, kInt4 = F == KVFIX_POOL_INT4;
     constexpr int KW = C::kKeyBytes / 4, VW = C::kValBytes / 4;
-    constexpr int kScaleBytes = kInt4 ? D / 8 : 1;  // of a row
+    constexpr int kScaleBytes = C::kScaleBytes;
+    extern __shared__ __align__(128) unsigned char few_smem[];
+    unsigned char* const ring = few_smem + (threadIdx.x >> 5) * (C::kStages * C::kStage);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     constexpr int kSteps = D / 16;  // products of 16 along D; blocks of 16 values of the output
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
@@ -106,7 +124,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
     AtWalk walk;
     walk.open(w.plan->start[3][blockIdx.x], w.entries[kFew], a.pool.heads, kFew);
     const long long piece = w.plan->chunk[kFew];
-    const long long slot_row = w.few_rows + ((long long)blockIdx.x * C::warps(NT) + warp) * w.few;
+    const long long slot_row = w.few_rows + ((long long)blockIdx.x * C::kWarps + warp) * w.few;
     walk.lo += piece * warp;
     walk.hi = min(walk.hi, walk.lo + piece);
     int head, t0, t1;
@@ -122,60 +140,52 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
         };
         int page_now = fetch_pages(t0), page_next = fetch_pages(t0 + 32);
 
-        struct Keys {
-            uint32_t x[2][C::kKeyLoads][KW];
-            uint32_t s[2];
-        } kr;
-        struct Values {
-            uint32_t x[4][C::kValLoads][VW];
-            uint32_t s[kInt4 ? 4 : 2];
-        } vr;
-        int keys_k = 0, keys_v = 0;  // keys there are in the tiles that kr and vr hold
         // this lane's places in a tile's first rows
         const unsigned char* const k0 = a.pool.plane[0].codes + (long long)head * C::kRow + g * a.pool.ss + t * C::kKeyBytes;
         const unsigned char* const v0 = a.pool.plane[1].codes + (long long)head * C::kRow + 2 * t * a.pool.ss + g * C::kValBytes;
-        const unsigned char* const ks0 = a.pool.plane[0].scales + ((long long)head * a.pool.slots + g) * kScaleBytes;
-        const unsigned char* const vs0 =
-            a.pool.plane[1].scales + ((long long)head * a.pool.slots + (kInt4 ? 2 * t : g)) * kScaleBytes;
-        auto slot_of = [&](int tile, int page) { return (long long)page * a.page + ((tile * 16) & (a.page - 1)); };
-        auto load_keys = [&](int tile, int page) {
-            keys_k = page >= 0 && page < pool_pages ? min(16, e.keys - tile * 16) : 0;
-            const long long slot = slot_of(tile, page);
-            const unsigned char* const p = k0 + slot * a.pool.ss;
-            const unsigned char* const ps = ks0 + slot * kScaleBytes;
+        // its 16 bytes of a tile's scales: keys' then values' (lanes beyond have none)
+        constexpr int kScaleCopies = C::kScalePart / 16;
+        const unsigned char* const s0 = a.pool.plane[lane >= kScaleCopies].scales + (long long)head * a.pool.slots * kScaleBytes +
+                                        (lane >= kScaleCopies ? lane - kScaleCopies : lane) * 16;
+        unsigned gone = 0;  // by tile mod 32: a tile on its way whose page is not there
+        auto load = [&](int tile) {
+            const int at = tile - t0;
+            if (tile < t1) {
+                if ((at & 31) == 0 && at > 0) {
+                    page_now = page_next;
+                    page_next = fetch_pages(tile + 32);
+                }
+                const int page = __shfl_sync(0xffffffffu, page_now, at & 31);
+                const bool stray = page < 0 || page >= pool_pages;
+                bad |= stray;
+                gone = (gone & ~(1u << (tile & 31))) | ((stray ? 1u : 0u) << (tile & 31));
+                const int keys = stray ? 0 : min(16, e.keys - tile * 16);
+                const long long slot = stray ? 0 : (long long)page * a.page + ((tile * 16) & (a.page - 1));
+                const uint32_t dst = ring_at + at % C::kStages * C::kStage;
+                const unsigned char* const pk = k0 + slot * a.pool.ss;
+                const unsigned char* const pv = v0 + slot * a.pool.ss;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const bool there = g + 8 * r < keys_k;
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int i = 0; i < C::kKeyLoads; ++i)
-                    load_words<C::kKeyBytes>(kr.x[r][i], p + 8 * r * a.pool.ss + i * 4 * C::kKeyBytes, there);
-                if (kE4m3) kr.s[r] = there ? __ldg(ps + 8 * r) : 127u;
-                if (kInt4) load_words<4>(&kr.s[r], ps + 8 * r * kScaleBytes + t * C::kKeyVals / 32 * 4, there);
+                    for (int i = 0; i < C::kKeyLoads; ++i)
+                        copy_async<C::kKeyBytes>(dst + (r * C::kKeyLoads + i) * 32 * C::kKeyBytes + lane * C::kKeyBytes,
+                                                 pk + 8 * r * a.pool.ss + i * 4 * C::kKeyBytes, g + 8 * r < keys);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = (r & 1) + 8 * (r >> 1);
+#pragma unroll
+                    for (int i = 0; i < C::kValLoads; ++i)
+                        copy_async<C::kValBytes>(dst + C::kKeyPart + (r * C::kValLoads + i) * 32 * C::kValBytes + lane * C::kValBytes,
+                                                 pv + row * a.pool.ss + i * 8 * C::kValBytes, 2 * t + row < keys);
+                }
+                if (kScaleCopies > 0 && lane < 2 * kScaleCopies)
+                    copy_async<16>(dst + 2 * C::kKeyPart + lane * 16, s0 + slot * kScaleBytes, true);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto load_values = [&](int tile, int page) {
-            keys_v = page >= 0 && page < pool_pages ? min(16, e.keys - tile * 16) : 0;
-            const long long slot = slot_of(tile, page);
-            const unsigned char* const p = v0 + slot * a.pool.ss;
-            const unsigned char* const ps = vs0 + slot * kScaleBytes;
-            if (kE4m3) {
+        __syncwarp();
 #pragma unroll
-                for (int r = 0; r < 2; ++r) vr.s[r] = g + 8 * r < keys_v ? __ldg(ps + 8 * r) : 127u;
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = (r & 1) + 8 * (r >> 1);
-                const bool there = 2 * t + row < keys_v;
-#pragma unroll
-                for (int i = 0; i < C::kValLoads; ++i)
-                    load_words<C::kValBytes>(vr.x[r][i], p + row * a.pool.ss + i * 8 * C::kValBytes, there);
-                if (kInt4) load_words<4>(&vr.s[r], ps + row * kScaleBytes + g * C::kValVals / 32 * 4, there);
-            }
-        };
-        int page = __shfl_sync(0xffffffffu, page_now, 0);
-        bad |= page < 0 || page >= pool_pages;
-        load_keys(t0, page);
-        load_values(t0, page);
+        for (int i = 0; i < C::kStages - 1; ++i) load(t0 + i);
 
         // queries, and how many keys each of this lane's columns sees
         uint32_t qf[NT][kSteps][2];
@@ -238,15 +248,28 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
 
 #pragma unroll 1
         for (int tile = t0; tile < t1; ++tile) {
-            // the next tile's page
-            const int next = tile + 1 - t0;
-            if ((next & 31) == 0) {
-                page_now = page_next;
-                page_next = fetch_pages(tile + 1 + 32);
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+            __syncwarp();  // the scales come from several lanes; and the tile before is read by all
+            load(tile + C::kStages - 1);
+            const unsigned char* const st_k = ring + (tile - t0) % C::kStages * C::kStage;
+            const unsigned char* const st_v = st_k + C::kKeyPart;
+            const unsigned char* const st_s = st_k + 2 * C::kKeyPart;
+            const int keys_here = (gone >> (tile & 31)) & 1u ? 0 : min(16, e.keys - tile * 16);
+            uint32_t ksz[2], vsz[4];
+            if (kInt4) {
+                // (rows that are not there are zeros, whatever their scales hold)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    read_words<4>(&ksz[r], st_s + (g + 8 * r) * kScaleBytes + t * C::kKeyVals / 32 * 4);
+                    if (g + 8 * r >= keys_here) ksz[r] = 0;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int key = 2 * t + (r & 1) + 8 * (r >> 1);
+                    read_words<4>(&vsz[r], st_s + C::kScalePart + key * kScaleBytes + g * C::kValVals / 32 * 4);
+                    if (key >= keys_here) vsz[r] = 0;
+                }
             }
-            page = __shfl_sync(0xffffffffu, page_now, next & 31);
-            const bool more = tile + 1 < t1;
-            if (more) bad |= page < 0 || page >= pool_pages;
 
             float s[NT][4];
 #pragma unroll
@@ -255,20 +278,24 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                 for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
             // ---- logits
 #pragma unroll
-            for (int i = 0; i < C::kKeyLoads; ++i)
+            for (int i = 0; i < C::kKeyLoads; ++i) {
+                uint32_t kx[2][KW];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    read_words<C::kKeyBytes>(kx[r], st_k + (r * C::kKeyLoads + i) * 32 * C::kKeyBytes + lane * C::kKeyBytes);
 #pragma unroll
                 for (int x = 0; x < KW; ++x) {
                     constexpr int kSub = F == KVFIX_POOL_BF16 ? 1 : kE4m3 ? 2 : 4;  // pairs in a word
                     uint32_t p[2][kSub];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const uint32_t word = kr.x[r][i][x];
+                        const uint32_t word = kx[r][x];
                         if constexpr (kE4m3) {
                             const uint2 y = e4m3x4_to_f16(word);  // (the row's scale comes with the logit)
                             p[r][0] = y.x;
                             p[r][1] = y.y;
                         } else if constexpr (kInt4) {
-                            const unsigned ss = __byte_perm(kr.s[r], 0u, 0x1010), zz = __byte_perm(kr.s[r], 0u, 0x3232);
+                            const unsigned ss = __byte_perm(ksz[r], 0u, 0x1010), zz = __byte_perm(ksz[r], 0u, 0x3232);
                             const uint4 y = int4x8_to_bf16(word, *reinterpret_cast<const __nv_bfloat162*>(&ss),
                                                            *reinterpret_cast<const __nv_bfloat162*>(&zz));
                             p[r][0] = y.x;
@@ -284,7 +311,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                             const int st = (i * KW + x) / 2;
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                mma_16816<kE4m3>(s[n], kr.x[0][i][x - 1], kr.x[1][i][x - 1], p[0][0], p[1][0], qf[n][st][0], qf[n][st][1]);
+                                mma_16816<kE4m3>(s[n], kx[0][x - 1], kx[1][x - 1], p[0][0], p[1][0], qf[n][st][0], qf[n][st][1]);
                         }
                     } else {
 #pragma unroll
@@ -296,16 +323,16 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                         }
                     }
                 }
-            const int keys_here = keys_k;
+            }
             float ke[2], ve[2];  // e4m3: the key's factor, the value's exponent
             if (kE4m3) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    ke[r] = kr.s[r] == kE4m3NanByte ? __int_as_float(0x7fffffff) : pow2f((int)kr.s[r] - 127);
-                    ve[r] = vr.s[r] == kE4m3NanByte ? __int_as_float(0x7fffffff) : (float)((int)vr.s[r] - 127);
+                    const int kb = st_s[g + 8 * r], vb = st_s[C::kScalePart + g + 8 * r];
+                    ke[r] = kb == (int)kE4m3NanByte ? __int_as_float(0x7fffffff) : pow2f(kb - 127);
+                    ve[r] = vb == (int)kE4m3NanByte ? __int_as_float(0x7fffffff) : (float)(vb - 127);
                 }
             }
-            if (more) load_keys(tile + 1, page);
             // ---- softmax: key g + 8 (x / 2), column 2t + x % 2
             // e4m3: weights come with their value row's power of two, against a maximum of their own,
             // so that the largest summand has f16's full precision whatever the rows' scales are
@@ -380,10 +407,14 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
             }
             // ---- values: blocks st of 16 rows, this lane's values 2 st and 2 st + 1
 #pragma unroll
-            for (int i = 0; i < C::kValLoads; ++i)
+            for (int i = 0; i < C::kValLoads; ++i) {
+                uint32_t vx[4][VW];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    read_words<C::kValBytes>(vx[r], st_v + (r * C::kValLoads + i) * 32 * C::kValBytes + lane * C::kValBytes);
 #pragma unroll
                 for (int x = 0; x < VW; ++x) {
-                    uint32_t w0 = vr.x[0][i][x], w1 = vr.x[1][i][x], w2 = vr.x[2][i][x], w3 = vr.x[3][i][x];
+                    const uint32_t w0 = vx[0][x], w1 = vx[1][x], w2 = vx[2][x], w3 = vx[3][x];
                     if constexpr (kE4m3) {
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
@@ -398,7 +429,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                         const uint32_t ww[4] = {w0, w1, w2, w3};
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const unsigned ss = __byte_perm(vr.s[r], 0u, 0x1010), zz = __byte_perm(vr.s[r], 0u, 0x3232);
+                            const unsigned ss = __byte_perm(vsz[r], 0u, 0x1010), zz = __byte_perm(vsz[r], 0u, 0x3232);
                             y[r] = int4x8_to_bf16(ww[r], *reinterpret_cast<const __nv_bfloat162*>(&ss),
                                                   *reinterpret_cast<const __nv_bfloat162*>(&zz));
                         }
@@ -422,7 +453,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D>::warps(NT), 1)
                         for (int n = 0; n < NT; ++n) mma_16816<kE4m3>(o[st][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
                     }
                 }
-            if (more) load_values(tile + 1, page);
+            }
         }
 
         // ---- the part: the sums over the lanes of a column, then values as the lanes hold them

@@ -263,13 +263,17 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     }
     __syncthreads();
     // The two kernels share the GPU: CTAs of the first that have no piece end at once, and the
-    // second's take their places.  128 keys cost a CTA of the first about as long as one of the
-    // second where both are bound by memory (bf16), twice that where it converts whole tiles.
-    const long long cost_many = (total.line[kPairs] + total.line[kSingles]) * (a.pool.format == KVFIX_POOL_BF16 ? 2 : 8);
-    const long long cost_few = 3 * total.line[kFew] / (kAtKeys / at_keys(kFew));
+    // second's take their places.  The split has both end together, from what 128 keys cost a CTA
+    // of each and what the first takes before and after its tiles, in microseconds as measured:
+    // F + X / n = Y / (ctas - n), solved for n.
     int nm = w.ctas, nf = w.ctas;
-    if (cost_many > 0 && total.line[kFew] > 0) {
-        nm = (int)((float)w.ctas * ((float)cost_many / (float)(cost_many + cost_few)) + 0.5f);
+    if (total.line[kPairs] + total.line[kSingles] > 0 && total.line[kFew] > 0) {
+        const bool stored = a.pool.format != KVFIX_POOL_BF16;
+        const float F = 4.f, S = (float)w.ctas;
+        const float X = (stored ? 2.5f : 1.6f) * (float)(total.line[kPairs] + total.line[kSingles]);
+        const float Y = (stored ? 1.1f : 1.5f) * (float)total.line[kFew] / (float)(kAtKeys / at_keys(kFew));
+        const float B = F * S - X - Y;
+        nm = (int)((B + sqrtf(B * B + 4.f * F * X * S)) / (2.f * F) + 0.5f);
         nm = min(max(nm, 1), w.ctas - 1);
         nf = w.ctas - nm;
     }
