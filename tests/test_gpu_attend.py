@@ -158,6 +158,87 @@ def test_attention(kvfix, fmt, name):
     r.check(out, lse)
 
 
+# blocks of 8, 16 and more rows, own and shared: each size goes its own way through the kernels
+FEW = {
+    "eight_rows": (2, 4, 128, 16, 1, [90], [0, 2], [33, 70]),
+    "sixteen_rows": (2, 8, 128, 16, 1, [100], [0, 2], [33, 70]),
+    "sixteen_of_one": (2, 4, 64, 16, 4, [50], [0, 1], [20]),
+    "nine_then_eighteen": (1, 3, 64, 32, 3, [77], [0, 2], [3, 50]),
+    "sixteen_then_many": (1, 4, 128, 64, 4, [200], [0, 20], [4 + 9 * i for i in range(20)]),
+    "seventeen_rows": (1, 17, 64, 16, 1, [40], [0, 1], [30]),
+    "own_alone": (2, 4, 128, 32, 1, [], [], [37 * i % 500 for i in range(24)]),
+    "own_long": (1, 8, 64, 128, 1, [], [], [20000, 1, 15]),
+    "a_last_block_of_few": (1, 8, 64, 16, 1, [300], [0, 33], [5] * 33),
+}
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", list(FEW))
+def test_few_rows(kvfix, fmt, name):
+    r = Round(kvfix, fmt, *FEW[name], seed=len(name))
+    out, lse = r.call()
+    kvfix.check_status()
+    r.check(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("heads,group", ((2, 4), (1, 24)))
+def test_scales_far_apart(kvfix, heads, group):
+    """e4m3 rows whose scales differ by many powers of two, queries that undo the keys'."""
+    r = Round(kvfix, "e4m3", heads, group, 128, 16, 1, [200], [0, 3], [30, 77, 5])
+    rng = np.random.default_rng(3)
+    used = (r.pool.k_scales[0] != 0xFF).cpu().numpy()            # [heads][slots]
+    shift = np.where(used, rng.integers(-50, 51, used.shape), 0)
+    v = r.pool.v_scales[0].cpu().numpy().astype(np.int64) + shift
+    r.pool.v_scales[0] = torch.from_numpy(v.astype(np.uint8)).cuda()
+    k = r.pool.k_scales[0].cpu().numpy().astype(np.int64) - np.where(used, 40, 0)
+    r.pool.k_scales[0] = torch.from_numpy(k.astype(np.uint8)).cuda()
+    r.q.mul_(2.0 ** 40)
+    r.q_words = words_of(r.q)
+    out, lse = r.call()
+    kvfix.check_status()
+    r.check(out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ("bf16", "e4m3"))
+@pytest.mark.parametrize("group", (3, 24))
+def test_a_row_of_nan_reaches_its_own_queries_alone(kvfix, fmt, group):
+    r = Round(kvfix, fmt, 2, group, 64, 16, 1, [40], [0, 2], [30, 21])
+    want, want_lse = r.call()
+    at = int(r.rows(r.tables[1][1], 21)[7])
+    for plane, scales in (("k", "k_scales"), ("v", "v_scales")):
+        t = getattr(r.pool, plane if fmt == "bf16" else scales)
+        where = (0, at, 1) if fmt == "bf16" else (0, 1, at)
+        was = t[where].clone()
+        t[where] = float("nan") if fmt == "bf16" else 0xFF       # key 7 of agent 1, KV head 1
+        out, lse = r.call()
+        kvfix.check_status()
+        t[where] = was
+        assert torch.isnan(out[1, :, group:].float()).all()
+        assert torch.isnan(lse[1, :, group:]).all() if plane == "k" else torch.equal(lse, want_lse)
+        out[1, :, group:], lse[1, :, group:] = want[1, :, group:], want_lse[1, :, group:]
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("group,new", ((4, 1), (5, 2), (6, 4)))
+def test_same_bits_every_time(kvfix, fmt, group, new):
+    """Many short units on every SM, again and again: nothing depends on who comes first."""
+    own = [new + 53 * i % 700 for i in range(24)]
+    r = Round(kvfix, fmt, 8, group, 128, 16, new, [900, 300], [0, 16, 24], own)
+    first = None
+    for _ in range(60):
+        out, lse = r.call()
+        kvfix.check_status()
+        if first is None:
+            first = out, lse
+        assert torch.equal(out.view(torch.int16), first[0].view(torch.int16))
+        assert torch.equal(lse.view(torch.int32), first[1].view(torch.int32))
+
+
 @gpu
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_same_bits_whatever_the_workspace_holds(kvfix, fmt):
