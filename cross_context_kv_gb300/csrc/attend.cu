@@ -10,20 +10,24 @@
 // anywhere.
 //
 // Work.  An entry is a block of up to 256 rows of a segment; a unit is an entry and a KV
-// head; its work is ceil(keys / 128) tiles of 128 keys (causally trimmed), plus a few for its
-// fixed cost.  One plan kernel lays all units on a line; CTA i of the persistent grid takes
-// the i-th equal piece of it, whole units and parts of units alike, and writes one part per
-// unit it touches; the join kernel finds a row's parts from the same line.  Everything
-// depends on lengths that lie on the device, so a captured graph follows them.
+// head; its work is its keys in tiles (causally trimmed), plus a few tiles for its fixed cost.
+// One plan kernel lays all units on lines and cuts the lines into equal pieces
+// (attend_plan.cuh); a worker writes one part per unit that its piece touches, and the join
+// kernel finds a row's parts from the same lines.  Blocks of up to 16 rows go to a kernel
+// without tensor memory (attend_few.cuh), the others to the one below.  Everything depends on
+// lengths that lie on the device, so a captured graph follows them.
 //
-// The attention kernel is bound by HBM for decode (a group's rows fill up to 256 lanes of the
-// MMA per key read) and by the tensor pipe and the exponentials for many new tokens:
+// What bounds the kernel below: HBM for bf16 prefixes of a decoding round (131072 keys and
+// 128 rows of 8 heads: 537 MB in 95 us, 5.6 TB/s), the conversion of stored tiles and the chain
+// from logits to weights for e4m3 and int4 (138 us for the same keys as e4m3), the
+// exponentials and the tensor pipe for many new tokens (0.89 PFLOP/s):
 //   warps 0-3, 4-7  softmax: each group owns one 128-row accumulator.  Blocks of more than
-//                   128 rows give each group its half of the rows and both use every tile;
-//                   smaller blocks give both groups the same rows and alternate tiles.  A
-//                   thread owns a row (a TMEM lane): no cross-lane reduction.
-//   warp 10         scheduler: walks the CTA's pieces of the line, reads the page lists and hands
-//                   each tile of either group to the other roles.
+//                   128 rows (pairs) give each group its half of the rows, and both use every
+//                   tile; smaller ones (singles) are one group's alone, and the two groups
+//                   walk pieces of their own.  A thread owns a row (a TMEM lane): no
+//                   cross-lane reduction.
+//   warp 10         scheduler: walks the CTA's pieces of the lines, reads the page lists and
+//                   hands each tile of either group to the other roles.
 //   warp 8          TMA producer: pages of K and V tiles (128 keys x D) into their rings.
 //   warps 9, 11     one per softmax group: loads a unit's queries and issues tcgen05.mma,
 //                   S = Q K^T (both K-major in shared memory), and O += P V with P from tensor
@@ -31,6 +35,9 @@
 //   warps 12-19     (stored forms) converters: code tiles and their scales, loaded as they lie,
 //                   to bf16 tiles for the MMA; four warps for keys, four for values.
 // S occupies 128 TMEM columns per group, P (bf16) overwrites the first half of S, O takes D.
+// (e4m3 codes as operands of 8-bit products, with queries in two pieces and the scales on the
+// logits, are right too and were slower: 186 us against 169 for the e4m3 case above, as the
+// softmax warps, which are the bound, get the factors' work.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

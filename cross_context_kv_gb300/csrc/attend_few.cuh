@@ -5,17 +5,22 @@
 // matrix instruction, queries along its 8 columns) and the output O^T = V^T P^T, so few queries
 // leave nothing of an instruction empty that costs more than the keys' own loading.
 //
-// Layout.  A warp takes 16 keys at a time, alone: no shared memory, no barrier.  The order of a
-// contraction's terms is free, so lane (g = lane / 4, t = lane % 4) loads 16 contiguous bytes of
-// key rows g and g + 8 and takes them as its own terms of consecutive instructions, and of value
-// rows 2t, 2t+1, 2t+8, 2t+9 the same D/8 values, which are its rows of consecutive instructions:
-// every load is as wide as the rows allow, and stored codes become operands in the registers that
-// feed the tensor cores: int4 as bf16, e4m3 as f16, which holds every code.  A logit's key belongs
-// to one lane, so an e4m3 row's scales are one multiplication of the logit and one exponent added
-// in the weight; maxima are lanes' own until a row's has to be raised.  Weights go from the logits' layout to the operand's by movmatrix.
+// Layout.  A warp takes 16 keys at a time, alone, without barriers.  The order of a
+// contraction's terms is free, so lane (g = lane / 4, t = lane % 4) takes up to 16 contiguous
+// bytes of key rows g and g + 8 as its own terms of consecutive instructions, and of value rows
+// 2t, 2t+1, 2t+8, 2t+9 the same D/8 values, which are its rows of consecutive instructions:
+// copies are as wide as the rows allow, a lane reads from shared memory only what it copied
+// there itself (scales excepted), and stored codes become operands in the registers that feed
+// the tensor cores: int4 as bf16, e4m3 as f16, which holds every code.  A logit's key belongs
+// to one lane, so an e4m3 row's scales are one multiplication of the logit and one exponent
+// added in the weight; maxima are lanes' own until a row's has to be raised.  Weights go from
+// the logits' layout to the operand's by movmatrix.
 //
-// What bounds it: HBM (the next 16 keys' rows are on their way while these are worked on:
-// 4 to 8 KB per warp, 8 or 12 warps per SM), then the conversions of the stored forms.
+// What bounds it: latency and the issue of its instructions, about 350 for 16 keys of an e4m3
+// head of 128 (IPC 1.6 of 4, HBM at half its rate).  48 agents' own keys (200 MB of e4m3, 4 rows
+// each): 45 us beside a prefix's kernel, 136 us for the call when 128-row tiles held these rows,
+// 72 us now; the loads of the next tiles in registers instead of a ring in shared memory: 74 us;
+// e4m3 as bf16 operands: 79 us.
 #pragma once
 
 #include "attend_plan.cuh"
@@ -232,10 +237,19 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D, NT>::kWarps, 1)
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int col = 8 * n + 2 * t + x, rc = e.row0 + col;
-                // a prefix is seen whole; new token i sees the keys up to its own
-                const int unseen = prefix ? 0 : (e.row0 + e.rows - 1) / G - rc / G;
-                sees[n][x] = col < e.rows ? e.keys - unseen : 0;
+                // The new tokens stand at the end of the sequence: new token i sees the own keys up
+                // to its own, and with fewer own keys than new tokens the first ones miss part of
+                // the prefix.
+                const int col = 8 * n + 2 * t + x, rc = e.row0 + col, ag = rc / TG, tok = (rc - ag * TG) / G;
+                if (col >= e.rows) {
+                    sees[n][x] = 0;
+                } else if (prefix) {
+                    bool ignore = false;
+                    const int mine = clamp_len(__ldg(a.suffix_len + e.agent0 + ag), (long long)a.max_suffix_pages * a.page, ignore);
+                    sees[n][x] = min(e.keys, e.keys + mine - T + 1 + tok);
+                } else {
+                    sees[n][x] = e.keys - (e.row0 + e.rows - 1) / G + rc / G;
+                }
                 m[n][x] = my[n][x] = -INFINITY;
                 if (!kE4m3) unit[n][x] = c;
                 l[n][x] = 0.f;

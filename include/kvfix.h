@@ -690,10 +690,15 @@ KVFIX_API kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapp
  * kvfix_check_status).  Page entries past a length are not read.
  * Limits: (max_prefix_pages + max_suffix_pages) * page_tokens < 2^30 and agents * new tokens *
  * q_heads < 2^27.
- * Arithmetic: bf16 tensor-core products with float accumulation (stored values are bf16
- * values, so no operand is rounded but the softmax weights, to bf16 before their product with
- * the values); maxima, sums and lse in float; one rounding of out to bf16.  The same inputs
- * give the same bits on every run; the order of sums depends on the lengths.
+ * Arithmetic: bf16 or f16 tensor-core products with float accumulation.  Stored values are
+ * exact operands; only the softmax weights are rounded, to bf16 (or more) before their product
+ * with the values, and, for blocks of up to 16 rows over e4m3, a query's components below
+ * 2^-26 of its largest.  Maxima, sums and lse in float; one rounding of out to bf16.  The same
+ * inputs give the same bits on every run; the order of sums depends on the lengths.
+ * A NaN or infinity in a key that a query sees reaches that query, one in a value every query
+ * that sees its key; with several new tokens a value row that only the later of them see may
+ * reach the earlier ones too (a weight of zero times NaN).  Rows that belong to no key, or to
+ * none that a block of queries sees, may hold anything.
  */
 KVFIX_API size_t kvfix_shared_attend_workspace_bytes(int32_t agents, int32_t new_tokens, int32_t q_heads,
                                                      int32_t kv_heads, int32_t head_dim, int32_t groups);

@@ -168,6 +168,8 @@ FEW = {
     "seventeen_rows": (1, 17, 64, 16, 1, [40], [0, 1], [30]),
     "own_alone": (2, 4, 128, 32, 1, [], [], [37 * i % 500 for i in range(24)]),
     "own_long": (1, 8, 64, 128, 1, [], [], [20000, 1, 15]),
+    "fewer_own_than_new": (2, 2, 64, 16, 3, [40], [0, 1], [0]),
+    "fewer_own_than_new_of_two": (1, 2, 128, 16, 4, [21, 2], [0, 1, 2], [1, 3]),
     "a_last_block_of_few": (1, 8, 64, 16, 1, [300], [0, 33], [5] * 33),
 }
 
