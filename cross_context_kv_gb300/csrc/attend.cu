@@ -951,6 +951,79 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[q][i] = 0.f;
     }
+    // first part row of the segment's rows from r0 on, in the j-th piece that holds them
+    auto part_of = [&](const Place& p, int j, int r0) {
+        if (j == 0) return p.own + r0;
+        const long long i = p.i0 + j;
+        if (p.kind == kFew) return w.few_rows + i * w.few + (r0 - p.row0);
+        const int half = p.kind == kSingles && i >= many_ctas ? 1 : 0, cta = (int)i - half * many_ctas;
+        return w.own_rows + (long long)cta * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half) + (r0 - p.row0);
+    };
+    if constexpr (RPW > 1) {
+        // few parts per row: one after another, the next one's rows on their way
+        struct Part {
+            float2 ml[RPW];
+            float x[RPW][V];
+        };
+        int s = -1, q0 = rows, q1 = rows, j = 0;  // the segment, its rows in one block, their part
+        Place p = {0, 0, 0, 0, 0};
+        auto fetch = [&](Part& d) {
+            for (++j; j >= p.n || q0 >= rows;) {
+                q0 = q1;
+                if (q0 >= rows) {
+                    if (++s > 1) return false;
+                    q0 = 0;
+                    if (!live || (s == 0 && group < 0)) {
+                        q0 = q1 = rows;
+                        continue;
+                    }
+                }
+                const int r0 = (agent - agent0[s]) * TG + in0;
+                q1 = min(rows, (r0 + q0) / kAtBlock * kAtBlock + kAtBlock - r0);
+                p = q0 == 0 ? at[s] : find(s, r0 + q0, seg[s], agent0[s], seg_rows[s]);
+                j = 0;
+            }
+            const long long part = part_of(p, j, (agent - agent0[s]) * TG + in0);
+#pragma unroll
+            for (int q = 0; q < RPW; ++q) {
+                const bool in = q >= q0 && q < q1;
+                d.ml[q] = in ? __ldcg(w.ml + part + q) : make_float2(-INFINITY, 0.f);
+                const float* src = w.o + (part + q) * D + V * lane;
+                if (V == 4) {
+                    const float4 v = in ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    d.x[q][0] = v.x;
+                    d.x[q][1] = v.y;
+                    d.x[q][V - 2] = v.z;
+                    d.x[q][V - 1] = v.w;
+                } else {
+                    const float2 v = in ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+                    d.x[q][0] = v.x;
+                    d.x[q][1] = v.y;
+                }
+            }
+            return true;
+        };
+        Part now;
+        bool have = fetch(now);
+        while (have) {
+            Part next;
+            const bool more = fetch(next);
+#pragma unroll
+            for (int q = 0; q < RPW; ++q) {
+                const float2 ml = now.ml[q];
+                if (ml.y == 0.f) continue;  // (a row with a NaN logit has l = NaN and must keep it)
+                const float N = fmaxf(M[q], ml.x);
+                const float f = M[q] == -INFINITY ? 1.f : exp2f(M[q] - N);  // (nothing there yet, or NaN)
+                const float wt = ml.x == -INFINITY ? 1.f : exp2f(ml.x - N);
+                M[q] = N;
+                L[q] = L[q] * f + ml.y * wt;
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[q][i] = fmaf(now.x[q][i], wt, acc[q][i] * f);
+            }
+            now = next;
+            have = more;
+        }
+    } else {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         if (!live || (s == 0 && group < 0)) continue;
@@ -962,17 +1035,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
             for (int j0 = sub; j0 < p.n; j0 += 32 * WPR) {
                 const int j = j0 + lane * WPR;
                 const bool in_unit = j < p.n;
-                long long part = p.own + r0;
-                if (j > 0 && in_unit) {
-                    const long long i = p.i0 + j;
-                    if (p.kind == kFew) {
-                        part = w.few_rows + i * w.few;
-                    } else {
-                        const int half = p.kind == kSingles && i >= many_ctas ? 1 : 0, cta = (int)i - half * many_ctas;
-                        part = w.own_rows + (long long)cta * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half);
-                    }
-                    part += r0 - p.row0;
-                }
+                const long long part = in_unit ? part_of(p, j, r0) : 0;
                 float wt[RPW];
                 unsigned has[RPW], any = 0;
 #pragma unroll
@@ -999,7 +1062,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
                     any |= has[q];
                 }
                 const int count = 32 - __clz(any);
-                constexpr int B = RPW > 1 ? 2 : 8;  // parts whose rows are on their way at once
+                constexpr int B = 8;  // parts whose rows are on their way at once
 #pragma unroll 1
                 for (int b0 = 0; b0 < count; b0 += B) {
                     float x[B][RPW][V], wb[B][RPW];
@@ -1035,6 +1098,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
             }
             q0 = q1;
         }
+    }
     }
     if (WPR > 1) {
         if (lane == 0) {

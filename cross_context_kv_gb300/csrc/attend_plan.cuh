@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     __shared__ PlanSums warp_sums[kPlanThreads / 32];
     __shared__ int warp_max[kPlanThreads / 32];
     __shared__ AtEntry kept[3][kPlanKept];
+    __shared__ long long pair_line[kPlanThreads];  // where a segment's pairs begin on their line
     pdl_wait();  // the lengths may be the work of the kernel before
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -212,55 +213,110 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         }
         __syncthreads();
     }
-    // a segment's blocks in turn
-    auto each_block = [&](int s, auto&& f) {
-        const bool prefix = s < a.groups;
-        const int agent0 = prefix ? w.bounds[s] : s - a.groups;
-        const int count = prefix ? w.bounds[s + 1] - agent0 : 1;
-        const int given = s == s0 ? len0 : prefix ? __ldg(a.prefix_len + s) : __ldg(a.suffix_len + agent0);
-        const int n = clamp_len(given, prefix ? most_p : most_s, bad);
-        const int rows = count * TG;
-        for (int r0 = 0; r0 < rows; r0 += kAtBlock) {
-            AtEntry e;
-            e.rows = min(kAtBlock, rows - r0);
-            e.row0 = r0;
-            e.seg = s;
-            e.agent0 = agent0;
-            // own keys are seen up to the place of the block's last row
-            e.keys = prefix ? n : max(0, n - T + 1 + (r0 + e.rows - 1) / G);
-            const int k = at_kind(e.rows, w.few);
-            e.tiles = (e.keys + at_keys(k) - 1) / at_keys(k);
-            f(e, k, e.tiles > 0 ? (long long)H * (e.tiles + at_pad(k)) : 0ll);
-        }
+    struct Seg {
+        int agent0, rows, keys;
+        bool prefix;
+    };
+    auto segment = [&](int s) {
+        Seg g;
+        g.prefix = s < a.groups;
+        g.agent0 = g.prefix ? w.bounds[s] : s - a.groups;
+        const int given = s == s0 ? len0 : g.prefix ? __ldg(a.prefix_len + s) : __ldg(a.suffix_len + g.agent0);
+        g.keys = clamp_len(given, g.prefix ? most_p : most_s, bad);
+        g.rows = (g.prefix ? w.bounds[s + 1] - g.agent0 : 1) * TG;
+        return g;
+    };
+    auto block = [&](const Seg& g, int s, int r0, int& kind) {
+        AtEntry e;
+        e.rows = min(kAtBlock, g.rows - r0);
+        e.row0 = r0;
+        e.seg = s;
+        e.agent0 = g.agent0;
+        // own keys are seen up to the place of the block's last row
+        e.keys = g.prefix ? g.keys : max(0, g.keys - T + 1 + (r0 + e.rows - 1) / G);
+        kind = at_kind(e.rows, w.few);
+        e.tiles = (e.keys + at_keys(kind) - 1) / at_keys(kind);
+        return e;
+    };
+    auto cost = [&](const AtEntry& e, int kind) { return e.tiles > 0 ? (long long)H * (e.tiles + at_pad(kind)) : 0ll; };
+    // what a segment's first n blocks, pairs all, take: a prefix's are alike
+    auto pairs_cost = [&](const Seg& g, int s, int n) {
+        int k;
+        if (g.prefix) return n > 0 ? n * cost(block(g, s, 0, k), kPairs) : 0ll;
+        long long sum = 0;
+        for (int b = 0; b < n; ++b) sum += cost(block(g, s, b * kAtBlock, k), kPairs);
+        return sum;
+    };
+    auto full_pairs = [&](const Seg& g) { return g.rows / kAtBlock; };
+    auto keep = [&](AtEntry e, int k, int i, long long begin) {
+        e.begin = begin;
+        w.entries[k][i] = e;
+        if (i < kPlanKept) kept[k][i] = e;
     };
     PlanSums mine = {};
-    for (int s = s0; s < s1; ++s)
-        each_block(s, [&](const AtEntry&, int k, long long cost) {
+    for (int s = s0; s < s1; ++s) {
+        const Seg g = segment(s);
+        const int full = full_pairs(g);
+        mine.n[kPairs] += full;
+        mine.line[kPairs] += pairs_cost(g, s, full);
+        if (g.rows > full * kAtBlock) {
+            int k;
+            const long long c = cost(block(g, s, full * kAtBlock, k), k);
 #pragma unroll
             for (int x = 0; x < 3; ++x)
                 if (x == k) {
                     mine.n[x] += 1;
-                    mine.line[x] += cost;
+                    mine.line[x] += c;
                 }
-        });
+        }
+    }
     PlanSums total;
     PlanSums at = plan_scan(mine, warp_sums, &total);
     for (int s = s0; s < s1; ++s) {
+        const Seg g = segment(s);
+        const int full = full_pairs(g);
         int2 first = make_int2(at.n[kPairs], 0);
-        each_block(s, [&](AtEntry e, int k, long long cost) {
+        // full blocks: by all threads below, where each has one segment at most
+        if (per > 1)
+            for (int b = 0; b < full; ++b) {
+                int k;
+                const AtEntry e = block(g, s, b * kAtBlock, k);
+                keep(e, kPairs, at.n[kPairs] + b, at.line[kPairs] + pairs_cost(g, s, b));
+            }
+        else
+            pair_line[s] = at.line[kPairs];
+        at.n[kPairs] += full;
+        at.line[kPairs] += pairs_cost(g, s, full);
+        if (g.rows > full * kAtBlock) {
+            int k;
+            const AtEntry e = block(g, s, full * kAtBlock, k);
+            const long long c = cost(e, k);
 #pragma unroll
             for (int x = 0; x < 3; ++x)
                 if (x == k) {
-                    e.begin = at.line[x];
-                    w.entries[x][at.n[x]] = e;
-                    if (at.n[x] < kPlanKept) kept[x][at.n[x]] = e;
+                    keep(e, x, at.n[x], at.line[x]);
                     if (x != kPairs) first.y = at.n[x];
                     at.n[x] += 1;
-                    at.line[x] += cost;
+                    at.line[x] += c;
                 }
-        });
+        }
         w.first[s] = first;
     }
+    __syncthreads();
+    if (per == 1)
+        for (int i = tid; i < total.n[kPairs]; i += kPlanThreads) {
+            int x = 0, y = segs;  // the last segment whose pairs begin at or before i
+            while (y - x > 1) {
+                const int m = (x + y) / 2;
+                if (w.first[m].x <= i) x = m;
+                else y = m;
+            }
+            const Seg g = segment(x);
+            const int b = i - w.first[x].x;
+            if (b >= full_pairs(g)) continue;  // (the last block's, written above)
+            int k;
+            keep(block(g, x, b * kAtBlock, k), kPairs, i, pair_line[x] + pairs_cost(g, x, b));
+        }
     __syncthreads();
     // The two kernels share the GPU: CTAs of the first that have no piece end at once, and the
     // second's take their places.  The split has both end together, from what 128 keys cost a CTA
