@@ -1173,18 +1173,16 @@ static cudaError_t allow_smem(Kernel* kernel, int bytes, int device) {
 
 template <int F, int D, int NT>
 static cudaError_t launch_few(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
-    using C = FewCfg<F, D, NT>;
+    using C = FewCfg<F, D>;
     const cudaError_t e = allow_smem<F, D, NT>(attend_few_kernel<F, D, NT>, C::kSmem, device);
     if (e != cudaSuccess) return e;
-    return launch_chained(attend_few_kernel<F, D, NT>, dim3(w.ctas), dim3(32 * C::kWarps), C::kSmem, s, a, w);
+    return launch_chained(attend_few_kernel<F, D, NT>, dim3(w.ctas), dim3(32 * kFewWarps), C::kSmem, s, a, w);
 }
 
 template <int F, int D>
-static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& work, int device, cudaStream_t s) {
+static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
     using C = AtCfg<F, D>;
     cudaError_t e;
-    AtWork w = work;
-    w.few_warps = w.few == 16 ? FewCfg<F, D, 2>::kWarps : FewCfg<F, D, 1>::kWarps;
     if ((e = launch_chained(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
     if (w.many) {
         CUtensorMap mk, mv;
@@ -1198,8 +1196,9 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& work, i
         if (e != cudaSuccess) return e;
     }
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;
-    // four warps per row while that leaves them all resident in two turns, one while rows are few
-    if (rows <= (long long)w.ctas * 16) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
+    // four warps per row while that leaves them all resident (48 rows of 32 heads, 1536, join in
+    // 7 us less by one), one while rows are few
+    if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
     const int tg = a.new_tokens * (a.q_heads / a.pool.heads);
     if (tg >= 4 && rows > (long long)w.ctas * 128) {
         const long long warps = (long long)a.agents * a.pool.heads * ((tg + 3) / 4);

@@ -62,7 +62,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
-template <int F, int D, int NT>
+template <int F, int D>
 struct FewCfg {
     static constexpr int kRow = F == KVFIX_POOL_BF16 ? 2 * D : F == KVFIX_POOL_E4M3 ? D : D / 2;  // bytes
     static constexpr int kKeyBytes = kRow / 4 < 16 ? kRow / 4 : 16;   // of one load of a key row
@@ -76,9 +76,7 @@ struct FewCfg {
     static constexpr int kKeyPart = 16 * kRow, kScalePart = 16 * kScaleBytes;
     static constexpr int kStage = 2 * kKeyPart + 2 * kScalePart;
     static constexpr int kStages = F == KVFIX_POOL_BF16 && D == 128 ? 3 : 4;
-    // (16 queries' output and operands take twice the registers of 8)
-    static constexpr int kWarps = D == 128 && (F == KVFIX_POOL_BF16 || NT == 2) ? 8 : kFewWarps;
-    static constexpr int kSmem = kWarps * kStages * kStage;
+    static constexpr int kSmem = kFewWarps * kStages * kStage;
 };
 
 // N (4, 8, 16) bytes from global to shared memory; nothing is read, and zeros come, where `there`
@@ -107,9 +105,9 @@ __device__ __forceinline__ void read_words(uint32_t* w, const unsigned char* p) 
 
 // NT: groups of 8 queries.
 template <int F, int D, int NT>
-__global__ void __launch_bounds__(32 * FewCfg<F, D, NT>::kWarps, 1)
+__global__ void __launch_bounds__(32 * kFewWarps, 1)
     attend_few_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ AtWork w) {
-    using C = FewCfg<F, D, NT>;
+    using C = FewCfg<F, D>;
     constexpr bool kE4m3 = F == KVFIX_POOL_E4M3, kInt4 = F == KVFIX_POOL_INT4;
     constexpr int KW = C::kKeyBytes / 4, VW = C::kValBytes / 4;
     constexpr int kScaleBytes = C::kScaleBytes;
@@ -129,7 +127,7 @@ __global__ void __launch_bounds__(32 * FewCfg<F, D, NT>::kWarps, 1)
     AtWalk walk;
     walk.open(w.plan->start[3][blockIdx.x], w.entries[kFew], a.pool.heads, kFew);
     const long long piece = w.plan->chunk[kFew];
-    const long long slot_row = w.few_rows + ((long long)blockIdx.x * C::kWarps + warp) * w.few;
+    const long long slot_row = w.few_rows + ((long long)blockIdx.x * kFewWarps + warp) * w.few;
     walk.lo += piece * warp;
     walk.hi = min(walk.hi, walk.lo + piece);
     int head, t0, t1;

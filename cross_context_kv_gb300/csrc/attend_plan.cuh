@@ -18,7 +18,7 @@ constexpr int kAtKeys = 128;      // keys per tile
 constexpr int kAtRows = 128;      // rows per accumulator (MMA M)
 constexpr int kAtBlock = 256;     // rows per entry
 constexpr int kAtMaxCtas = 256;   // bound of the persistent grid
-constexpr int kFewWarps = 12;     // most warps of a few-row CTA
+constexpr int kFewWarps = 8;      // warps of a few-row CTA (12 or 16 are no faster)
 
 // A row's maximum is raised (and its accumulator rescaled) once a logit passes it by more
 // than this many powers of two: weights stay below 2^8, and bf16 keeps 8 bits of any of them.
@@ -104,7 +104,7 @@ struct AtWork {
     float2* ml;           // part rows: (max in base-2 units, sum)
     float* o;             // part rows x D
     long long own_rows, few_rows;
-    int ctas, few, few_warps;
+    int ctas, few;
     bool many;            // the kernel for larger blocks runs too
 };
 
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         nm = min(max(nm, 1), w.ctas - 1);
         nf = w.ctas - nm;
     }
-    const int few_pieces = nf * w.few_warps;
+    const int few_pieces = nf * kFewWarps;
     const long long chunk[3] = {max(1ll, quotient(total.line[0] + nm - 1, nm)),
                                 max(1ll, quotient(total.line[1] + 2 * nm - 1, 2 * nm)),
                                 max(1ll, quotient(total.line[2] + few_pieces - 1, few_pieces))};
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     for (int i = tid; i < 4 * w.ctas; i += kPlanThreads) {
         const int cta = i % w.ctas, set = i / w.ctas, k = set == 0 ? kPairs : set == 3 ? kFew : kSingles;
         AtStart* st = &w.plan->start[set][cta];
-        const long long size = k == kFew ? chunk[kFew] * w.few_warps : k == kSingles ? chunk[kSingles] : chunk[kPairs];
+        const long long size = k == kFew ? chunk[kFew] * kFewWarps : k == kSingles ? chunk[kSingles] : chunk[kPairs];
         const long long lo = k != kFew && cta >= nm ? total.line[k] : size * (set == 2 ? cta + nm : cta);
         if (lo >= total.line[k]) {
             st->have = 0;
