@@ -13,6 +13,7 @@ import os
 from typing import NamedTuple
 
 import torch
+from torch._C._dynamo.guards import _empty_strided_cuda
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvfix.so")
@@ -631,7 +632,14 @@ def pool_empty(format: str, layers: int, slots: int, kv_heads: int, head_dim: in
 
 def _raw_stream(t) -> int:
     """The current stream of a CUDA tensor's device, as an address (no Stream object on the way)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _empty(dev: int, shape, stride, dtype):
+    """torch.empty_strided on CUDA device `dev`, in half its host time (2 against 4.5 us each
+    beside a launch) where that is the current one."""
+    t = _empty_strided_cuda(shape, stride, dtype)
+    return t if t.get_device() == dev else torch.empty_strided(shape, stride, dtype=dtype, device=f"cuda:{dev}")
 
 
 def pool_desc(pool: Pool) -> PoolDesc:
@@ -742,14 +750,14 @@ def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, pre
     Returns out, shaped like q, or (out, lse [agents][T][q_heads])."""
     if q.dim() != 4:
         raise ValueError("q must be [agents][new tokens][heads][dim]")
-    qd, pd, dev = _rows_desc(q, "q"), pool_desc(pool), q.device
+    qd, pd, dev = _rows_desc(q, "q"), pool_desc(pool), q.get_device()
     A, T, Hq, Dh = q.shape
     groups = 0 if prefix_len is None else prefix_len.numel()
     _i32(suffix_pages, "suffix_pages")
     _i32(suffix_len, "suffix_len")
     if suffix_pages.dim() != 2 or suffix_pages.shape[0] != A or suffix_len.numel() != A:
         raise ValueError(f"suffix_pages must be [{A}][pages] and suffix_len hold {A} lengths")
-    if pool.k.device != dev or suffix_pages.device != dev or suffix_len.device != dev:
+    if pool.k.get_device() != dev or suffix_pages.get_device() != dev or suffix_len.get_device() != dev:
         raise ValueError("q, the pool, pages and lengths must be on one device")
     shared = (None, 0, None, None)
     if groups:
@@ -760,21 +768,22 @@ def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, pre
         _i32(group_begin, "group_begin")
         if prefix_pages.dim() != 2 or prefix_pages.shape[0] != groups or group_begin.numel() != groups + 1:
             raise ValueError(f"prefix_pages must be [{groups}][pages] and group_begin hold {groups + 1} bounds")
-        if prefix_pages.device != dev or prefix_len.device != dev or group_begin.device != dev:
+        if prefix_pages.get_device() != dev or prefix_len.get_device() != dev or group_begin.get_device() != dev:
             raise ValueError("q, the pool, pages and lengths must be on one device")
         shared = (prefix_pages.data_ptr(), prefix_pages.shape[1], prefix_len.data_ptr(), group_begin.data_ptr())
     if out is None:
-        out = torch.empty((A, T, Hq, Dh), dtype=torch.bfloat16, device=dev)
+        out = _empty(dev, (A, T, Hq, Dh), (T * Hq * Dh, Hq * Dh, Dh, 1), torch.bfloat16)
     od = _rows_desc(out, "out")
-    lse = torch.empty((A, T, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    lse = _empty(dev, (A, T, Hq), (T * Hq, Hq, 1), torch.float32) if return_lse else None
     if workspace is None:
-        workspace = torch.empty(lib.kvfix_shared_attend_workspace_bytes(A, T, Hq, pd.kv_heads, Dh, groups),
-                                dtype=torch.uint8, device=dev)
-    if out.device != dev or workspace.device != dev:
+        size = lib.kvfix_shared_attend_workspace_bytes(A, T, Hq, pd.kv_heads, Dh, groups)
+        workspace = _empty(dev, (size,), (1,), torch.uint8)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    if out.get_device() != dev or workspace.get_device() != dev:
         raise ValueError("out and workspace must be on q's device")
     _check(lib.kvfix_shared_attend(
         q.data_ptr(), qd, pd, int(page_tokens), *shared, groups, suffix_pages.data_ptr(), suffix_pages.shape[1],
         suffix_len.data_ptr(), Dh ** -0.5 if scale is None else float(scale), out.data_ptr(), od,
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _raw_stream(q)))
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), size, _raw_stream(q)))
     return (out, lse) if return_lse else out
