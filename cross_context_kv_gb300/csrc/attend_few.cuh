@@ -18,9 +18,9 @@
 //
 // What bounds it: latency and the issue of its instructions, about 350 for 16 keys of an e4m3
 // head of 128 (IPC 1.6 of 4, HBM at half its rate).  48 agents' own keys (200 MB of e4m3, 4 rows
-// each): 45 us beside a prefix's kernel, 136 us for the call when 128-row tiles held these rows,
-// 72 us now; the loads of the next tiles in registers instead of a ring in shared memory: 74 us;
-// e4m3 as bf16 operands: 79 us.
+// each): 45 us beside a prefix's kernel, 66 us for the call, 136 when 128-row tiles held these
+// rows.  The next tiles' loads in registers instead of a ring in shared memory cost 2 us more,
+// e4m3 as bf16 operands 7.
 #pragma once
 
 #include "attend_plan.cuh"
