@@ -43,6 +43,7 @@ static RopeTheta theta_if(const int32_t* delta, double base, int head_dim) {
 }
 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // Checks one plane descriptor and its pointer.  `what` names the argument.
 static kvfix_status check_plane(const void* ptr, const kvfix_kv_desc& d, const char* what,
@@ -947,6 +948,8 @@ static kvfix_status check_pool_rows(const char* fn, const kvfix_bf16* k, const k
     if ((long long)d.tokens * d.kv_heads > 0x7fff0000ll)
         return fail(KVFIX_EINVAL, "%s: tokens * kv_heads must be at most 2^31 - 2^16", fn);
     if (d.chunks > 0 && d.tokens > 0 && !slot_mapping) return fail(KVFIX_EINVAL, "%s: slot_mapping is null", fn);
+    if (!aligned4(slot_mapping) || !aligned4(delta))
+        return fail(KVFIX_EINVAL, "%s: slot_mapping and delta must be 4-byte aligned", fn);
     if (delta && (!(rope_base > 1.0) || !isfinite(rope_base)))
         return fail(KVFIX_EINVAL, "%s: rope_base must be finite and > 1", fn);
     if (pool_meets_plane(pool, k, d) || pool_meets_plane(pool, v, d))
@@ -1014,6 +1017,9 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
         return fail(KVFIX_EINVAL, "%s: prefix_pages, prefix_len and group_begin are required with groups", fn);
     if (agents > 0 && (!suffix_len || (max_suffix_pages > 0 && !suffix_pages)))
         return fail(KVFIX_EINVAL, "%s: suffix_pages and suffix_len are required", fn);
+    if (!aligned4(prefix_pages) || !aligned4(prefix_len) || !aligned4(group_begin) || !aligned4(suffix_pages) ||
+        !aligned4(suffix_len) || !aligned4(lse))
+        return fail(KVFIX_EINVAL, "%s: page lists, lengths, group bounds and lse must be 4-byte aligned", fn);
     if (!(scale > 0.0) || !isfinite(scale)) return fail(KVFIX_EINVAL, "%s: scale must be finite and > 0", fn);
     const size_t need = kvfix_shared_attend_workspace_bytes(agents, T, qd.kv_heads, pool.kv_heads, pool.head_dim, groups);
     if (!workspace || !aligned16(workspace) || workspace_bytes < need)
