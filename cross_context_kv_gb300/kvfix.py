@@ -778,6 +778,8 @@ def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, pre
     if workspace is None:
         size = lib.kvfix_shared_attend_workspace_bytes(A, T, Hq, pd.kv_heads, Dh, groups)
         workspace = _empty(dev, (size,), (1,), torch.uint8)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     else:
         size = workspace.numel() * workspace.element_size()
     if out.get_device() != dev or workspace.get_device() != dev:

@@ -3,6 +3,7 @@ nothing to do: all on the host, without a GPU."""
 import ctypes
 
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -62,3 +63,72 @@ def test_arrays_of_words_are_aligned(kvfix, calls, byte):
     for call in (calls.write, calls.read):
         refused(kvfix, call(slots=at(6, byte)), b"4-byte aligned")
         refused(kvfix, call(delta=at(6, byte)), b"4-byte aligned")
+
+
+# ------------------------------------------------------------------ the binding, on stand-ins
+
+class OnGpu:
+    """What the binding asks of a CUDA tensor, without one: the shape and strides of a meta
+    tensor, a device of its own and a made-up address."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.int32, device=0, like=None):
+        self.meta = torch.empty(shape, dtype=dtype, device="meta") if like is None else like
+        self.device = torch.device("cuda", device)
+
+    def __getattr__(self, name):
+        return getattr(self.meta, name)
+
+    def __getitem__(self, i):
+        return OnGpu(like=self.meta[i], device=self.device.index)
+
+    def get_device(self):
+        return self.device.index
+
+    def data_ptr(self):
+        return 1 << 32
+
+
+class NoLaunch:
+    """The library with its launching entry points in place of a GPU: they note that they were
+    called."""
+
+    def __init__(self, lib):
+        self.lib, self.called = lib, []
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes") or name == "kvfix_last_error":
+            return getattr(self.lib, name)
+        return lambda *a: self.called.append(name) or 0
+
+
+@pytest.fixture
+def lib(kvfix, monkeypatch):
+    lib = NoLaunch(kvfix.lib)
+    monkeypatch.setattr(kvfix, "lib", lib)
+    monkeypatch.setattr(kvfix, "_raw_stream", lambda t: 0)
+    monkeypatch.setattr(kvfix, "_empty", lambda dev, shape, stride, dtype: OnGpu(*shape, dtype=dtype, device=dev))
+    return lib
+
+
+def attend_args(device=0, **kw):
+    bf16 = dict(dtype=torch.bfloat16, device=device)
+    pool = OnGpu(1, 64, 2, 64, **bf16)
+    from cross_context_kv_gb300 import kvfix
+    args = dict(q=OnGpu(2, 1, 4, 64, **bf16), pool=kvfix.Pool("bf16", pool, pool), page_tokens=16,
+                suffix_pages=OnGpu(2, 3, device=device), suffix_len=OnGpu(2, device=device),
+                prefix_pages=OnGpu(1, 4, device=device), prefix_len=OnGpu(1, device=device),
+                group_begin=OnGpu(2, device=device))
+    return {**args, **kw}
+
+
+def test_workspace_is_contiguous(kvfix, lib):
+    """A view with gaps has fewer bytes behind its address than its elements count."""
+    n = kvfix.lib.kvfix_shared_attend_workspace_bytes(2, 1, 4, 2, 64, 1)
+    kvfix.shared_attend(**attend_args(workspace=OnGpu(n, dtype=torch.uint8)))
+    assert lib.called == ["kvfix_shared_attend"]
+    for w in (OnGpu(2 * n, dtype=torch.uint8)[::2], OnGpu(n // 4, 4, dtype=torch.uint8)[:, :3],
+              OnGpu(like=torch.empty(1, dtype=torch.uint8, device="meta").expand(n))):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            kvfix.shared_attend(**attend_args(workspace=w))
+    assert lib.called == ["kvfix_shared_attend"]
