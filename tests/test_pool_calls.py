@@ -107,7 +107,8 @@ def lib(kvfix, monkeypatch):
     lib = NoLaunch(kvfix.lib)
     monkeypatch.setattr(kvfix, "lib", lib)
     monkeypatch.setattr(kvfix, "_raw_stream", lambda t: 0)
-    monkeypatch.setattr(kvfix, "_empty", lambda dev, shape, stride, dtype: OnGpu(*shape, dtype=dtype, device=dev))
+    monkeypatch.setattr(kvfix, "_empty", lambda shape, stride, dtype: OnGpu(*shape, dtype=dtype))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     return lib
 
 
@@ -132,3 +133,29 @@ def test_workspace_is_contiguous(kvfix, lib):
         with pytest.raises(ValueError, match="workspace must be contiguous"):
             kvfix.shared_attend(**attend_args(workspace=w))
     assert lib.called == ["kvfix_shared_attend"]
+
+
+def test_tensors_of_another_device_are_refused(kvfix, lib, monkeypatch):
+    """The library launches on the current device: tensors of another one never reach it."""
+    current = [0]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(kvfix, "_empty", lambda shape, stride, dtype: OnGpu(*shape, dtype=dtype, device=current[0]))
+    rows = lambda device: OnGpu(2, 1, 3, 2, 64, dtype=torch.bfloat16, device=device)  # noqa: E731
+
+    def calls(device):
+        pool = attend_args(device)["pool"]
+        slots = OnGpu(2, 3, device=device)
+        return [lambda: kvfix.shared_attend(**attend_args(device)),
+                lambda: kvfix.pool_write(pool, rows(device), rows(device), slots),
+                lambda: kvfix.pool_read(pool, slots, k_out=rows(device), v_out=rows(device))]
+
+    for device in (0, 1):
+        current[0] = device
+        for call in calls(device):
+            call()
+    assert len(lib.called) == 6
+    for current[0] in (0, 2):
+        for call in calls(1) + [lambda: kvfix.rerope(rows(1), OnGpu(2, device=1), 1e4, out=rows(1))]:
+            with pytest.raises(ValueError, match="current device"):
+                call()
+    assert len(lib.called) == 6
