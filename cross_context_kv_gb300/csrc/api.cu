@@ -1020,7 +1020,10 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
     if (!aligned4(prefix_pages) || !aligned4(prefix_len) || !aligned4(group_begin) || !aligned4(suffix_pages) ||
         !aligned4(suffix_len) || !aligned4(lse))
         return fail(KVFIX_EINVAL, "%s: page lists, lengths, group bounds and lse must be 4-byte aligned", fn);
-    if (!(scale > 0.0) || !isfinite(scale)) return fail(KVFIX_EINVAL, "%s: scale must be finite and > 0", fn);
+    // the kernels multiply by this float: 0 or infinity would make NaN of a masked logit or of 0
+    const float scale_log2 = (float)(scale * 1.4426950408889634);
+    if (!(scale > 0.0) || !isnormal(scale_log2))
+        return fail(KVFIX_EINVAL, "%s: scale must be > 0, and scale * log2(e) a normal float", fn);
     const size_t need = kvfix_shared_attend_workspace_bytes(agents, T, qd.kv_heads, pool.kv_heads, pool.head_dim, groups);
     if (!workspace || !aligned16(workspace) || workspace_bytes < need)
         return fail(KVFIX_EINVAL, "%s: workspace needs %zu bytes, 16-byte aligned (got %zu)", fn, need, workspace_bytes);
@@ -1053,7 +1056,7 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
     a.group_begin = group_begin;
     a.suffix_pages = suffix_pages;
     a.suffix_len = suffix_len;
-    a.scale_log2 = (float)(scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.workspace = workspace;
     return launched(launch_attend(a, (cudaStream_t)stream), fn);
 }

@@ -679,7 +679,7 @@ KVFIX_API kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapp
  *                group_begin: device int32[groups + 1], ascending within 0..agents.  groups
  *                may be 0 (all three NULL).
  * suffix_pages : device int32[agents][max_suffix_pages]; suffix_len: device int32[agents].
- * scale        : finite, > 0 (usually head_dim^-1/2).
+ * scale        : > 0, with scale * log2(e) a normal float (usually head_dim^-1/2).
  * lse          : device float[agents][new tokens][q_heads], or NULL.
  * workspace    : device buffer of kvfix_shared_attend_workspace_bytes(agents, new tokens,
  *                q_heads, kv_heads, head_dim, groups) bytes, 16-byte aligned, contents

@@ -159,3 +159,19 @@ def test_tensors_of_another_device_are_refused(kvfix, lib, monkeypatch):
             with pytest.raises(ValueError, match="current device"):
                 call()
     assert len(lib.called) == 6
+
+
+def attend_scale(calls, scale):
+    none = calls.desc(C=0)
+    return calls.attend(qd=none, groups=0, sp=None, sl=None, lse=None, scale=scale)
+
+
+@pytest.mark.parametrize("scale", (1e-300, 1e-46, 5e-39, 2.4e38, 1e39, 1e300, -0.125, 0.0))
+def test_a_scale_beyond_float_is_refused(kvfix, calls, scale):
+    """The kernels multiply by the float scale * log2 e: 0 would make a masked logit NaN."""
+    refused(kvfix, attend_scale(calls, scale), b"scale")
+
+
+@pytest.mark.parametrize("scale", (1e-38, 1e-6, 0.125, 1.0, 3.0, 2.3e38))
+def test_a_scale_within_float_is_taken(kvfix, calls, scale):
+    assert attend_scale(calls, scale) == kvfix.OK, kvfix.lib.kvfix_last_error()
