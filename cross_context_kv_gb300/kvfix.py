@@ -761,6 +761,8 @@ def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, pre
     qd, pd, dev = _rows_desc(q, "q"), pool_desc(pool), q.get_device()
     _launch_device(dev)
     A, T, Hq, Dh = q.shape
+    if prefix_len is None and not (prefix_pages is None and group_begin is None):
+        raise ValueError("prefix_len is required with prefix_pages and group_begin")
     groups = 0 if prefix_len is None else prefix_len.numel()
     _i32(suffix_pages, "suffix_pages")
     _i32(suffix_len, "suffix_len")

@@ -175,3 +175,16 @@ def test_a_scale_beyond_float_is_refused(kvfix, calls, scale):
 @pytest.mark.parametrize("scale", (1e-38, 1e-6, 0.125, 1.0, 3.0, 2.3e38))
 def test_a_scale_within_float_is_taken(kvfix, calls, scale):
     assert attend_scale(calls, scale) == kvfix.OK, kvfix.lib.kvfix_last_error()
+
+
+@pytest.mark.parametrize("given", (("prefix_pages",), ("group_begin",), ("prefix_pages", "group_begin")))
+def test_a_prefix_without_lengths_is_refused(kvfix, lib, given):
+    """Half a prefix is not taken for none."""
+    kw = {name: None for name in ("prefix_pages", "prefix_len", "group_begin") if name not in given}
+    with pytest.raises(ValueError, match="prefix_len"):
+        kvfix.shared_attend(**attend_args(**kw))
+    assert not lib.called
+    kvfix.shared_attend(**attend_args(prefix_pages=None, prefix_len=None, group_begin=None))
+    # no group at all: lists without an entry
+    kvfix.shared_attend(**attend_args(prefix_pages=OnGpu(0, 4), prefix_len=OnGpu(0), group_begin=OnGpu(1)))
+    assert len(lib.called) == 2
