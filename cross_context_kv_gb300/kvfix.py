@@ -13,7 +13,15 @@ import os
 from typing import NamedTuple
 
 import torch
-from torch._C._dynamo.guards import _empty_strided_cuda
+
+# Two parts of torch that its releases do not promise, for their host time alone: a small
+# shared_attend call allocates three tensors (2 us each beside a launch, 4.5 by empty_strided).
+# Without them the public ways are taken.
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvfix.so")
@@ -640,12 +648,15 @@ def pool_empty(format: str, layers: int, slots: int, kv_heads: int, head_dim: in
 
 def _raw_stream(t) -> int:
     """The current stream of a CUDA tensor's device, as an address (no Stream object on the way)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if _raw_stream_of is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream_of(t.get_device())
 
 
 def _empty(shape, stride, dtype):
-    """torch.empty_strided on the current CUDA device, in half its host time (2 against 4.5 us
-    each beside a launch)."""
+    """torch.empty_strided on the current CUDA device."""
+    if _empty_strided_cuda is None:
+        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
     return _empty_strided_cuda(shape, stride, dtype)
 
 

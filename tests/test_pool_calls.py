@@ -188,3 +188,27 @@ def test_a_prefix_without_lengths_is_refused(kvfix, lib, given):
     # no group at all: lists without an entry
     kvfix.shared_attend(**attend_args(prefix_pages=OnGpu(0, 4), prefix_len=OnGpu(0), group_begin=OnGpu(1)))
     assert len(lib.called) == 2
+
+
+def test_the_binding_needs_no_private_part_of_torch(kvfix, monkeypatch):
+    """A torch without the private allocator and stream look-up has every entry point all the same."""
+    import importlib.util
+    import sys
+
+    monkeypatch.setitem(sys.modules, "torch._C._dynamo.guards", None)      # (importing it raises)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("kvfix_on_another_torch", kvfix.__file__)
+    other = importlib.util.module_from_spec(spec)
+    monkeypatch.setitem(sys.modules, spec.name, other)
+    spec.loader.exec_module(other)
+    assert all(hasattr(other, name) for name in dir(kvfix) if not name.startswith("_"))
+    asked = []
+    monkeypatch.setattr(torch, "empty_strided", lambda *a, **kw: asked.append((a, kw)) or "tensor")
+    assert other._empty((2, 3), (3, 1), torch.uint8) == "tensor"
+    assert asked == [(((2, 3), (3, 1)), dict(dtype=torch.uint8, device="cuda"))]
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream)
+    assert other._raw_stream(OnGpu(1)) == 77
