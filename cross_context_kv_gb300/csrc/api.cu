@@ -144,14 +144,37 @@ static bool pool_meets_plane(const kvfix_pool& p, const void* a, const kvfix_kv_
     extent(a, d, &lo, &hi);
     return pool_meets(p, (const void*)lo, (size_t)(hi - lo));
 }
+// Whether blocks of n bytes at multiples of `every` from two bases `apart` bytes apart can meet.
+static bool blocks_meet(size_t apart, size_t n, size_t every) {
+    return every == 0 || apart % every < n || apart % every + n > every;
+}
+// Whether a row of the K codes may meet a row of the V codes.  Planes that interleave are apart if
+// one stride's blocks of the other's rows are (a layer's V behind its K), or rows at multiples of
+// the strides' greatest common divisor (a slot's V behind its K).
+static bool code_planes_meet(const kvfix_pool& p) {
+    if (!overlaps_bytes(p.k, pool_code_bytes(p), p.v, pool_code_bytes(p))) return false;
+    const size_t row = (size_t)p.kv_heads * (p.format == KVFIX_POOL_BF16 ? 2 * p.head_dim
+                                             : p.format == KVFIX_POOL_E4M3 ? p.head_dim : p.head_dim / 2);
+    const uintptr_t k = (uintptr_t)p.k, v = (uintptr_t)p.v;
+    const size_t apart = k < v ? v - k : k - v;
+    const size_t sl = p.layers > 1 ? (size_t)p.stride_layer : 0, ss = p.slots > 1 ? (size_t)p.stride_slot : 0;
+    size_t g = sl, b = ss;
+    while (b) {
+        const size_t r = g % b;
+        g = b;
+        b = r;
+    }
+    return blocks_meet(apart, row, g) && blocks_meet(apart, (size_t)(p.slots - 1) * ss + row, sl) &&
+           blocks_meet(apart, (size_t)(p.layers - 1) * sl + row, ss);
+}
 // Whether two of the pool's own buffers meet (a pool that is written needs them apart).
 static bool pool_meets_itself(const kvfix_pool& p) {
     const void* b[4] = {p.k, p.v, p.k_scales, p.v_scales};
     const size_t n[4] = {pool_code_bytes(p), pool_code_bytes(p), pool_scale_bytes(p), pool_scale_bytes(p)};
-    for (int i = 0; i < 4; ++i)
+    for (int i = 2; i < 4; ++i)
         for (int j = 0; j < i; ++j)
             if (overlaps_bytes(b[i], n[i], b[j], n[j])) return true;
-    return false;
+    return code_planes_meet(p);
 }
 
 static kvfix_status launched(cudaError_t e, const char* what) {

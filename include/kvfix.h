@@ -599,7 +599,7 @@ KVFIX_API kvfix_status kvfix_anchor_gate_correct(
  * kvfix_pool describes a pool (or some consecutive layers of one):
  *   code bytes of (l, slot, h): k + l*stride_layer + slot*stride_slot + h*B with B = 2 D,
  *       D or D/2 (strides in BYTES, multiples of 16; stride_slot >= kv_heads*B; 16-byte
- *       aligned bases);
+ *       aligned bases).  K and V rows may interleave, a slot's V behind its K, say;
  *   scales: contiguous [layers][kv_heads][slots] bytes (e4m3), or
  *       [layers][kv_heads][slots][D/32] 32-bit words, 4-byte aligned (int4); NULL for bf16.
  * head_dim D is 64 or 128.  The heads-major scales put the scales of one head's consecutive

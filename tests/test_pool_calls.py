@@ -212,3 +212,42 @@ def test_the_binding_needs_no_private_part_of_torch(kvfix, monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream)
     assert other._raw_stream(OnGpu(1)) == 77
+
+
+def test_interleaved_planes_are_written(kvfix, calls):
+    """K and V side by side in a slot, in a layer or in a slot's layers share no byte."""
+    none = calls.desc(C=1, n=0, H=2, layers=3)
+    base, row = 7 << 32, 2 * 64 * 2
+    for ss, sl, apart in ((2 * row, 64 * 2 * row, row),            # [layer][slot][2]
+                          (row, 2 * 64 * row, 64 * row),           # [layer][2][slot]
+                          (3 * 2 * row, 2 * row, row),             # [slot][layer][2]
+                          (3 * 2 * row, row, 3 * row),             # [slot][2][layer]
+                          (2 * row + 32, 64 * (2 * row + 32), row + 16)):
+        for k, v in ((base, base + apart), (base + apart, base)):
+            p = calls.pool(layers=3, ss=ss, sl=sl, k=k, v=v)
+            assert calls.write(d=none, p=p) == kvfix.OK, kvfix.lib.kvfix_last_error()
+            p = calls.pool(layers=3, ss=ss, sl=sl, k=k, v=v + 16 if v > k else v - 16)
+            if ss != 2 * row + 32:                                 # (this one has room for the 16 bytes)
+                refused(kvfix, calls.write(d=none, p=p), b"each other")
+    one = calls.desc(C=1, n=0, H=2)
+    assert calls.write(d=one, p=calls.pool(slots=1, k=base, v=base + row)) == kvfix.OK
+    refused(kvfix, calls.write(d=one, p=calls.pool(slots=1, k=base, v=base + row - 16)), b"each other")
+    refused(kvfix, calls.write(d=one, p=calls.pool(k=base, v=base)), b"each other")
+
+
+def test_no_two_rows_of_planes_that_are_written_meet(kvfix, calls):
+    """Random small layouts against the rows' addresses one by one."""
+    import random
+
+    r, taken = random.Random(5), 0
+    none = {L: calls.desc(C=1, n=0, H=1, layers=L) for L in (1, 2, 3)}
+    for _ in range(4000):
+        L, n, row = r.choice((1, 2, 3)), r.choice((1, 2, 3, 5)), 64
+        ss, sl = 16 * r.randint(4, 30), 16 * r.randint(0, 90)
+        k, v = ((1 << 32) + 16 * r.randint(0, 120) for _ in range(2))
+        st = calls.write(d=none[L], p=calls.pool(fmt=1, layers=L, slots=n, H=1, ss=ss, sl=sl, k=k, v=v))
+        at = [{b + l * sl + s * ss + i for l in range(L) for s in range(n) for i in range(0, row, 16)} for b in (k, v)]
+        if st == kvfix.OK:
+            taken += 1
+            assert not at[0] & at[1], (L, n, ss, sl, k, v)
+    assert taken > 400
