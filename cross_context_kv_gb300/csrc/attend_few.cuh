@@ -340,9 +340,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
             if (kE4m3) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int kb = st_s[g + 8 * r], vb = st_s[C::kScalePart + g + 8 * r];
-                    ke[r] = kb == (int)kE4m3NanByte ? __int_as_float(0x7fffffff) : pow2f(kb - 127);
-                    ve[r] = vb == (int)kE4m3NanByte ? __int_as_float(0x7fffffff) : (float)(vb - 127);
+                    const unsigned kb = st_s[g + 8 * r], vb = st_s[C::kScalePart + g + 8 * r];
+                    ke[r] = kb == kE4m3NanByte ? __int_as_float(0x7fffffff) : pow2f((int)e4m3_scale_within(kb) - 127);
+                    ve[r] = vb == kE4m3NanByte ? __int_as_float(0x7fffffff) : (float)((int)e4m3_scale_within(vb) - 127);
                 }
             }
             // ---- softmax: key g + 8 (x / 2), column 2t + x % 2

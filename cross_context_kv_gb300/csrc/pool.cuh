@@ -67,10 +67,14 @@ struct E4m3Scale {
 
 constexpr unsigned kE4m3NanByte = 255;  // the scale byte of a row that holds a NaN: all of it reads NaN
 
-// From a stored scale byte, kept within the format's limits.
+// A stored scale byte (not the NaN one) kept within the format's limits.
+__device__ __forceinline__ unsigned e4m3_scale_within(unsigned byte) {
+    return min(max(byte, (unsigned)(kE4m3MinExp + 127)), (unsigned)(kE4m3MaxExp + 127));
+}
+
 __device__ __forceinline__ E4m3Scale e4m3_scale_byte(unsigned byte) {
     E4m3Scale s;
-    const unsigned b = min(max(byte, (unsigned)(kE4m3MinExp + 127)), (unsigned)(kE4m3MaxExp + 127));
+    const unsigned b = e4m3_scale_within(byte);
     // a bf16 power of two in both halves: (exponent field) * (2^7 + 2^23)
     unsigned aa = (min(b, 134u) + 120u) * 0x00800080u;
     const unsigned bb = (max(b, 134u) - 134u + 127u) * 0x00800080u;

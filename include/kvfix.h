@@ -585,7 +585,9 @@ KVFIX_API kvfix_status kvfix_anchor_gate_correct(
  *                    x / 2^(b-127) rounded to nearest even; infinities saturate to the
  *                    largest code.  A row that holds a NaN gets b = 255 and codes 0, and reads
  *                    as NaN throughout (the codes 0x7f and 0xff are not written, and mean
- *                    nothing).  Every stored value is exactly a bf16 value.
+ *                    nothing).  Bytes that are not written otherwise count as the nearest
+ *                    that are: below 17 as 17, 247 to 254 as 246.  Every stored value is
+ *                    exactly a bf16 value.
  *   KVFIX_POOL_INT4  head_dim/2 bytes: each 32-bit word (little endian) holds 8 codes 0..15,
  *                    value 2i in bits [4i, 4i+4) and value 2i+1 in bits [16+4i, 20+4i).
  *                    Groups of 32 values share a bf16 scale and a bf16 zero (one 32-bit
