@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
                     // (weights up to 2^8 before a maximum is raised: 2^15 here, of f16's 2^16)
                     if (kE4m3) p[x] = ex2(y[n][x] - (my[n][x & 1] == -INFINITY ? 0.f : my[n][x & 1] - 7.f));
                 }
-                // weights rounded to the operand's type: half a step, 2^-9 of each for bf16, 2^-12 for f16
+                // weights rounded to the operand's type, by half a step: up to 2^-8 of each for bf16, 2^-11
+                // for f16.  An f16 below 2^-14, 2^-21 of what the largest is or exceeds, has fewer bits and is
+                // off by up to 2^-25: 2^-32 of the largest, where a row's codes are off by 2^-10 of its scale.
                 pf[n][0] = transpose_8x8(kE4m3 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
                 pf[n][1] = transpose_8x8(kE4m3 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
             }

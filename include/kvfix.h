@@ -693,10 +693,14 @@ KVFIX_API kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapp
  * Limits: (max_prefix_pages + max_suffix_pages) * page_tokens < 2^30 and agents * new tokens *
  * q_heads < 2^27.
  * Arithmetic: bf16 or f16 tensor-core products with float accumulation.  Stored values are
- * exact operands; only the softmax weights are rounded, to bf16 (or more) before their product
- * with the values, and, for blocks of up to 16 rows over e4m3, a query's components below
- * 2^-26 of its largest.  Maxima, sums and lse in float; one rounding of out to bf16.  The same
- * inputs give the same bits on every run; the order of sums depends on the lengths.
+ * exact operands; the softmax weights exp(z_j) are rounded to bf16 before their product with
+ * the values (by up to 2^-8 of each).  Where a block of queries is small (at most 16 rows, a row
+ * being a new token and a query head of one KV head) an e4m3 pool may go by f16 instead: the
+ * products of a weight and its value row's scale are rounded, by up to 2^-11 of each, or, below
+ * 2^-21 of the query's largest such product, by up to 2^-32 of that; and a query's components
+ * below 2^-26 of its largest lose bits.  Maxima, sums and lse in float; one rounding of out to
+ * bf16.  The same inputs give the same bits on every run; the order of sums depends on the
+ * lengths.
  * A NaN or infinity in a key that a query sees reaches that query, one in a value every query
  * that sees its key; with several new tokens a value row that only the later of them see may
  * reach the earlier ones too (a weight of zero times NaN).  Rows that belong to no key, or to
