@@ -66,6 +66,9 @@ static kvfix_status check_plane(const void* ptr, const kvfix_kv_desc& d, const c
     return KVFIX_OK;
 }
 
+// A plane without rows needs no address (tensors without elements have none).
+static bool no_rows(const kvfix_kv_desc& d) { return d.chunks == 0 || d.layers == 0 || d.tokens == 0; }
+
 static bool same_shape(const kvfix_kv_desc& a, const kvfix_kv_desc& b) {
     return a.layers == b.layers && a.tokens == b.tokens && a.kv_heads == b.kv_heads &&
            a.head_dim == b.head_dim;
@@ -959,9 +962,9 @@ static kvfix_status check_pool_rows(const char* fn, const kvfix_bf16* k, const k
     kvfix_status st;
     char what[64];
     snprintf(what, sizeof what, "%s: k", fn);
-    if ((st = check_plane(k, d, what)) != KVFIX_OK) return st;
+    if ((st = check_plane(k, d, what, no_rows(d))) != KVFIX_OK) return st;
     snprintf(what, sizeof what, "%s: v", fn);
-    if ((st = check_plane(v, d, what)) != KVFIX_OK) return st;
+    if ((st = check_plane(v, d, what, no_rows(d))) != KVFIX_OK) return st;
     if ((st = check_pool(pool, fn)) != KVFIX_OK) return st;
     if (pool.layers != d.layers || pool.kv_heads != d.kv_heads || pool.head_dim != d.head_dim)
         return fail(KVFIX_EINVAL, "%s: the pool must have the planes' layers, heads and head_dim", fn);
@@ -1015,8 +1018,8 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
                                  kvfix_kv_desc od, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "kvfix_shared_attend";
     kvfix_status st;
-    if ((st = check_plane(q, qd, "kvfix_shared_attend: q")) != KVFIX_OK) return st;
-    if ((st = check_plane(out, od, "kvfix_shared_attend: out")) != KVFIX_OK) return st;
+    if ((st = check_plane(q, qd, "kvfix_shared_attend: q", no_rows(qd))) != KVFIX_OK) return st;
+    if ((st = check_plane(out, od, "kvfix_shared_attend: out", no_rows(od))) != KVFIX_OK) return st;
     if ((st = check_pool(pool, fn)) != KVFIX_OK) return st;
     if (!same_shape(qd, od) || qd.chunks != od.chunks) return fail(KVFIX_EINVAL, "%s: q and out shapes differ", fn);
     if (qd.layers != 1 || pool.layers != 1) return fail(KVFIX_EINVAL, "%s: q, out and the pool must have one layer", fn);

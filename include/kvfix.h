@@ -606,6 +606,7 @@ KVFIX_API kvfix_status kvfix_anchor_gate_correct(
  *       [layers][kv_heads][slots][D/32] 32-bit words, 4-byte aligned (int4); NULL for bf16.
  * head_dim D is 64 or 128.  The heads-major scales put the scales of one head's consecutive
  * slots side by side, as attention reads them.
+ * In the calls below planes without rows (no chunks or tokens) may be NULL, and nothing is done.
  */
 typedef enum { KVFIX_POOL_BF16 = 0, KVFIX_POOL_E4M3 = 1, KVFIX_POOL_INT4 = 2 } kvfix_pool_format;
 typedef struct {

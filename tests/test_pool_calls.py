@@ -251,3 +251,16 @@ def test_no_two_rows_of_planes_that_are_written_meet(kvfix, calls):
             taken += 1
             assert not at[0] & at[1], (L, n, ss, sl, k, v)
     assert taken > 400
+
+
+def test_calls_without_rows_do_nothing(kvfix, calls):
+    """Tensors without elements have no address: no rows, no agents or no new tokens are no error."""
+    for none in (calls.desc(C=0, H=2), calls.desc(n=0, H=2)):
+        for call in (calls.write, calls.read):
+            for kw in (dict(), dict(slots=None), dict(k=None, v=None, slots=None)):
+                assert call(d=none, **kw) == kvfix.OK, kvfix.lib.kvfix_last_error()
+            refused(kvfix, call(d=calls.desc(H=2), k=None), b"null")
+    for none, lists in ((calls.desc(C=0), dict(sp=None, sl=None)), (calls.desc(n=0), {})):
+        assert calls.attend(qd=none, q=None, out=None, lse=None, **lists) == kvfix.OK, kvfix.lib.kvfix_last_error()
+    for name in ("q", "out"):
+        refused(kvfix, calls.attend(**{name: None}), b"null")
