@@ -13,14 +13,15 @@
 // head; its work is its keys in tiles (causally trimmed), plus a few tiles for its fixed cost.
 // One plan kernel lays all units on lines and cuts the lines into equal pieces
 // (attend_plan.cuh); a worker writes one part per unit that its piece touches, and the join
-// kernel finds a row's parts from the same lines.  Blocks of up to 16 rows go to a kernel
-// without tensor memory (attend_few.cuh), the others to the one below.  Everything depends on
-// lengths that lie on the device, so a captured graph follows them.
+// kernel finds a row's parts from the same lines.  Small blocks go to a kernel without tensor
+// memory (attend_few.cuh), the others to the one below; a call's rows decide how many are few
+// (at_layout: 8, 16, or none).  Everything depends on lengths that lie on the device, so a
+// captured graph follows them.
 //
 // What bounds the kernel below: HBM for bf16 prefixes of a decoding round (131072 keys and
 // 128 rows of 8 heads: 537 MB in 95 us, 5.6 TB/s), the conversion of stored tiles and the chain
 // from logits to weights for e4m3 and int4 (138 us for the same keys as e4m3), the
-// exponentials and the tensor pipe for many new tokens (0.89 PFLOP/s):
+// exponentials and the tensor pipe for many new tokens (288 GFLOP in 256 us, 1.12 PFLOP/s):
 //   warps 0-3, 4-7  softmax: each group owns one 128-row accumulator.  Blocks of more than
 //                   128 rows (pairs) give each group its half of the rows, and both use every
 //                   tile; smaller ones (singles) are one group's alone, and the two groups

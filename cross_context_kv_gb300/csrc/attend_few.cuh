@@ -1,5 +1,5 @@
-// attend_few.cuh -- kvfix_shared_attend for blocks of up to 16 query rows: an agent's own tokens
-// while it decodes, and a short round's prefix.
+// attend_few.cuh -- kvfix_shared_attend for small blocks of query rows, up to AtWork::few (8 or
+// 16) of them: an agent's own tokens while it decodes, and a short round's prefix.
 //
 // Mathematics.  The products are turned around: logits are S^T = K Q^T (keys along the rows of the
 // matrix instruction, queries along its 8 columns) and the output O^T = V^T P^T, so few queries

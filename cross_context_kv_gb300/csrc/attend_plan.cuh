@@ -34,8 +34,8 @@ constexpr float kAtSlack = 8.f;
 enum : int { kPairs = 0, kSingles = 1, kFew = 2 };
 __host__ __device__ constexpr int at_keys(int kind) { return kind == kFew ? 16 : kAtKeys; }
 // What a unit costs beside its tiles (queries in, masks, its part out), in tiles: measured on
-// pairs of short own segments, 17000 cycles a unit against 4000 a tile; with 1 there, the CTAs
-// that had those units ran 1.7 times as long as the others.
+// pairs of short own segments at head_dim 128, 17000 cycles a unit against 4000 a tile; with 1
+// there, the CTAs that had those units ran 1.7 times as long as the others.
 __host__ __device__ constexpr int at_pad(int kind) { return kind == kPairs ? 4 : kind == kSingles ? 1 : 2; }
 
 struct __align__(16) AtEntry {
@@ -71,7 +71,8 @@ static AtLayout at_layout(int agents, int T, int q_heads, int kv_heads, int head
     const long long tg = (long long)T * (q_heads / kv_heads), all = (long long)agents * tg;
     AtLayout l;
     // An agent's rows decide: an own segment has tg, a prefix between tg and all.  Blocks of up to
-    // 16 rows where that leaves nothing for the other kernel, else the suffixes' 8 or 16.
+    // 16 rows where that leaves nothing for the other kernel, else the suffixes' 8 or 16; with more
+    // rows an agent the other kernel has all blocks, small last ones too.
     const long long most = groups > 0 ? all : tg;
     l.few = most <= 8 ? 8 : most <= 16 ? 16 : tg <= 8 ? 8 : tg <= 16 ? 16 : 0;
     l.many = most > l.few;
@@ -320,8 +321,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     __syncthreads();
     // The two kernels share the GPU: CTAs of the first that have no piece end at once, and the
     // second's take their places.  The split has both end together, from what 128 keys cost a CTA
-    // of each and what the first takes before and after its tiles, in microseconds as measured:
-    // F + X / n = Y / (ctas - n), solved for n.
+    // of each and what the first takes before and after its tiles, in microseconds as measured at
+    // head_dim 128: F + X / n = Y / (ctas - n), solved for n.  (Only the split depends on them.)
     int nm = w.ctas, nf = w.ctas;
     if (total.line[kPairs] + total.line[kSingles] > 0 && total.line[kFew] > 0) {
         const bool stored = a.pool.format != KVFIX_POOL_BF16;

@@ -11,7 +11,7 @@
 //
 // Measured: 4096 tokens x 32 layers x 8 heads of 128 written rotated as e4m3 in 146 us, 5.5 TB/s
 // (a copy's bytes take 119); 512 tokens x 8 chunks x 48 layers read back rotated in 203 us,
-// 6.0 TB/s.  int4 is bound by issue: 3 x 1237 tokens x 9 layers x 5 heads of 64 in 18.4 us,
+// 6.0 TB/s.  int4 is bound by issue: 3 x 1237 tokens x 9 layers x 5 heads of 64 in 18.7 us,
 // 2.7 TB/s, 68 % of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

@@ -2,8 +2,8 @@
 
 Argument marshalling only: every function checks tensor dtypes/devices, builds the
 plane descriptors from tensor shapes and strides, allocates outputs with torch on the
-tensors' device and calls the C entry point of the same name on the current CUDA
-stream.  All arithmetic runs in the library's CUDA kernels.  If libkvfix.so is
+tensors' device, which has to be the current one, and calls the C entry point of the
+same name on the current CUDA stream.  All arithmetic runs in the library's CUDA kernels.  If libkvfix.so is
 missing, importing this module raises: there is no fallback.
 """
 from __future__ import annotations

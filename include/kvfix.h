@@ -686,7 +686,10 @@ KVFIX_API kvfix_status kvfix_pool_read(kvfix_pool pool, const int32_t* slot_mapp
  * lse          : device float[agents][new tokens][q_heads], or NULL.
  * workspace    : device buffer of kvfix_shared_attend_workspace_bytes(agents, new tokens,
  *                q_heads, kv_heads, head_dim, groups) bytes, 16-byte aligned, contents
- *                irrelevant on entry.
+ *                irrelevant on entry.  Two float rows of head_dim per (agent, new token, query
+ *                head), and whatever the call's size 131072 rows (67 MB at head_dim 128) where
+ *                a block may be larger than the small ones below, 16384 or 32768 where one may
+ *                be small.
  * Pages, lengths and groups are read on the device, so a captured call follows them as they
  * change.  A page out of range counts as absent (its keys are not seen), a length outside its
  * page list and a group boundary out of order are clamped; each is flagged (KVFIX_EDEVICE in
