@@ -270,6 +270,8 @@ def draft_rank(k, q, layer_begin: int, k_rows: int, k_fresh=None, v_fresh=None, 
     ws_bytes = draft_rank_workspace_bytes(k, layer_begin)
     if workspace is None:
         workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=k.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     idx = torch.empty(C, max(k_rows, 0), dtype=torch.int32, device=k.device)
     scores = torch.empty(C, n, dtype=torch.float64, device=k.device)
     fd = plane_desc(k_fresh) if k_fresh is not None else (plane_desc(v_fresh) if v_fresh is not None else d)
@@ -300,6 +302,8 @@ def lowrank_draft(x, A, B, q, layer_begin: int, k_rows: int, out=None, k_fresh=N
     ws_bytes = lowrank_draft_workspace_bytes(out, layer_begin)
     if workspace is None:
         workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=x.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     idx = torch.empty(C, max(k_rows, 0), dtype=torch.int32, device=x.device)
     scores = torch.empty(C, n, dtype=torch.float64, device=x.device)
     fd = plane_desc(k_fresh) if k_fresh is not None else (plane_desc(v_fresh) if v_fresh is not None else d)

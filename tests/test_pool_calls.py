@@ -264,3 +264,14 @@ def test_calls_without_rows_do_nothing(kvfix, calls):
         assert calls.attend(qd=none, q=None, out=None, lse=None, **lists) == kvfix.OK, kvfix.lib.kvfix_last_error()
     for name in ("q", "out"):
         refused(kvfix, calls.attend(**{name: None}), b"null")
+
+
+def test_the_rankings_workspaces_are_contiguous(kvfix, lib):
+    bf16 = dict(dtype=torch.bfloat16)
+    k, q = OnGpu(1, 2, 128, 2, 64, **bf16), OnGpu(1, 2, 4, 4, 64, **bf16)
+    A, B = OnGpu(1, 2, 2, 128, 16, **bf16), OnGpu(1, 2, 2, 16, 64, **bf16)
+    for call in (lambda w: kvfix.draft_rank(k, q, 1, 8, workspace=w),
+                 lambda w: kvfix.lowrank_draft(k, A, B, q, 1, 8, out=k, workspace=w)):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            call(OnGpu(1 << 24, dtype=torch.uint8)[::2])
+    assert not lib.called
