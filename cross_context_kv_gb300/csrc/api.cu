@@ -9,6 +9,8 @@
 
 #include "attend.h"
 #include "internal.h"
+#include "pages.h"
+#include "rotary.h"
 
 namespace kvfix {
 
@@ -97,6 +99,47 @@ static bool overlaps_bytes(const void* a, size_t na, const void* b, size_t nb) {
     if (!a || !b || !na || !nb) return false;
     uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
     return a0 < b0 + nb && b0 < a0 + na;
+}
+
+// Whether a row of one plane may meet a row of the other.  Views of one buffer may interleave (the
+// queries and the keys of a token behind each other): their rows are apart if blocks of their
+// sizes at multiples of the strides' greatest common divisor are.
+static bool rows_meet(const void* a, const kvfix_kv_desc& da, const void* b, const kvfix_kv_desc& db) {
+    if (!overlaps(a, da, b, db)) return false;
+    size_t g = 0;
+    for (const kvfix_kv_desc* d : {&da, &db}) {
+        const long long strides[3] = {d->chunks > 1 ? d->stride_chunk : 0, d->layers > 1 ? d->stride_layer : 0,
+                                      d->tokens > 1 ? d->stride_token : 0};
+        for (long long s : strides) {
+            size_t x = 2 * (size_t)s;
+            while (x) {
+                const size_t r = g % x;
+                g = x;
+                x = r;
+            }
+        }
+    }
+    if (g == 0) return true;
+    const size_t na = 2 * (size_t)da.kv_heads * da.head_dim, nb = 2 * (size_t)db.kv_heads * db.head_dim;
+    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+    const size_t apart = pb >= pa ? (pb - pa) % g : (g - (pa - pb) % g) % g;  // of b's blocks behind a's
+    return apart < na || apart + nb > g;
+}
+
+// Whether a plane's rows are apart from each other, one dimension inside the next.
+static bool rows_apart(const kvfix_kv_desc& d) {
+    long long strides[3] = {d.stride_token, d.stride_layer, d.stride_chunk}, counts[3] = {d.tokens, d.layers, d.chunks};
+    double covered = (double)d.kv_heads * d.head_dim;
+    for (int i = 0; i < 3; ++i) {
+        int least = -1;
+        for (int k = 0; k < 3; ++k)
+            if (counts[k] > 1 && (least < 0 || strides[k] < strides[least])) least = k;
+        if (least < 0) return true;
+        if ((double)strides[least] < covered) return false;
+        covered += (double)strides[least] * (double)(counts[least] - 1);
+        counts[least] = 0;
+    }
+    return true;
 }
 
 // Checks a pool: format, shape, strides, pointers and their alignment.
@@ -202,12 +245,12 @@ kvfix_status kvfix_check_status(void* stream) {
     unsigned bits = read_status_repair(s) | read_status_diff(s) | read_status_draft(s) | read_status_lowrank(s) |
                     read_status_anchor(s) | read_status_layout(s) | read_status_selftest(s) |
                     read_status_lowrank_draft(s) | read_status_pool(s) |
-                    read_status_attend(s);
+                    read_status_attend(s) | read_status_pages(s);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "kvfix_check_status: status read");
     if (bits & 8u) return fail(KVFIX_EDEVICE, "a kernel's shared-memory layout check failed; its work was skipped");
     if (bits & 4u) return fail(KVFIX_ETIMEOUT, "a bounded device wait gave up");
-    if (bits & 2u) return fail(KVFIX_ENOSPACE, "diff payload entries beyond the capacity were skipped");
+    if (bits & 2u) return fail(KVFIX_ENOSPACE, "diff payload entries beyond the capacity, or lists whose pages the pool does not have, were skipped");
     if (bits & 1u) return fail(KVFIX_EDEVICE, "an index in caller data was out of range and skipped");
     g_last_error[0] = '\0';
     return KVFIX_OK;
@@ -1011,15 +1054,19 @@ size_t kvfix_shared_attend_workspace_bytes(int32_t agents, int32_t new_tokens, i
     return attend_workspace_bytes(agents, new_tokens, q_heads, kv_heads, head_dim, groups);
 }
 
-kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_pool pool, int32_t page_tokens,
-                                 const int32_t* prefix_pages, int32_t max_prefix_pages, const int32_t* prefix_len,
-                                 const int32_t* group_begin, int32_t groups, const int32_t* suffix_pages,
-                                 int32_t max_suffix_pages, const int32_t* suffix_len, double scale, kvfix_bf16* out,
-                                 kvfix_kv_desc od, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-    const char* fn = "kvfix_shared_attend";
+// The checks and the launch of both attention calls; is_tree: kvfix_tree_attend's.
+static kvfix_status attend(const char* fn, bool is_tree, const int32_t* nodes, const uint32_t* tree,
+                           const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_pool pool, int32_t page_tokens,
+                           const int32_t* prefix_pages, int32_t max_prefix_pages, const int32_t* prefix_len,
+                           const int32_t* group_begin, int32_t groups, const int32_t* suffix_pages,
+                           int32_t max_suffix_pages, const int32_t* suffix_len, double scale, kvfix_bf16* out,
+                           kvfix_kv_desc od, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
     kvfix_status st;
-    if ((st = check_plane(q, qd, "kvfix_shared_attend: q", no_rows(qd))) != KVFIX_OK) return st;
-    if ((st = check_plane(out, od, "kvfix_shared_attend: out", no_rows(od))) != KVFIX_OK) return st;
+    char what_q[64], what_out[64];
+    snprintf(what_q, sizeof what_q, "%s: q", fn);
+    snprintf(what_out, sizeof what_out, "%s: out", fn);
+    if ((st = check_plane(q, qd, what_q, no_rows(qd))) != KVFIX_OK) return st;
+    if ((st = check_plane(out, od, what_out, no_rows(od))) != KVFIX_OK) return st;
     if ((st = check_pool(pool, fn)) != KVFIX_OK) return st;
     if (!same_shape(qd, od) || qd.chunks != od.chunks) return fail(KVFIX_EINVAL, "%s: q and out shapes differ", fn);
     if (qd.layers != 1 || pool.layers != 1) return fail(KVFIX_EINVAL, "%s: q, out and the pool must have one layer", fn);
@@ -1046,6 +1093,10 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
     if (!aligned4(prefix_pages) || !aligned4(prefix_len) || !aligned4(group_begin) || !aligned4(suffix_pages) ||
         !aligned4(suffix_len) || !aligned4(lse))
         return fail(KVFIX_EINVAL, "%s: page lists, lengths, group bounds and lse must be 4-byte aligned", fn);
+    const int tree_words = (T + 31) / 32;
+    const size_t tree_bytes = tree ? 4 * (size_t)agents * (size_t)T * (size_t)tree_words : 0;
+    if (is_tree && !no_rows(qd) && !tree) return fail(KVFIX_EINVAL, "%s: tree_mask is null", fn);
+    if (!aligned4(nodes) || !aligned4(tree)) return fail(KVFIX_EINVAL, "%s: nodes and tree_mask must be 4-byte aligned", fn);
     // the kernels multiply by this float: 0 or infinity would make NaN of a masked logit or of 0
     const float scale_log2 = (float)(scale * 1.4426950408889634);
     if (!(scale > 0.0) || !isnormal(scale_log2))
@@ -1063,6 +1114,9 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
         overlaps_bytes(workspace, need, (const void*)o0, o1 - o0) ||
         overlaps_bytes(workspace, need, (const void*)q0, q1 - q0) || overlaps_bytes(workspace, need, lse, lse_bytes))
         return fail(KVFIX_EINVAL, "%s: out, lse and workspace must not overlap each other, q or the pool", fn);
+    if (overlaps_bytes(tree, tree_bytes, (const void*)o0, o1 - o0) || overlaps_bytes(tree, tree_bytes, lse, lse_bytes) ||
+        overlaps_bytes(tree, tree_bytes, workspace, need))
+        return fail(KVFIX_EINVAL, "%s: out, lse and workspace must not overlap tree_mask", fn);
     AttendArgs a = {};
     a.q = q;
     a.qp = plane_of(qd);
@@ -1084,7 +1138,211 @@ kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_po
     a.suffix_len = suffix_len;
     a.scale_log2 = scale_log2;
     a.workspace = workspace;
+    a.tree = tree;
+    a.nodes = nodes;
+    a.tree_words = tree_words;
     return launched(launch_attend(a, (cudaStream_t)stream), fn);
+}
+
+kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_pool pool, int32_t page_tokens,
+                                 const int32_t* prefix_pages, int32_t max_prefix_pages, const int32_t* prefix_len,
+                                 const int32_t* group_begin, int32_t groups, const int32_t* suffix_pages,
+                                 int32_t max_suffix_pages, const int32_t* suffix_len, double scale, kvfix_bf16* out,
+                                 kvfix_kv_desc od, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    return attend("kvfix_shared_attend", false, nullptr, nullptr, q, qd, pool, page_tokens, prefix_pages, max_prefix_pages,
+                  prefix_len, group_begin, groups, suffix_pages, max_suffix_pages, suffix_len, scale, out, od, lse, workspace,
+                  workspace_bytes, stream);
+}
+
+kvfix_status kvfix_tree_attend(const kvfix_bf16* q, kvfix_kv_desc qd, kvfix_pool pool, int32_t page_tokens,
+                               const int32_t* prefix_pages, int32_t max_prefix_pages, const int32_t* prefix_len,
+                               const int32_t* group_begin, int32_t groups, const int32_t* suffix_pages,
+                               int32_t max_suffix_pages, const int32_t* suffix_len, const int32_t* nodes,
+                               const uint32_t* tree_mask, double scale, kvfix_bf16* out, kvfix_kv_desc od, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    return attend("kvfix_tree_attend", true, nodes, tree_mask, q, qd, pool, page_tokens, prefix_pages, max_prefix_pages,
+                  prefix_len, group_begin, groups, suffix_pages, max_suffix_pages, suffix_len, scale, out, od, lse, workspace,
+                  workspace_bytes, stream);
+}
+
+static kvfix_status check_rope(const kvfix_rope& r, int head_dim, const char* fn) {
+    if (r.layout != KVFIX_ROPE_HALF && r.layout != KVFIX_ROPE_INTERLEAVED)
+        return fail(KVFIX_EINVAL, "%s: unknown rope layout %d", fn, r.layout);
+    if (r.scaling < KVFIX_ROPE_PLAIN || r.scaling > KVFIX_ROPE_YARN)
+        return fail(KVFIX_EINVAL, "%s: unknown rope scaling %d", fn, r.scaling);
+    if (r.rotary_dim < 2 || r.rotary_dim % 2 || r.rotary_dim > head_dim)
+        return fail(KVFIX_EINVAL, "%s: rotary_dim must be even, in [2, head_dim] (got %d of %d)", fn, r.rotary_dim, head_dim);
+    if (!(r.base > 1.0) || !isfinite(r.base)) return fail(KVFIX_EINVAL, "%s: rope base must be finite and > 1", fn);
+    if (!(r.attention > 0.0) || !isnormal((float)r.attention))
+        return fail(KVFIX_EINVAL, "%s: rope attention must be > 0, a normal float", fn);
+    if (r.scaling != KVFIX_ROPE_PLAIN && (!(r.factor >= 1.0) || !isfinite(r.factor)))
+        return fail(KVFIX_EINVAL, "%s: rope factor must be finite and >= 1", fn);
+    if (r.scaling == KVFIX_ROPE_BANDS || r.scaling == KVFIX_ROPE_YARN) {
+        if (r.original_tokens < 1) return fail(KVFIX_EINVAL, "%s: rope original_tokens must be positive", fn);
+        if (!(r.low > 0.0) || !(r.high > r.low) || !isfinite(r.high))
+            return fail(KVFIX_EINVAL, "%s: rope bounds must be finite, 0 < low < high", fn);
+    }
+    return KVFIX_OK;
+}
+
+kvfix_status kvfix_rotary(const kvfix_bf16* q, kvfix_kv_desc qd, const kvfix_bf16* k, kvfix_kv_desc kd,
+                          const int32_t* positions, kvfix_rope rope, kvfix_bf16* q_out, kvfix_kv_desc qod,
+                          kvfix_bf16* k_out, kvfix_kv_desc kod, void* stream) {
+    const char* fn = "kvfix_rotary";
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    const kvfix_kv_desc* di[2] = {&qd, &kd};
+    const kvfix_kv_desc* dst[2] = {&qod, &kod};
+    RotaryArgs a;
+    memset(&a, 0, sizeof a);
+    a.in_place = true;
+    const kvfix_kv_desc* ref = nullptr;
+    kvfix_status st;
+    for (int i = 0; i < 2; ++i) {
+        if (di[i]->kv_heads == 0) continue;  // left out
+        char what[64];
+        snprintf(what, sizeof what, "%s: %s", fn, i ? "k" : "q");
+        if ((st = check_plane(in[i], *di[i], what, no_rows(*di[i]))) != KVFIX_OK) return st;
+        snprintf(what, sizeof what, "%s: %s_out", fn, i ? "k" : "q");
+        if ((st = check_plane(out[i], *dst[i], what, no_rows(*dst[i]))) != KVFIX_OK) return st;
+        if (!same_shape(*di[i], *dst[i]) || di[i]->chunks != dst[i]->chunks)
+            return fail(KVFIX_EINVAL, "%s: %s and its output differ in shape", fn, i ? "k" : "q");
+        if ((long long)di[i]->kv_heads * di[i]->head_dim >= (1ll << 30))
+            return fail(KVFIX_EINVAL, "%s: a token row must have fewer than 2^30 values", fn);
+        if (ref && (ref->chunks != di[i]->chunks || ref->layers != di[i]->layers || ref->tokens != di[i]->tokens ||
+                    ref->head_dim != di[i]->head_dim))
+            return fail(KVFIX_EINVAL, "%s: q and k must have the same chunks, layers, tokens and head_dim", fn);
+        ref = di[i];
+        if (!no_rows(*dst[i]) && !rows_apart(*dst[i]))
+            return fail(KVFIX_EINVAL, "%s: rows of %s_out overlap each other", fn, i ? "k" : "q");
+        const bool same = in[i] == out[i] && same_desc(*di[i], *dst[i]);
+        if (!same && rows_meet(in[i], *di[i], out[i], *dst[i]))
+            return fail(KVFIX_EINVAL, "%s: %s_out overlaps its input (only exactly in place)", fn, i ? "k" : "q");
+        a.in_place = a.in_place && same;
+        a.in[i] = (const uint16_t*)in[i];
+        a.out[i] = (uint16_t*)out[i];
+        a.ip[i] = plane_of(*di[i]);
+        a.op[i] = plane_of(*dst[i]);
+    }
+    if (!ref) return fail(KVFIX_EINVAL, "%s: neither queries nor keys", fn);
+    if (a.ip[0].heads && a.ip[1].heads && (rows_meet(q, qd, k_out, kod) || rows_meet(k, kd, q_out, qod) || rows_meet(q_out, qod, k_out, kod)))
+        return fail(KVFIX_EINVAL, "%s: an output overlaps the other plane", fn);
+    if ((st = check_rope(rope, ref->head_dim, fn)) != KVFIX_OK) return st;
+    if (!no_rows(*ref) && !positions) return fail(KVFIX_EINVAL, "%s: positions is null", fn);
+    if (!aligned4(positions)) return fail(KVFIX_EINVAL, "%s: positions must be 4-byte aligned", fn);
+    if ((double)ref->chunks * ref->layers * ref->tokens >= 2147483648.0)
+        return fail(KVFIX_EINVAL, "%s: chunks * layers * tokens must be below 2^31", fn);
+    a.positions = positions;
+    a.chunks = ref->chunks;
+    a.layers = ref->layers;
+    a.tokens = ref->tokens;
+    a.dim = ref->head_dim;
+    rotary_angles(rope, &a);
+    return launched(launch_rotary(a, (cudaStream_t)stream), fn);
+}
+
+// The checks of the page calls: the pool, and the books on it.
+static kvfix_status check_pages(const char* fn, const kvfix_pool& pool, int page_tokens, const int32_t* refs,
+                                const int32_t* pages, int max_pages, const int32_t* len, int lists, PagesArgs* a) {
+    kvfix_status st;
+    if ((st = check_pool(pool, fn)) != KVFIX_OK) return st;
+    if (pool_meets_itself(pool)) return fail(KVFIX_EINVAL, "%s: the pool's buffers overlap each other", fn);
+    if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128)
+        return fail(KVFIX_EINVAL, "%s: page_tokens must be 16, 32, 64 or 128 (got %d)", fn, page_tokens);
+    if (pool.slots < page_tokens || pool.slots % page_tokens)
+        return fail(KVFIX_EINVAL, "%s: the pool's slots must be a positive multiple of page_tokens", fn);
+    if (lists < 0 || max_pages < 0 || lists > (1 << 24) || (double)lists * max_pages >= 1073741824.0 ||
+        (double)max_pages * page_tokens >= 1073741824.0)
+        return fail(KVFIX_EINVAL, "%s: at most 2^24 lists, of fewer than 2^30 pages together and 2^30 tokens each", fn);
+    // a page's rows, and the items of a call, are counted in 32 bits
+    if ((double)pool.kv_heads * pool.head_dim >= (double)(1 << 22) || pool.layers > 65535)
+        return fail(KVFIX_EINVAL, "%s: at most 65535 layers, of fewer than 2^22 values a row", fn);
+    if (!refs || (lists > 0 && (!len || (max_pages > 0 && !pages))))
+        return fail(KVFIX_EINVAL, "%s: refs, pages and len are required", fn);
+    if (!aligned4(refs) || !aligned4(pages) || !aligned4(len))
+        return fail(KVFIX_EINVAL, "%s: refs, pages and len must be 4-byte aligned", fn);
+    const size_t nr = 4 * (size_t)(pool.slots / page_tokens), np = 4 * (size_t)lists * max_pages, nl = 4 * (size_t)lists;
+    if (pool_meets(pool, refs, nr) || pool_meets(pool, pages, np) || pool_meets(pool, len, nl) ||
+        overlaps_bytes(refs, nr, pages, np) || overlaps_bytes(refs, nr, len, nl) || overlaps_bytes(pages, np, len, nl))
+        return fail(KVFIX_EINVAL, "%s: refs, pages, len and the pool must not overlap each other", fn);
+    *a = PagesArgs{};
+    a->pool = view_of(pool);
+    a->page = page_tokens;
+    a->total = pool.slots / page_tokens;
+    a->refs = const_cast<int32_t*>(refs);
+    a->pages = const_cast<int32_t*>(pages);
+    a->len = const_cast<int32_t*>(len);
+    a->lists = lists;
+    a->wide = max_pages;
+    return KVFIX_OK;
+}
+
+// Whether [p, p + n) meets the books or the pool.
+static bool books_meet(const PagesArgs& a, const kvfix_pool& pool, const void* p, size_t n) {
+    return pool_meets(pool, p, n) || overlaps_bytes(p, n, a.refs, 4 * (size_t)a.total) ||
+           overlaps_bytes(p, n, a.pages, 4 * (size_t)a.lists * a.wide) || overlaps_bytes(p, n, a.len, 4 * (size_t)a.lists);
+}
+
+size_t kvfix_pages_extend_workspace_bytes(int32_t pool_pages, int32_t lists) {
+    return pool_pages < 1 || lists < 0 ? 0 : extend_workspace_bytes(pool_pages, lists);
+}
+
+kvfix_status kvfix_pages_extend(kvfix_pool pool, int32_t page_tokens, int32_t* refs, int32_t* pages, int32_t max_pages,
+                                int32_t* len, int32_t lists, const int32_t* parent, const int32_t* extra, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    const char* fn = "kvfix_pages_extend";
+    PagesArgs a;
+    kvfix_status st;
+    if ((st = check_pages(fn, pool, page_tokens, refs, pages, max_pages, len, lists, &a)) != KVFIX_OK) return st;
+    if (lists > 0 && !extra) return fail(KVFIX_EINVAL, "%s: extra is null", fn);
+    if (!aligned4(parent) || !aligned4(extra)) return fail(KVFIX_EINVAL, "%s: parent and extra must be 4-byte aligned", fn);
+    const size_t need = extend_workspace_bytes(a.total, lists), n = 4 * (size_t)lists;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+        return fail(KVFIX_EINVAL, "%s: workspace needs %zu bytes, 16-byte aligned (got %zu)", fn, need, workspace_bytes);
+    if (books_meet(a, pool, workspace, need) || books_meet(a, pool, parent, n) || books_meet(a, pool, extra, n) ||
+        overlaps_bytes(workspace, need, parent, n) || overlaps_bytes(workspace, need, extra, n))
+        return fail(KVFIX_EINVAL, "%s: workspace, parent and extra must not overlap the books, the pool or each other", fn);
+    return launched(launch_pages_extend(a, parent, extra, workspace, (cudaStream_t)stream), fn);
+}
+
+kvfix_status kvfix_pages_cut(kvfix_pool pool, int32_t page_tokens, int32_t* refs, int32_t* pages, int32_t max_pages,
+                             int32_t* len, int32_t lists, const int32_t* base, const int32_t* path, int32_t max_path,
+                             const int32_t* kept, void* stream) {
+    const char* fn = "kvfix_pages_cut";
+    PagesArgs a;
+    kvfix_status st;
+    if ((st = check_pages(fn, pool, page_tokens, refs, pages, max_pages, len, lists, &a)) != KVFIX_OK) return st;
+    if (lists > 0 && !base) return fail(KVFIX_EINVAL, "%s: base is null", fn);
+    if (max_path < 0 || (double)lists * max_path >= 1073741824.0)
+        return fail(KVFIX_EINVAL, "%s: max_path must be >= 0, with fewer than 2^30 entries together", fn);
+    if (lists > 0 && max_path > 0 && (!path || !kept)) return fail(KVFIX_EINVAL, "%s: path and kept are required with max_path", fn);
+    if (max_path == 0 && (path || kept)) return fail(KVFIX_EINVAL, "%s: path and kept need max_path", fn);
+    if (!aligned4(base) || !aligned4(path) || !aligned4(kept))
+        return fail(KVFIX_EINVAL, "%s: base, path and kept must be 4-byte aligned", fn);
+    const size_t n = 4 * (size_t)lists;
+    if (books_meet(a, pool, base, n) || books_meet(a, pool, path, n * max_path) || books_meet(a, pool, kept, n))
+        return fail(KVFIX_EINVAL, "%s: base, path and kept must not overlap the books or the pool", fn);
+    return launched(launch_pages_cut(a, base, path, max_path, kept, (cudaStream_t)stream), fn);
+}
+
+size_t kvfix_pages_compact_workspace_bytes(int32_t pool_pages) {
+    return pool_pages < 1 ? 0 : compact_workspace_bytes(pool_pages);
+}
+
+kvfix_status kvfix_pages_compact(kvfix_pool pool, int32_t page_tokens, int32_t* refs, int32_t* pages, int32_t max_pages,
+                                 const int32_t* len, int32_t lists, int32_t* live, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    const char* fn = "kvfix_pages_compact";
+    PagesArgs a;
+    kvfix_status st;
+    if ((st = check_pages(fn, pool, page_tokens, refs, pages, max_pages, len, lists, &a)) != KVFIX_OK) return st;
+    if (!live || !aligned4(live)) return fail(KVFIX_EINVAL, "%s: live must be a 4-byte aligned device pointer", fn);
+    const size_t need = compact_workspace_bytes(a.total);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+        return fail(KVFIX_EINVAL, "%s: workspace needs %zu bytes, 16-byte aligned (got %zu)", fn, need, workspace_bytes);
+    if (books_meet(a, pool, workspace, need) || books_meet(a, pool, live, 4) || overlaps_bytes(workspace, need, live, 4))
+        return fail(KVFIX_EINVAL, "%s: live and workspace must not overlap each other, the books or the pool", fn);
+    return launched(launch_pages_compact(a, live, workspace, (cudaStream_t)stream), fn);
 }
 
 kvfix_status kvfix_selftest_wait(int64_t limit_cycles, const int32_t* flag, void* stream) {

@@ -1,5 +1,6 @@
-// attend.cu -- kvfix_shared_attend: attention of a round's agents over a shared prefix and
-// their own tokens, straight from a paged pool.
+// attend.cu -- kvfix_shared_attend and kvfix_tree_attend: attention of a round's agents over a
+// shared prefix and their own tokens, the last of them new ones in a row or a tree of drafts,
+// straight from a paged pool.
 //
 // Mathematics.  The keys of a query lie in two segments, its group's prefix and its agent's
 // suffix.  Softmax over their union is joined from parts: a part (any set of keys) keeps per
@@ -246,7 +247,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-template <int F, int D>
+// TREE: kvfix_tree_attend's, whose rows see the nodes of their tree by bits.
+template <int F, int D, bool TREE>
 __global__ void __launch_bounds__(AtCfg<F, D>::kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ AttendArgs a, const __grid_constant__ AtWork w) {
@@ -690,6 +692,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         bool ok = true;
         unsigned at = 0, units = 0;
         int rows = 0, sees = 0;   // of the unit: the group's rows; keys this row sees
+        int tree0 = 0x7fffffff;   // trees: where the tree begins, in own keys
+        const uint32_t* mask = nullptr;  // and this row's view of it
         float m = -INFINITY, l = 0.f;
         while (true) {
             ok = item_wait(g, at);
@@ -704,10 +708,21 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 m = -INFINITY;
                 l = 0.f;
                 sees = 0;
+                tree0 = 0x7fffffff;
                 if (row < rows) {
                     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
                     const int x = it.row0 + row, ag = x / TG, t = (x - ag * TG) / G;
-                    if (flags & kPrefix) {
+                    if constexpr (TREE) {
+                        bool ignore = false;
+                        const int agent = it.agent0 + ag;
+                        const int own = clamp_len(__ldg(a.suffix_len + agent), (long long)a.max_suffix_pages * a.page, ignore);
+                        const int nodes = tree_nodes(a, agent, own, ignore);
+                        if (t < nodes) {
+                            sees = flags & kPrefix ? it.sees0 : own - nodes + 1 + t;
+                            if (!(flags & kPrefix)) tree0 = own - nodes;
+                            mask = a.tree + ((long long)agent * T + t) * a.tree_words;
+                        }
+                    } else if (flags & kPrefix) {
                         // the new tokens stand at the end of the sequence: with fewer own keys
                         // than new tokens the first ones miss part of the prefix
                         bool ignore = false;
@@ -745,13 +760,20 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 // one is worked on: the maximum, then the weights
                 uint32_t x[2][32];
                 float mx = -INFINITY;
-                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys)) {
+                if (__any_sync(0xffffffffu, absent != 0u || nv < kAtKeys || (TREE && key0 + kAtKeys > tree0))) {
                     // columns that hold no key, or none that this row sees: -inf (on the side, so
                     // that the sweeps' code stays small)
 #pragma unroll 1
                     for (int c0 = 0; c0 < kAtKeys; c0 += 32) {
                         tmem_ld32(s_at + c0, x[0]);
                         tmem_wait_ld32(x[0]);
+                        if constexpr (TREE) {
+                            const uint32_t view = key0 + c0 + 32 > tree0 ? tree_view(a, mask, key0 + c0 - tree0) : 0xffffffffu;
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(view >> i & 1u)) x[0][i] = 0xff800000u;
+                        }
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const int n = (absent >> (c0 / 16 + b)) & 1u ? 0 : nv - c0 - 16 * b;
@@ -1172,28 +1194,28 @@ static cudaError_t allow_smem(Kernel* kernel, int bytes, int device) {
     return e;
 }
 
-template <int F, int D, int NT>
+template <int F, int D, int NT, bool TREE>
 static cudaError_t launch_few(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
     using C = FewCfg<F, D>;
-    const cudaError_t e = allow_smem<F, D, NT>(attend_few_kernel<F, D, NT>, C::kSmem, device);
+    const cudaError_t e = allow_smem<F, D, NT + 4 * TREE>(attend_few_kernel<F, D, NT, TREE>, C::kSmem, device);
     if (e != cudaSuccess) return e;
-    return launch_chained(attend_few_kernel<F, D, NT>, dim3(w.ctas), dim3(32 * kFewWarps), C::kSmem, s, a, w);
+    return launch_chained(attend_few_kernel<F, D, NT, TREE>, dim3(w.ctas), dim3(32 * kFewWarps), C::kSmem, s, a, w);
 }
 
-template <int F, int D>
+template <int F, int D, bool TREE>
 static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
     using C = AtCfg<F, D>;
     cudaError_t e;
-    if ((e = launch_chained(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
+    if ((e = launch_chained(attend_plan_kernel<TREE>, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
     if (w.many) {
         CUtensorMap mk, mv;
         if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;
-        if ((e = allow_smem<F, D, 0>(attend_kernel<F, D>, C::kSmem, device)) != cudaSuccess) return e;
-        e = launch_chained(attend_kernel<F, D>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w);
+        if ((e = allow_smem<F, D, 4 * TREE>(attend_kernel<F, D, TREE>, C::kSmem, device)) != cudaSuccess) return e;
+        e = launch_chained(attend_kernel<F, D, TREE>, dim3(w.ctas), dim3(C::kThreads), C::kSmem, s, mk, mv, a, w);
         if (e != cudaSuccess) return e;
     }
     if (w.few > 0) {
-        e = w.few == 8 ? launch_few<F, D, 1>(a, w, device, s) : launch_few<F, D, 2>(a, w, device, s);
+        e = w.few == 8 ? launch_few<F, D, 1, TREE>(a, w, device, s) : launch_few<F, D, 2, TREE>(a, w, device, s);
         if (e != cudaSuccess) return e;
     }
     const long long rows = (long long)a.agents * a.new_tokens * a.q_heads;
@@ -1206,6 +1228,18 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int 
         return launch_chained(attend_join_kernel<D, 1, 4>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a, w);
     }
     return launch_chained(attend_join_kernel<D, 1, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, w);
+}
+
+template <bool TREE>
+static cudaError_t launch_attend_any(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
+    switch (a.pool.format * 2 + (a.pool.dim == 128)) {
+        case KVFIX_POOL_BF16 * 2: return launch_attend_form<KVFIX_POOL_BF16, 64, TREE>(a, w, device, s);
+        case KVFIX_POOL_BF16 * 2 + 1: return launch_attend_form<KVFIX_POOL_BF16, 128, TREE>(a, w, device, s);
+        case KVFIX_POOL_E4M3 * 2: return launch_attend_form<KVFIX_POOL_E4M3, 64, TREE>(a, w, device, s);
+        case KVFIX_POOL_E4M3 * 2 + 1: return launch_attend_form<KVFIX_POOL_E4M3, 128, TREE>(a, w, device, s);
+        case KVFIX_POOL_INT4 * 2: return launch_attend_form<KVFIX_POOL_INT4, 64, TREE>(a, w, device, s);
+        default: return launch_attend_form<KVFIX_POOL_INT4, 128, TREE>(a, w, device, s);
+    }
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
@@ -1228,14 +1262,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t s) {
     w.few = l.few;
     w.many = l.many;
     w.ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
-    switch (a.pool.format * 2 + (a.pool.dim == 128)) {
-        case KVFIX_POOL_BF16 * 2: return launch_attend_form<KVFIX_POOL_BF16, 64>(a, w, dev, s);
-        case KVFIX_POOL_BF16 * 2 + 1: return launch_attend_form<KVFIX_POOL_BF16, 128>(a, w, dev, s);
-        case KVFIX_POOL_E4M3 * 2: return launch_attend_form<KVFIX_POOL_E4M3, 64>(a, w, dev, s);
-        case KVFIX_POOL_E4M3 * 2 + 1: return launch_attend_form<KVFIX_POOL_E4M3, 128>(a, w, dev, s);
-        case KVFIX_POOL_INT4 * 2: return launch_attend_form<KVFIX_POOL_INT4, 64>(a, w, dev, s);
-        default: return launch_attend_form<KVFIX_POOL_INT4, 128>(a, w, dev, s);
-    }
+    return a.tree ? launch_attend_any<true>(a, w, dev, s) : launch_attend_any<false>(a, w, dev, s);
 }
 
 }  // namespace kvfix

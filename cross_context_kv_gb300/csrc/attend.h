@@ -1,4 +1,4 @@
-// attend.h -- the arguments of one kvfix_shared_attend call, as the kernels take them.
+// attend.h -- the arguments of one kvfix_shared_attend or kvfix_tree_attend call, as the kernels take them.
 #pragma once
 
 #include "pool.cuh"
@@ -21,6 +21,10 @@ struct AttendArgs {
     const int32_t* suffix_len;    // [agents]
     float scale_log2;             // softmax scale times log2 e
     void* workspace;
+    // kvfix_tree_attend
+    const uint32_t* tree;  // [agents][new_tokens][tree_words], or null: new tokens see all before them
+    const int32_t* nodes;  // [agents], or null: new_tokens each
+    int tree_words;
 };
 
 size_t attend_workspace_bytes(int agents, int new_tokens, int q_heads, int kv_heads, int head_dim, int groups);

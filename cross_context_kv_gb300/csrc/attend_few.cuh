@@ -103,8 +103,8 @@ __device__ __forceinline__ void read_words(uint32_t* w, const unsigned char* p) 
     }
 }
 
-// NT: groups of 8 queries.
-template <int F, int D, int NT>
+// NT: groups of 8 queries.  TREE: kvfix_tree_attend's.
+template <int F, int D, int NT, bool TREE>
 __global__ void __launch_bounds__(32 * kFewWarps, 1)
     attend_few_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ AtWork w) {
     using C = FewCfg<F, D>;
@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         // queries, and how many keys each of this lane's columns sees
         uint32_t qf[NT][kSteps][2];
         int sees[NT][2];
+        const uint32_t* mask[NT][2];  // trees: the columns' views of their tree
+        int tree0 = 0x7fffffff;       // and where it begins
         // running maxima of the logits, and of the logits with the values' exponents (e4m3); sums
         float m[NT][2], my[NT][2], l[NT][2], o[kSteps][NT][4];
         float unit[NT][2];  // what a product of a query and a key's codes counts, in base-2 logits
@@ -239,8 +241,16 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
                 // to its own, and with fewer own keys than new tokens the first ones miss part of
                 // the prefix.
                 const int col = 8 * n + 2 * t + x, rc = e.row0 + col, ag = rc / TG, tok = (rc - ag * TG) / G;
+                if constexpr (TREE) mask[n][x] = a.tree;
                 if (col >= e.rows) {
                     sees[n][x] = 0;
+                } else if constexpr (TREE) {
+                    bool ignore = false;
+                    const int mine = clamp_len(__ldg(a.suffix_len + e.agent0 + ag), (long long)a.max_suffix_pages * a.page, ignore);
+                    const int nodes = tree_nodes(a, e.agent0 + ag, mine, ignore);
+                    if (tok < nodes) mask[n][x] += ((long long)(e.agent0 + ag) * T + tok) * a.tree_words;
+                    sees[n][x] = tok >= nodes ? 0 : prefix ? e.keys : mine - nodes + 1 + tok;
+                    if (!prefix) tree0 = mine - nodes;
                 } else if (prefix) {
                     bool ignore = false;
                     const int mine = clamp_len(__ldg(a.suffix_len + e.agent0 + ag), (long long)a.max_suffix_pages * a.page, ignore);
@@ -350,12 +360,22 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
             // so that the largest summand has f16's full precision whatever the rows' scales are
             bool raise = false;
             float top[NT][2], y[NT][4], top_y[NT][2];
+            // (tree0 is the segment's, but columns without a row have not read it)
+            uint32_t view[NT][2];
+            if constexpr (TREE) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        view[n][x] = tile * 16 + 16 > tree0 ? tree_view(a, mask[n][x], tile * 16 - tree0) >> g : 0xffffffffu;
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int r = x >> 1, key = g + 8 * r;
-                    const bool seen = key < keys_here && tile * 16 + key < sees[n][x & 1];
+                    bool seen = key < keys_here && tile * 16 + key < sees[n][x & 1];
+                    if constexpr (TREE) seen = seen && (view[n][x & 1] >> (8 * r) & 1u);
                     float z = s[n][x] * unit[n][x & 1];
                     if (kE4m3) z *= ke[r];
                     s[n][x] = seen ? z : -INFINITY;

@@ -116,6 +116,22 @@ __device__ __forceinline__ int clamp_len(int n, long long most, bool& bad) {
     return (int)min(max((long long)n, 0ll), most);
 }
 
+// Trees: an agent's number of nodes, with `keys` own keys.
+__device__ __forceinline__ int tree_nodes(const AttendArgs& a, int agent, int keys, bool& bad) {
+    const int given = a.nodes ? __ldg(a.nodes + agent) : a.new_tokens;
+    return clamp_len(given, min(a.new_tokens, keys), bad);
+}
+
+// Trees: 32 keys of node t's view as bits, the first of them node d of its tree (below 0: before
+// the tree, and seen).  Bits past t mean nothing.
+__device__ __forceinline__ uint32_t tree_view(const AttendArgs& a, const uint32_t* mask, int d) {
+    if (d <= -32) return 0xffffffffu;
+    if (d < 0) return (__ldg(mask) << -d) | ((1u << -d) - 1u);
+    const int w = d >> 5;
+    const uint32_t lo = w < a.tree_words ? __ldg(mask + w) : 0u, hi = w + 1 < a.tree_words ? __ldg(mask + w + 1) : 0u;
+    return __funnelshift_r(lo, hi, d & 31);
+}
+
 // A quotient of non-negative numbers, in 32 bits where they fit (a 64-bit division takes
 // about a hundred instructions).
 __device__ __forceinline__ long long quotient(long long x, long long y) {
@@ -170,6 +186,8 @@ __device__ __forceinline__ PlanSums plan_scan(const PlanSums& x, PlanSums* warp_
 
 constexpr int kPlanKept = 256;  // entries of a line that stay in shared memory
 
+// TREE: kvfix_tree_attend's, whose agents have numbers of new tokens of their own.
+template <bool TREE>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendArgs a,
                                                                    const __grid_constant__ AtWork w) {
     __shared__ PlanSums warp_sums[kPlanThreads / 32];
@@ -216,6 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     }
     struct Seg {
         int agent0, rows, keys;
+        int nodes;  // trees: of a suffix
         bool prefix;
     };
     auto segment = [&](int s) {
@@ -225,6 +244,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         const int given = s == s0 ? len0 : g.prefix ? __ldg(a.prefix_len + s) : __ldg(a.suffix_len + g.agent0);
         g.keys = clamp_len(given, g.prefix ? most_p : most_s, bad);
         g.rows = (g.prefix ? w.bounds[s + 1] - g.agent0 : 1) * TG;
+        g.nodes = TREE && !g.prefix ? tree_nodes(a, g.agent0, g.keys, bad) : T;
         return g;
     };
     auto block = [&](const Seg& g, int s, int r0, int& kind) {
@@ -234,7 +254,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         e.seg = s;
         e.agent0 = g.agent0;
         // own keys are seen up to the place of the block's last row
-        e.keys = g.prefix ? g.keys : max(0, g.keys - T + 1 + (r0 + e.rows - 1) / G);
+        if constexpr (TREE)
+            e.keys = g.prefix ? g.keys : r0 / G >= g.nodes ? 0 : g.keys - g.nodes + 1 + min(g.nodes - 1, (r0 + e.rows - 1) / G);
+        else
+            e.keys = g.prefix ? g.keys : max(0, g.keys - T + 1 + (r0 + e.rows - 1) / G);
         kind = at_kind(e.rows, w.few);
         e.tiles = (e.keys + at_keys(kind) - 1) / at_keys(kind);
         return e;

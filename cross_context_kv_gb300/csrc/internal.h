@@ -169,6 +169,9 @@ cudaError_t launch_pool_read(const kvfix_pool& pool, const int32_t* slots, const
 // Shared-prefix attention (attend.h).
 unsigned read_status_attend(cudaStream_t stream);
 
+// Page books (pages.h).
+unsigned read_status_pages(cudaStream_t stream);
+
 // Bounded-wait self test.
 unsigned read_status_selftest(cudaStream_t stream);
 cudaError_t launch_selftest_wait(long long limit_cycles, const int* flag, cudaStream_t s);

@@ -1,0 +1,223 @@
+// rotary.cu -- kvfix_rotary: rotary positions of queries and keys, one position per token.
+//
+// Mathematics.  A pair (a, b) of a head turns by the angle p theta_i: (a c - b s, b c + a s) with
+// c, s = m cos, m sin.  Positions reach 2^31 and theta_i is a double, so the angle is kept in
+// turns as a 64-bit fraction: p (theta_i / 2 pi) 2^64 modulo 2^64 is one integer product, exact
+// but for the rounding of theta_i itself (2^-54 of it), where a product of doubles would lose
+// what lies beyond 53 bits and this part has few double units.  One conversion to float and
+// sincospi follow: both are off by 2^-23 or less of their value.
+//
+// Layout.  A thread owns a column of its token's heads: two 8-wide vectors, the ones that turn into each
+// other (half layout) or neighbours (interleaved), so it computes eight (cos, sin) once and uses
+// them for every head of queries and keys, and for the layers of its block; four heads' loads
+// are in flight together.  Where little work is left for each, the heads of a token are spread over
+// threads, then every thread has its own head.  Values beyond rotary_dim are columns that are
+// copied, or left out when the call works in place.  A rotary_dim that is no multiple of 16 has
+// columns of one pair, loaded as two 16-bit values.
+//
+// Bound by HBM: see the measured figures at launch_rotary.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "rotary.h"
+
+namespace kvfix {
+
+constexpr int kRotaryThreads = 256;
+constexpr int kRotaryHeads = 4;  // heads whose loads are in flight together
+
+struct RotarySplit {
+    int columns;      // threads per (token, run of heads)
+    int runs;         // threads that share a token's heads
+    int tile;         // tokens per block
+    int tiles;        // blocks per (chunk, layers)
+    int layer_block;  // layers per block
+    int layer_blocks;
+};
+
+template <bool VEC>
+struct RotaryValues;
+template <>
+struct RotaryValues<true> {
+    static constexpr int kPairs = 8;
+    uint4 lo, hi;
+    __device__ __forceinline__ void load(const uint16_t* p, int a, int b) {
+        lo = *reinterpret_cast<const uint4*>(p + a);
+        hi = *reinterpret_cast<const uint4*>(p + b);
+    }
+    __device__ __forceinline__ void store(uint16_t* p, int a, int b) const {
+        *reinterpret_cast<uint4*>(p + a) = lo;
+        *reinterpret_cast<uint4*>(p + b) = hi;
+    }
+    template <int LAYOUT>
+    __device__ __forceinline__ void turn(const float* c, const float* s) {
+        float x[8], y[8];
+        unpack8(lo, x);
+        unpack8(hi, y);
+        if (LAYOUT == KVFIX_ROPE_HALF) {
+            rotate_pair(x, y, c, s);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float a = x[2 * k], b = x[2 * k + 1];
+                x[2 * k] = __fmaf_rn(a, c[k], __fmul_rn(b, -s[k]));
+                x[2 * k + 1] = __fmaf_rn(b, c[k], __fmul_rn(a, s[k]));
+                const float d = y[2 * k], e = y[2 * k + 1];
+                y[2 * k] = __fmaf_rn(d, c[k + 4], __fmul_rn(e, -s[k + 4]));
+                y[2 * k + 1] = __fmaf_rn(e, c[k + 4], __fmul_rn(d, s[k + 4]));
+            }
+        }
+        lo = pack8(x);
+        hi = pack8(y);
+    }
+};
+template <>
+struct RotaryValues<false> {
+    static constexpr int kPairs = 1;
+    uint16_t lo, hi;
+    __device__ __forceinline__ void load(const uint16_t* p, int a, int b) {
+        lo = p[a];
+        hi = p[b];
+    }
+    __device__ __forceinline__ void store(uint16_t* p, int a, int b) const {
+        p[a] = lo;
+        p[b] = hi;
+    }
+    template <int LAYOUT>
+    __device__ __forceinline__ void turn(const float* c, const float* s) {
+        const float x = __bfloat162float(__ushort_as_bfloat16(lo)), y = __bfloat162float(__ushort_as_bfloat16(hi));
+        lo = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(x, c[0], __fmul_rn(y, -s[0]))));
+        hi = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(y, c[0], __fmul_rn(x, s[0]))));
+    }
+};
+
+template <int LAYOUT, bool VEC>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a,
+                                                                const __grid_constant__ RotarySplit w) {
+    using V = RotaryValues<VEC>;
+    constexpr int N = V::kPairs;
+    const int slot = threadIdx.x / w.columns, col = threadIdx.x - slot * w.columns;
+    const int in_tile = slot / w.runs, run = slot - in_tile * w.runs;
+    unsigned b = blockIdx.x;
+    const int lb = (int)(b % (unsigned)w.layer_blocks);
+    b /= (unsigned)w.layer_blocks;
+    const int chunk = (int)(b / (unsigned)w.tiles), tile = (int)(b - (unsigned)chunk * (unsigned)w.tiles);
+    const int t = tile * w.tile + in_tile;
+    if (in_tile >= w.tile || t >= a.tokens) return;
+    const int turning = a.rotary_dim / (2 * N);  // columns that turn
+    // places of the column's two parts in a head
+    int pa, pb;
+    if (col >= turning) {
+        pa = a.rotary_dim + (col - turning) * 2 * N;
+        pb = pa + N;
+    } else if (LAYOUT == KVFIX_ROPE_HALF) {
+        pa = col * N;
+        pb = pa + a.rotary_dim / 2;
+    } else {
+        pa = col * 2 * N;
+        pb = pa + N;
+    }
+    const int p = __ldg(a.positions + (long long)chunk * a.tokens + t);
+    // (position 0 and no factor: the values as they are, infinities and signs of zeros too)
+    const bool turns = col < turning && (p != 0 || a.attention != 1.f);
+    float c[N], s[N];
+    if (turns) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const long long phase = (long long)((unsigned long long)(long long)p * a.turns[col * N + k]);
+            sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s[k], &c[k]);  // 2^-63: half turns
+            c[k] *= a.attention;
+            s[k] *= a.attention;
+        }
+    }
+    const int heads0 = a.ip[0].heads, heads = heads0 + a.ip[1].heads;
+    const int l1 = min(a.layers, (lb + 1) * w.layer_block);
+    for (int l = lb * w.layer_block; l < l1; ++l) {
+        const uint16_t* in0 = a.in[0] + a.ip[0].row(chunk, l, t);
+        const uint16_t* in1 = a.in[1] + a.ip[1].row(chunk, l, t);
+        uint16_t* out0 = a.out[0] + a.op[0].row(chunk, l, t);
+        uint16_t* out1 = a.out[1] + a.op[1].row(chunk, l, t);
+        for (int h0 = run; h0 < heads; h0 += kRotaryHeads * w.runs) {
+            V v[kRotaryHeads];
+#pragma unroll
+            for (int i = 0; i < kRotaryHeads; ++i) {
+                const int h = h0 + i * w.runs;
+                if (h < heads) v[i].load(h < heads0 ? in0 + h * a.dim : in1 + (h - heads0) * a.dim, pa, pb);
+            }
+#pragma unroll
+            for (int i = 0; i < kRotaryHeads; ++i) {
+                const int h = h0 + i * w.runs;
+                if (h >= heads) continue;
+                if (turns) v[i].template turn<LAYOUT>(c, s);
+                v[i].store(h < heads0 ? out0 + h * a.dim : out1 + (h - heads0) * a.dim, pa, pb);
+            }
+        }
+    }
+}
+
+void rotary_angles(const kvfix_rope& r, RotaryArgs* a) {
+    const int n = r.rotary_dim;
+    const double kTwoPi = 6.283185307179586;
+    double lo = 0.0, width = 1.0;  // yarn: the pair from which frequencies change, and over how many
+    if (r.scaling == KVFIX_ROPE_YARN) {
+        auto pair = [&](double turns) { return n * log(r.original_tokens / (kTwoPi * turns)) / (2.0 * log(r.base)); };
+        const double hi = fmin(ceil(pair(r.low)), (double)(n - 1));
+        lo = fmax(floor(pair(r.high)), 0.0);
+        width = fmax(hi - lo, 1e-3);
+    }
+    memset(a->turns, 0, sizeof a->turns);
+    for (int i = 0; i < n / 2; ++i) {
+        double theta = pow(r.base, -2.0 * (double)i / (double)n);
+        double keep = 1.0;  // the share that keeps its frequency
+        if (r.scaling == KVFIX_ROPE_LINEAR) keep = 0.0;
+        if (r.scaling == KVFIX_ROPE_BANDS) keep = (r.original_tokens * theta / kTwoPi - r.low) / (r.high - r.low);
+        if (r.scaling == KVFIX_ROPE_YARN) keep = 1.0 - (i - lo) / width;
+        keep = fmin(fmax(keep, 0.0), 1.0);
+        if (r.scaling != KVFIX_ROPE_PLAIN) theta *= keep + (1.0 - keep) / r.factor;
+        const double turn = theta / kTwoPi;
+        a->turns[i] = (unsigned long long)ldexp(turn - floor(turn), 64);
+    }
+    a->rotary_dim = n;
+    a->layout = r.layout;
+    a->attention = (float)r.attention;
+}
+
+// The split.  A thread has a token's heads one after another, four in flight, while that leaves
+// enough threads to fill the GPU; with fewer tokens the heads are spread over 2, 4, ... threads until
+// each has one.  Blocks take several layers (a thread's angles are used for all of them) where
+// that leaves four blocks an SM.
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
+    const int heads = a.ip[0].heads + a.ip[1].heads;
+    if (a.chunks == 0 || a.layers == 0 || a.tokens == 0 || heads == 0) return cudaSuccess;
+    const bool vec = a.rotary_dim % 16 == 0;
+    RotarySplit w;
+    w.columns = (a.in_place ? a.rotary_dim : a.dim) / (vec ? 16 : 2);
+    const int slots = kRotaryThreads / w.columns;
+    const double rows = (double)a.chunks * a.layers * a.tokens, full = 152.0 * 1536.0;
+    w.runs = 1;
+    while (w.runs * 2 <= slots && w.runs < heads && rows * w.columns * w.runs < full) w.runs *= 2;
+    w.tile = slots / w.runs;
+    if (w.tile > a.tokens) w.tile = a.tokens;
+    w.tiles = (a.tokens + w.tile - 1) / w.tile;
+    w.layer_block = 1;
+    while (w.layer_block < 8 && w.layer_block * 2 <= a.layers &&
+           (double)a.chunks * w.tiles * ((a.layers + 2 * w.layer_block - 1) / (2 * w.layer_block)) >= 4.0 * 152)
+        w.layer_block *= 2;
+    w.layer_blocks = (a.layers + w.layer_block - 1) / w.layer_block;
+    const double blocks = (double)a.chunks * w.tiles * w.layer_blocks;
+    if (blocks > 2147483647.0) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)((long long)a.chunks * w.tiles * w.layer_blocks)), threads(kRotaryThreads);
+    if (vec) {
+        if (a.layout == KVFIX_ROPE_HALF) rotary_kernel<KVFIX_ROPE_HALF, true><<<grid, threads, 0, s>>>(a, w);
+        else rotary_kernel<KVFIX_ROPE_INTERLEAVED, true><<<grid, threads, 0, s>>>(a, w);
+    } else {
+        if (a.layout == KVFIX_ROPE_HALF) rotary_kernel<KVFIX_ROPE_HALF, false><<<grid, threads, 0, s>>>(a, w);
+        else rotary_kernel<KVFIX_ROPE_INTERLEAVED, false><<<grid, threads, 0, s>>>(a, w);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace kvfix

@@ -53,10 +53,17 @@ class PoolDesc(ctypes.Structure):
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
+class RopeDesc(ctypes.Structure):
+    """kvfix_rope."""
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_tokens", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("attention", ctypes.c_double)]
+
+
 # name -> (restype, argtypes); mirrors include/kvfix.h
 P, I32, I64, F64, SZ, D = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double,
                            ctypes.c_size_t, KvDesc)
-PD = PoolDesc
+PD, RD = PoolDesc, RopeDesc
 SIGNATURES = {
     "kvfix_version": (ctypes.c_int, []),
     "kvfix_last_error": (ctypes.c_char_p, []),
@@ -86,6 +93,13 @@ SIGNATURES = {
     "kvfix_pool_read": (ctypes.c_int, [PD, P, P, F64, P, P, D, P]),
     "kvfix_shared_attend_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
     "kvfix_shared_attend": (ctypes.c_int, [P, D, PD, I32, P, I32, P, P, I32, P, I32, P, F64, P, D, P, P, SZ, P]),
+    "kvfix_rotary": (ctypes.c_int, [P, D, P, D, P, RD, P, D, P, D, P]),
+    "kvfix_tree_attend": (ctypes.c_int, [P, D, PD, I32, P, I32, P, P, I32, P, I32, P, P, P, F64, P, D, P, P, SZ, P]),
+    "kvfix_pages_extend_workspace_bytes": (SZ, [I32, I32]),
+    "kvfix_pages_extend": (ctypes.c_int, [PD, I32, P, P, I32, P, I32, P, P, P, SZ, P]),
+    "kvfix_pages_cut": (ctypes.c_int, [PD, I32, P, P, I32, P, I32, P, P, I32, P, P]),
+    "kvfix_pages_compact_workspace_bytes": (SZ, [I32]),
+    "kvfix_pages_compact": (ctypes.c_int, [PD, I32, P, P, I32, P, I32, P, P, SZ, P]),
     "kvfix_repair_rows": (ctypes.c_int, [P, P, D, P, P, D, P, I32, P, P]),
     "kvfix_anchor_gate_workspace_bytes": (SZ, [D, I32, I32]),
     "kvfix_anchor_gate": (ctypes.c_int, [P, D, P, P, I32, I32, I32, F64, F64, P, P, P, P, P, SZ, P]),
@@ -771,6 +785,59 @@ def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, pre
     the first suffix_len[a] on suffix_pages[a], the T newest of them its own queries' places.
     Groups are the runs of agents group_begin[g] .. group_begin[g+1].  scale: dim^-1/2 if None.
     Returns out, shaped like q, or (out, lse [agents][T][q_heads])."""
+    return _attend(lib.kvfix_shared_attend, (), q, pool, page_tokens, suffix_pages, suffix_len, prefix_pages, prefix_len,
+                   group_begin, scale, out, return_lse, workspace)
+
+
+def tree_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, tree_mask, nodes=None, prefix_pages=None,
+                prefix_len=None, group_begin=None, scale: float | None = None, out=None, return_lse: bool = False,
+                workspace=None):
+    """shared_attend of a tree of drafts: the last nodes[a] (T if nodes is None) of agent a's own
+    keys are the nodes that its first queries stand for, and node t sees of them those j <= t whose
+    bit is set in tree_mask [agents][T][ceil(T/32)] int32 (see tree_masks).  Queries past nodes[a]
+    give 0, and -inf.  The workspace is shared_attend's."""
+    _i32(tree_mask, "tree_mask")
+    if q.dim() != 4:
+        raise ValueError("q must be [agents][new tokens][heads][dim]")
+    A, T = q.shape[:2]
+    if tree_mask.shape != (A, T, (T + 31) // 32):
+        raise ValueError(f"tree_mask must be [{A}][{T}][{(T + 31) // 32}]")
+    if nodes is not None:
+        _i32(nodes, "nodes")
+        if nodes.numel() != A:
+            raise ValueError(f"nodes must hold {A} numbers")
+    if tree_mask.get_device() != q.get_device() or (nodes is not None and nodes.get_device() != q.get_device()):
+        raise ValueError("tree_mask and nodes must be on q's device")
+    tree = (None if nodes is None else nodes.data_ptr(), tree_mask.data_ptr())
+    return _attend(lib.kvfix_tree_attend, tree, q, pool, page_tokens, suffix_pages, suffix_len, prefix_pages, prefix_len,
+                   group_begin, scale, out, return_lse, workspace)
+
+
+def tree_masks(parents, device="cpu"):
+    """Masks and depths of drafted trees from their nodes' parents (each before its children; -1:
+    the node hangs on the context).  parents: a list of nodes for each agent, of any lengths.
+    Returns (tree_mask int32 [agents][T][ceil(T/32)], depth int32 [agents][T], nodes int32 [agents]):
+    node t of agent a stands at its context's length + depth[a][t]."""
+    T = max([len(p) for p in parents], default=0)
+    W = (T + 31) // 32
+    mask, depth = [], []
+    for p in parents:
+        line, deep = [], []
+        for t, up in enumerate(p):
+            if not -1 <= up < t:
+                raise ValueError(f"node {t} hangs on {up}: a parent comes before its children")
+            line.append((line[up] if up >= 0 else 0) | 1 << t)
+            deep.append(deep[up] + 1 if up >= 0 else 0)
+        line += [0] * (T - len(line))
+        # (bit 31 of a word is an int32's sign)
+        mask.append([[((x >> 32 * w & 0xffffffff) ^ 0x80000000) - 0x80000000 for w in range(W)] for x in line])
+        depth.append(deep + [0] * (T - len(deep)))
+    i32 = lambda x, *shape: torch.tensor(x, dtype=torch.int32).view(*shape).to(device)  # noqa: E731
+    return (i32(mask, len(parents), T, W), i32(depth, len(parents), T), i32([len(p) for p in parents], len(parents)))
+
+
+def _attend(call, tree, q, pool, page_tokens, suffix_pages, suffix_len, prefix_pages, prefix_len, group_begin, scale, out,
+            return_lse, workspace):
     if q.dim() != 4:
         raise ValueError("q must be [agents][new tokens][heads][dim]")
     qd, pd, dev = _rows_desc(q, "q"), pool_desc(pool), q.get_device()
@@ -810,8 +877,149 @@ def shared_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, pre
         size = workspace.numel() * workspace.element_size()
     if out.get_device() != dev or workspace.get_device() != dev:
         raise ValueError("out and workspace must be on q's device")
-    _check(lib.kvfix_shared_attend(
+    _check(call(
         q.data_ptr(), qd, pd, int(page_tokens), *shared, groups, suffix_pages.data_ptr(), suffix_pages.shape[1],
-        suffix_len.data_ptr(), Dh ** -0.5 if scale is None else float(scale), out.data_ptr(), od,
+        suffix_len.data_ptr(), *tree, Dh ** -0.5 if scale is None else float(scale), out.data_ptr(), od,
         None if lse is None else lse.data_ptr(), workspace.data_ptr(), size, _raw_stream(q)))
     return (out, lse) if return_lse else out
+
+
+# --------------------------------------------------------------------- rotary positions
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+class Rope(NamedTuple):
+    """How a model turns its queries and keys (kvfix_rope).
+    rotary_dim  the first values of a head that turn (None: all)
+    layout      "half" (pairs i, i + rotary_dim/2) or "interleaved" (pairs 2i, 2i + 1)
+    scaling     "none", "linear", "bands" or "yarn", with factor, and for the last two low, high
+                (turns over the original context) and original (its tokens)
+    attention   factor of cos and sin"""
+    base: float
+    rotary_dim: int | None = None
+    layout: str = "half"
+    scaling: str = "none"
+    factor: float = 1.0
+    low: float = 0.0
+    high: float = 0.0
+    original: int = 0
+    attention: float = 1.0
+
+
+def rope_desc(rope: Rope, head_dim: int) -> RopeDesc:
+    layout, scaling = ROPE_LAYOUTS.get(rope.layout), ROPE_SCALINGS.get(rope.scaling)
+    if layout is None or scaling is None:
+        raise ValueError(f"unknown rope layout {rope.layout!r} or scaling {rope.scaling!r}")
+    return RopeDesc(layout, head_dim if rope.rotary_dim is None else rope.rotary_dim, scaling, rope.original, rope.base,
+                    rope.factor, rope.low, rope.high, rope.attention)
+
+
+def rotary(q, k, positions, rope: Rope, q_out=None, k_out=None):
+    """Rows q and k ([C][T][heads][dim] or [C][L][T][heads][dim]; either may be None) turned to
+    positions int32 [C][T], the same in every layer.  q_out, k_out: where to (the inputs
+    themselves for in place).  Returns (q_out, k_out)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("neither queries nor keys")
+    dev = ref.get_device()
+    _launch_device(dev)
+    _i32(positions, "positions")
+    if positions.get_device() != dev:
+        raise ValueError("q, k, positions and outputs must be on one device")
+    planes = []
+    outs = []
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{name}_out without {name}")
+            planes += [None, KvDesc(), None, KvDesc()]
+            outs.append(None)
+            continue
+        d = _rows_desc(x, name)
+        if positions.numel() != d.chunks * d.tokens:
+            raise ValueError(f"positions must hold {d.chunks} x {d.tokens} numbers")
+        if y is None:
+            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        elif y.shape != x.shape:
+            raise ValueError(f"{name}_out must have {name}'s shape")
+        if x.get_device() != dev or y.get_device() != dev:
+            raise ValueError("q, k, positions and outputs must be on one device")
+        planes += [x.data_ptr(), d, y.data_ptr(), _rows_desc(y, name + "_out")]
+        outs.append(y)
+    qi, qd, qo, qod, ki, kd, ko, kod = planes
+    _check(lib.kvfix_rotary(qi, qd, ki, kd, positions.data_ptr(), rope_desc(rope, ref.shape[-1]), qo, qod, ko, kod,
+                            _raw_stream(ref)))
+    return tuple(outs)
+
+
+# --------------------------------------------------------------------- page books
+
+def _books(pool, page_tokens, refs, pages, lens, more=()):
+    """Checks the books of a pool and the call's other int32 arrays; returns the first arguments of the page calls."""
+    pd = pool_desc(pool)
+    dev = pool.k.get_device()
+    _launch_device(dev)
+    for t, name in ((refs, "refs"), (pages, "pages"), (lens, "lens"), *more):
+        if t is None:
+            continue
+        _i32(t, name)
+        if t.get_device() != dev:
+            raise ValueError("the pool, the books and their arguments must be on one device")
+    if pages.dim() != 2 or lens.numel() != pages.shape[0]:
+        raise ValueError("pages must be [lists][pages] and lens hold a length for each list")
+    if page_tokens < 1 or refs.numel() != pd.slots // page_tokens:
+        raise ValueError(f"refs must hold a count for each of the pool's {pd.slots} / {page_tokens} pages")
+    for t, name in more:
+        if t is not None and t.shape[0] != lens.numel():
+            raise ValueError(f"{name} must have a row for each list")
+    return pd, int(page_tokens), refs.data_ptr(), pages.data_ptr(), pages.shape[1], lens.data_ptr(), lens.numel()
+
+
+def _workspace(given, need, device):
+    if given is None:
+        return _empty((need,), (1,), torch.uint8)
+    if not given.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if given.get_device() != device:
+        raise ValueError("workspace must be on the pool's device")
+    return given
+
+
+def pages_extend(pool: Pool, page_tokens: int, refs, pages, lens, extra, parent=None, workspace=None):
+    """Room for extra [lists] tokens behind each list of pages [lists][max_pages] with lengths lens
+    [lists], all int32 and changed in place, refs [pages of the pool] the lists that hold each page.
+    parent [lists]: a list of which list i, empty until now, becomes a fork first (itself: it
+    grows; below 0: nothing happens).  Last pages that others hold are copied."""
+    books = _books(pool, page_tokens, refs, pages, lens, ((extra, "extra"), (parent, "parent")))
+    ws = _workspace(workspace, lib.kvfix_pages_extend_workspace_bytes(refs.numel(), lens.numel()), pool.k.get_device())
+    _check(lib.kvfix_pages_extend(*books, None if parent is None else parent.data_ptr(), extra.data_ptr(), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _raw_stream(refs)))
+
+
+def pages_cut(pool: Pool, page_tokens: int, refs, pages, lens, base, path=None, kept=None):
+    """Each list keeps its first base [lists] tokens (below 0: all of it) and behind them the tokens
+    base + path[i][j], j < kept[i] (path [lists][most], ascending); pages behind its new end are
+    given back.  All int32, the books changed in place."""
+    if (path is None) != (kept is None):
+        raise ValueError("path and kept come together")
+    books = _books(pool, page_tokens, refs, pages, lens, ((base, "base"), (path, "path"), (kept, "kept")))
+    most = 0
+    if path is not None:
+        if path.dim() != 2:
+            raise ValueError("path must be [lists][most]")
+        most = path.shape[1]
+    _check(lib.kvfix_pages_cut(*books, base.data_ptr(), path.data_ptr() if most else None, most,
+                               kept.data_ptr() if most else None, _raw_stream(refs)))
+
+
+def pages_compact(pool: Pool, page_tokens: int, refs, pages, lens, workspace=None):
+    """Pages in use move to the front of the pool, refs and the lists follow.  Returns the number of
+    pages in use, int32 [1] on the device."""
+    books = _books(pool, page_tokens, refs, pages, lens)
+    live = _empty((1,), (1,), torch.int32)
+    ws = _workspace(workspace, lib.kvfix_pages_compact_workspace_bytes(refs.numel()), pool.k.get_device())
+    _check(lib.kvfix_pages_compact(*books, live.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                   _raw_stream(refs)))
+    return live

@@ -722,6 +722,163 @@ KVFIX_API kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc q_
                                            size_t workspace_bytes, void* stream);
 
 /*
+ * kvfix_rotary -- rotary positions of queries and keys, one position per token: what a step's
+ * new rows need before they are written and attended over, and the re-alignment of cached
+ * keys whose model scales its frequencies, rotates part of a head or pairs neighbours, which
+ * kvfix_rerope does not cover.  [KVCMAS] section 2.2 and App. A.3; [BCR] App. A.
+ *
+ * With p = positions[c][t], n = rope.rotary_dim and pairs (x_a, x_b), a = i, b = i + n/2
+ * (KVFIX_ROPE_HALF) or a = 2i, b = 2i + 1 (KVFIX_ROPE_INTERLEAVED), i < n/2, in every layer and head:
+ *     y_a = m (x_a cos(p theta_i) - x_b sin(p theta_i)),  y_b = m (x_b cos(p theta_i) + x_a sin(p theta_i))
+ * and y_d = x_d for d >= n.  m = rope.attention; theta_i = base^(-2i/n), scaled by what the pair
+ * keeps of its frequency, s_i in [0, 1]: theta_i (s_i + (1 - s_i) / factor), with
+ *   KVFIX_ROPE_PLAIN   s = 1 (factor, low, high and original_tokens are not read);
+ *   KVFIX_ROPE_LINEAR  s = 0;
+ *   KVFIX_ROPE_BANDS   s = (r_i - low) / (high - low) within [0, 1], r_i = original_tokens theta_i / 2 pi
+ *                      the pair's turns over the original context;
+ *   KVFIX_ROPE_YARN    s falls with the pair's number: 1 up to lo, 0 from hi, s = 1 - (i - lo) /
+ *                      max(hi - lo, 0.001) between, lo = max(floor(z(high)), 0) and hi =
+ *                      min(ceil(z(low)), n - 1), z(r) = n log(original_tokens / (2 pi r)) / (2 log base).
+ * Rotations add up: rows at p turned by d (attention 1) are rows at p + d, so positions may be
+ * shifts, of any sign; and the gradient of a rotation is the rotation of the outputs' gradient
+ * by the negated positions, attention as it was.
+ *
+ * q, k         : planes of the same chunks, layers, tokens and head_dim, each with its heads; either
+ *                may be left out (kv_heads 0 in q_desc or k_desc: its pointers and its output's
+ *                descriptor are not read).
+ * q_out, k_out : shaped like q and k; each exactly its input (in place) or apart from both, its rows
+ *                apart from each other.  Planes may be views of one buffer whose rows
+ *                interleave, as a projection leaves them.
+ * positions    : device int32[chunks][tokens], any sign.
+ * rope         : rotary_dim even, 2..head_dim; base > 1; attention > 0 (1: a rotation alone); scaled
+ *                forms want factor >= 1, bands and yarn original_tokens >= 1 and 0 < low < high.
+ * Limits: chunks * layers * tokens < 2^31.
+ * Arithmetic: the frequencies in double on the host; angles exact modulo a turn (64-bit
+ * fractions of it); cos, sin and the rotation in float; one rounding to bf16.  Position 0 with
+ * attention 1 gives the input bit for bit.
+ */
+typedef enum { KVFIX_ROPE_HALF = 0, KVFIX_ROPE_INTERLEAVED = 1 } kvfix_rope_layout;
+typedef enum {
+    KVFIX_ROPE_PLAIN = 0,
+    KVFIX_ROPE_LINEAR = 1,
+    KVFIX_ROPE_BANDS = 2,
+    KVFIX_ROPE_YARN = 3
+} kvfix_rope_scaling;
+typedef struct {
+    int32_t layout;  /* kvfix_rope_layout */
+    int32_t rotary_dim;
+    int32_t scaling; /* kvfix_rope_scaling */
+    int32_t original_tokens;
+    double base;
+    double factor;
+    double low;  /* turns over the original context: at most low, the frequency is divided by factor; */
+    double high; /* at least high, it is kept */
+    double attention;
+} kvfix_rope;
+KVFIX_API kvfix_status kvfix_rotary(const kvfix_bf16* q, kvfix_kv_desc q_desc, const kvfix_bf16* k,
+                                    kvfix_kv_desc k_desc, const int32_t* positions, kvfix_rope rope,
+                                    kvfix_bf16* q_out, kvfix_kv_desc q_out_desc, kvfix_bf16* k_out,
+                                    kvfix_kv_desc k_out_desc, void* stream);
+
+/*
+ * kvfix_tree_attend -- kvfix_shared_attend for trees of drafted tokens: each agent's drafts are
+ * verified in one pass, every node seeing its own line of descent.  [TD] section 2.1; [BCR]
+ * App. B, Algorithm 2 (draft queries over the cache).
+ *
+ * The last N = nodes[a] of agent a's suffix_len[a] own keys are its tree's nodes, in an order in
+ * which a node comes after its ancestors; query t < N stands for node t.  It sees the agent's
+ * whole prefix, the own keys before the tree, and node j of the tree where j <= t and bit j % 32 of
+ * tree_mask[a][t][j / 32] is set (its own bit included: a mask without it hides a node from
+ * itself).  A query t >= N sees nothing: out = 0, lse = -inf, as for a row that no key is left to.
+ * nodes        : device int32[agents], or NULL: new_tokens each.  A number outside 0..min(q.tokens,
+ *                suffix_len) is clamped and flagged (KVFIX_EDEVICE in kvfix_check_status).
+ * tree_mask    : device uint32[agents][q.tokens][ceil(q.tokens / 32)]; rows of queries t >= N and
+ *                bits past t are not read.
+ * All else, the workspace (kvfix_shared_attend_workspace_bytes) and the limits are kvfix_shared_attend's,
+ * with N in the place of new_tokens.  So is the arithmetic: chains of q.tokens nodes (every bit up
+ * to t set) give the bits that kvfix_shared_attend gives for as many new tokens.  A NaN or
+ * infinity in the value row of a node may reach the agent's other nodes (a weight of zero times
+ * NaN); one in a key reaches those that see it alone.
+ */
+KVFIX_API kvfix_status kvfix_tree_attend(const kvfix_bf16* q, kvfix_kv_desc q_desc, kvfix_pool pool,
+                                         int32_t page_tokens, const int32_t* prefix_pages,
+                                         int32_t max_prefix_pages, const int32_t* prefix_len,
+                                         const int32_t* group_begin, int32_t groups,
+                                         const int32_t* suffix_pages, int32_t max_suffix_pages,
+                                         const int32_t* suffix_len, const int32_t* nodes,
+                                         const uint32_t* tree_mask, double scale, kvfix_bf16* out,
+                                         kvfix_kv_desc out_desc, float* lse, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
+ * Page books.  A list is a sequence's page list (as kvfix_shared_attend reads them) and its length:
+ * list i's token t lies in pool row pages[i][t / page_tokens] * page_tokens + t % page_tokens, for
+ * t < len[i].  refs counts, for every page of the pool, the lists that hold it; a page with none
+ * is free.  [TD] section 2.1 (agents of a round hold the same blocks) and section 4.3 (one master, many
+ * mirrors).  Prefix and suffix lists of a round may be rows of one table.  The books lie on the device and
+ * the calls below change them there, so captured graphs follow them; the same books give
+ * the same pages on every run.
+ * pool        : every layer of the pool (all are copied alike); any format.
+ * page_tokens : 16, 32, 64 or 128; pool.slots a positive multiple of it.
+ * refs        : device int32[pool.slots / page_tokens].
+ * pages       : device int32[lists][max_pages]; entries at and past ceil(len / page_tokens) mean nothing.
+ * len         : device int32[lists], each within 0..max_pages * page_tokens.
+ * Limits: lists <= 2^24, lists * max_pages < 2^30, max_pages * page_tokens < 2^30.
+ * A list whose length, pages or arguments are out of range is left as it is and flagged
+ * (KVFIX_EDEVICE in kvfix_check_status); such an entry elsewhere in its pages is skipped and flagged.
+ *
+ * kvfix_pages_extend -- room for extra[i] >= 0 tokens behind list i, which may begin as a fork:
+ *   parent[i] = i (or parent NULL): the list grows.
+ *   parent[i] = j, another list   : list i, empty until now, takes over j's tokens as they are on entry
+ *                                   and shares their pages (their counts rise).
+ *   parent[i] < 0                 : nothing happens to list i.
+ * Tokens len .. len + extra get pages; len[i] becomes that sum.  Where extra > 0 and the last page
+ * is partly full, and the list is a fork or others hold that page too (refs > 1 on entry), the
+ * list gets a copy of it instead (the rows of its own tokens, all layers), and the page counts one
+ * list less.  So rows behind a list's old length are its own to write.  New pages are the lowest
+ * free ones: list by list, a copy's first, then the others in order; pages that become free in
+ * this call are not among them.  Where the free pages do not reach, that list and every later one
+ * that needs a page are left as they were and flagged (KVFIX_ENOSPACE): their len tells.  Rows of
+ * new pages keep what they held.
+ * workspace   : device, kvfix_pages_extend_workspace_bytes(pool pages, lists) bytes, 16-byte aligned.
+ */
+KVFIX_API size_t kvfix_pages_extend_workspace_bytes(int32_t pool_pages, int32_t lists);
+KVFIX_API kvfix_status kvfix_pages_extend(kvfix_pool pool, int32_t page_tokens, int32_t* refs, int32_t* pages,
+                                          int32_t max_pages, int32_t* len, int32_t lists, const int32_t* parent,
+                                          const int32_t* extra, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/*
+ * kvfix_pages_cut -- what a list keeps: its first base[i] tokens, then, moved up behind them, the
+ * tokens base[i] + path[i][j] for j < kept[i] (a tree's accepted nodes, in ascending order); the
+ * rest is dropped, and pages behind the new length lose this list (their entries become -1).
+ *   base[i] = len[i] - T, path: nodes of a tree of T      accepts that path;
+ *   base[i] = a shorter length, kept[i] = 0 (or max_path 0) rolls the list back;
+ *   base[i] = 0, kept[i] = 0                              frees it;
+ *   base[i] < 0                                           leaves it alone.
+ * Rows move in all layers, codes and scales bit for bit.  The rows from base on have to be the
+ * list's own (kvfix_pages_extend makes them so).  Rows that are not moved to keep what they held.
+ * path        : device int32[lists][max_path], ascending from 0 or more, base + path < len.
+ * kept        : device int32[lists], each within 0..max_path.  Both NULL with max_path 0.
+ */
+KVFIX_API kvfix_status kvfix_pages_cut(kvfix_pool pool, int32_t page_tokens, int32_t* refs, int32_t* pages,
+                                       int32_t max_pages, int32_t* len, int32_t lists, const int32_t* base,
+                                       const int32_t* path, int32_t max_path, const int32_t* kept, void* stream);
+
+/*
+ * kvfix_pages_compact -- pages in use move to the front of the pool, so that what lies behind can be
+ * given back or handed to others: with n pages in use, the j-th lowest of those at n and behind
+ * moves to the j-th lowest free page below n (all layers, codes and scales bit for bit), refs and
+ * the lists' pages follow, and *live = n.  Every list that holds a page has to be among the lists.
+ * live        : device int32[1].
+ * workspace   : device, kvfix_pages_compact_workspace_bytes(pool pages) bytes, 16-byte aligned.
+ */
+KVFIX_API size_t kvfix_pages_compact_workspace_bytes(int32_t pool_pages);
+KVFIX_API kvfix_status kvfix_pages_compact(kvfix_pool pool, int32_t page_tokens, int32_t* refs, int32_t* pages,
+                                           int32_t max_pages, const int32_t* len, int32_t lists, int32_t* live,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * kvfix_selftest_wait -- exercise the bounded wait that every pipelined kernel uses, with
  * no hang: one warp waits on a barrier phase that never completes and then on the device
  * int32 *flag (optional; 0 = not set), each for at most limit_cycles SM clocks, and records
