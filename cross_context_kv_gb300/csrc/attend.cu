@@ -692,6 +692,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         bool ok = true;
         unsigned at = 0, units = 0;
         int rows = 0, sees = 0;   // of the unit: the group's rows; keys this row sees
+        bool live = false;        // whether this lane has a row that sees any: the others are computed and left
         int tree0 = 0x7fffffff;   // trees: where the tree begins, in own keys
         const uint32_t* mask = nullptr;  // and this row's view of it
         float m = -INFINITY, l = 0.f;
@@ -707,7 +708,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 rows = it.rows;
                 m = -INFINITY;
                 l = 0.f;
-                sees = 0;
+                // (a lane without a row sees every key, so that it asks for no mask)
+                sees = 0x7fffffff;
+                live = row < rows;
                 tree0 = 0x7fffffff;
                 if (row < rows) {
                     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
@@ -717,7 +720,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         const int agent = it.agent0 + ag;
                         const int own = clamp_len(__ldg(a.suffix_len + agent), (long long)a.max_suffix_pages * a.page, ignore);
                         const int nodes = tree_nodes(a, agent, own, ignore);
-                        if (t < nodes) {
+                        live = t < nodes;
+                        if (live) {
                             sees = flags & kPrefix ? it.sees0 : own - nodes + 1 + t;
                             if (!(flags & kPrefix)) tree0 = own - nodes;
                             mask = a.tree + ((long long)agent * T + t) * a.tree_words;
@@ -806,7 +810,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 }
                 tmem_ld32(s_at, x[0]);
                 const float z = mx * c;
-                const bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
+                const bool raise = live && (z > m + kAtSlack || (m == -INFINITY && z > m));
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m - z) : 1.f;  // m = -inf: 0
                     if (raise) {
@@ -876,7 +880,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                             if (r + 8 < rows) *reinterpret_cast<uint2*>(out + 8 * D + 8 * k) = make_uint2(o[4 * k + 2], o[4 * k + 3]);
                         }
                     }
-                    if (row < rows) w.ml[part + row] = make_float2(m, l);
+                    if (row < rows) w.ml[part + row] = live ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
                     tc_fence_before();
                 }
             }

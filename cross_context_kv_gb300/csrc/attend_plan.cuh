@@ -193,7 +193,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     __shared__ PlanSums warp_sums[kPlanThreads / 32];
     __shared__ int warp_max[kPlanThreads / 32];
     __shared__ AtEntry kept[3][kPlanKept];
-    __shared__ long long pair_line[kPlanThreads];  // where a segment's pairs begin on their line
+    // Few enough segments for one a thread: where their pairs begin on their line and among the
+    // entries, and the group bounds (read again at once, and a trip to memory is a microsecond).
+    __shared__ long long pair_line[kPlanThreads];
+    __shared__ int pair_first[kPlanThreads], near_bounds[kPlanThreads + 1];
     pdl_wait();  // the lengths may be the work of the kernel before
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -204,8 +207,13 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     const long long most_p = (long long)a.max_prefix_pages * a.page, most_s = (long long)a.max_suffix_pages * a.page;
     bool bad = false;
     // the first segment's length is on its way while the bounds are worked out
-    int len0 = 0;
-    if (s0 < s1) len0 = s0 < a.groups ? __ldg(a.prefix_len + s0) : __ldg(a.suffix_len + s0 - a.groups);
+    int len0 = 0, nodes0 = T;
+    if (s0 < s1) {
+        len0 = s0 < a.groups ? __ldg(a.prefix_len + s0) : __ldg(a.suffix_len + s0 - a.groups);
+        if (TREE && a.nodes && s0 >= a.groups) nodes0 = __ldg(a.nodes + s0 - a.groups);
+    }
+    const bool near = segs <= kPlanThreads;
+    auto bound = [&](int g) { return near ? near_bounds[g] : w.bounds[g]; };
     // group bounds: the running maximum of the given ones, kept within 0..agents
     if (a.groups > 0) {
         const int n = a.groups + 1, each = (n + kPlanThreads - 1) / kPlanThreads;
@@ -229,6 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             if (b < run || b > a.agents) bad = true;
             run = max(run, min(max(b, 0), a.agents));
             w.bounds[g] = run;
+            if (near) near_bounds[g] = run;
         }
         __syncthreads();
     }
@@ -240,11 +249,13 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     auto segment = [&](int s) {
         Seg g;
         g.prefix = s < a.groups;
-        g.agent0 = g.prefix ? w.bounds[s] : s - a.groups;
+        g.agent0 = g.prefix ? bound(s) : s - a.groups;
         const int given = s == s0 ? len0 : g.prefix ? __ldg(a.prefix_len + s) : __ldg(a.suffix_len + g.agent0);
         g.keys = clamp_len(given, g.prefix ? most_p : most_s, bad);
-        g.rows = (g.prefix ? w.bounds[s + 1] - g.agent0 : 1) * TG;
-        g.nodes = TREE && !g.prefix ? tree_nodes(a, g.agent0, g.keys, bad) : T;
+        g.rows = (g.prefix ? bound(s + 1) - g.agent0 : 1) * TG;
+        g.nodes = T;
+        if (TREE && !g.prefix)
+            g.nodes = s == s0 ? clamp_len(nodes0, min(T, g.keys), bad) : tree_nodes(a, g.agent0, g.keys, bad);
         return g;
     };
     auto block = [&](const Seg& g, int s, int r0, int& kind) {
@@ -307,8 +318,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
                 const AtEntry e = block(g, s, b * kAtBlock, k);
                 keep(e, kPairs, at.n[kPairs] + b, at.line[kPairs] + pairs_cost(g, s, b));
             }
-        else
+        else {
             pair_line[s] = at.line[kPairs];
+            pair_first[s] = at.n[kPairs];
+        }
         at.n[kPairs] += full;
         at.line[kPairs] += pairs_cost(g, s, full);
         if (g.rows > full * kAtBlock) {
@@ -332,11 +345,11 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             int x = 0, y = segs;  // the last segment whose pairs begin at or before i
             while (y - x > 1) {
                 const int m = (x + y) / 2;
-                if (w.first[m].x <= i) x = m;
+                if (pair_first[m] <= i) x = m;
                 else y = m;
             }
             const Seg g = segment(x);
-            const int b = i - w.first[x].x;
+            const int b = i - pair_first[x];
             if (b >= full_pairs(g)) continue;  // (the last block's, written above)
             int k;
             keep(block(g, x, b * kAtBlock, k), kPairs, i, pair_line[x] + pairs_cost(g, x, b));
