@@ -1210,7 +1210,7 @@ template <int F, int D, bool TREE>
 static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
     using C = AtCfg<F, D>;
     cudaError_t e;
-    if ((e = launch_chained(attend_plan_kernel<TREE>, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
+    if ((e = launch_chained(attend_plan_kernel<TREE>, dim3(1), dim3(kPlanBlock), 0, s, a, w)) != cudaSuccess) return e;
     if (w.many) {
         CUtensorMap mk, mv;
         if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;

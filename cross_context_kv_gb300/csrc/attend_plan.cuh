@@ -138,28 +138,34 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
     return (x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
 }
 
-constexpr int kPlanThreads = 256;
+// The plan is one CTA whose code runs once, so its time is latency: trips to memory and fetches of
+// instructions.  256 threads share out the segments; 640 write the entries and the pieces'
+// beginnings, one each (608 of 152 CTAs).  Scans are loops, and what a segment's thread worked out
+// for the scan it keeps for what comes after.
+constexpr int kPlanThreads = 256, kPlanBlock = 640;
 
 struct PlanSums {
     int n[3];
     long long line[3];
 };
-// Exclusive scan over the block, and the totals.
+// Exclusive scan over the first kPlanThreads threads, and the totals.
 __device__ __forceinline__ PlanSums plan_scan(const PlanSums& x, PlanSums* warp_sums, PlanSums* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PlanSums inc = x;
+    if (warp < kPlanThreads / 32) {
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const int a = __shfl_up_sync(0xffffffffu, inc.n[k], o);
-            const long long b = __shfl_up_sync(0xffffffffu, inc.line[k], o);
-            if (lane >= o) {
-                inc.n[k] += a;
-                inc.line[k] += b;
+            for (int k = 0; k < 3; ++k) {
+                const int a = __shfl_up_sync(0xffffffffu, inc.n[k], o);
+                const long long b = __shfl_up_sync(0xffffffffu, inc.line[k], o);
+                if (lane >= o) {
+                    inc.n[k] += a;
+                    inc.line[k] += b;
+                }
             }
-        }
-    if (lane == 31) warp_sums[warp] = inc;
+        if (lane == 31) warp_sums[warp] = inc;
+    }
     __syncthreads();
     PlanSums ex, all = {};
 #pragma unroll
@@ -167,7 +173,7 @@ __device__ __forceinline__ PlanSums plan_scan(const PlanSums& x, PlanSums* warp_
         ex.n[k] = inc.n[k] - x.n[k];
         ex.line[k] = inc.line[k] - x.line[k];
     }
-#pragma unroll
+#pragma unroll 2
     for (int w = 0; w < kPlanThreads / 32; ++w)
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -188,13 +194,20 @@ constexpr int kPlanKept = 256;  // entries of a line that stay in shared memory
 
 // TREE: kvfix_tree_attend's, whose agents have numbers of new tokens of their own.
 template <bool TREE>
-__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendArgs a,
+__global__ void __launch_bounds__(kPlanBlock) attend_plan_kernel(const __grid_constant__ AttendArgs a,
                                                                    const __grid_constant__ AtWork w) {
     __shared__ PlanSums warp_sums[kPlanThreads / 32];
     __shared__ int warp_max[kPlanThreads / 32];
     __shared__ AtEntry kept[3][kPlanKept];
-    // Few enough segments for one a thread: where their pairs begin on their line and among the
-    // entries, and the group bounds (read again at once, and a trip to memory is a microsecond).
+    struct Seg {
+        int agent0, rows, keys;
+        int nodes;  // trees: of a suffix
+        bool prefix;
+    };
+    // Few enough segments for one a thread: what they are, where their pairs begin on their line
+    // and among the entries, and the group bounds (read again at once, and a trip to memory is a
+    // microsecond).
+    __shared__ Seg near_seg[kPlanThreads];
     __shared__ long long pair_line[kPlanThreads];
     __shared__ int pair_first[kPlanThreads], near_bounds[kPlanThreads + 1];
     pdl_wait();  // the lengths may be the work of the kernel before
@@ -226,10 +239,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             const int y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc = max(inc, y);
         }
-        if (lane == 31) warp_max[warp] = inc;
+        if (lane == 31 && warp < kPlanThreads / 32) warp_max[warp] = inc;
         __syncthreads();
         int run = 0;
-        for (int x = 0; x < warp; ++x) run = max(run, warp_max[x]);
+        for (int x = 0; x < min(warp, kPlanThreads / 32); ++x) run = max(run, warp_max[x]);
         const int left = __shfl_up_sync(0xffffffffu, inc, 1);
         if (lane > 0) run = max(run, left);
         for (int g = g0; g < g1; ++g) {
@@ -241,11 +254,6 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         }
         __syncthreads();
     }
-    struct Seg {
-        int agent0, rows, keys;
-        int nodes;  // trees: of a suffix
-        bool prefix;
-    };
     auto segment = [&](int s) {
         Seg g;
         g.prefix = s < a.groups;
@@ -288,31 +296,50 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         w.entries[k][i] = e;
         if (i < kPlanKept) kept[k][i] = e;
     };
+    // a segment, its full blocks and what they take, its last block and what that takes
+    struct Look {
+        Seg g;
+        int full, kind;
+        long long pairs, cost;
+        AtEntry last;  // no rows: there is none
+    };
+    auto look = [&](int s) {
+        Look l;
+        l.g = segment(s);
+        l.full = full_pairs(l.g);
+        l.pairs = pairs_cost(l.g, s, l.full);
+        l.last.rows = 0;
+        if (l.g.rows > l.full * kAtBlock) {
+            l.last = block(l.g, s, l.full * kAtBlock, l.kind);
+            l.cost = cost(l.last, l.kind);
+        }
+        return l;
+    };
     PlanSums mine = {};
+    Look now;
     for (int s = s0; s < s1; ++s) {
-        const Seg g = segment(s);
-        const int full = full_pairs(g);
-        mine.n[kPairs] += full;
-        mine.line[kPairs] += pairs_cost(g, s, full);
-        if (g.rows > full * kAtBlock) {
-            int k;
-            const long long c = cost(block(g, s, full * kAtBlock, k), k);
+        now = look(s);
+        if (near) near_seg[s] = now.g;
+        mine.n[kPairs] += now.full;
+        mine.line[kPairs] += now.pairs;
+        if (now.last.rows > 0) {
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                if (x == k) {
+                if (x == now.kind) {
                     mine.n[x] += 1;
-                    mine.line[x] += c;
+                    mine.line[x] += now.cost;
                 }
         }
     }
     PlanSums total;
     PlanSums at = plan_scan(mine, warp_sums, &total);
     for (int s = s0; s < s1; ++s) {
-        const Seg g = segment(s);
-        const int full = full_pairs(g);
+        if (!near) now = look(s);
+        const Seg& g = now.g;
+        const int full = now.full;
         int2 first = make_int2(at.n[kPairs], 0);
         // full blocks: by all threads below, where each has one segment at most
-        if (per > 1)
+        if (!near)
             for (int b = 0; b < full; ++b) {
                 int k;
                 const AtEntry e = block(g, s, b * kAtBlock, k);
@@ -323,32 +350,29 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             pair_first[s] = at.n[kPairs];
         }
         at.n[kPairs] += full;
-        at.line[kPairs] += pairs_cost(g, s, full);
-        if (g.rows > full * kAtBlock) {
-            int k;
-            const AtEntry e = block(g, s, full * kAtBlock, k);
-            const long long c = cost(e, k);
+        at.line[kPairs] += now.pairs;
+        if (now.last.rows > 0) {
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                if (x == k) {
-                    keep(e, x, at.n[x], at.line[x]);
+                if (x == now.kind) {
+                    keep(now.last, x, at.n[x], at.line[x]);
                     if (x != kPairs) first.y = at.n[x];
                     at.n[x] += 1;
-                    at.line[x] += c;
+                    at.line[x] += now.cost;
                 }
         }
         w.first[s] = first;
     }
     __syncthreads();
-    if (per == 1)
-        for (int i = tid; i < total.n[kPairs]; i += kPlanThreads) {
+    if (near)
+        for (int i = tid; i < total.n[kPairs]; i += kPlanBlock) {
             int x = 0, y = segs;  // the last segment whose pairs begin at or before i
             while (y - x > 1) {
                 const int m = (x + y) / 2;
                 if (pair_first[m] <= i) x = m;
                 else y = m;
             }
-            const Seg g = segment(x);
+            const Seg g = near_seg[x];
             const int b = i - pair_first[x];
             if (b >= full_pairs(g)) continue;  // (the last block's, written above)
             int k;
@@ -375,7 +399,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
                                 max(1ll, quotient(total.line[1] + 2 * nm - 1, 2 * nm)),
                                 max(1ll, quotient(total.line[2] + few_pieces - 1, few_pieces))};
     // (a few-row CTA has its warps' pieces as one)
-    for (int i = tid; i < 4 * w.ctas; i += kPlanThreads) {
+    for (int i = tid; i < 4 * w.ctas; i += kPlanBlock) {
         const int cta = i % w.ctas, set = i / w.ctas, k = set == 0 ? kPairs : set == 3 ? kFew : kSingles;
         AtStart* st = &w.plan->start[set][cta];
         const long long size = k == kFew ? chunk[kFew] * kFewWarps : k == kSingles ? chunk[kSingles] : chunk[kPairs];

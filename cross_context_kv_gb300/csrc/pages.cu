@@ -311,32 +311,21 @@ cudaError_t launch_pages_extend(const PagesArgs& a, const int32_t* parent, const
 }
 
 // ------------------------------------------------------------------ cut
-// What a list keeps, checked alike by both kernels (by a whole block; every thread gets the answer).
-struct CutList {
-    int len, base, kept;
-    bool act, bad;
-};
-__device__ __forceinline__ CutList cut_list(const PagesArgs& a, const int32_t* base, const int32_t* path, int max_path,
-                                            const int32_t* kept, int i) {
-    CutList c;
-    c.base = base[i];
-    c.len = a.len[i];
-    c.kept = kept ? kept[i] : 0;
-    c.act = c.bad = false;
-    if (c.base < 0) return c;
-    bool fine = c.len >= 0 && c.len <= (long long)a.wide * a.page && c.base <= c.len && c.kept >= 0 && c.kept <= max_path;
-    if (fine)
-        for (int j = threadIdx.x; j < c.kept; j += blockDim.x) {
-            const int32_t* p = path + (long long)i * max_path + j;
-            fine = fine && *p > (j > 0 ? p[-1] : -1) && *p < c.len - c.base;
-        }
-    fine = __syncthreads_and(fine) != 0;
-    c.act = fine;
-    c.bad = !fine;
-    return c;
-}
+// One cluster of CTAs per list: all of them read what the list keeps and move its rows, and the
+// first gives its pages back once no other has the list's pages or length left to read (a cluster
+// barrier in the place of a second kernel).
+constexpr int kCutThreads = 384;
+constexpr int kCutCtas = 8;    // of a cluster at most
+constexpr int kCutRows = 128;  // rows whose places are in shared memory at a time
 
-constexpr int kCutRows = 64;  // rows of a list whose places a CTA has in shared memory at a time
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // A thread owns a column of a list's rows (16 bytes of a layer and plane, or a scale) and moves
 // it row after row: row j comes from path[j] >= j, paths ascend, so no row is overwritten before
@@ -355,26 +344,36 @@ __device__ __forceinline__ void cut_column(unsigned char* col, long long stride,
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) cut_move_kernel(const __grid_constant__ PagesArgs a, const int32_t* base,
-                                                                const int32_t* path, int max_path, const int32_t* kept,
-                                                                int blocks) {
+__global__ void __launch_bounds__(kCutThreads, 2) cut_kernel(const __grid_constant__ PagesArgs a, const int32_t* base,
+                                                             const int32_t* path, int max_path, const int32_t* kept, int ctas) {
     __shared__ int src[kCutRows], dst[kCutRows];
     pdl_wait();
-    pdl_trigger();
-    const int i = blockIdx.x / blocks, block = blockIdx.x - i * blocks;
-    const CutList c = cut_list(a, base, path, max_path, kept, i);
-    if (!c.act || c.kept == 0) return;  // (the kernel behind this one reports what is wrong)
+    const int i = blockIdx.x / ctas, tid = threadIdx.x;
+    const bool first = cluster_rank() == 0;
+    const int keep = base[i], len = a.len[i], rows = kept ? kept[i] : 0;
+    if (keep < 0 || (rows == 0 && !first)) return;
+    bool fine = len >= 0 && len <= (long long)a.wide * a.page && keep <= len && rows >= 0 && rows <= max_path;
+    if (fine)
+        for (int j = tid; j < rows; j += kCutThreads) {
+            const int32_t* p = path + (long long)i * max_path + j;
+            fine = fine && *p > (j > 0 ? p[-1] : -1) && *p < len - keep;
+        }
+    // (every CTA of the cluster comes to the same answer)
+    if (!__syncthreads_and(fine)) {
+        if (first && tid == 0) atomicOr(&g_status_pages, FLAG_BOUNDS);
+        return;
+    }
     const PoolView& v = a.pool;
-    const int row = v.heads * pool_head_bytes(v.format, v.dim) / 16;                                   // columns of codes
+    const int row = v.heads * pool_head_bytes(v.format, v.dim) / 16;  // columns of codes, then of scales
     const int marks = v.format == KVFIX_POOL_BF16 ? 0 : v.format == KVFIX_POOL_E4M3 ? v.heads : v.heads * (v.dim / kQGroup);
     const long long columns = 2ll * v.layers * (row + marks);
+    int32_t* const table = a.pages + (long long)i * a.wide;
     bool bad = false;
-    for (int j0 = 0; j0 < c.kept; j0 += kCutRows) {
-        const int rows = min(kCutRows, c.kept - j0);
+    for (int j0 = 0; j0 < rows; j0 += kCutRows) {
+        const int n = min(kCutRows, rows - j0);
         __syncthreads();
-        for (int j = threadIdx.x; j < rows; j += kMoveThreads) {
-            const int to = c.base + j0 + j, from = c.base + path[(long long)i * max_path + j0 + j];
-            const int32_t* const table = a.pages + (long long)i * a.wide;
+        for (int j = tid; j < n; j += kCutThreads) {
+            const int to = keep + j0 + j, from = keep + path[(long long)i * max_path + j0 + j];
             const int pf = table[from / a.page], pt = table[to / a.page];
             const bool there = pf >= 0 && pf < a.total && pt >= 0 && pt < a.total;
             bad |= !there;
@@ -382,33 +381,25 @@ __global__ void __launch_bounds__(kMoveThreads) cut_move_kernel(const __grid_con
             dst[j] = there ? pt * a.page + to % a.page : -1;
         }
         __syncthreads();
-        for (long long col = (long long)block * kMoveThreads + threadIdx.x; col < columns; col += (long long)blocks * kMoveThreads) {
+        // the last places are known: nothing of the list's books is read any more
+        if (j0 + n == rows) cluster_sync();
+        for (long long col = (long long)(blockIdx.x - i * ctas) * kCutThreads + tid; col < columns; col += (long long)ctas * kCutThreads) {
             const int lp = (int)(col / (row + marks)), at = (int)(col - (long long)lp * (row + marks));
             const PoolPlane& pl = v.plane[lp & 1];
             const int layer = lp >> 1;
             if (at < row) {
-                cut_column<uint4>(pl.codes + layer * v.sl + 16 * at, v.ss, src, dst, rows);
+                cut_column<uint4>(pl.codes + layer * v.sl + 16 * at, v.ss, src, dst, n);
             } else if (v.format == KVFIX_POOL_E4M3) {
-                cut_column<unsigned char>(pl.scales + ((long long)layer * v.heads + at - row) * v.slots, 1, src, dst, rows);
+                cut_column<unsigned char>(pl.scales + ((long long)layer * v.heads + at - row) * v.slots, 1, src, dst, n);
             } else {
                 const int per = v.dim / kQGroup, h = (at - row) / per, q = at - row - h * per;
-                cut_column<uint32_t>(pl.scales + 4 * (((long long)layer * v.heads + h) * v.slots * per + q), 4 * per, src, dst, rows);
+                cut_column<uint32_t>(pl.scales + 4 * (((long long)layer * v.heads + h) * v.slots * per + q), 4 * per, src, dst, n);
             }
         }
     }
-    if (bad) atomicOr(&g_status_pages, FLAG_BOUNDS);
-}
-
-__global__ void __launch_bounds__(128) cut_release_kernel(const __grid_constant__ PagesArgs a, const int32_t* base,
-                                                          const int32_t* path, int max_path, const int32_t* kept) {
-    pdl_wait();
-    const int i = blockIdx.x;
-    const CutList c = cut_list(a, base, path, max_path, kept, i);
-    bool bad = c.bad;
-    if (c.act) {
-        const int end = c.base + c.kept;
-        int32_t* const table = a.pages + (long long)i * a.wide;
-        for (int k = pages_of(end, a.page) + (int)threadIdx.x; k < pages_of(c.len, a.page); k += blockDim.x) {
+    if (first) {
+        const int end = keep + rows;
+        for (int k = pages_of(end, a.page) + tid; k < pages_of(len, a.page); k += kCutThreads) {
             const int p = table[k];
             if (p < 0 || p >= a.total) {
                 bad = true;
@@ -418,8 +409,7 @@ __global__ void __launch_bounds__(128) cut_release_kernel(const __grid_constant_
             }
             table[k] = -1;
         }
-        __syncthreads();  // (every thread has read the length)
-        if (threadIdx.x == 0) a.len[i] = end;
+        if (tid == 0) a.len[i] = end;
     }
     if (bad) atomicOr(&g_status_pages, FLAG_BOUNDS);
 }
@@ -427,18 +417,27 @@ __global__ void __launch_bounds__(128) cut_release_kernel(const __grid_constant_
 cudaError_t launch_pages_cut(const PagesArgs& a, const int32_t* base, const int32_t* path, int max_path,
                              const int32_t* kept, cudaStream_t s) {
     if (a.lists == 0) return cudaSuccess;
-    if (path && max_path > 0 && a.pool.layers > 0) {
-        // a column per thread while the CTAs stay below eight an SM
+    // as many CTAs a list as give every thread a column, eight at most
+    int ctas = 1;
+    if (max_path > 0) {
         const PoolView& v = a.pool;
         const int per = v.format == KVFIX_POOL_BF16 ? 0 : v.format == KVFIX_POOL_E4M3 ? 1 : v.dim / kQGroup;
         const long long columns = 2ll * v.layers * v.heads * (pool_head_bytes(v.format, v.dim) / 16 + per);
-        const long long want = (columns + kMoveThreads - 1) / kMoveThreads, most = (8 * 152 + a.lists - 1) / a.lists;
-        const long long blocks = want < most ? want : most;
-        const cudaError_t e = launch_chained(cut_move_kernel, dim3((unsigned)(blocks * a.lists)), dim3(kMoveThreads), 0, s, a, base,
-                                             path, max_path, kept, (int)blocks);
-        if (e != cudaSuccess) return e;
+        while (ctas < kCutCtas && (long long)ctas * kCutThreads < columns) ctas *= 2;
     }
-    return launch_chained(cut_release_kernel, dim3((unsigned)a.lists), dim3(128), 0, s, a, base, path, max_path, kept);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.lists * ctas));
+    cfg.blockDim = dim3(kCutThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, cut_kernel, a, base, path, max_path, kept, ctas);
 }
 
 // ------------------------------------------------------------------ compact

@@ -171,6 +171,18 @@ def _i32(t, name):
         raise TypeError(f"{name} must be a contiguous CUDA int32 tensor")
 
 
+_INT32 = torch.int32
+
+
+def _ints(dev: int, tensors) -> bool:
+    """Whether all are contiguous int32 tensors of CUDA device `dev` (None is skipped): what a call
+    wants, in one pass; where it is false, the checks one by one say what is wrong."""
+    for t in tensors:
+        if t is not None and (t.dtype is not _INT32 or t.get_device() != dev or not t.is_contiguous()):
+            return False
+    return True
+
+
 def _f32(t, name):
     if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA float32 tensor")
@@ -796,18 +808,18 @@ def tree_attend(q, pool: Pool, page_tokens: int, suffix_pages, suffix_len, tree_
     keys are the nodes that its first queries stand for, and node t sees of them those j <= t whose
     bit is set in tree_mask [agents][T][ceil(T/32)] int32 (see tree_masks).  Queries past nodes[a]
     give 0, and -inf.  The workspace is shared_attend's."""
-    _i32(tree_mask, "tree_mask")
     if q.dim() != 4:
         raise ValueError("q must be [agents][new tokens][heads][dim]")
-    A, T = q.shape[:2]
+    A, T, dev = q.shape[0], q.shape[1], q.get_device()
+    if not _ints(dev, (tree_mask, nodes)):
+        _i32(tree_mask, "tree_mask")
+        if nodes is not None:
+            _i32(nodes, "nodes")
+        raise ValueError("tree_mask and nodes must be on q's device")
     if tree_mask.shape != (A, T, (T + 31) // 32):
         raise ValueError(f"tree_mask must be [{A}][{T}][{(T + 31) // 32}]")
-    if nodes is not None:
-        _i32(nodes, "nodes")
-        if nodes.numel() != A:
-            raise ValueError(f"nodes must hold {A} numbers")
-    if tree_mask.get_device() != q.get_device() or (nodes is not None and nodes.get_device() != q.get_device()):
-        raise ValueError("tree_mask and nodes must be on q's device")
+    if nodes is not None and nodes.numel() != A:
+        raise ValueError(f"nodes must hold {A} numbers")
     tree = (None if nodes is None else nodes.data_ptr(), tree_mask.data_ptr())
     return _attend(lib.kvfix_tree_attend, tree, q, pool, page_tokens, suffix_pages, suffix_len, prefix_pages, prefix_len,
                    group_begin, scale, out, return_lse, workspace)
@@ -846,27 +858,32 @@ def _attend(call, tree, q, pool, page_tokens, suffix_pages, suffix_len, prefix_p
     if prefix_len is None and not (prefix_pages is None and group_begin is None):
         raise ValueError("prefix_len is required with prefix_pages and group_begin")
     groups = 0 if prefix_len is None else prefix_len.numel()
-    _i32(suffix_pages, "suffix_pages")
-    _i32(suffix_len, "suffix_len")
+    if not _ints(dev, (suffix_pages, suffix_len)) or pool.k.get_device() != dev:
+        _i32(suffix_pages, "suffix_pages")
+        _i32(suffix_len, "suffix_len")
+        raise ValueError("q, the pool, pages and lengths must be on one device")
     if suffix_pages.dim() != 2 or suffix_pages.shape[0] != A or suffix_len.numel() != A:
         raise ValueError(f"suffix_pages must be [{A}][pages] and suffix_len hold {A} lengths")
-    if pool.k.get_device() != dev or suffix_pages.get_device() != dev or suffix_len.get_device() != dev:
-        raise ValueError("q, the pool, pages and lengths must be on one device")
     shared = (None, 0, None, None)
     if groups:
         if prefix_pages is None or group_begin is None:
             raise ValueError("prefix_pages and group_begin are required with prefix_len")
-        _i32(prefix_pages, "prefix_pages")
-        _i32(prefix_len, "prefix_len")
-        _i32(group_begin, "group_begin")
+        if not _ints(dev, (prefix_pages, prefix_len, group_begin)):
+            _i32(prefix_pages, "prefix_pages")
+            _i32(prefix_len, "prefix_len")
+            _i32(group_begin, "group_begin")
+            raise ValueError("q, the pool, pages and lengths must be on one device")
         if prefix_pages.dim() != 2 or prefix_pages.shape[0] != groups or group_begin.numel() != groups + 1:
             raise ValueError(f"prefix_pages must be [{groups}][pages] and group_begin hold {groups + 1} bounds")
-        if prefix_pages.get_device() != dev or prefix_len.get_device() != dev or group_begin.get_device() != dev:
-            raise ValueError("q, the pool, pages and lengths must be on one device")
         shared = (prefix_pages.data_ptr(), prefix_pages.shape[1], prefix_len.data_ptr(), group_begin.data_ptr())
     if out is None:
-        out = _empty((A, T, Hq, Dh), (T * Hq * Dh, Hq * Dh, Dh, 1), torch.bfloat16)
-    od = _rows_desc(out, "out")
+        row = Hq * Dh
+        out = _empty((A, T, Hq, Dh), (T * row, row, Dh, 1), torch.bfloat16)
+        od = KvDesc(A, 1, T, Hq, Dh, T * row if A > 1 else 0, 0, row)
+    else:
+        od = _rows_desc(out, "out")
+        if out.get_device() != dev:
+            raise ValueError("out and workspace must be on q's device")
     lse = _empty((A, T, Hq), (T * Hq, Hq, 1), torch.float32) if return_lse else None
     if workspace is None:
         size = lib.kvfix_shared_attend_workspace_bytes(A, T, Hq, pd.kv_heads, Dh, groups)
@@ -875,8 +892,8 @@ def _attend(call, tree, q, pool, page_tokens, suffix_pages, suffix_len, prefix_p
         raise ValueError("workspace must be contiguous")
     else:
         size = workspace.numel() * workspace.element_size()
-    if out.get_device() != dev or workspace.get_device() != dev:
-        raise ValueError("out and workspace must be on q's device")
+        if workspace.get_device() != dev:
+            raise ValueError("out and workspace must be on q's device")
     _check(call(
         q.data_ptr(), qd, pd, int(page_tokens), *shared, groups, suffix_pages.data_ptr(), suffix_pages.shape[1],
         suffix_len.data_ptr(), *tree, Dh ** -0.5 if scale is None else float(scale), out.data_ptr(), od,
@@ -925,66 +942,70 @@ def rotary(q, k, positions, rope: Rope, q_out=None, k_out=None):
         raise ValueError("neither queries nor keys")
     dev = ref.get_device()
     _launch_device(dev)
-    _i32(positions, "positions")
-    if positions.get_device() != dev:
+    if not _ints(dev, (positions,)):
+        _i32(positions, "positions")
         raise ValueError("q, k, positions and outputs must be on one device")
-    planes = []
-    outs = []
-    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            if y is not None:
-                raise ValueError(f"{name}_out without {name}")
-            planes += [None, KvDesc(), None, KvDesc()]
-            outs.append(None)
-            continue
-        d = _rows_desc(x, name)
-        if positions.numel() != d.chunks * d.tokens:
-            raise ValueError(f"positions must hold {d.chunks} x {d.tokens} numbers")
-        if y is None:
-            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        elif y.shape != x.shape:
-            raise ValueError(f"{name}_out must have {name}'s shape")
-        if x.get_device() != dev or y.get_device() != dev:
-            raise ValueError("q, k, positions and outputs must be on one device")
-        planes += [x.data_ptr(), d, y.data_ptr(), _rows_desc(y, name + "_out")]
-        outs.append(y)
-    qi, qd, qo, qod, ki, kd, ko, kod = planes
+    qi, qd, q_out, qo, qod = _turned(q, q_out, "q", dev, positions)
+    ki, kd, k_out, ko, kod = _turned(k, k_out, "k", dev, positions)
     _check(lib.kvfix_rotary(qi, qd, ki, kd, positions.data_ptr(), rope_desc(rope, ref.shape[-1]), qo, qod, ko, kod,
                             _raw_stream(ref)))
-    return tuple(outs)
+    return q_out, k_out
+
+
+_NO_ROWS = KvDesc()
+
+
+def _turned(x, y, name, dev, positions):
+    """A plane of a rotary call and where it goes: (address, descriptor, output, its address, its
+    descriptor)."""
+    if x is None:
+        if y is not None:
+            raise ValueError(f"{name}_out without {name}")
+        return None, _NO_ROWS, None, None, _NO_ROWS
+    d = _rows_desc(x, name)
+    if positions.numel() != d.chunks * d.tokens:
+        raise ValueError(f"positions must hold {d.chunks} x {d.tokens} numbers")
+    if y is None:
+        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    elif y.shape != x.shape:
+        raise ValueError(f"{name}_out must have {name}'s shape")
+    if x.get_device() != dev or y.get_device() != dev:
+        raise ValueError("q, k, positions and outputs must be on one device")
+    return x.data_ptr(), d, y, y.data_ptr(), d if y is x else _rows_desc(y, name + "_out")
 
 
 # --------------------------------------------------------------------- page books
 
-def _books(pool, page_tokens, refs, pages, lens, more=()):
-    """Checks the books of a pool and the call's other int32 arrays; returns the first arguments of the page calls."""
-    pd = pool_desc(pool)
-    dev = pool.k.get_device()
+def _books(pool, page_tokens, refs, pages, lens, names, more):
+    """Checks the books of a pool and the call's other int32 arrays; returns the first arguments of
+    the page calls."""
+    pd, dev = pool_desc(pool), pool.k.get_device()
     _launch_device(dev)
-    for t, name in ((refs, "refs"), (pages, "pages"), (lens, "lens"), *more):
-        if t is None:
-            continue
-        _i32(t, name)
-        if t.get_device() != dev:
-            raise ValueError("the pool, the books and their arguments must be on one device")
-    if pages.dim() != 2 or lens.numel() != pages.shape[0]:
+    if not _ints(dev, (refs, pages, lens, *more)):
+        for t, name in zip((refs, pages, lens, *more), ("refs", "pages", "lens", *names)):
+            if t is not None:
+                _i32(t, name)
+        raise ValueError("the pool, the books and their arguments must be on one device")
+    shape, lists = pages.shape, lens.numel()
+    if len(shape) != 2 or lists != shape[0]:
         raise ValueError("pages must be [lists][pages] and lens hold a length for each list")
     if page_tokens < 1 or refs.numel() != pd.slots // page_tokens:
         raise ValueError(f"refs must hold a count for each of the pool's {pd.slots} / {page_tokens} pages")
-    for t, name in more:
-        if t is not None and t.shape[0] != lens.numel():
+    for t, name in zip(more, names):
+        if t is not None and t.shape[:1] != (lists,):
             raise ValueError(f"{name} must have a row for each list")
-    return pd, int(page_tokens), refs.data_ptr(), pages.data_ptr(), pages.shape[1], lens.data_ptr(), lens.numel()
+    return pd, page_tokens, refs.data_ptr(), pages.data_ptr(), shape[1], lens.data_ptr(), lists
 
 
-def _workspace(given, need, device):
+def _workspace(given, need, like):
+    """A workspace and its bytes: the given one, or a new one beside `like`."""
     if given is None:
-        return _empty((need,), (1,), torch.uint8)
+        return _empty((need,), (1,), torch.uint8), need
     if not given.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    if given.get_device() != device:
+    if given.get_device() != like.get_device():
         raise ValueError("workspace must be on the pool's device")
-    return given
+    return given, given.numel() * given.element_size()
 
 
 def pages_extend(pool: Pool, page_tokens: int, refs, pages, lens, extra, parent=None, workspace=None):
@@ -992,10 +1013,10 @@ def pages_extend(pool: Pool, page_tokens: int, refs, pages, lens, extra, parent=
     [lists], all int32 and changed in place, refs [pages of the pool] the lists that hold each page.
     parent [lists]: a list of which list i, empty until now, becomes a fork first (itself: it
     grows; below 0: nothing happens).  Last pages that others hold are copied."""
-    books = _books(pool, page_tokens, refs, pages, lens, ((extra, "extra"), (parent, "parent")))
-    ws = _workspace(workspace, lib.kvfix_pages_extend_workspace_bytes(refs.numel(), lens.numel()), pool.k.get_device())
+    books = _books(pool, page_tokens, refs, pages, lens, ("extra", "parent"), (extra, parent))
+    ws, size = _workspace(workspace, lib.kvfix_pages_extend_workspace_bytes(refs.numel(), books[-1]), refs)
     _check(lib.kvfix_pages_extend(*books, None if parent is None else parent.data_ptr(), extra.data_ptr(), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), _raw_stream(refs)))
+                                  size, _raw_stream(refs)))
 
 
 def pages_cut(pool: Pool, page_tokens: int, refs, pages, lens, base, path=None, kept=None):
@@ -1004,7 +1025,7 @@ def pages_cut(pool: Pool, page_tokens: int, refs, pages, lens, base, path=None, 
     given back.  All int32, the books changed in place."""
     if (path is None) != (kept is None):
         raise ValueError("path and kept come together")
-    books = _books(pool, page_tokens, refs, pages, lens, ((base, "base"), (path, "path"), (kept, "kept")))
+    books = _books(pool, page_tokens, refs, pages, lens, ("base", "path", "kept"), (base, path, kept))
     most = 0
     if path is not None:
         if path.dim() != 2:
@@ -1017,9 +1038,8 @@ def pages_cut(pool: Pool, page_tokens: int, refs, pages, lens, base, path=None, 
 def pages_compact(pool: Pool, page_tokens: int, refs, pages, lens, workspace=None):
     """Pages in use move to the front of the pool, refs and the lists follow.  Returns the number of
     pages in use, int32 [1] on the device."""
-    books = _books(pool, page_tokens, refs, pages, lens)
+    books = _books(pool, page_tokens, refs, pages, lens, (), ())
     live = _empty((1,), (1,), torch.int32)
-    ws = _workspace(workspace, lib.kvfix_pages_compact_workspace_bytes(refs.numel()), pool.k.get_device())
-    _check(lib.kvfix_pages_compact(*books, live.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                   _raw_stream(refs)))
+    ws, size = _workspace(workspace, lib.kvfix_pages_compact_workspace_bytes(refs.numel()), refs)
+    _check(lib.kvfix_pages_compact(*books, live.data_ptr(), ws.data_ptr(), size, _raw_stream(refs)))
     return live
