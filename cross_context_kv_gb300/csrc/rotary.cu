@@ -121,6 +121,19 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
         pb = pa + N;
     }
     const int p = __ldg(a.positions + (long long)chunk * a.tokens + t);
+    const int heads0 = a.ip[0].heads, heads = heads0 + a.ip[1].heads;
+    const int l0 = lb * w.layer_block, l1 = min(a.layers, l0 + w.layer_block);
+    V v[kRotaryHeads];
+    auto load = [&](int l, int h0) {
+        const uint16_t* in0 = a.in[0] + a.ip[0].row(chunk, l, t);
+        const uint16_t* in1 = a.in[1] + a.ip[1].row(chunk, l, t);
+#pragma unroll
+        for (int i = 0; i < kRotaryHeads; ++i) {
+            const int h = h0 + i * w.runs;
+            if (h < heads) v[i].load(h < heads0 ? in0 + h * a.dim : in1 + (h - heads0) * a.dim, pa, pb);
+        }
+    };
+    load(l0, run);  // (on their way while the angles are worked out)
     // (position 0 and no factor: the values as they are, infinities and signs of zeros too)
     const bool turns = col < turning && (p != 0 || a.attention != 1.f);
     float c[N], s[N];
@@ -133,20 +146,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
             s[k] *= a.attention;
         }
     }
-    const int heads0 = a.ip[0].heads, heads = heads0 + a.ip[1].heads;
-    const int l1 = min(a.layers, (lb + 1) * w.layer_block);
-    for (int l = lb * w.layer_block; l < l1; ++l) {
-        const uint16_t* in0 = a.in[0] + a.ip[0].row(chunk, l, t);
-        const uint16_t* in1 = a.in[1] + a.ip[1].row(chunk, l, t);
+    for (int l = l0; l < l1; ++l) {
         uint16_t* out0 = a.out[0] + a.op[0].row(chunk, l, t);
         uint16_t* out1 = a.out[1] + a.op[1].row(chunk, l, t);
         for (int h0 = run; h0 < heads; h0 += kRotaryHeads * w.runs) {
-            V v[kRotaryHeads];
-#pragma unroll
-            for (int i = 0; i < kRotaryHeads; ++i) {
-                const int h = h0 + i * w.runs;
-                if (h < heads) v[i].load(h < heads0 ? in0 + h * a.dim : in1 + (h - heads0) * a.dim, pa, pb);
-            }
+            if (l > l0 || h0 > run) load(l, h0);
 #pragma unroll
             for (int i = 0; i < kRotaryHeads; ++i) {
                 const int h = h0 + i * w.runs;

@@ -795,8 +795,8 @@ KVFIX_API kvfix_status kvfix_rotary(const kvfix_bf16* q, kvfix_kv_desc q_desc, c
  * tree_mask    : device uint32[agents][q.tokens][ceil(q.tokens / 32)]; rows of queries t >= N and
  *                bits past t are not read.
  * All else, the workspace (kvfix_shared_attend_workspace_bytes) and the limits are kvfix_shared_attend's,
- * with N in the place of new_tokens.  So is the arithmetic: chains of q.tokens nodes (every bit up
- * to t set) give the bits that kvfix_shared_attend gives for as many new tokens.  A NaN or
+ * with N in the place of new_tokens, and so is the arithmetic (parts may be cut elsewhere, so that
+ * a chain of nodes and as many new tokens in a row may differ in their last bits).  A NaN or
  * infinity in the value row of a node may reach the agent's other nodes (a weight of zero times
  * NaN); one in a key reaches those that see it alone.
  */
