@@ -1169,6 +1169,173 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     }
 }
 
+// The join of many trees' rows: a CTA takes 16 consecutive rows of an agent's KV head, a warp two
+// of them.  The attention kernel leaves no registers beside it, so the join's CTAs start as SMs
+// come free, and what counts is how many waves of them follow its end and what each waits for:
+// four lanes look up where the rows' parts lie (by segment, before and behind a border of blocks)
+// for all 16, a lane reads one part's (max, sum) of either segment, and both rows' parts are
+// loaded four at a time.  (The kernel above has 2048 CTAs for 8192 rows, 912 of them at a time, whose
+// last began 12.6 us after the attention's end.)
+constexpr int kTreeJoinRows = 16;
+template <int D>
+__global__ void __launch_bounds__(256, 3) attend_tree_join_kernel(const __grid_constant__ AttendArgs a,
+                                                                  const __grid_constant__ AtWork w) {
+    constexpr int V = D / 32, R = 2, B = 4;  // values per lane, rows per warp, parts on their way
+    struct Place {
+        long long own;  // part row of the segment's row 0, first part
+        long long i0;   // first piece
+        int n, kind, row0;
+    };
+    __shared__ Place places[2][2];
+    __shared__ int row_of[2];  // of the CTA's first row, in either segment
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G, H = a.pool.heads;
+    const int chunks = (TG + kTreeJoinRows - 1) / kTreeJoinRows;
+    const int ah = blockIdx.x / chunks, in0 = (blockIdx.x - ah * chunks) * kTreeJoinRows, agent = ah / H, head = ah - agent * H;
+    const int rows = min(kTreeJoinRows, TG - in0);
+    const long long all = (long long)a.agents * TG;
+    // (the plan lies ready, as for attend_join_kernel)
+    const int many_ctas = w.plan->many_ctas;
+    if (threadIdx.x < 4) {
+        const int s = threadIdx.x & 1, behind = threadIdx.x >> 1;
+        int seg = a.groups + agent, agent0 = agent, seg_rows = TG;
+        if (s == 0) {
+            seg = -1;
+            if (a.groups > 0 && agent >= w.bounds[0] && agent < w.bounds[a.groups]) {
+                int lo = 0, hi = a.groups;  // bounds[lo] <= agent < bounds[hi]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (w.bounds[mid] <= agent) lo = mid;
+                    else hi = mid;
+                }
+                seg = lo;
+                agent0 = w.bounds[lo];
+                seg_rows = (w.bounds[lo + 1] - agent0) * TG;
+            }
+        }
+        const int r0 = (agent - agent0) * TG + in0, r = behind ? (r0 / kAtBlock + 1) * kAtBlock : r0;
+        Place p = {0, 0, 0, 0, 0};
+        if (seg >= 0 && r < r0 + rows) {
+            const int block = r / kAtBlock, k = at_kind(seg_rows - block * kAtBlock, w.few);
+            const int2 first = w.first[seg];
+            const AtEntry e = w.entries[k][k == kPairs ? first.x + block : first.y];
+            if (e.tiles > 0) {
+                const long long chunk = w.plan->chunk[k], base = e.begin + (long long)head * (e.tiles + at_pad(k));
+                p.own = (s * H + (long long)head) * all + (long long)agent0 * TG;
+                p.i0 = quotient(base, chunk);
+                p.n = (int)(quotient(base + e.tiles - 1, chunk) - p.i0) + 1;  // pieces that hold tiles
+                p.kind = k;
+                p.row0 = e.row0;
+            }
+        }
+        places[s][behind] = p;
+        if (!behind) row_of[s] = r0;
+    }
+    __syncthreads();
+    pdl_wait();
+    if (R * warp >= rows) return;
+    const Place* at[R][2];
+    int row[R][2], parts[R];
+    float M[R], L[R], acc[R][V];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            row[q][s] = row_of[s] + R * warp + q;
+            at[q][s] = &places[s][row[q][s] / kAtBlock > row_of[s] / kAtBlock];
+        }
+        parts[q] = R * warp + q < rows ? at[q][0]->n + at[q][1]->n : 0;
+        M[q] = -INFINITY;
+        L[q] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[q][i] = 0.f;
+    }
+    for (int j0 = 0; j0 < max(parts[0], parts[R - 1]); j0 += 32) {
+        long long part[R];
+        float wt[R];
+        float2 ml[R];
+        unsigned has[R], any = 0;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            // this lane's part of the row: the prefix's come first
+            const int s = j0 + lane >= at[q][0]->n, j = j0 + lane - (s ? at[q][0]->n : 0);
+            const Place& p = s ? *at[q][1] : *at[q][0];
+            const long long i = p.i0 + j;
+            const int half = p.kind == kSingles && i >= many_ctas ? 1 : 0, r = s ? row[q][1] : row[q][0];
+            part[q] = j == 0          ? p.own + r
+                      : p.kind == kFew ? w.few_rows + i * w.few + (r - p.row0)
+                                       : w.own_rows + (i - half * many_ctas) * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half) + (r - p.row0);
+            ml[q] = j0 + lane < parts[q] ? __ldcg(w.ml + part[q]) : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            float top = ml[q].x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float N = fmaxf(M[q], top), f = M[q] == -INFINITY ? 0.f : exp2f(M[q] - N);
+            wt[q] = ml[q].x == -INFINITY ? 0.f : exp2f(ml[q].x - N);
+            // (a row with a NaN logit has a sum of NaN and must keep it)
+            float sum = ml[q].y == 0.f ? 0.f : ml[q].y * (ml[q].x == -INFINITY ? 1.f : wt[q]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (top != -INFINITY || !(sum == 0.f)) {
+                L[q] = L[q] * (M[q] == -INFINITY ? (L[q] == 0.f ? 0.f : 1.f) : f) + sum;
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[q][i] *= f;
+                M[q] = N;
+            }
+            has[q] = __ballot_sync(0xffffffffu, !(ml[q].y == 0.f));
+            any |= has[q];
+        }
+        const int count = 32 - __clz(any);
+#pragma unroll 1
+        for (int b0 = 0; b0 < count; b0 += B) {
+            float x[B][R][V], wb[B][R];
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    const bool there = b0 + b < count && ((has[q] >> ((b0 + b) & 31)) & 1u);
+                    const long long from = __shfl_sync(0xffffffffu, part[q], (b0 + b) & 31);
+                    wb[b][q] = __shfl_sync(0xffffffffu, wt[q], (b0 + b) & 31);
+                    if (!there) wb[b][q] = 0.f;
+                    const float* src = w.o + from * D + V * lane;
+                    if (V == 4) {
+                        const float4 v = there ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[b][q][0] = v.x;
+                        x[b][q][1] = v.y;
+                        x[b][q][V - 2] = v.z;
+                        x[b][q][V - 1] = v.w;
+                    } else {
+                        const float2 v = there ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+                        x[b][q][0] = v.x;
+                        x[b][q][1] = v.y;
+                    }
+                }
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[q][i] = fmaf(x[b][q][i], wb[b][q], acc[q][i]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int in = in0 + R * warp + q, t = in / G, qh = head * G + in - t * G;
+        if (in >= in0 + rows) continue;
+        const float inv = L[q] == 0.f ? 0.f : 1.f / L[q];
+        uint16_t* out = a.out + a.op.row(agent, 0, t) + (long long)qh * D + V * lane;
+        if (V == 4)
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[q][0] * inv, acc[q][1] * inv),
+                                                        pack_bf16(acc[q][V - 2] * inv, acc[q][V - 1] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(out) = pack_bf16(acc[q][0] * inv, acc[q][1] * inv);
+        if (a.lse && lane == 0)
+            a.lse[((long long)agent * T + t) * a.q_heads + qh] = L[q] == 0.f ? -INFINITY : (M[q] + log2f(L[q])) * 0.69314718055994531f;
+    }
+}
+
 // ------------------------------------------------------------------ host
 size_t attend_workspace_bytes(int agents, int T, int q_heads, int kv_heads, int head_dim, int groups) {
     return at_layout(agents, T, q_heads, kv_heads, head_dim, groups).bytes;
@@ -1227,6 +1394,12 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int 
     // 7 us less by one), one while rows are few
     if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
     const int tg = a.new_tokens * (a.q_heads / a.pool.heads);
+    // (8192 rows: 69.5 us a call against 73.3 by the kernel below, 3072 rows 142 against 143; but 2048
+    // rows of many parts 47 against 39)
+    if (TREE && tg >= kTreeJoinRows && rows > (long long)w.ctas * 16) {
+        const long long ctas = (long long)a.agents * a.pool.heads * ((tg + kTreeJoinRows - 1) / kTreeJoinRows);
+        return launch_chained(attend_tree_join_kernel<D>, dim3((unsigned)ctas), dim3(256), 0, s, a, w);
+    }
     if (tg >= 4 && rows > (long long)w.ctas * 128) {
         const long long warps = (long long)a.agents * a.pool.heads * ((tg + 3) / 4);
         return launch_chained(attend_join_kernel<D, 1, 4>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, s, a, w);

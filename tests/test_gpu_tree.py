@@ -120,6 +120,26 @@ def test_trees(kvfix, fmt, name, kind):
     r.check(out, lse)
 
 
+# rows enough for the join that takes many at a time: borders of blocks inside its runs of rows, last runs
+# that are short, parts of long prefixes and of several pieces
+LARGE = {
+    "borders": (4, 5, 128, 16, 33, [700], [0, 6], [10, 64, 0, 200, 33, 5], [33, 30, 33, 0, 1, 33]),
+    "ragged_64": (5, 3, 64, 64, 61, [3001, 0], [0, 2, 4], [900, 3, 0, 77], [61, 54, 47, 33]),
+    "no_prefix": (8, 4, 64, 32, 17, [], [], [300, 0, 5, 90, 1200, 7], [17] * 6),
+}
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("name", list(LARGE))
+def test_many_rows(kvfix, fmt, name):
+    r = Trees(kvfix, fmt, *LARGE[name], kind="any", seed=len(name))
+    out, lse = r.call()
+    kvfix.check_status()
+    assert lse.numel() > 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    r.check(out, lse)
+
+
 @gpu
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("case", ((2, 2, 64, 16, 3, [40], [0, 2], [2, 50], [3, 3]), (2, 4, 128, 16, 40, [300], [0, 3], [3, 140, 0], [40] * 3),
