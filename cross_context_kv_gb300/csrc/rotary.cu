@@ -3,17 +3,18 @@
 // Mathematics.  A pair (a, b) of a head turns by the angle p theta_i: (a c - b s, b c + a s) with
 // c, s = m cos, m sin.  Positions reach 2^31 and theta_i is a double, so the angle is kept in
 // turns as a 64-bit fraction: p (theta_i / 2 pi) 2^64 modulo 2^64 is one integer product, exact
-// but for the rounding of theta_i itself (2^-54 of it), where a product of doubles would lose
-// what lies beyond 53 bits and this part has few double units.  One conversion to float and
-// sincospi follow: both are off by 2^-23 or less of their value.
+// but for the rounding of theta_i / 2 pi itself (2^-52 of it), where a product of doubles would
+// lose what lies beyond 53 bits and this part has few double units.  One conversion to float
+// and sincospi follow: both are off by 2^-23 or less of their value.
 //
 // Layout.  A thread owns a column of its token's heads: two 8-wide vectors, the ones that turn into each
 // other (half layout) or neighbours (interleaved), so it computes eight (cos, sin) once and uses
 // them for every head of queries and keys, and for the layers of its block; four heads' loads
 // are in flight together.  Where little work is left for each, the heads of a token are spread over
 // threads, then every thread has its own head.  Values beyond rotary_dim are columns that are
-// copied, or left out when the call works in place.  A rotary_dim that is no multiple of 16 has
-// columns of one pair, loaded as two 16-bit values.
+// copied, or left out when the call works in place.  In the half layout a rotary_dim that is no
+// multiple of 16 has halves that vectors do not meet: its columns are pairs of 16-bit values, and
+// vectors of what does not turn.
 //
 // Bound by HBM: see the measured figures at launch_rotary.
 #include <cuda_bf16.h>
@@ -38,67 +39,76 @@ struct RotarySplit {
     int layer_blocks;
 };
 
-template <bool VEC>
-struct RotaryValues;
-template <>
-struct RotaryValues<true> {
+// What a thread has of a head.  Vectors: two 8-wide ones.
+struct RotaryVectors {
     static constexpr int kPairs = 8;
     uint4 lo, hi;
-    __device__ __forceinline__ void load(const uint16_t* p, int a, int b) {
+    __device__ __forceinline__ void load(const uint16_t* p, int a, int b, bool) {
         lo = *reinterpret_cast<const uint4*>(p + a);
         hi = *reinterpret_cast<const uint4*>(p + b);
     }
-    __device__ __forceinline__ void store(uint16_t* p, int a, int b) const {
+    __device__ __forceinline__ void store(uint16_t* p, int a, int b, bool) const {
         *reinterpret_cast<uint4*>(p + a) = lo;
         *reinterpret_cast<uint4*>(p + b) = hi;
     }
+    // `pairs`: the first of them turn (half layout: all)
     template <int LAYOUT>
-    __device__ __forceinline__ void turn(const float* c, const float* s) {
-        float x[8], y[8];
-        unpack8(lo, x);
-        unpack8(hi, y);
+    __device__ __forceinline__ void turn(const float* c, const float* s, int pairs) {
         if (LAYOUT == KVFIX_ROPE_HALF) {
+            float x[8], y[8];
+            unpack8(lo, x);
+            unpack8(hi, y);
             rotate_pair(x, y, c, s);
+            lo = pack8(x);
+            hi = pack8(y);
         } else {
+            unsigned w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};  // a pair each
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float a = x[2 * k], b = x[2 * k + 1];
-                x[2 * k] = __fmaf_rn(a, c[k], __fmul_rn(b, -s[k]));
-                x[2 * k + 1] = __fmaf_rn(b, c[k], __fmul_rn(a, s[k]));
-                const float d = y[2 * k], e = y[2 * k + 1];
-                y[2 * k] = __fmaf_rn(d, c[k + 4], __fmul_rn(e, -s[k + 4]));
-                y[2 * k + 1] = __fmaf_rn(e, c[k + 4], __fmul_rn(d, s[k + 4]));
+            for (int k = 0; k < 8; ++k) {
+                const float x = __uint_as_float(w[k] << 16), y = __uint_as_float(w[k] & 0xffff0000u);
+                const __nv_bfloat162 r = __floats2bfloat162_rn(__fmaf_rn(x, c[k], __fmul_rn(y, -s[k])),
+                                                               __fmaf_rn(y, c[k], __fmul_rn(x, s[k])));
+                if (k < pairs) w[k] = *reinterpret_cast<const unsigned*>(&r);
             }
+            lo = make_uint4(w[0], w[1], w[2], w[3]);
+            hi = make_uint4(w[4], w[5], w[6], w[7]);
         }
-        lo = pack8(x);
-        hi = pack8(y);
     }
 };
-template <>
-struct RotaryValues<false> {
+// Half layout with halves that no vector border meets: a pair of 16-bit values, or a vector of those
+// that do not turn.
+struct RotaryMixed {
     static constexpr int kPairs = 1;
-    uint16_t lo, hi;
-    __device__ __forceinline__ void load(const uint16_t* p, int a, int b) {
-        lo = p[a];
-        hi = p[b];
+    uint4 x;
+    __device__ __forceinline__ void load(const uint16_t* p, int a, int b, bool wide) {
+        if (wide) {
+            x = *reinterpret_cast<const uint4*>(p + a);
+        } else {
+            x.x = p[a];
+            x.y = p[b];
+        }
     }
-    __device__ __forceinline__ void store(uint16_t* p, int a, int b) const {
-        p[a] = lo;
-        p[b] = hi;
+    __device__ __forceinline__ void store(uint16_t* p, int a, int b, bool wide) const {
+        if (wide) {
+            *reinterpret_cast<uint4*>(p + a) = x;
+        } else {
+            p[a] = (uint16_t)x.x;
+            p[b] = (uint16_t)x.y;
+        }
     }
     template <int LAYOUT>
-    __device__ __forceinline__ void turn(const float* c, const float* s) {
-        const float x = __bfloat162float(__ushort_as_bfloat16(lo)), y = __bfloat162float(__ushort_as_bfloat16(hi));
-        lo = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(x, c[0], __fmul_rn(y, -s[0]))));
-        hi = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(y, c[0], __fmul_rn(x, s[0]))));
+    __device__ __forceinline__ void turn(const float* c, const float* s, int) {
+        const float u = __uint_as_float(x.x << 16), v = __uint_as_float(x.y << 16);
+        x.x = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(u, c[0], __fmul_rn(v, -s[0]))));
+        x.y = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(v, c[0], __fmul_rn(u, s[0]))));
     }
 };
 
-template <int LAYOUT, bool VEC>
+template <int LAYOUT, typename V>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a,
                                                                 const __grid_constant__ RotarySplit w) {
-    using V = RotaryValues<VEC>;
     constexpr int N = V::kPairs;
+    constexpr bool kMixed = N == 1;
     const int slot = threadIdx.x / w.columns, col = threadIdx.x - slot * w.columns;
     const int in_tile = slot / w.runs, run = slot - in_tile * w.runs;
     unsigned b = blockIdx.x;
@@ -107,18 +117,23 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     const int chunk = (int)(b / (unsigned)w.tiles), tile = (int)(b - (unsigned)chunk * (unsigned)w.tiles);
     const int t = tile * w.tile + in_tile;
     if (in_tile >= w.tile || t >= a.tokens) return;
-    const int turning = a.rotary_dim / (2 * N);  // columns that turn
+    const int turning = (a.rotary_dim + 2 * N - 1) / (2 * N);  // columns that turn
+    const int pairs = a.rotary_dim / 2 - col * N;              // (of this one)
     // places of the column's two parts in a head
     int pa, pb;
-    if (col >= turning) {
-        pa = a.rotary_dim + (col - turning) * 2 * N;
-        pb = pa + N;
-    } else if (LAYOUT == KVFIX_ROPE_HALF) {
+    bool wide = false;
+    if (LAYOUT == KVFIX_ROPE_HALF && col < turning) {
         pa = col * N;
         pb = pa + a.rotary_dim / 2;
-    } else {
+    } else if (!kMixed) {
         pa = col * 2 * N;
         pb = pa + N;
+    } else {
+        // behind those that turn: pairs up to a border of vectors, then vectors
+        const int behind = col - turning, border = (a.rotary_dim + 7) / 8 * 8, odd = (border - a.rotary_dim) / 2;
+        wide = behind >= odd;
+        pa = wide ? border + 8 * (behind - odd) : a.rotary_dim + 2 * behind;
+        pb = pa + 1;
     }
     const int p = __ldg(a.positions + (long long)chunk * a.tokens + t);
     const int heads0 = a.ip[0].heads, heads = heads0 + a.ip[1].heads;
@@ -130,7 +145,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < kRotaryHeads; ++i) {
             const int h = h0 + i * w.runs;
-            if (h < heads) v[i].load(h < heads0 ? in0 + h * a.dim : in1 + (h - heads0) * a.dim, pa, pb);
+            if (h < heads) v[i].load(h < heads0 ? in0 + h * a.dim : in1 + (h - heads0) * a.dim, pa, pb, wide);
         }
     };
     load(l0, run);  // (on their way while the angles are worked out)
@@ -140,6 +155,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     if (turns) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
+            // (turns is 0 behind the last pair)
             const long long phase = (long long)((unsigned long long)(long long)p * a.turns[col * N + k]);
             sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s[k], &c[k]);  // 2^-63: half turns
             c[k] *= a.attention;
@@ -155,8 +171,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
             for (int i = 0; i < kRotaryHeads; ++i) {
                 const int h = h0 + i * w.runs;
                 if (h >= heads) continue;
-                if (turns) v[i].template turn<LAYOUT>(c, s);
-                v[i].store(h < heads0 ? out0 + h * a.dim : out1 + (h - heads0) * a.dim, pa, pb);
+                if (turns) v[i].template turn<LAYOUT>(c, s, pairs);
+                v[i].store(h < heads0 ? out0 + h * a.dim : out1 + (h - heads0) * a.dim, pa, pb, wide);
             }
         }
     }
@@ -189,16 +205,27 @@ void rotary_angles(const kvfix_rope& r, RotaryArgs* a) {
     a->attention = (float)r.attention;
 }
 
+// Measured: 4096 tokens x 32 layers x 8 heads of 128, half of each head turned: 87 us, 6.2 TB/s (a
+// copy's bytes take 79); 8192 tokens x 40 heads of 128 in place: 29 us, 5.7 TB/s (32 with the first
+// loads behind the angles); 16 x 8 tokens x 40 heads: 3.4 us, one launch and two trips to memory.
+// Columns of pairs (20 of 128 turned, half layout): 4.4 TB/s, 2.1 when all of the head went by pairs.
+// Two or eight heads in flight, streaming loads or stores: even, or up to 10 % slower.
+//
 // The split.  A thread has a token's heads one after another, four in flight, while that leaves
 // enough threads to fill the GPU; with fewer tokens the heads are spread over 2, 4, ... threads until
-// each has one.  Blocks take several layers (a thread's angles are used for all of them) where
+// each has one (8 x 512 tokens x 40 heads: 16.6 us, 32 if spread four times as far).  Blocks take several layers (a thread's angles are used for all of them) where
 // that leaves four blocks an SM.
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const int heads = a.ip[0].heads + a.ip[1].heads;
     if (a.chunks == 0 || a.layers == 0 || a.tokens == 0 || heads == 0) return cudaSuccess;
-    const bool vec = a.rotary_dim % 16 == 0;
+    const bool half = a.layout == KVFIX_ROPE_HALF, mixed = half && a.rotary_dim % 16 != 0;
     RotarySplit w;
-    w.columns = (a.in_place ? a.rotary_dim : a.dim) / (vec ? 16 : 2);
+    if (mixed) {
+        const int border = (a.rotary_dim + 7) / 8 * 8;
+        w.columns = a.in_place ? a.rotary_dim / 2 : border / 2 + (a.dim - border) / 8;
+    } else {
+        w.columns = a.in_place ? (a.rotary_dim + 15) / 16 : a.dim / 16;
+    }
     const int slots = kRotaryThreads / w.columns;
     const double rows = (double)a.chunks * a.layers * a.tokens, full = 152.0 * 1536.0;
     w.runs = 1;
@@ -214,13 +241,9 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const double blocks = (double)a.chunks * w.tiles * w.layer_blocks;
     if (blocks > 2147483647.0) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)((long long)a.chunks * w.tiles * w.layer_blocks)), threads(kRotaryThreads);
-    if (vec) {
-        if (a.layout == KVFIX_ROPE_HALF) rotary_kernel<KVFIX_ROPE_HALF, true><<<grid, threads, 0, s>>>(a, w);
-        else rotary_kernel<KVFIX_ROPE_INTERLEAVED, true><<<grid, threads, 0, s>>>(a, w);
-    } else {
-        if (a.layout == KVFIX_ROPE_HALF) rotary_kernel<KVFIX_ROPE_HALF, false><<<grid, threads, 0, s>>>(a, w);
-        else rotary_kernel<KVFIX_ROPE_INTERLEAVED, false><<<grid, threads, 0, s>>>(a, w);
-    }
+    if (mixed) rotary_kernel<KVFIX_ROPE_HALF, RotaryMixed><<<grid, threads, 0, s>>>(a, w);
+    else if (half) rotary_kernel<KVFIX_ROPE_HALF, RotaryVectors><<<grid, threads, 0, s>>>(a, w);
+    else rotary_kernel<KVFIX_ROPE_INTERLEAVED, RotaryVectors><<<grid, threads, 0, s>>>(a, w);
     return cudaGetLastError();
 }
 
