@@ -992,8 +992,8 @@ def _books(pool, page_tokens, refs, pages, lens, names, more):
     if page_tokens < 1 or refs.numel() != pd.slots // page_tokens:
         raise ValueError(f"refs must hold a count for each of the pool's {pd.slots} / {page_tokens} pages")
     for t, name in zip(more, names):
-        if t is not None and t.shape[:1] != (lists,):
-            raise ValueError(f"{name} must have a row for each list")
+        if t is not None and t.numel() != lists:
+            raise ValueError(f"{name} must hold a number for each list")
     return pd, page_tokens, refs.data_ptr(), pages.data_ptr(), shape[1], lens.data_ptr(), lists
 
 
@@ -1025,10 +1025,13 @@ def pages_cut(pool: Pool, page_tokens: int, refs, pages, lens, base, path=None, 
     given back.  All int32, the books changed in place."""
     if (path is None) != (kept is None):
         raise ValueError("path and kept come together")
-    books = _books(pool, page_tokens, refs, pages, lens, ("base", "path", "kept"), (base, path, kept))
+    books = _books(pool, page_tokens, refs, pages, lens, ("base", "kept"), (base, kept))
     most = 0
     if path is not None:
-        if path.dim() != 2:
+        if not _ints(pool.k.get_device(), (path,)):
+            _i32(path, "path")
+            raise ValueError("the pool, the books and their arguments must be on one device")
+        if path.dim() != 2 or path.shape[0] != books[-1]:
             raise ValueError("path must be [lists][most]")
         most = path.shape[1]
     _check(lib.kvfix_pages_cut(*books, base.data_ptr(), path.data_ptr() if most else None, most,

@@ -260,7 +260,9 @@ def test_the_binding_checks_what_it_is_given(kvfix, lib):
     kvfix.pages_cut(**books(kvfix), base=OnGpu(3), path=OnGpu(3, 0), kept=OnGpu(3))
     kvfix.pages_compact(**books(kvfix))
     for call, kw, error in (
-            (kvfix.pages_extend, dict(extra=OnGpu(2)), "extra"), (kvfix.pages_extend, dict(extra=OnGpu(3), parent=OnGpu(4)), "parent"),
+            (kvfix.pages_extend, dict(extra=OnGpu(2)), "extra"), (kvfix.pages_extend, dict(extra=OnGpu(3, 2)), "extra"),
+            (kvfix.pages_cut, dict(base=OnGpu(3), path=OnGpu(3, 2), kept=OnGpu(2)), "kept"),
+            (kvfix.pages_cut, dict(base=OnGpu(3), path=OnGpu(3, 2, device=1), kept=OnGpu(3)), "one device"), (kvfix.pages_extend, dict(extra=OnGpu(3), parent=OnGpu(4)), "parent"),
             (kvfix.pages_extend, dict(extra=OnGpu(3), refs=OnGpu(5)), "refs"), (kvfix.pages_extend, dict(extra=OnGpu(3), lens=OnGpu(2)), "pages"),
             (kvfix.pages_extend, dict(extra=OnGpu(3), workspace=OnGpu(1 << 20, dtype=torch.uint8)[::2]), "contiguous"),
             (kvfix.pages_compact, dict(workspace=OnGpu(1 << 20, dtype=torch.uint8)[::2]), "contiguous"),

@@ -60,7 +60,8 @@ class Trees(Round):
         return self.kvfix.tree_attend(self.q, self.pool, self.page, tree_mask=self.words,
                                       **{**self.args, "nodes": self.nodes_t, "return_lse": True, **kw})
 
-    def check(self, out, lse):
+    def check(self, out, lse, absent=()):
+        """`absent`: (agent, place in its sequence) pairs of keys that count as not there."""
         K, V, q = self.values("k"), self.values("v"), pool_ref.of_bf16(self.q_words)
         got, got_lse = pool_ref.of_bf16(words_of(out)), lse.cpu().numpy().astype(np.float64)
         T, D = self.new, q.shape[-1]
@@ -69,10 +70,13 @@ class Trees(Round):
             n0 = 0 if g is None else self.prefix[g]
             at = np.concatenate((self.rows(self.tables[0][g], n0) if n0 else np.zeros(0, np.int64),
                                  self.rows(self.tables[1][a], self.own[a])))
+            gone = [p for b, p in absent if b == a]
+            at[gone] = 0
             k, v, n, N = K(at), V(at), len(at), self.nodes[a]
             sees = np.zeros((T, n), bool)
             sees[:N, :n - N] = True
             sees[:N, n - N:] = self.bits[a, :N, :N]
+            sees[:, gone] = False
             want, want_lse = ref.attend(q[a], k, v, sees, self.scale)
             mean, _ = ref.attend(q[a], k, np.abs(v), sees, self.scale)
             mags = np.zeros(want_lse.shape)
@@ -168,6 +172,33 @@ def test_numbers_of_nodes_out_of_range_are_clamped(kvfix, T, group):
     out, lse = r.call(nodes=None)                   # T each, of which agents 0 and 2 have 2 and 5 own keys
     with pytest.raises(kvfix.KvfixError):
         kvfix.check_status()
+    kvfix.check_status()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,group", ((4, 2), (40, 2)))
+def test_pages_out_of_range_count_as_absent(kvfix, fmt, T, group):
+    """Before the trees, in them, and in the prefix."""
+    r = Trees(kvfix, fmt, 2, group, 64, 16, T, [100], [0, 2], [40, 20], [T, T], kind="any")
+    # (row 0 of the pool, which stands for the keys that are not there, must be some key's)
+    zero = [i for t in r.tables for i in np.argwhere(t == 0)]
+    if not zero:
+        r.pool.k[:, 0], r.pool.v[:, 0] = r.pool.k[:, int(r.tables[1][0, 0]) * 16], r.pool.v[:, int(r.tables[1][0, 0]) * 16]
+        for s in r.pool[3:]:
+            if s is not None:
+                s[:, :, 0] = s[:, :, int(r.tables[1][0, 0]) * 16]
+    r.args["prefix_pages"][0, 2] = -1
+    r.args["suffix_pages"][0, 1] = -5
+    last = (20 + T - 1) // 16
+    r.args["suffix_pages"][1, last] = r.pool.k.shape[1] // 16
+    out, lse = r.call()
+    with pytest.raises(kvfix.KvfixError) as e:
+        kvfix.check_status()
+    assert e.value.status == kvfix.EDEVICE
+    absent = [(a, 32 + i) for a in (0, 1) for i in range(16)] + [(0, 100 + 16 + i) for i in range(16)]
+    absent += [(1, 100 + i) for i in range(16 * last, 20 + T)]
+    r.check(out, lse, absent)
     kvfix.check_status()
 
 
