@@ -1268,6 +1268,7 @@ static kvfix_status check_pages(const char* fn, const kvfix_pool& pool, int page
     *a = PagesArgs{};
     a->pool = view_of(pool);
     a->page = page_tokens;
+    a->page_log = page_tokens == 16 ? 4 : page_tokens == 32 ? 5 : page_tokens == 64 ? 6 : 7;
     a->total = pool.slots / page_tokens;
     a->refs = const_cast<int32_t*>(refs);
     a->pages = const_cast<int32_t*>(pages);

@@ -77,7 +77,8 @@ __device__ __forceinline__ void for_pages(const int32_t* refs, int lo, int hi, F
 
 __device__ __forceinline__ int span_of(int total) { return ((total + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32; }
 
-__device__ __forceinline__ int pages_of(long long tokens, int page) { return (int)((tokens + page - 1) / page); }
+// Pages of a number of tokens (below 2^30 + 2^7).
+__device__ __forceinline__ int pages_of(int tokens, const PagesArgs& a) { return (tokens + a.page - 1) >> a.page_log; }
 
 // `n` 16-byte vectors by `threads` threads, four in flight each.
 __device__ __forceinline__ void copy_vectors(const unsigned char* src, unsigned char* dst, int n, int tid, int threads) {
@@ -200,9 +201,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
                 const int n = x.from < a.lists ? a.len[x.from] : -1;
                 bool fine = n >= 0 && n <= most && add >= 0 && n + (long long)add <= most && (!fork || own == 0);
                 if (fine) {
-                    x.have = pages_of(n, a.page);
-                    x.want = pages_of((long long)n + add, a.page);
-                    x.rows = n % a.page;
+                    x.have = pages_of(n, a);
+                    x.want = pages_of(n + add, a);
+                    x.rows = n & (a.page - 1);
                     if (x.have > 0) {
                         x.last = a.pages[(long long)x.from * a.wide + x.have - 1];
                         fine = x.last >= 0 && x.last < a.total;
@@ -374,11 +375,11 @@ __global__ void __launch_bounds__(kCutThreads, 2) cut_kernel(const __grid_consta
         __syncthreads();
         for (int j = tid; j < n; j += kCutThreads) {
             const int to = keep + j0 + j, from = keep + path[(long long)i * max_path + j0 + j];
-            const int pf = table[from / a.page], pt = table[to / a.page];
+            const int pf = table[from >> a.page_log], pt = table[to >> a.page_log], in = a.page - 1;
             const bool there = pf >= 0 && pf < a.total && pt >= 0 && pt < a.total;
             bad |= !there;
-            src[j] = there && from != to ? pf * a.page + from % a.page : -1;
-            dst[j] = there ? pt * a.page + to % a.page : -1;
+            src[j] = there && from != to ? pf * a.page + (from & in) : -1;
+            dst[j] = there ? pt * a.page + (to & in) : -1;
         }
         __syncthreads();
         // the last places are known: nothing of the list's books is read any more
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kCutThreads, 2) cut_kernel(const __grid_consta
     }
     if (first) {
         const int end = keep + rows;
-        for (int k = pages_of(end, a.page) + tid; k < pages_of(len, a.page); k += kCutThreads) {
+        for (int k = pages_of(end, a) + tid; k < pages_of(len, a); k += kCutThreads) {
             const int p = table[k];
             if (p < 0 || p >= a.total) {
                 bad = true;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
                 continue;
             }
             int32_t* const table = a.pages + (long long)i * a.wide;
-            const int c1 = min(pages_of(n, a.page), (part + 1) * kTablePart);
+            const int c1 = min(pages_of(n, a), (part + 1) * kTablePart);
             for (int x = part * kTablePart + threadIdx.x; x < c1; x += kMoveThreads) {
                 const int p = table[x];
                 if (p < 0 || p >= a.total) bad = true;

@@ -8,7 +8,7 @@ namespace kvfix {
 // The pool and its books: how many lists hold each page, the lists' pages and their lengths.
 struct PagesArgs {
     PoolView pool;
-    int page, total;  // tokens per page, pages of the pool
+    int page, page_log, total;  // tokens per page (2^page_log), pages of the pool
     int32_t* refs;    // [total]
     int32_t* pages;   // [lists][wide]
     int32_t* len;     // [lists]
