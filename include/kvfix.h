@@ -57,7 +57,7 @@ typedef uint16_t kvfix_bf16;
 typedef enum {
     KVFIX_OK = 0,
     KVFIX_EINVAL = 1,   /* bad argument; nothing was launched */
-    KVFIX_ENOSPACE = 2, /* diff payload capacity too small (see kvfix_diff_encode) */
+    KVFIX_ENOSPACE = 2, /* diff payload capacity too small (see kvfix_diff_encode), or no free page */
     KVFIX_ECUDA = 3,    /* a CUDA runtime call or launch failed */
     KVFIX_ETIMEOUT = 4, /* a bounded device-side wait gave up */
     KVFIX_EDEVICE = 5   /* the device flagged bad caller data (index out of range) */
@@ -83,7 +83,8 @@ KVFIX_API const char* kvfix_last_error(void);
 
 /* Synchronise `stream`, then read and clear the device status word.
  * Returns KVFIX_OK, KVFIX_EDEVICE (an index out of range was skipped),
- * KVFIX_ENOSPACE (a payload write was skipped), KVFIX_ETIMEOUT or KVFIX_ECUDA. */
+ * KVFIX_ENOSPACE (a payload write was skipped, or lists wanted more pages than the pool has
+ * free), KVFIX_ETIMEOUT or KVFIX_ECUDA. */
 KVFIX_API kvfix_status kvfix_check_status(void* stream);
 
 /*
