@@ -1062,9 +1062,8 @@ static kvfix_status attend(const char* fn, bool is_tree, const int32_t* nodes, c
                            int32_t max_suffix_pages, const int32_t* suffix_len, double scale, kvfix_bf16* out,
                            kvfix_kv_desc od, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
     kvfix_status st;
-    char what_q[64], what_out[64];
-    snprintf(what_q, sizeof what_q, "%s: q", fn);
-    snprintf(what_out, sizeof what_out, "%s: out", fn);
+    const char* what_q = is_tree ? "kvfix_tree_attend: q" : "kvfix_shared_attend: q";
+    const char* what_out = is_tree ? "kvfix_tree_attend: out" : "kvfix_shared_attend: out";
     if ((st = check_plane(q, qd, what_q, no_rows(qd))) != KVFIX_OK) return st;
     if ((st = check_plane(out, od, what_out, no_rows(od))) != KVFIX_OK) return st;
     if ((st = check_pool(pool, fn)) != KVFIX_OK) return st;

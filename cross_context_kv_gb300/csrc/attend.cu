@@ -695,7 +695,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         bool ok = true;
         unsigned at = 0, units = 0;
         int rows = 0, sees = 0;   // of the unit: the group's rows; keys this row sees
-        bool live = false;        // whether this lane has a row that sees any: the others are computed and left
+        bool live = true;         // trees: whether this lane has a row that sees any (the others are computed and left)
         int tree0 = 0x7fffffff;   // trees: where the tree begins, in own keys
         const uint32_t* mask = nullptr;  // and this row's view of it
         float m = -INFINITY, l = 0.f;
@@ -711,10 +711,13 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 rows = it.rows;
                 m = -INFINITY;
                 l = 0.f;
-                // (a lane without a row sees every key, so that it asks for no mask)
-                sees = 0x7fffffff;
-                live = row < rows;
-                tree0 = 0x7fffffff;
+                sees = 0;
+                if constexpr (TREE) {
+                    // (a lane without a row sees every key, so that it asks for no mask)
+                    sees = 0x7fffffff;
+                    live = row < rows;
+                    tree0 = 0x7fffffff;
+                }
                 if (row < rows) {
                     const int G = a.q_heads / a.pool.heads, T = a.new_tokens, TG = T * G;
                     const int x = it.row0 + row, ag = x / TG, t = (x - ag * TG) / G;
@@ -813,7 +816,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 }
                 tmem_ld32(s_at, x[0]);
                 const float z = mx * c;
-                const bool raise = live && (z > m + kAtSlack || (m == -INFINITY && z > m));
+                bool raise = z > m + kAtSlack || (m == -INFINITY && z > m);
+                if constexpr (TREE) raise = raise && live;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m - z) : 1.f;  // m = -inf: 0
                     if (raise) {
@@ -883,7 +887,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                             if (r + 8 < rows) *reinterpret_cast<uint2*>(out + 8 * D + 8 * k) = make_uint2(o[4 * k + 2], o[4 * k + 3]);
                         }
                     }
-                    if (row < rows) w.ml[part + row] = live ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+                    if (row < rows) w.ml[part + row] = !TREE || live ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
                     tc_fence_before();
                 }
             }
@@ -1380,7 +1384,7 @@ template <int F, int D, bool TREE>
 static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int device, cudaStream_t s) {
     using C = AtCfg<F, D>;
     cudaError_t e;
-    if ((e = launch_chained(attend_plan_kernel<TREE>, dim3(1), dim3(kPlanBlock), 0, s, a, w)) != cudaSuccess) return e;
+    if ((e = launch_chained(attend_plan_kernel<TREE>, dim3(1), dim3(kPlanThreads), 0, s, a, w)) != cudaSuccess) return e;
     if (w.many) {
         CUtensorMap mk, mv;
         if (!pool_map<F, D>(&mk, a.pool, 0, a.page) || !pool_map<F, D>(&mv, a.pool, 1, a.page)) return cudaErrorInvalidValue;

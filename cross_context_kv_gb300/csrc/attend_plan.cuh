@@ -139,33 +139,31 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 }
 
 // The plan is one CTA whose code runs once, so its time is latency: trips to memory and fetches of
-// instructions.  256 threads share out the segments; 640 write the entries and the pieces'
-// beginnings, one each (608 of 152 CTAs).  Scans are loops, and what a segment's thread worked out
-// for the scan it keeps for what comes after.
-constexpr int kPlanThreads = 256, kPlanBlock = 640;
+// instructions.  Scans are loops, and what a segment's thread worked out for the scan it keeps for
+// what comes after.  (640 threads, one for each piece's beginning: 68.6 us against 69.2 for a round
+// of 8 trees, but 14.2 against 13.6 for one small tree.)
+constexpr int kPlanThreads = 256;
 
 struct PlanSums {
     int n[3];
     long long line[3];
 };
-// Exclusive scan over the first kPlanThreads threads, and the totals.
+// Exclusive scan over the block, and the totals.
 __device__ __forceinline__ PlanSums plan_scan(const PlanSums& x, PlanSums* warp_sums, PlanSums* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     PlanSums inc = x;
-    if (warp < kPlanThreads / 32) {
 #pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1)
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const int a = __shfl_up_sync(0xffffffffu, inc.n[k], o);
-                const long long b = __shfl_up_sync(0xffffffffu, inc.line[k], o);
-                if (lane >= o) {
-                    inc.n[k] += a;
-                    inc.line[k] += b;
-                }
+        for (int k = 0; k < 3; ++k) {
+            const int a = __shfl_up_sync(0xffffffffu, inc.n[k], o);
+            const long long b = __shfl_up_sync(0xffffffffu, inc.line[k], o);
+            if (lane >= o) {
+                inc.n[k] += a;
+                inc.line[k] += b;
             }
-        if (lane == 31) warp_sums[warp] = inc;
-    }
+        }
+    if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
     PlanSums ex, all = {};
 #pragma unroll
@@ -194,7 +192,7 @@ constexpr int kPlanKept = 256;  // entries of a line that stay in shared memory
 
 // TREE: kvfix_tree_attend's, whose agents have numbers of new tokens of their own.
 template <bool TREE>
-__global__ void __launch_bounds__(kPlanBlock) attend_plan_kernel(const __grid_constant__ AttendArgs a,
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendArgs a,
                                                                    const __grid_constant__ AtWork w) {
     __shared__ PlanSums warp_sums[kPlanThreads / 32];
     __shared__ int warp_max[kPlanThreads / 32];
@@ -239,10 +237,10 @@ __global__ void __launch_bounds__(kPlanBlock) attend_plan_kernel(const __grid_co
             const int y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc = max(inc, y);
         }
-        if (lane == 31 && warp < kPlanThreads / 32) warp_max[warp] = inc;
+        if (lane == 31) warp_max[warp] = inc;
         __syncthreads();
         int run = 0;
-        for (int x = 0; x < min(warp, kPlanThreads / 32); ++x) run = max(run, warp_max[x]);
+        for (int x = 0; x < warp; ++x) run = max(run, warp_max[x]);
         const int left = __shfl_up_sync(0xffffffffu, inc, 1);
         if (lane > 0) run = max(run, left);
         for (int g = g0; g < g1; ++g) {
@@ -365,7 +363,7 @@ __global__ void __launch_bounds__(kPlanBlock) attend_plan_kernel(const __grid_co
     }
     __syncthreads();
     if (near)
-        for (int i = tid; i < total.n[kPairs]; i += kPlanBlock) {
+        for (int i = tid; i < total.n[kPairs]; i += kPlanThreads) {
             int x = 0, y = segs;  // the last segment whose pairs begin at or before i
             while (y - x > 1) {
                 const int m = (x + y) / 2;
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(kPlanBlock) attend_plan_kernel(const __grid_co
                                 max(1ll, quotient(total.line[1] + 2 * nm - 1, 2 * nm)),
                                 max(1ll, quotient(total.line[2] + few_pieces - 1, few_pieces))};
     // (a few-row CTA has its warps' pieces as one)
-    for (int i = tid; i < 4 * w.ctas; i += kPlanBlock) {
+    for (int i = tid; i < 4 * w.ctas; i += kPlanThreads) {
         const int cta = i % w.ctas, set = i / w.ctas, k = set == 0 ? kPairs : set == 3 ? kFew : kSingles;
         AtStart* st = &w.plan->start[set][cta];
         const long long size = k == kFew ? chunk[kFew] * kFewWarps : k == kSingles ? chunk[kSingles] : chunk[kPairs];

@@ -109,6 +109,9 @@ CASES = {
     "blocks": (1, 8, 64, 16, 70, [500], [0, 3], [10, 64, 0], [70, 33, 64]),
     "groups": (4, 3, 64, 32, 10, [64, 0, 1, 200], [0, 2, 3, 3, 6], [5, 0, 70, 0, 31, 90], [10, 4, 0, 10, 1, 9]),
     "some_outside": (2, 5, 128, 16, 7, [40], [1, 3], [3, 0, 8, 20, 0], [7, 0, 7, 2, 7]),
+    "many_agents": (1, 2, 64, 16, 3, [20, 7], [0, 150, 290], [5 * i % 37 for i in range(300)], [i % 4 for i in range(300)]),
+    "many_groups": (1, 1, 64, 16, 17, [3 * g % 50 for g in range(270)], list(range(271)), [i % 5 for i in range(280)],
+                    [17 - i % 3 for i in range(280)]),
     "nobody": (2, 2, 64, 16, 5, [40], [0, 2], [0, 20], [0, 0]),
 }
 
