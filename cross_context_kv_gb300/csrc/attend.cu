@@ -153,82 +153,83 @@ __device__ __forceinline__ void regs_dec() {
 
 // One stored tile (codes [128][kCodeRow], scales [128][kScaleRow]) to the bf16 tile the MMA
 // reads: rows of 128 bytes per 64-column half, 128-byte swizzle.  Rows that hold no key become
-// zero.  A team of N threads first takes the whole stored tile into registers, so that the
-// next one can be on its way while this one is converted; a thread has 16 code bytes of a row
-// at a time, and the order in which it writes their 16-byte chunks puts the eight threads of a
-// store phase on different banks.
+// zero.  A team's thread has a row: its scale and addresses are worked out once, and a vector's
+// place is one exclusive or away.  It first takes the whole row into registers, so that the
+// next tile can be on its way while this one is converted.  Row r takes its vectors in the order
+// i ^ m(r): the eight threads of a phase then read different banks (a row is one, two or four of 128
+// bytes) and write different ones too, the swizzle being a row's own exclusive or.  (Neighbouring
+// threads on a row's vectors, a scale and addresses for each: 8 instructions a value instead of
+// AFTER.)
 template <int F, int D, int N>
 struct StoredTile {
     using C = AtCfg<F, D>;
-    static constexpr int V = C::kCodeRow / 16;  // vectors per row
-    static constexpr int P = kAtKeys * V / N;   // vectors per thread
-    uint4 x[P];
-    unsigned sc[P];
+    static_assert(N == kAtKeys, "a thread per row");
+    static constexpr bool kE4m3 = F == KVFIX_POOL_E4M3;
+    static constexpr int V = C::kCodeRow / 16;            // vectors per row
+    static constexpr int B = kE4m3 ? 4 : 2;               // in a round, the rest moving down between rounds:
+    static constexpr int kRounds = V / B;                 // the roles' code has to fit the instruction caches
+    static constexpr int kScales = kE4m3 ? 1 : V;
+    uint4 x[V];
+    unsigned sc[kScales];
 
-    __device__ __forceinline__ void take(const unsigned char* raw, int tid) {
-        const unsigned char* scales = raw + kAtKeys * C::kCodeRow;
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-            const int r = tid / V + k * (N / V);
-            x[k] = *reinterpret_cast<const uint4*>(raw + 16 * (tid + k * N));
-            if (F == KVFIX_POOL_E4M3) sc[k] = scales[r];
-            else sc[k] = *reinterpret_cast<const unsigned*>(scales + r * C::kScaleRow + 4 * (tid % V));
-        }
+    static __device__ __forceinline__ int mix(int r) {
+        const int k = (r >> 1) & 3;
+        if (V == 8) return r & 7;
+        if (V == 4) return kE4m3 ? ((k & 1) << 1) ^ ((k >> 1) * 3) : k;  // (both k -> m and, for e4m3, m ^ k one to one)
+        return 0;                                                         // (two vectors: loads meet in pairs)
     }
 
-    // In rounds of two vectors, the rest moving down between them: with all eight unrolled the
-    // roles' code outgrows the instruction caches (a quarter of the stalls were for
-    // instructions).
-    __device__ __forceinline__ void put(unsigned char* tile, int tid, int in_tile, unsigned absent) {
-        constexpr int B = P < 2 ? P : 2;
-        int r0 = tid / V;
-        const int v = tid % V;
-        const bool partial = in_tile < kAtKeys || absent != 0u;
+    __device__ __forceinline__ void take(const unsigned char* raw, int r) {
+        const unsigned char* scales = raw + kAtKeys * C::kCodeRow + r * C::kScaleRow;
+        const int m = mix(r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + r * C::kCodeRow + 16 * (i ^ m));
+#pragma unroll
+        for (int i = 0; i < kScales; ++i)
+            sc[i] = kE4m3 ? (unsigned)*scales : *reinterpret_cast<const unsigned*>(scales + 4 * (i ^ m));
+    }
+
+    __device__ __forceinline__ void put(unsigned char* tile, int r, int in_tile, unsigned absent) {
+        const bool gone = r >= in_tile || ((absent >> (r >> 4)) & 1u);
+        const int m = mix(r);
+        unsigned char* const row = tile + r * 128;
+        E4m3Scale es;
+        if (kE4m3) {
+            es = e4m3_scale_byte(sc[0]);
+            if (gone) es.a = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+        }
+        // where vector i's first chunk goes: the half's bit, and the chunk under the row's swizzle
+        auto place = [](int i) { return kE4m3 ? ((i & 4) << 12) | ((i & 3) << 5) : ((i & 2) << 13) | ((i & 1) << 6); };
+        int at = place(m) ^ ((r & 7) << 4);
 #pragma unroll 1
-        for (int k0 = 0; k0 < P; k0 += B, r0 += B * (N / V)) {
-            put_some<B>(tile, r0, v, partial, in_tile, absent);
+        for (int t = 0; t < kRounds; ++t) {
 #pragma unroll
-            for (int k = 0; k + B < P; ++k) {
-                x[k] = x[k + B];
-                sc[k] = sc[k + B];
-            }
-        }
-    }
-
-    template <int B>
-    __device__ __forceinline__ void put_some(unsigned char* tile, int r0, int v, bool partial, int in_tile,
-                                             unsigned absent) const {
+            for (int b = 0; b < B; ++b) {
+                const int to = at ^ place(b);
+                if constexpr (kE4m3) {
+                    uint4 o0, o1;
+                    e4m3x16_to_bf16(x[b], es, o0, o1);
+                    *reinterpret_cast<uint4*>(row + to) = o0;
+                    *reinterpret_cast<uint4*>(row + (to ^ 16)) = o1;
+                } else {
+                    const unsigned sz = gone ? 0u : sc[b];
+                    const unsigned ss = __byte_perm(sz, 0u, 0x1010), zz = __byte_perm(sz, 0u, 0x3232);
+                    const unsigned c[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
 #pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const int r = r0 + k * (N / V);
-            const bool gone = partial && (r >= in_tile || ((absent >> (r >> 4)) & 1u));
-            const unsigned c[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            if (F == KVFIX_POOL_E4M3) {
-                E4m3Scale es = e4m3_scale_byte(sc[k]);
-                if (gone) es.a = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
-                uint4 o0, o1;
-                e4m3x16_to_bf16(x[k], es, o0, o1);
-                unsigned char* dst = tile + (v / 4) * (kAtKeys * 128) + r * 128;
-                const int c0 = 2 * (v % 4), sw = (v / 4) & 1;  // the upper half's odd chunk first
-                const int a0 = ((c0 ^ (r & 7)) << 4), a1 = (((c0 + 1) ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4*>(dst + (sw ? a1 : a0)) = sw ? o1 : o0;
-                *reinterpret_cast<uint4*>(dst + (sw ? a0 : a1)) = sw ? o0 : o1;
-            } else {
-                const unsigned sz = gone ? 0u : sc[k];
-                const unsigned ss = __byte_perm(sz, 0u, 0x1010), zz = __byte_perm(sz, 0u, 0x3232);
-                unsigned char* dst = tile + (v / 2) * (kAtKeys * 128) + r * 128;
-                const int sw = ((v / 2) & 1) ? 2 : 0;  // the upper half's chunks in the order 2 3 0 1
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 o = int4x8_to_bf16(sw ? c[q ^ 2] : c[q], *reinterpret_cast<const __nv_bfloat162*>(&ss),
-                                                   *reinterpret_cast<const __nv_bfloat162*>(&zz));
-                    *reinterpret_cast<uint4*>(dst + (((4 * (v % 2) + (q ^ sw)) ^ (r & 7)) << 4)) = o;
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(row + (to ^ (q << 4))) = int4x8_to_bf16(
+                            c[q], *reinterpret_cast<const __nv_bfloat162*>(&ss), *reinterpret_cast<const __nv_bfloat162*>(&zz));
                 }
+            }
+            at ^= 1 << 14;  // (the second round has the other half)
+#pragma unroll
+            for (int b = 0; b + B < V; ++b) {
+                x[b] = x[b + B];
+                if (!kE4m3) sc[b] = sc[b + B];
             }
         }
     }
 };
-
 
 // Two floats at once (packed 32-bit arithmetic).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
