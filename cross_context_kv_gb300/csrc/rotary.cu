@@ -13,8 +13,8 @@
 // are in flight together.  Where little work is left for each, the heads of a token are spread over
 // threads, then every thread has its own head.  Values beyond rotary_dim are columns that are
 // copied, or left out when the call works in place.  In the half layout a rotary_dim that is no
-// multiple of 16 has halves that vectors do not meet: its columns are pairs of 16-bit values, and
-// vectors of what does not turn.
+// multiple of 16 has halves that vectors do not meet: its columns are runs of 4, 2 or 1 values of
+// either half, and vectors of what does not turn.
 //
 // Bound by HBM: see the measured figures at launch_rotary.
 #include <cuda_bf16.h>
@@ -75,40 +75,66 @@ struct RotaryVectors {
         }
     }
 };
-// Half layout with halves that no vector border meets: a pair of 16-bit values, or a vector of those
-// that do not turn.
+// Half layout with halves that no vector border meets: P pairs whose parts are two runs of P 16-bit
+// values (4, 2 or 1 of them, as the halves' length is a multiple of that), or a vector of those that do
+// not turn.
+template <int P>
 struct RotaryMixed {
-    static constexpr int kPairs = 1;
-    uint4 x;
+    static constexpr int kPairs = P;
+    uint4 x;  // the runs in x, y and z, w
+    static __device__ __forceinline__ void get(const uint16_t* p, unsigned& a, unsigned& b) {
+        if (P == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            a = v.x;
+            b = v.y;
+        } else {
+            a = P == 2 ? *reinterpret_cast<const unsigned*>(p) : (unsigned)*p;
+        }
+    }
+    static __device__ __forceinline__ void put(uint16_t* p, unsigned a, unsigned b) {
+        if (P == 4) *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+        else if (P == 2) *reinterpret_cast<unsigned*>(p) = a;
+        else *p = (uint16_t)a;
+    }
     __device__ __forceinline__ void load(const uint16_t* p, int a, int b, bool wide) {
         if (wide) {
             x = *reinterpret_cast<const uint4*>(p + a);
         } else {
-            x.x = p[a];
-            x.y = p[b];
+            get(p + a, x.x, x.y);
+            get(p + b, x.z, x.w);
         }
     }
     __device__ __forceinline__ void store(uint16_t* p, int a, int b, bool wide) const {
         if (wide) {
             *reinterpret_cast<uint4*>(p + a) = x;
         } else {
-            p[a] = (uint16_t)x.x;
-            p[b] = (uint16_t)x.y;
+            put(p + a, x.x, x.y);
+            put(p + b, x.z, x.w);
         }
     }
     template <int LAYOUT>
     __device__ __forceinline__ void turn(const float* c, const float* s, int) {
-        const float u = __uint_as_float(x.x << 16), v = __uint_as_float(x.y << 16);
-        x.x = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(u, c[0], __fmul_rn(v, -s[0]))));
-        x.y = __bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(v, c[0], __fmul_rn(u, s[0]))));
+        const unsigned lo[2] = {x.x, x.y}, hi[2] = {x.z, x.w};
+        unsigned u[2] = {0, 0}, v[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            const int w = k >> 1, at = 16 * (k & 1);
+            const float a = __uint_as_float(lo[w] >> at << 16), b = __uint_as_float(hi[w] >> at << 16);
+            u[w] |= (unsigned)__bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(a, c[k], __fmul_rn(b, -s[k])))) << at;
+            v[w] |= (unsigned)__bfloat16_as_ushort(__float2bfloat16_rn(__fmaf_rn(b, c[k], __fmul_rn(a, s[k])))) << at;
+        }
+        x = make_uint4(u[0], u[1], v[0], v[1]);
     }
 };
+
+// The pairs of a column of such halves.
+static int mixed_pairs(int rotary_dim) { return rotary_dim % 8 == 0 ? 4 : rotary_dim % 4 == 0 ? 2 : 1; }
 
 template <int LAYOUT, typename V>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a,
                                                                 const __grid_constant__ RotarySplit w) {
     constexpr int N = V::kPairs;
-    constexpr bool kMixed = N == 1;
+    constexpr bool kMixed = N < 8;
     const int slot = threadIdx.x / w.columns, col = threadIdx.x - slot * w.columns;
     const int in_tile = slot / w.runs, run = slot - in_tile * w.runs;
     unsigned b = blockIdx.x;
@@ -129,11 +155,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
         pa = col * 2 * N;
         pb = pa + N;
     } else {
-        // behind those that turn: pairs up to a border of vectors, then vectors
-        const int behind = col - turning, border = (a.rotary_dim + 7) / 8 * 8, odd = (border - a.rotary_dim) / 2;
+        // behind those that turn: runs up to a border of vectors, then vectors
+        const int behind = col - turning, border = (a.rotary_dim + 7) / 8 * 8, odd = (border - a.rotary_dim) / (2 * N);
         wide = behind >= odd;
-        pa = wide ? border + 8 * (behind - odd) : a.rotary_dim + 2 * behind;
-        pb = pa + 1;
+        pa = wide ? border + 8 * (behind - odd) : a.rotary_dim + 2 * N * behind;
+        pb = pa + N;
     }
     const int p = __ldg(a.positions + (long long)chunk * a.tokens + t);
     const int heads0 = a.ip[0].heads, heads = heads0 + a.ip[1].heads;
@@ -208,7 +234,8 @@ void rotary_angles(const kvfix_rope& r, RotaryArgs* a) {
 // Measured: 4096 tokens x 32 layers x 8 heads of 128, half of each head turned: 87 us, 6.2 TB/s (a
 // copy's bytes take 79); 8192 tokens x 40 heads of 128 in place: 29 us, 5.7 TB/s (32 with the first
 // loads behind the angles); 16 x 8 tokens x 40 heads: 3.4 us, one launch and two trips to memory.
-// Columns of pairs (20 of 128 turned, half layout): 4.4 TB/s, 2.1 when all of the head went by pairs.
+// Halves that vectors do not meet: 24 of 96 turned 4.5 TB/s (3.6 by single pairs), 60 of 64 3.4 (2.5),
+// 20 of 128 4.2 (4.4); all of a head by pairs: 2.1.
 // Two or eight heads in flight, streaming loads or stores: even, or up to 10 % slower.
 //
 // The split.  A thread has a token's heads one after another, four in flight, while that leaves
@@ -219,10 +246,11 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const int heads = a.ip[0].heads + a.ip[1].heads;
     if (a.chunks == 0 || a.layers == 0 || a.tokens == 0 || heads == 0) return cudaSuccess;
     const bool half = a.layout == KVFIX_ROPE_HALF, mixed = half && a.rotary_dim % 16 != 0;
+    const int P = mixed_pairs(a.rotary_dim);
     RotarySplit w;
     if (mixed) {
         const int border = (a.rotary_dim + 7) / 8 * 8;
-        w.columns = a.in_place ? a.rotary_dim / 2 : border / 2 + (a.dim - border) / 8;
+        w.columns = a.in_place ? a.rotary_dim / (2 * P) : border / (2 * P) + (a.dim - border) / 8;
     } else {
         w.columns = a.in_place ? (a.rotary_dim + 15) / 16 : a.dim / 16;
     }
@@ -241,7 +269,9 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const double blocks = (double)a.chunks * w.tiles * w.layer_blocks;
     if (blocks > 2147483647.0) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)((long long)a.chunks * w.tiles * w.layer_blocks)), threads(kRotaryThreads);
-    if (mixed) rotary_kernel<KVFIX_ROPE_HALF, RotaryMixed><<<grid, threads, 0, s>>>(a, w);
+    if (mixed && P == 4) rotary_kernel<KVFIX_ROPE_HALF, RotaryMixed<4>><<<grid, threads, 0, s>>>(a, w);
+    else if (mixed && P == 2) rotary_kernel<KVFIX_ROPE_HALF, RotaryMixed<2>><<<grid, threads, 0, s>>>(a, w);
+    else if (mixed) rotary_kernel<KVFIX_ROPE_HALF, RotaryMixed<1>><<<grid, threads, 0, s>>>(a, w);
     else if (half) rotary_kernel<KVFIX_ROPE_HALF, RotaryVectors><<<grid, threads, 0, s>>>(a, w);
     else rotary_kernel<KVFIX_ROPE_INTERLEAVED, RotaryVectors><<<grid, threads, 0, s>>>(a, w);
     return cudaGetLastError();

@@ -59,6 +59,9 @@ SHAPES = {
     "keys": (2, 3, 37, 0, 5, 128, 64),
     "odd_heads": (3, 1, 5, 7, 3, 96, 48),
     "part_of_20": (2, 2, 9, 5, 1, 80, 20),
+    "part_of_24": (2, 1, 19, 4, 2, 96, 24),
+    "all_but_eight": (1, 3, 21, 3, 2, 64, 56),
+    "part_of_6": (3, 1, 7, 2, 3, 32, 6),
     "two_values": (1, 2, 3, 2, 2, 16, 2),
     "all_but_two": (2, 1, 4, 3, 1, 16, 14),
     "wide": (1, 1, 70, 3, 2, 256, 256),
