@@ -1402,7 +1402,7 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int 
     // 7 us less by one), one while rows are few
     if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
     const int tg = a.new_tokens * (a.q_heads / a.pool.heads);
-    // (8192 rows: 69.5 us a call against 73.3 by the kernel below, 3072 rows 142 against 143; but 2048
+    // (8192 rows: 69.5 us a call against 73.3 by the kernel below, some 3000 rows 142 against 143; but 2048
     // rows of many parts 47 against 39)
     if (TREE && tg >= kTreeJoinRows && rows > (long long)w.ctas * 16) {
         const long long ctas = (long long)a.agents * a.pool.heads * ((tg + kTreeJoinRows - 1) / kTreeJoinRows);
