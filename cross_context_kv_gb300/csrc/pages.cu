@@ -56,11 +56,12 @@ __device__ __forceinline__ int block_sum(int x, int* warp_sums, int* total) {
     return x + before;
 }
 
-// The pages of a warp's span, 32 at a time and eight loads ahead: f(page, refs, there).
-template <typename F>
-__device__ __forceinline__ void for_pages(const int32_t* refs, int lo, int hi, F f) {
+// The pages of a warp's span, 32 at a time and eight loads ahead: f(page, refs, there), until
+// done() says that the rest is of no interest.
+template <typename F, typename Done>
+__device__ __forceinline__ void for_pages(const int32_t* refs, int lo, int hi, F f, Done done) {
     const int lane = threadIdx.x & 31;
-    for (int p0 = lo; p0 < hi; p0 += 8 * 32) {
+    for (int p0 = lo; p0 < hi && !done(); p0 += 8 * 32) {
         int r[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -73,6 +74,14 @@ __device__ __forceinline__ void for_pages(const int32_t* refs, int lo, int hi, F
             if (p0 + 32 * i < hi) f(p, r[i], p < hi);
         }
     }
+}
+
+// Pages in use of a warp's span.  (Lanes add for themselves: with a vote for every 32 pages one
+// SM's issue was the bound, 31 us of an extend over 131072 pages instead of 15.)
+__device__ __forceinline__ int used_pages(const int32_t* refs, int lo, int hi) {
+    int n = 0;
+    for_pages(refs, lo, hi, [&](int, int r, bool) { n += r > 0; }, [] { return false; });
+    return __reduce_add_sync(0xffffffffu, n);
 }
 
 __device__ __forceinline__ int span_of(int total) { return ((total + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32; }
@@ -175,8 +184,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int span = span_of(a.total), lo = min(a.total, warp * span), hi = min(a.total, lo + span);
-    int mine = 0;
-    for_pages(a.refs, lo, hi, [&](int, int r, bool there) { mine += __popc(__ballot_sync(0xffffffffu, there && r <= 0)); });
+    const int mine = hi - lo - used_pages(a.refs, lo, hi);
     if (lane == 0) free_of[warp] = mine;
     __syncthreads();
     int free_pages = 0, before = 0;  // free pages, those of the warps before
@@ -239,13 +247,13 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     // (an upper bound where some did not fit: more entries of fresh than are read)
     taken = (int)min(asked, (long long)free_pages);
     if (threadIdx.x == 0) *e.count = copies;
-    if (before < taken)
+    if (mine > 0 && before < taken)
         for_pages(a.refs, lo, hi, [&](int p, int r, bool there) {
             const unsigned m = __ballot_sync(0xffffffffu, there && r <= 0);
             const int place = before + __popc(m & ((1u << lane) - 1u));
             if (there && r <= 0 && place < taken) e.fresh[place] = p;
             before += __popc(m);
-        });
+        }, [&] { return before >= taken; });
     if (bad) atomicOr(&g_status_pages, FLAG_BOUNDS);
     if (full) atomicOr(&g_status_pages, FLAG_NOSPACE);
 }
@@ -471,18 +479,16 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int span = span_of(a.total), lo = min(a.total, warp * span), hi = min(a.total, lo + span);
-    int used = 0;
-    for_pages(a.refs, lo, hi, [&](int, int r, bool) { used += __popc(__ballot_sync(0xffffffffu, r > 0)); });
+    const int used = used_pages(a.refs, lo, hi);
     if (lane == 0) used_of[warp] = used;
     __syncthreads();
     int live = 0;
 #pragma unroll
     for (int w = 0; w < kPlanWarps; ++w) live += used_of[w];
-    int holes = 0, movers = 0;
-    for_pages(a.refs, lo, hi, [&](int p, int r, bool) {
-        holes += __popc(__ballot_sync(0xffffffffu, r <= 0 && p < live));
-        movers += __popc(__ballot_sync(0xffffffffu, r > 0 && p >= live));
-    });
+    // pages in use below the border at `live`: all of a span before it, none of one behind
+    const int border = min(max(live, lo), hi);
+    const int below = border == hi ? used : border == lo ? 0 : used_pages(a.refs, lo, border);
+    const int holes = border - lo - below, movers = used - below;
     if (lane == 0) {
         holes_of[warp] = holes;
         movers_of[warp] = movers;
@@ -497,17 +503,19 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
         }
         moves += movers_of[w];
     }
-    // (live <= total, so pages below it exist; lanes past the span have r = 0 and p >= hi)
-    for_pages(a.refs, lo, hi, [&](int p, int r, bool there) {
-        const unsigned below = (1u << lane) - 1u;
-        const bool is_hole = there && r <= 0 && p < live, is_mover = r > 0 && p >= live;
-        const unsigned mh = __ballot_sync(0xffffffffu, is_hole), mm = __ballot_sync(0xffffffffu, is_mover);
-        if (is_hole) c.hole[at_hole + __popc(mh & below)] = p;
-        if (is_mover) c.mover[at_mover + __popc(mm & below)] = p;
-        if (there && p >= live && !is_mover) c.to[p] = p;
-        at_hole += __popc(mh);
-        at_mover += __popc(mm);
-    });
+    for (int p = live + (int)threadIdx.x; p < a.total; p += kPlanThreads) c.to[p] = p;
+    const unsigned lanes_below = (1u << lane) - 1u;
+    const int holes_end = at_hole + holes, movers_end = at_mover + movers;
+    for_pages(a.refs, lo, border, [&](int p, int r, bool there) {
+        const unsigned m = __ballot_sync(0xffffffffu, there && r <= 0);
+        if (there && r <= 0) c.hole[at_hole + __popc(m & lanes_below)] = p;
+        at_hole += __popc(m);
+    }, [&] { return at_hole >= holes_end; });
+    for_pages(a.refs, border, hi, [&](int p, int r, bool) {
+        const unsigned m = __ballot_sync(0xffffffffu, r > 0);
+        if (r > 0) c.mover[at_mover + __popc(m & lanes_below)] = p;
+        at_mover += __popc(m);
+    }, [&] { return at_mover >= movers_end; });
     __syncthreads();
     for (int j = threadIdx.x; j < moves; j += kPlanThreads) c.to[c.mover[j]] = c.hole[j];
     if (threadIdx.x == 0) {

@@ -209,6 +209,28 @@ def test_many_lists_and_pages(kvfix):
     p.compact()
 
 
+@gpu
+@pytest.mark.parametrize("free", ("behind", "before", "between"))
+def test_free_pages_in_runs(kvfix, free):
+    """Whole spans of pages without a free one, or with nothing else; the pool moved together after."""
+    n, each, gap = 8, 600, 700
+    p = Paged(kvfix, "int4", 16, lens=[16 * each - 5] * n, spare=gap, layers=1, heads=1)
+    first = {"behind": 0, "before": gap, "between": 0}[free]
+    rows = np.arange(n * each).reshape(n, each) + first
+    if free == "between":
+        rows[3:] += gap
+    p.pages[:, :each] = i32(rows)
+    p.refs.zero_()
+    p.refs[torch.from_numpy(rows.reshape(-1)).cuda()] = 1
+    p.snap()
+    p.extend([3, 40, 0, 6, 5, 64, 1, 20])
+    p.cut([-1, 0, -1, 16, -1, -1, -1, -1])
+    p.extend([64] * n, flags=("bounds",))                       # (list 5 has 64 already, and a table of 604 pages)
+    p.compact()
+    p.cut([-1] * 7 + [0])
+    p.compact()
+
+
 # ------------------------------------------------------------------ cut
 
 @gpu
