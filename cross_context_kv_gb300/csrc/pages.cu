@@ -2,17 +2,17 @@
 // paged pool take, share, give back and leave behind, all decided on the device, so that a captured
 // graph follows the lists as they change.
 //
-// The books.  refs[p] counts the lists that hold page p, and a page is free where there are none: there is no
-// list of free pages to keep in order, and the same books always give the same pages (the
-// lowest free ones, in the order of lists).  Counts change by whole numbers, whose order of
+// The books.  refs[p] counts the lists that hold page p, and a page is free where there are none:
+// there is no list of free pages to keep in order, and the same books always give the same pages
+// (the lowest free ones, in the order of lists).  Counts change by whole numbers, whose order of
 // addition does not matter.
 //
-// Each call is a small kernel that decides (one CTA: a scan over the lists, and one over refs whose
-// spans belong to a warp each, so it takes one block-wide step, not one per thousand pages), and
-// one that moves: page tables and counts, and rows in all layers, both planes, codes and
-// scales.  (A call's last kernel triggers nothing early: what follows on the stream may read
-// the books before it waits.)  The moving kernels are bound by HBM (a row is read and written once), the deciding ones
-// by latency; measured figures at the launches below.
+// Extend and compact are a small kernel that decides (one CTA: a scan over the lists, and one over
+// refs whose spans belong to a warp each, so it takes one block-wide step, not one per thousand
+// pages), and one that moves: page tables and counts, and rows in all layers, both planes, codes
+// and scales.  Cut is one kernel, a cluster of CTAs per list.  (A call's last kernel triggers
+// nothing early: what follows on the stream may read the books before it waits.)  Moving is bound
+// by HBM (a row is read and written once), deciding by latency; measured figures at the launches.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
