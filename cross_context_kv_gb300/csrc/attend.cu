@@ -1177,18 +1177,18 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     }
 }
 
-// The join of many trees' rows: a CTA takes 16 consecutive rows of an agent's KV head, a warp two
-// of them.  The attention kernel leaves no registers beside it, so the join's CTAs start as SMs
-// come free, and what counts is how many waves of them follow its end and what each waits for:
-// four lanes look up where the rows' parts lie (by segment, before and behind a border of blocks)
-// for all 16, a lane reads one part's (max, sum) of either segment, and both rows' parts are
-// loaded four at a time.  (The kernel above has 2048 CTAs for 8192 rows, 912 of them at a time, whose
-// last began 12.6 us after the attention's end.)
-constexpr int kTreeJoinRows = 16;
+// The join of many trees' rows: a CTA takes 8 consecutive rows of an agent's KV head, a warp one.
+// The attention kernel leaves no registers beside it, so the join's CTAs start as SMs come free,
+// and what counts is how many waves of them follow its end and what each waits for: four lanes
+// look up where the rows' parts lie (by segment, before and behind a border of blocks) for all 8,
+// a lane reads one part's (max, sum) of either segment, and the parts are loaded four at a time,
+// which 40 registers hold: 48 warps of an SM.  (The kernel above has 2048 CTAs for 8192 rows, 912
+// of them at a time, whose last began 12.6 us after the attention's end.)
+constexpr int kTreeJoinRows = 8;
 template <int D>
-__global__ void __launch_bounds__(256, 3) attend_tree_join_kernel(const __grid_constant__ AttendArgs a,
-                                                                  const __grid_constant__ AtWork w) {
-    constexpr int V = D / 32, R = 2, B = 4;  // values per lane, rows per warp, parts on their way
+__global__ void __launch_bounds__(32 * kTreeJoinRows, 6) attend_tree_join_kernel(const __grid_constant__ AttendArgs a,
+                                                                                      const __grid_constant__ AtWork w) {
+    constexpr int V = D / 32, B = 4;  // values per lane, parts on their way
     struct Place {
         long long own;  // part row of the segment's row 0, first part
         long long i0;   // first piece
@@ -1241,107 +1241,77 @@ __global__ void __launch_bounds__(256, 3) attend_tree_join_kernel(const __grid_c
     }
     __syncthreads();
     pdl_wait();
-    if (R * warp >= rows) return;
-    const Place* at[R][2];
-    int row[R][2], parts[R];
-    float M[R], L[R], acc[R][V];
+    if (warp >= rows) return;
+    const int row[2] = {row_of[0] + warp, row_of[1] + warp};
+    const Place& pre = places[0][row[0] / kAtBlock > row_of[0] / kAtBlock];
+    const Place& own = places[1][row[1] / kAtBlock > row_of[1] / kAtBlock];
+    const int parts = pre.n + own.n;
+    float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < parts; j0 += 32) {
+        // this lane's part of the row: the prefix's come first
+        const int s = j0 + lane >= pre.n, j = j0 + lane - (s ? pre.n : 0);
+        const Place& p = s ? own : pre;
+        const long long i = p.i0 + j;
+        const int half = p.kind == kSingles && i >= many_ctas ? 1 : 0, r = s ? row[1] : row[0];
+        const long long part = j == 0          ? p.own + r
+                               : p.kind == kFew ? w.few_rows + i * w.few + (r - p.row0)
+                                                : w.own_rows + (i - half * many_ctas) * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half) + (r - p.row0);
+        const float2 ml = j0 + lane < parts ? __ldcg(w.ml + part) : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            row[q][s] = row_of[s] + R * warp + q;
-            at[q][s] = &places[s][row[q][s] / kAtBlock > row_of[s] / kAtBlock];
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float N = fmaxf(M, top), f = M == -INFINITY ? 0.f : exp2f(M - N), wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - N);
+        // (a row with a NaN logit has a sum of NaN and must keep it)
+        float sum = ml.y == 0.f ? 0.f : ml.y * (ml.x == -INFINITY ? 1.f : wt);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (top != -INFINITY || !(sum == 0.f)) {
+            L = L * (M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : f) + sum;
+#pragma unroll
+            for (int i2 = 0; i2 < V; ++i2) acc[i2] *= f;
+            M = N;
         }
-        parts[q] = R * warp + q < rows ? at[q][0]->n + at[q][1]->n : 0;
-        M[q] = -INFINITY;
-        L[q] = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[q][i] = 0.f;
-    }
-    for (int j0 = 0; j0 < max(parts[0], parts[R - 1]); j0 += 32) {
-        long long part[R];
-        float wt[R];
-        float2 ml[R];
-        unsigned has[R], any = 0;
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            // this lane's part of the row: the prefix's come first
-            const int s = j0 + lane >= at[q][0]->n, j = j0 + lane - (s ? at[q][0]->n : 0);
-            const Place& p = s ? *at[q][1] : *at[q][0];
-            const long long i = p.i0 + j;
-            const int half = p.kind == kSingles && i >= many_ctas ? 1 : 0, r = s ? row[q][1] : row[q][0];
-            part[q] = j == 0          ? p.own + r
-                      : p.kind == kFew ? w.few_rows + i * w.few + (r - p.row0)
-                                       : w.own_rows + (i - half * many_ctas) * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half) + (r - p.row0);
-            ml[q] = j0 + lane < parts[q] ? __ldcg(w.ml + part[q]) : make_float2(-INFINITY, 0.f);
-        }
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            float top = ml[q].x;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float N = fmaxf(M[q], top), f = M[q] == -INFINITY ? 0.f : exp2f(M[q] - N);
-            wt[q] = ml[q].x == -INFINITY ? 0.f : exp2f(ml[q].x - N);
-            // (a row with a NaN logit has a sum of NaN and must keep it)
-            float sum = ml[q].y == 0.f ? 0.f : ml[q].y * (ml[q].x == -INFINITY ? 1.f : wt[q]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (top != -INFINITY || !(sum == 0.f)) {
-                L[q] = L[q] * (M[q] == -INFINITY ? (L[q] == 0.f ? 0.f : 1.f) : f) + sum;
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[q][i] *= f;
-                M[q] = N;
-            }
-            has[q] = __ballot_sync(0xffffffffu, !(ml[q].y == 0.f));
-            any |= has[q];
-        }
-        const int count = 32 - __clz(any);
+        const unsigned has = __ballot_sync(0xffffffffu, !(ml.y == 0.f));
+        const int count = 32 - __clz(has);
 #pragma unroll 1
         for (int b0 = 0; b0 < count; b0 += B) {
-            float x[B][R][V], wb[B][R];
+            float x[B][V], wb[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-                for (int q = 0; q < R; ++q) {
-                    const bool there = b0 + b < count && ((has[q] >> ((b0 + b) & 31)) & 1u);
-                    const long long from = __shfl_sync(0xffffffffu, part[q], (b0 + b) & 31);
-                    wb[b][q] = __shfl_sync(0xffffffffu, wt[q], (b0 + b) & 31);
-                    if (!there) wb[b][q] = 0.f;
-                    const float* src = w.o + from * D + V * lane;
-                    if (V == 4) {
-                        const float4 v = there ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[b][q][0] = v.x;
-                        x[b][q][1] = v.y;
-                        x[b][q][V - 2] = v.z;
-                        x[b][q][V - 1] = v.w;
-                    } else {
-                        const float2 v = there ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
-                        x[b][q][0] = v.x;
-                        x[b][q][1] = v.y;
-                    }
+            for (int b = 0; b < B; ++b) {
+                const bool there = b0 + b < count && ((has >> ((b0 + b) & 31)) & 1u);
+                const long long from = __shfl_sync(0xffffffffu, part, (b0 + b) & 31);
+                wb[b] = __shfl_sync(0xffffffffu, wt, (b0 + b) & 31);
+                if (!there) wb[b] = 0.f;
+                const float* src = w.o + from * D + V * lane;
+                if (V == 4) {
+                    const float4 v = there ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[b][0] = v.x;
+                    x[b][1] = v.y;
+                    x[b][V - 2] = v.z;
+                    x[b][V - 1] = v.w;
+                } else {
+                    const float2 v = there ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+                    x[b][0] = v.x;
+                    x[b][1] = v.y;
                 }
+            }
 #pragma unroll
             for (int b = 0; b < B; ++b)
 #pragma unroll
-                for (int q = 0; q < R; ++q)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) acc[q][i] = fmaf(x[b][q][i], wb[b][q], acc[q][i]);
+                for (int i2 = 0; i2 < V; ++i2) acc[i2] = fmaf(x[b][i2], wb[b], acc[i2]);
         }
     }
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-        const int in = in0 + R * warp + q, t = in / G, qh = head * G + in - t * G;
-        if (in >= in0 + rows) continue;
-        const float inv = L[q] == 0.f ? 0.f : 1.f / L[q];
-        uint16_t* out = a.out + a.op.row(agent, 0, t) + (long long)qh * D + V * lane;
-        if (V == 4)
-            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[q][0] * inv, acc[q][1] * inv),
-                                                        pack_bf16(acc[q][V - 2] * inv, acc[q][V - 1] * inv));
-        else
-            *reinterpret_cast<uint32_t*>(out) = pack_bf16(acc[q][0] * inv, acc[q][1] * inv);
-        if (a.lse && lane == 0)
-            a.lse[((long long)agent * T + t) * a.q_heads + qh] = L[q] == 0.f ? -INFINITY : (M[q] + log2f(L[q])) * 0.69314718055994531f;
-    }
+    const int in = in0 + warp, t = in / G, qh = head * G + in - t * G;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint16_t* out = a.out + a.op.row(agent, 0, t) + (long long)qh * D + V * lane;
+    if (V == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[V - 2] * inv, acc[V - 1] * inv));
+    else
+        *reinterpret_cast<uint32_t*>(out) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    if (a.lse && lane == 0)
+        a.lse[((long long)agent * T + t) * a.q_heads + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host
@@ -1402,11 +1372,11 @@ static cudaError_t launch_attend_form(const AttendArgs& a, const AtWork& w, int 
     // 7 us less by one), one while rows are few
     if (rows <= (long long)w.ctas * 8) return launch_chained(attend_join_kernel<D, 4, 1>, dim3((unsigned)rows), dim3(128), 0, s, a, w);
     const int tg = a.new_tokens * (a.q_heads / a.pool.heads);
-    // (8192 rows: 69.5 us a call against 73.3 by the kernel below, some 3000 rows 142 against 143; but 2048
-    // rows of many parts 47 against 39)
+    // (8192 rows: 64.1 us a call against 73.4 by the kernels below, 10240 of two nodes a tree 251 against
+    // 265, some 3000 rows 139.9 against 142.5; but 2048 rows of many parts 44.9 against 39.1)
     if (TREE && tg >= kTreeJoinRows && rows > (long long)w.ctas * 16) {
         const long long ctas = (long long)a.agents * a.pool.heads * ((tg + kTreeJoinRows - 1) / kTreeJoinRows);
-        return launch_chained(attend_tree_join_kernel<D>, dim3((unsigned)ctas), dim3(256), 0, s, a, w);
+        return launch_chained(attend_tree_join_kernel<D>, dim3((unsigned)ctas), dim3(32 * kTreeJoinRows), 0, s, a, w);
     }
     if (tg >= 4 && rows > (long long)w.ctas * 128) {
         const long long warps = (long long)a.agents * a.pool.heads * ((tg + 3) / 4);
