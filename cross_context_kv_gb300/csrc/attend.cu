@@ -250,8 +250,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // TREE: kvfix_tree_attend's, whose rows see the nodes of their tree by bits: a tile that the tree
 // reaches goes through the mask pass, where a row's word of 32 nodes is shifted to the tile's columns;
-// all other tiles are as they are without a tree (16 ragged trees of 16 over 32768 e4m3 keys 203 us,
-// 281 when rows without a node sent every tile through the pass).
+// all other tiles are as they are without a tree (rows without a node sent every tile through the
+// pass at first: 281 us for 16 ragged trees of 16 over 32768 e4m3 keys, 203 without that).
 template <int F, int D, bool TREE>
 __global__ void __launch_bounds__(AtCfg<F, D>::kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -1187,7 +1187,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 constexpr int kTreeJoinRows = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kTreeJoinRows, 6) attend_tree_join_kernel(const __grid_constant__ AttendArgs a,
-                                                                                      const __grid_constant__ AtWork w) {
+                                                                                 const __grid_constant__ AtWork w) {
     constexpr int V = D / 32, B = 4;  // values per lane, parts on their way
     struct Place {
         long long own;  // part row of the segment's row 0, first part
@@ -1255,9 +1255,10 @@ __global__ void __launch_bounds__(32 * kTreeJoinRows, 6) attend_tree_join_kernel
         const Place& p = s ? own : pre;
         const long long i = p.i0 + j;
         const int half = p.kind == kSingles && i >= many_ctas ? 1 : 0, r = s ? row[1] : row[0];
-        const long long part = j == 0          ? p.own + r
+        const int in_cta = p.kind == kPairs ? 0 : kAtBlock + kAtRows * half;
+        const long long part = j == 0           ? p.own + r
                                : p.kind == kFew ? w.few_rows + i * w.few + (r - p.row0)
-                                                : w.own_rows + (i - half * many_ctas) * (2 * kAtBlock) + (p.kind == kPairs ? 0 : kAtBlock + kAtRows * half) + (r - p.row0);
+                                                : w.own_rows + (i - half * many_ctas) * (2 * kAtBlock) + in_cta + (r - p.row0);
         const float2 ml = j0 + lane < parts ? __ldcg(w.ml + part) : make_float2(-INFINITY, 0.f);
         float top = ml.x;
 #pragma unroll
@@ -1307,7 +1308,8 @@ __global__ void __launch_bounds__(32 * kTreeJoinRows, 6) attend_tree_join_kernel
     const float inv = L == 0.f ? 0.f : 1.f / L;
     uint16_t* out = a.out + a.op.row(agent, 0, t) + (long long)qh * D + V * lane;
     if (V == 4)
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[V - 2] * inv, acc[V - 1] * inv));
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[V - 2] * inv, acc[V - 1] * inv));
     else
         *reinterpret_cast<uint32_t*>(out) = pack_bf16(acc[0] * inv, acc[1] * inv);
     if (a.lse && lane == 0)

@@ -240,8 +240,8 @@ void rotary_angles(const kvfix_rope& r, RotaryArgs* a) {
 //
 // The split.  A thread has a token's heads one after another, four in flight, while that leaves
 // enough threads to fill the GPU; with fewer tokens the heads are spread over 2, 4, ... threads until
-// each has one (8 x 512 tokens x 40 heads: 16.6 us, 32 if spread four times as far).  Blocks take several layers (a thread's angles are used for all of them) where
-// that leaves four blocks an SM.
+// each has one (8 x 512 tokens x 40 heads: 16.6 us, 32 if spread four times as far).  Blocks take
+// several layers (a thread's angles are used for all of them) where that leaves four blocks an SM.
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const int heads = a.ip[0].heads + a.ip[1].heads;
     if (a.chunks == 0 || a.layers == 0 || a.tokens == 0 || heads == 0) return cudaSuccess;
