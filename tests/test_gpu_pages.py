@@ -363,6 +363,28 @@ def test_on_a_stream_and_in_a_graph(kvfix):
 
 
 @gpu
+def test_two_pools_at_once(kvfix):
+    """Steps of two pools on two streams, in flight together, leave what they leave one by one."""
+    both = [Paged(kvfix, fmt, 16, lens=[30, 30, 5, 70], like={1: 0}, spare=40, room=20, seed=i) for i, fmt in enumerate(("e4m3", "int4"))]
+    extra, base, path, kept = [8] * 4, [30, 30, 5, 70], [[1, 4], [0, 2], [6, 0], [3, 7]], [2, 2, 1, 2]
+    args = [i32(x) for x in (extra, base, path, kept)]
+    moves = [p.books.extend(extra) + p.books.cut(base, path, kept) for p in both]
+    for p, m in zip(both, moves):
+        m += p.books.compact()[0]
+    torch.cuda.synchronize()
+    streams, lives = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for p, s in zip(both, streams):
+        with torch.cuda.stream(s):
+            kvfix.pages_extend(p.pool, 16, p.refs, p.pages, p.lens, args[0])
+            kvfix.pages_cut(p.pool, 16, p.refs, p.pages, p.lens, *args[1:])
+            lives.append(kvfix.pages_compact(p.pool, 16, p.refs, p.pages, p.lens))
+    torch.cuda.synchronize()
+    for p, m, n in zip(both, moves, lives):
+        assert n.item() == sum(x > 0 for x in p.books.refs)
+        p.check(m)
+
+
+@gpu
 def test_a_pool_beyond_32_bit_offsets(kvfix):
     """Pages past 4 GB of a plane are copied, moved up and moved to the front."""
     H, D, page = 8, 128, 128

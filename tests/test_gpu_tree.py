@@ -133,6 +133,8 @@ LARGE = {
     "borders": (4, 5, 128, 16, 33, [700], [0, 6], [10, 64, 0, 200, 33, 5], [33, 30, 33, 0, 1, 33]),
     "ragged_64": (5, 3, 64, 64, 61, [3001, 0], [0, 2, 4], [900, 3, 0, 77], [61, 54, 47, 33]),
     "no_prefix": (8, 4, 64, 32, 17, [], [], [300, 0, 5, 90, 1200, 7], [17] * 6),
+    "short_trees": (4, 3, 128, 16, 3, [700, 0], [0, 50, 90], [53 * i % 400 for i in range(100)], [i % 4 for i in range(100)]),
+    "a_run_and_one": (8, 3, 64, 16, 3, [90], [2, 30], [7 * i % 50 for i in range(40)], [3 - i % 2 for i in range(40)]),
 }
 
 
@@ -267,6 +269,34 @@ def test_on_a_stream_and_in_a_graph(kvfix, T, group):
         s.synchronize()
         r.check(out, lse)
     kvfix.check_status()
+
+
+@gpu
+@pytest.mark.parametrize("heads,T,group", ((2, 4, 2), (8, 30, 4)))
+def test_two_calls_at_once(kvfix, heads, T, group):
+    """Rounds on two streams, each with a workspace of its own, give what they give one by one."""
+    rounds, want = [], []
+    for i in range(2):
+        r = Trees(kvfix, ("bf16", "e4m3")[i], heads, group, 128, 16, T, [900 - 500 * i], [0, 12], [53 * j % 300 for j in range(12)],
+                  [T - j % 3 for j in range(12)], seed=i)
+        rounds.append(r)
+        want.append(r.call())
+        r.check(*want[i])
+    ws = [torch.empty(kvfix.shared_attend_workspace_bytes(r.q, r.pool, 1), dtype=torch.uint8, device="cuda") for r in rounds]
+    outs = [[torch.zeros_like(r.q) for _ in range(10)] for r in rounds]
+    lses = [[], []]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for j in range(10):
+        for i, r in enumerate(rounds):
+            with torch.cuda.stream(streams[i]):
+                lses[i].append(r.call(out=outs[i][j], workspace=ws[i])[1])
+    torch.cuda.synchronize()
+    kvfix.check_status()
+    for i in range(2):
+        for j in range(10):
+            assert torch.equal(outs[i][j].view(torch.int16), want[i][0].view(torch.int16))
+            assert torch.equal(lses[i][j].view(torch.int32), want[i][1].view(torch.int32))
 
 
 def test_masks_of_parents(kvfix):
