@@ -674,6 +674,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     if (!ok) break;
                     StoredTile<F, D, N> stored;
                     stored.take(rawsm + rs * C::kRaw, tid);
+                    // The next copy writes by another proxy, which an arrival alone does not hold back: without
+                    // the fence loads still under way took the next tile's bytes (in 1 to 7 % of the calls
+                    // beside another stream's; none of 192000 with it).
+                    fence_proxy_async_smem();
                     mbar_arrive(&raw_empty[rs]);
                     if (n >= (p ? SV : SK)) ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], released(p, n)));
                     if (!ok) break;
