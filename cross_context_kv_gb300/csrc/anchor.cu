@@ -359,8 +359,11 @@ anchor_dist_kernel(const __grid_constant__ CUtensorMap tm_x0, const __grid_const
                         nx[8 * q + 2 * k + 1] = (wd[k] & 0xffff0000u) ^ 0x80000000u;
                     }
                 }
+                // x is in registers once the loads are done, which the fence waits for: the next copy into
+                // the slot writes by another proxy, which an arrival alone does not hold back
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&xempty[xi]);  // x is in registers now
+                if (lane == 0) mbar_arrive(&xempty[xi]);
                 // the slots of the chunk's first steps (their previous steps were in earlier chunks)
                 for (int v = 0; v < V && v < kAdSlots; ++v) {
                     const uint32_t ts = tcol + ((qg + v) & (kAdSlots - 1)) * kAdCols;
