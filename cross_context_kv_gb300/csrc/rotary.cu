@@ -24,20 +24,11 @@
 #include <string.h>
 
 #include "rotary.h"
+#include "rotary_split.h"
 
 namespace kvfix {
 
-constexpr int kRotaryThreads = 256;
 constexpr int kRotaryHeads = 4;  // heads whose loads are in flight together
-
-struct RotarySplit {
-    int columns;      // threads per (token, run of heads)
-    int runs;         // threads that share a token's heads
-    int tile;         // tokens per block
-    int tiles;        // blocks per (chunk, layers)
-    int layer_block;  // layers per block
-    int layer_blocks;
-};
 
 // What a thread has of a head.  Vectors: two 8-wide ones.
 struct RotaryVectors {
@@ -127,22 +118,14 @@ struct RotaryMixed {
     }
 };
 
-// The pairs of a column of such halves.
-static int mixed_pairs(int rotary_dim) { return rotary_dim % 8 == 0 ? 4 : rotary_dim % 4 == 0 ? 2 : 1; }
-
 template <int LAYOUT, typename V>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a,
                                                                 const __grid_constant__ RotarySplit w) {
     constexpr int N = V::kPairs;
     constexpr bool kMixed = N < 8;
-    const int slot = threadIdx.x / w.columns, col = threadIdx.x - slot * w.columns;
-    const int in_tile = slot / w.runs, run = slot - in_tile * w.runs;
-    unsigned b = blockIdx.x;
-    const int lb = (int)(b % (unsigned)w.layer_blocks);
-    b /= (unsigned)w.layer_blocks;
-    const int chunk = (int)(b / (unsigned)w.tiles), tile = (int)(b - (unsigned)chunk * (unsigned)w.tiles);
-    const int t = tile * w.tile + in_tile;
-    if (in_tile >= w.tile || t >= a.tokens) return;
+    RotaryPlace at;
+    if (!rotary_place(w, a.tokens, blockIdx.x, threadIdx.x, at)) return;
+    const int t = (int)at.token, chunk = at.chunk, col = at.column, run = at.run;
     const int turning = (a.rotary_dim + 2 * N - 1) / (2 * N);  // columns that turn
     const int pairs = a.rotary_dim / 2 - col * N;              // (of this one)
     // places of the column's two parts in a head
@@ -163,7 +146,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     }
     const int p = __ldg(a.positions + (long long)chunk * a.tokens + t);
     const int heads0 = a.ip[0].heads, heads = heads0 + a.ip[1].heads;
-    const int l0 = lb * w.layer_block, l1 = min(a.layers, l0 + w.layer_block);
+    const int l0 = at.layer0, l1 = l0 + rotary_layers(w, a.layers, l0);
     V v[kRotaryHeads];
     auto load = [&](int l, int h0) {
         const uint16_t* in0 = a.in[0] + a.ip[0].row(chunk, l, t);
@@ -237,35 +220,12 @@ void rotary_angles(const kvfix_rope& r, RotaryArgs* a) {
 // Halves that vectors do not meet: 24 of 96 turned 4.5 TB/s (3.6 by single pairs), 60 of 64 3.4 (2.5),
 // 20 of 128 4.2 (4.4); all of a head by pairs: 2.1.
 // Two or eight heads in flight, streaming loads or stores: even, or up to 10 % slower.
-//
-// The split.  A thread has a token's heads one after another, four in flight, while that leaves
-// enough threads to fill the GPU; with fewer tokens the heads are spread over 2, 4, ... threads until
-// each has one (8 x 512 tokens x 40 heads: 16.6 us, 32 if spread four times as far).  Blocks take
-// several layers (a thread's angles are used for all of them) where that leaves four blocks an SM.
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const int heads = a.ip[0].heads + a.ip[1].heads;
     if (a.chunks == 0 || a.layers == 0 || a.tokens == 0 || heads == 0) return cudaSuccess;
     const bool half = a.layout == KVFIX_ROPE_HALF, mixed = half && a.rotary_dim % 16 != 0;
     const int P = mixed_pairs(a.rotary_dim);
-    RotarySplit w;
-    if (mixed) {
-        const int border = (a.rotary_dim + 7) / 8 * 8;
-        w.columns = a.in_place ? a.rotary_dim / (2 * P) : border / (2 * P) + (a.dim - border) / 8;
-    } else {
-        w.columns = a.in_place ? (a.rotary_dim + 15) / 16 : a.dim / 16;
-    }
-    const int slots = kRotaryThreads / w.columns;
-    const double rows = (double)a.chunks * a.layers * a.tokens, full = 152.0 * 1536.0;
-    w.runs = 1;
-    while (w.runs * 2 <= slots && w.runs < heads && rows * w.columns * w.runs < full) w.runs *= 2;
-    w.tile = slots / w.runs;
-    if (w.tile > a.tokens) w.tile = a.tokens;
-    w.tiles = (a.tokens + w.tile - 1) / w.tile;
-    w.layer_block = 1;
-    while (w.layer_block < 8 && w.layer_block * 2 <= a.layers &&
-           (double)a.chunks * w.tiles * ((a.layers + 2 * w.layer_block - 1) / (2 * w.layer_block)) >= 4.0 * 152)
-        w.layer_block *= 2;
-    w.layer_blocks = (a.layers + w.layer_block - 1) / w.layer_block;
+    const RotarySplit w = rotary_split(a.chunks, a.layers, a.tokens, heads, a.dim, a.rotary_dim, half, a.in_place);
     const double blocks = (double)a.chunks * w.tiles * w.layer_blocks;
     if (blocks > 2147483647.0) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)((long long)a.chunks * w.tiles * w.layer_blocks)), threads(kRotaryThreads);
