@@ -1033,9 +1033,14 @@ def pages_cut(pool: Pool, page_tokens: int, refs, pages, lens, base, path=None, 
             raise ValueError("the pool, the books and their arguments must be on one device")
         if path.dim() != 2 or path.shape[0] != books[-1]:
             raise ValueError("path must be [lists][most]")
+        if path.shape[1] == 0:
+            # no column to keep from: one that none may be kept of, so that lists which ask for some
+            # are left alone and flagged
+            path = _empty((books[-1], 1), (1, 1), torch.int32)
+            path.fill_(-1)
         most = path.shape[1]
-    _check(lib.kvfix_pages_cut(*books, base.data_ptr(), path.data_ptr() if most else None, most,
-                               kept.data_ptr() if most else None, _raw_stream(refs)))
+    _check(lib.kvfix_pages_cut(*books, base.data_ptr(), None if path is None else path.data_ptr(), most,
+                               None if kept is None else kept.data_ptr(), _raw_stream(refs)))
 
 
 def pages_compact(pool: Pool, page_tokens: int, refs, pages, lens, workspace=None):
