@@ -531,22 +531,22 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
     const int moves = c.count[0], live = c.count[1];
     bool bad = false;
     const int parts = max(1, (a.wide + kTablePart - 1) / kTablePart);
-    if (moves > 0)
-        for (long long k = blockIdx.x; k < (long long)a.lists * parts; k += gridDim.x) {
-            const int i = (int)(k / parts), part = (int)(k - (long long)i * parts);
-            const int n = a.len[i];
-            if (n < 0 || n > (long long)a.wide * a.page) {
-                bad = true;
-                continue;
-            }
-            int32_t* const table = a.pages + (long long)i * a.wide;
-            const int c1 = min(pages_of(n, a), (part + 1) * kTablePart);
-            for (int x = part * kTablePart + threadIdx.x; x < c1; x += kMoveThreads) {
-                const int p = table[x];
-                if (p < 0 || p >= a.total) bad = true;
-                else if (p >= live) table[x] = c.to[p];
-            }
+    // (also where nothing moves: lists and entries out of range are flagged)
+    for (long long k = blockIdx.x; k < (long long)a.lists * parts; k += gridDim.x) {
+        const int i = (int)(k / parts), part = (int)(k - (long long)i * parts);
+        const int n = a.len[i];
+        if (n < 0 || n > (long long)a.wide * a.page) {
+            bad = true;
+            continue;
         }
+        int32_t* const table = a.pages + (long long)i * a.wide;
+        const int c1 = min(pages_of(n, a), (part + 1) * kTablePart);
+        for (int x = part * kTablePart + threadIdx.x; x < c1; x += kMoveThreads) {
+            const int p = table[x];
+            if (p < 0 || p >= a.total) bad = true;
+            else if (p >= live) table[x] = c.to[p];
+        }
+    }
     for (int j = blockIdx.x * kMoveThreads + threadIdx.x; j < moves; j += gridDim.x * kMoveThreads) {
         const int from = c.mover[j];
         a.refs[c.hole[j]] = a.refs[from];

@@ -19,3 +19,28 @@ def test_kept_of_a_path_without_columns(kvfix):  # noqa: F811
     p.check(moves, flags=("bounds",))
     kvfix.pages_cut(p.pool, 16, p.refs, p.pages, p.lens, i32(base), none, i32([0] * 5))
     p.check(p.books.cut(base))
+
+
+@gpu
+@pytest.mark.parametrize("what", ("a length below 0", "a length past the table", "an entry below 0", "an entry past the pool"))
+@pytest.mark.parametrize("moves", (False, True))
+def test_compactions_flag_what_is_out_of_range(kvfix, what, moves):  # noqa: F811
+    """Whether some page moves or none, and whatever is in range follows its pages."""
+    p = Paged(kvfix, "e4m3", 16, lens=[40, 17, 70, 20], spare=9)
+    p.compact()                                                   # in place now
+    if moves:
+        p.cut([-1, 0, -1, -1])                                    # (two pages come free)
+    if "length" in what:
+        p.lens[3] = -1 if "below" in what else p.pages.shape[1] * 16 + 1
+    else:
+        p.pages[3, 1] = -1 if "below" in what else p.refs.numel()
+    p.snap()
+    books, length = p.books, p.books.lens[3]
+    if "length" in what:
+        books.lens[3] = 0                                         # such a list is left as it is
+    rows, live = books.compact()
+    books.lens[3] = length
+    books.flags.add("bounds")
+    assert bool(rows) == moves
+    assert kvfix.pages_compact(p.pool, 16, p.refs, p.pages, p.lens).item() == live
+    p.check(rows, flags=("bounds",))
