@@ -1226,11 +1226,17 @@ kvfix_status kvfix_rotary(const kvfix_bf16* q, kvfix_kv_desc qd, const kvfix_bf1
     if (!ref) return fail(KVFIX_EINVAL, "%s: neither queries nor keys", fn);
     if (a.ip[0].heads && a.ip[1].heads && (rows_meet(q, qd, k_out, kod) || rows_meet(k, kd, q_out, qod) || rows_meet(q_out, qod, k_out, kod)))
         return fail(KVFIX_EINVAL, "%s: an output overlaps the other plane", fn);
+    if ((double)ref->chunks * ref->layers * ref->tokens >= 2147483648.0)
+        return fail(KVFIX_EINVAL, "%s: chunks * layers * tokens must be below 2^31", fn);
+    // blocks that end early write while others still read their positions (one row of 4-byte numbers)
+    const kvfix_kv_desc pd = {1, 1, 1, (int)((long long)ref->chunks * ref->tokens), 2, 0, 0, 0};
+    if (!no_rows(*ref))
+        for (int i = 0; i < 2; ++i)
+            if (a.op[i].heads && rows_meet(positions, pd, out[i], *dst[i]))
+                return fail(KVFIX_EINVAL, "%s: %s_out overlaps positions", fn, i ? "k" : "q");
     if ((st = check_rope(rope, ref->head_dim, fn)) != KVFIX_OK) return st;
     if (!no_rows(*ref) && !positions) return fail(KVFIX_EINVAL, "%s: positions is null", fn);
     if (!aligned4(positions)) return fail(KVFIX_EINVAL, "%s: positions must be 4-byte aligned", fn);
-    if ((double)ref->chunks * ref->layers * ref->tokens >= 2147483648.0)
-        return fail(KVFIX_EINVAL, "%s: chunks * layers * tokens must be below 2^31", fn);
     a.positions = positions;
     a.chunks = ref->chunks;
     a.layers = ref->layers;

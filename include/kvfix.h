@@ -750,10 +750,10 @@ KVFIX_API kvfix_status kvfix_shared_attend(const kvfix_bf16* q, kvfix_kv_desc q_
  * q_out, k_out : shaped like q and k; each exactly its input (in place) or apart from both, its rows
  *                apart from each other.  Planes may be views of one buffer whose rows
  *                interleave, as a projection leaves them.
- * positions    : device int32[chunks][tokens], any sign.
+ * positions    : device int32[chunks][tokens], any sign; apart from the outputs.
  * rope         : rotary_dim even, 2..head_dim; base > 1; attention > 0 (1: a rotation alone); scaled
  *                forms want factor >= 1, bands and yarn original_tokens >= 1 and 0 < low < high.
- * Limits: chunks * layers * tokens < 2^31.
+ * Limits: chunks * layers * tokens < 2^31, fewer than 2^30 values a token row.
  * Arithmetic: the frequencies in double on the host; angles exact modulo a turn (64-bit
  * fractions of it); cos, sin and the rotation in float; one rounding to bf16.  Position 0 with
  * attention 1 gives the input bit for bit.
