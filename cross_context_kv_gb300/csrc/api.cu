@@ -1116,6 +1116,10 @@ static kvfix_status attend(const char* fn, bool is_tree, const int32_t* nodes, c
     if (overlaps_bytes(tree, tree_bytes, (const void*)o0, o1 - o0) || overlaps_bytes(tree, tree_bytes, lse, lse_bytes) ||
         overlaps_bytes(tree, tree_bytes, workspace, need))
         return fail(KVFIX_EINVAL, "%s: out, lse and workspace must not overlap tree_mask", fn);
+    const size_t nodes_bytes = 4 * (size_t)agents;
+    if (overlaps_bytes(nodes, nodes_bytes, (const void*)o0, o1 - o0) || overlaps_bytes(nodes, nodes_bytes, lse, lse_bytes) ||
+        overlaps_bytes(nodes, nodes_bytes, workspace, need))
+        return fail(KVFIX_EINVAL, "%s: out, lse and workspace must not overlap nodes", fn);
     AttendArgs a = {};
     a.q = q;
     a.qp = plane_of(qd);

@@ -793,6 +793,7 @@ KVFIX_API kvfix_status kvfix_rotary(const kvfix_bf16* q, kvfix_kv_desc q_desc, c
  * itself).  A query t >= N sees nothing: out = 0, lse = -inf, as for a row that no key is left to.
  * nodes        : device int32[agents], or NULL: new_tokens each.  A number outside 0..min(q.tokens,
  *                suffix_len) is clamped and flagged (KVFIX_EDEVICE in kvfix_check_status).
+ *                Apart from out, lse and the workspace, as tree_mask is.
  * tree_mask    : device uint32[agents][q.tokens][ceil(q.tokens / 32)]; rows of queries t >= N and
  *                bits past t are not read.
  * All else, the workspace (kvfix_shared_attend_workspace_bytes) and the limits are kvfix_shared_attend's,
@@ -824,7 +825,8 @@ KVFIX_API kvfix_status kvfix_tree_attend(const kvfix_bf16* q, kvfix_kv_desc q_de
  * refs        : device int32[pool.slots / page_tokens].
  * pages       : device int32[lists][max_pages]; entries at and past ceil(len / page_tokens) mean nothing.
  * len         : device int32[lists], each within 0..max_pages * page_tokens.
- * Limits: lists <= 2^24, lists * max_pages < 2^30, max_pages * page_tokens < 2^30.
+ * Limits: lists <= 2^24, lists * max_pages < 2^30, max_pages * page_tokens < 2^30; at most 65535 layers
+ * of fewer than 2^22 values a row.
  * A list whose length, pages or arguments are out of range is left as it is and flagged
  * (KVFIX_EDEVICE in kvfix_check_status); such an entry elsewhere in its pages is skipped and flagged.
  *
