@@ -38,7 +38,7 @@
 //                   to bf16 tiles for the MMA; four warps for keys, four for values.
 // S occupies 128 TMEM columns per group, P (bf16) overwrites the first half of S, O takes D.
 // (e4m3 codes as operands of 8-bit products, with queries in two pieces and the scales on the
-// logits, are right too and were slower: 186 us for the call of the e4m3 case above, then 169 and now 141, as the
+// logits, are right too and were slower: 186 us for the call of the e4m3 case above, then 169 and now 143, as the
 // softmax warps, which are the bound, get the factors' work.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -159,7 +159,8 @@ __device__ __forceinline__ void regs_dec() {
 // i ^ m(r): the eight threads of a phase then read different banks (a row is one, two or four of 128
 // bytes) and write different ones too, the swizzle being a row's own exclusive or.  (Neighbouring
 // threads on a row's vectors, with a scale and addresses for each: 8 instructions a value instead
-// of 5, and 166 us a call instead of 141 for 16 agents over 131072 e4m3 keys.)
+// of 5, and 166 us a call instead of 141 for 16 agents over 131072 e4m3 keys, 143 with the fence behind
+// the loads.)
 template <int F, int D, int N>
 struct StoredTile {
     using C = AtCfg<F, D>;
@@ -936,7 +937,9 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     const int agent = (int)quotient(ah, H), head = (int)(ah - (long long)agent * H);
     const long long all = (long long)a.agents * TG;
     // The plan lies ready before this kernel can start (the attention kernel lets it start only
-    // after its own wait for the plan); only the parts need the wait below.
+    // after its own wait for the plan); only the parts need the wait below.  (Nothing of an earlier plan
+    // was ever read here, in 360 million CTAs with two plans in turn at the same addresses; loads past the
+    // first-level cache took up to 4 % of a call more.)
     int group = -1;
     if (a.groups > 0 && agent >= w.bounds[0] && agent < w.bounds[a.groups]) {
         int lo = 0, hi = a.groups;  // bounds[lo] <= agent < bounds[hi]

@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(kMoveThreads) extend_move_kernel(const __grid_
     if (bad) atomicOr(&g_status_pages, FLAG_BOUNDS);
 }
 
-// 36 lists with up to 31 rows of a page to copy in 32 layers of 8 x 128 bf16 (155 MB read and written):
-// 24 us, 18 of them the copies; 64 lists that need 32 new pages and no copy: 8 us, two launches and the
-// plan's four dependent loads.
+// 40 lists (4 roots, 4 clones, 32 forks) with up to 24 rows of a page to copy in 32 layers of 8 x 128
+// bf16, 155 MB read and written: 24 us, 18 of them the copies (their sources are few lists' pages and come
+// from L2, so that is not what HBM moves); 64 lists that need 24 new pages and no copy: 8 us, two launches
+// and the plan's four dependent loads.
 cudaError_t launch_pages_extend(const PagesArgs& a, const int32_t* parent, const int32_t* extra, void* workspace,
                                 cudaStream_t s) {
     if (a.lists == 0) return cudaSuccess;
@@ -561,7 +562,8 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
     if (bad) atomicOr(&g_status_pages, FLAG_BOUNDS);
 }
 
-// 245 pages of 32 tokens in 32 layers of 8 x 128 e4m3 (1.04 GB read and written): 168 us, 6.2 TB/s.
+// 245 pages of 32 tokens in 32 layers of 8 x 128 e4m3 (1.04 GB read and written): 168 to 175 us from run
+// to run, 5.9 to 6.2 TB/s.
 cudaError_t launch_pages_compact(const PagesArgs& a, int32_t* live, void* workspace, cudaStream_t s) {
     const Compact c = compact_at(workspace, a.total, nullptr);
     const cudaError_t e = launch_chained(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, c, live);

@@ -218,7 +218,8 @@ void rotary_angles(const kvfix_rope& r, RotaryArgs* a) {
 // copy's bytes take 79); 8192 tokens x 40 heads of 128 in place: 29 us, 5.7 TB/s (32 with the first
 // loads behind the angles); 16 x 8 tokens x 40 heads: 3.4 us, one launch and two trips to memory.
 // Halves that vectors do not meet: 24 of 96 turned 4.5 TB/s (3.6 by single pairs), 60 of 64 3.4 (2.5),
-// 20 of 128 4.2 (4.4); all of a head by pairs: 2.1.
+// 20 of 128 4.2 (4.4); all of a head by pairs: 2.1.  In 4096 tokens x 32 layers x 8 heads: 81 us (5.0 TB/s),
+// 64 (4.2) and 102 (5.3).
 // Two or eight heads in flight, streaming loads or stores: even, or up to 10 % slower.
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
     const int heads = a.ip[0].heads + a.ip[1].heads;

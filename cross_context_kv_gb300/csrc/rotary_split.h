@@ -26,7 +26,7 @@ KVFIX_ON_BOTH int mixed_pairs(int rotary_dim) { return rotary_dim % 8 == 0 ? 4 :
 
 // The split.  A thread has a token's heads one after another, four in flight, while that leaves
 // enough threads to fill the GPU; with fewer tokens the heads are spread over 2, 4, ... threads until
-// each has one (8 x 512 tokens x 40 heads: 16.6 us, 32 if spread four times as far).  Blocks take
+// each has one (8 x 512 tokens x 40 heads: 14.3 us, about twice that if spread four times as far).  Blocks take
 // several layers (a thread's angles are used for all of them) where that leaves four blocks an SM.
 // chunks * layers * tokens is below 2^31 (and so are the blocks); sums past a size are 64 bits wide.
 inline RotarySplit rotary_split(int chunks, int layers, int tokens, int heads, int dim, int rotary_dim, bool half, bool in_place) {
