@@ -142,6 +142,28 @@ static bool rows_apart(const kvfix_kv_desc& d) {
     return true;
 }
 
+// Whether bytes [b, b + n) meet a row of a plane whose rows are apart (rows_apart).  Then rows lie in
+// the order of their places, outermost dimension first, and of those that begin before the bytes'
+// end the last one ends last.
+static bool row_meets_bytes(const void* a, const kvfix_kv_desc& d, const void* b, size_t n) {
+    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+    if (!a || !b || !n || no_rows(d) || pb + n <= pa) return false;
+    unsigned long long left = pb + n - 1 - pa, at = 0;
+    long long strides[3] = {d.stride_token, d.stride_layer, d.stride_chunk}, counts[3] = {d.tokens, d.layers, d.chunks};
+    for (int i = 0; i < 3; ++i) {
+        int most = -1;
+        for (int k = 0; k < 3; ++k)
+            if (counts[k] > 1 && (most < 0 || strides[k] > strides[most])) most = k;
+        if (most < 0) break;
+        const unsigned long long s = 2ull * (unsigned long long)strides[most], last = (unsigned long long)counts[most] - 1;
+        const unsigned long long j = left / s < last ? left / s : last;
+        at += j * s;
+        left -= j * s;
+        counts[most] = 0;
+    }
+    return pa + at + 2ull * (unsigned long long)d.kv_heads * (unsigned long long)d.head_dim > pb;
+}
+
 // Checks a pool: format, shape, strides, pointers and their alignment.
 static kvfix_status check_pool(const kvfix_pool& p, const char* fn) {
     if (p.format != KVFIX_POOL_BF16 && p.format != KVFIX_POOL_E4M3 && p.format != KVFIX_POOL_INT4)
@@ -1232,12 +1254,11 @@ kvfix_status kvfix_rotary(const kvfix_bf16* q, kvfix_kv_desc qd, const kvfix_bf1
         return fail(KVFIX_EINVAL, "%s: an output overlaps the other plane", fn);
     if ((double)ref->chunks * ref->layers * ref->tokens >= 2147483648.0)
         return fail(KVFIX_EINVAL, "%s: chunks * layers * tokens must be below 2^31", fn);
-    // blocks that end early write while others still read their positions (one row of 4-byte numbers)
-    const kvfix_kv_desc pd = {1, 1, 1, (int)((long long)ref->chunks * ref->tokens), 2, 0, 0, 0};
-    if (!no_rows(*ref))
-        for (int i = 0; i < 2; ++i)
-            if (a.op[i].heads && rows_meet(positions, pd, out[i], *dst[i]))
-                return fail(KVFIX_EINVAL, "%s: %s_out overlaps positions", fn, i ? "k" : "q");
+    // blocks that end early write while others still read their positions
+    const size_t position_bytes = 4 * (size_t)ref->chunks * (size_t)ref->tokens;
+    for (int i = 0; i < 2; ++i)
+        if (a.op[i].heads && row_meets_bytes(out[i], *dst[i], positions, position_bytes))
+            return fail(KVFIX_EINVAL, "%s: %s_out overlaps positions", fn, i ? "k" : "q");
     if ((st = check_rope(rope, ref->head_dim, fn)) != KVFIX_OK) return st;
     if (!no_rows(*ref) && !positions) return fail(KVFIX_EINVAL, "%s: positions is null", fn);
     if (!aligned4(positions)) return fail(KVFIX_EINVAL, "%s: positions must be 4-byte aligned", fn);

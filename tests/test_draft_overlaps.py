@@ -1,5 +1,7 @@
 """Index arrays of a drafting step's calls that lie where the calls write are refused: on the host, without
 a GPU."""
+import random
+
 from test_draft_calls import Rotary, at, desc, kvfix, pool, refused  # noqa: F401  (the fixture)
 
 
@@ -20,6 +22,31 @@ def test_positions_where_rows_go(kvfix):  # noqa: F811
         refused(kvfix, fn, call(rope=bad, **kw), b"rotary_dim")
     for kw in (dict(p=at(4, 636), **apart), dict(p=at(4, 780), **apart)):
         refused(kvfix, fn, call(rope=bad, **kw), b"overlaps positions")
+
+
+def test_positions_between_rows_of_any_layout(kvfix):  # noqa: F811
+    """Random layouts against the rows' addresses one by one."""
+    call, fn = Rotary(kvfix), b"kvfix_rotary"
+    r, base, seen = random.Random(5), 4 << 32, [0, 0]
+    none, bad = kvfix.KvDesc(), call.rope(rot=18)
+    for _ in range(6000):
+        C, n, L, H = r.choice((1, 2, 3)), r.choice((1, 2, 4)), r.choice((1, 2, 3)), r.choice((1, 2, 3))
+        row = 16 * H
+        dims = [("st", n), ("sl", L), ("sc", C)]
+        r.shuffle(dims)
+        strides, covered = {}, row
+        for name, count in dims:                               # one dimension inside the next, in any order
+            strides[name] = covered + 8 * r.choice((0, 0, 1, 3, 9))
+            covered = strides[name] * count
+        if n > 1 and strides["st"] < row:
+            continue
+        d = desc(kvfix, C=C, n=n, H=H, D=16, layers=L, **strides)
+        rows = [2 * (c * strides["sc"] + l * strides["sl"] + t * strides["st"]) for c in range(C) for l in range(L) for t in range(n)]
+        p, size = 4 * r.randint(-4 * C * n, covered // 2 + 4), 4 * C * n
+        meets = any(x < p + size and p < x + 2 * row for x in rows)
+        refused(kvfix, fn, call(q=1 << 32, qd=d, kd=none, p=base + p, rope=bad), b"overlaps positions" if meets else b"rotary_dim")
+        seen[meets] += 1
+    assert min(seen) > 500
 
 
 def test_numbers_of_nodes_where_results_go(kvfix):  # noqa: F811
